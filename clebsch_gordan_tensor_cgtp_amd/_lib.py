@@ -1,4 +1,5 @@
-"""ctypes binding of libcgtp.so (the C ABI declared in include/cgtp.h).
+"""ctypes binding of libcgtp.so (the C ABI declared in include/cgtp.h and
+include/cgtp_train.h).
 
 Argument marshalling only: every step of the convolution runs in the HIP
 kernels of libcgtp.so.  torch is imported first so that the library binds to
@@ -27,11 +28,20 @@ CGTP_FLAG_LOCALITY = 2
 CGTP_FLAG_SHARED_WEIGHTS = 4
 CGTP_FLAG_PATH_OUTPUTS = 8
 
+# include/cgtp_train.h
+CGTP_F32 = 0
+CGTP_BF16 = 1
+CGTP_ACT_NONE = 0
+CGTP_ACT_SILU = 1
+CGTP_ACT_TANH = 2
+
 _c_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _ip = ctypes.POINTER(ctypes.c_int)
+_int, _f32, _size = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_sp = ctypes.POINTER(ctypes.c_size_t)
 
-# name -> (restype, argtypes); mirrors include/cgtp.h
+# name -> (restype, argtypes); mirrors include/cgtp.h and include/cgtp_train.h
 SIGNATURES = {
     "cgtp_plan_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                         ctypes.c_int, ctypes.c_uint]),
@@ -59,6 +69,15 @@ SIGNATURES = {
     "cgtp_cp_conv_bwd": (ctypes.c_int, [_vp, ctypes.c_int, _c_i64, _c_i64] + [_vp] * 13 + [ctypes.c_size_t, _vp]),
     "cgtp_conv_bwd_noalloc": (ctypes.c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                              _vp]),
+    # cgtp_train.h
+    "cgtp_embed_fwd": (_int, [_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _f32, _vp, _c_i64, _vp]),
+    "cgtp_embed_bwd_workspace_size": (_int, [_int, _c_i64, _c_i64, _c_i64, _sp]),
+    "cgtp_embed_bwd": (_int, [_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64, _f32, _vp, _vp, _size, _vp]),
+    "cgtp_norm_act_workspace_size": (_int, [_int] + [_c_i64] * 4 + [_sp]),
+    "cgtp_norm_act_fwd": (_int, [_int, _int] + [_c_i64] * 4 + [_vp, _f32, _vp, _c_i64, _vp, _vp, _vp, _c_i64, _vp,
+                                                              _vp, _vp, _size, _vp]),
+    "cgtp_norm_act_bwd": (_int, [_int, _int] + [_c_i64] * 4 + [_vp, _vp, _c_i64] + [_vp] * 5 +
+                          [_c_i64, _vp, _c_i64, _vp, _vp, _vp, _size, _vp]),
     "cgtp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

@@ -1,0 +1,72 @@
+// cgtp_vec.h -- vectors of fp32 or bf16 elements in memory, fp32 in registers
+// (device code of the node-side operators).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+namespace cgtp {
+
+struct bf16_t {
+    uint16_t bits;
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float((uint32_t)v.bits << 16); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v)
+{
+    return v;
+}
+// round to nearest even (the hardware conversion)
+template <>
+__device__ __forceinline__ bf16_t from_f32<bf16_t>(float v)
+{
+    return bf16_t{__builtin_bit_cast(uint16_t, (__bf16)v)};
+}
+
+// elements of one 16-byte access
+template <class T>
+constexpr int kWide = 16 / (int)sizeof(T);
+
+// VEC consecutive elements (VEC = kWide<T>: one 16-byte access; VEC = 1: one element)
+template <class T, int VEC>
+__device__ __forceinline__ void load_vec(float (&v)[VEC], const T* __restrict__ p)
+{
+    if constexpr (VEC == 1) {
+        v[0] = to_f32(p[0]);
+    } else {
+        struct alignas(16) Pack {
+            T e[VEC];
+        };
+        const Pack q = *reinterpret_cast<const Pack*>(p);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = to_f32(q.e[j]);
+    }
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[VEC])
+{
+    if constexpr (VEC == 1) {
+        p[0] = from_f32<T>(v[0]);
+    } else {
+        struct alignas(16) Pack {
+            T e[VEC];
+        } q;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) q.e[j] = from_f32<T>(v[j]);
+        *reinterpret_cast<Pack*>(p) = q;
+    }
+}
+
+inline bool aligned_rows(const void* p, int64_t ld, int64_t elem)
+{
+    return ((uintptr_t)p & 15u) == 0 && ld * elem % 16 == 0;
+}
+
+}  // namespace cgtp

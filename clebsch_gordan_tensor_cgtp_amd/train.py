@@ -1,0 +1,243 @@
+"""The node-side operators of a training step, over the C ABI of
+include/cgtp_train.h: embedding of species (token) ids and its gradient, group
+normalisation with an activation over ragged segments and its gradient.
+
+Each function checks types, devices and shapes, allocates outputs and
+workspace with torch (device memory only) unless they are given, and calls the
+library on the current HIP stream of the arrays' device.  Large arrays are
+float32 or bfloat16; statistics, gamma, beta and their gradients float32;
+indices int32.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib as L
+
+_DTYPES = {torch.float32: L.CGTP_F32, torch.bfloat16: L.CGTP_BF16}
+_ACTS = {"none": L.CGTP_ACT_NONE, "silu": L.CGTP_ACT_SILU, "tanh": L.CGTP_ACT_TANH}
+
+
+def _dtype(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return d
+
+
+def _need(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name):
+    """Row stride of an array of rows: [N][C], or [B][S][C] with one stride for
+    all rows; the channels are contiguous."""
+    shape, stride = t.shape, t.stride()
+    width = shape[-1]
+    if width > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    n = t.numel() // width if width else 0
+    if n <= 1:
+        return width
+    if len(shape) == 2:
+        ld = stride[0]
+    elif shape[1] > 1:
+        ld = stride[1]
+        if shape[0] > 1 and stride[0] != ld * shape[1]:
+            raise ValueError(f"{name}: rows must be equally spaced")
+    else:
+        ld = stride[0]
+    if ld < width:
+        raise ValueError(f"{name}: rows overlap")
+    return ld
+
+
+def _like(t, name, dtype, shape, device):
+    """An array of rows given by the caller: type, device and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _workspace(ws, nbytes, device):
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous torch.uint8 tensor")
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, expected {device}")
+    return ws
+
+
+def _call(name, device, *args):
+    """The library call `name` on the device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs arrays on a GPU, got {device}")
+    f = getattr(L.lib(), name)
+    if device.index == torch.cuda.current_device():
+        L.check(name, f(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            L.check(name, f(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _bytes(name, *args):
+    b = ctypes.c_size_t()
+    L.check(name, getattr(L.lib(), name)(*args, ctypes.byref(b)))
+    return b.value
+
+
+# ---- embedding -------------------------------------------------------------------
+def embed_fwd(ids, table, scale: float = 1.0, out=None) -> torch.Tensor:
+    """out[n] = scale * table[ids[n]], zeros where ids[n] is outside the table
+    (padding).  ids [N] int32, table [V][C]; ``out`` [N][C] may be a view with
+    a row stride, such as the l = 0 rows ``x[:, 0, :]`` of node features."""
+    d = _dtype(table, "table")
+    if table.dim() != 2:
+        raise ValueError("table must be [V][C]")
+    V, C, dev = table.shape[0], table.shape[1], table.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise TypeError("ids must be a torch.Tensor [N]")
+    N = ids.shape[0]
+    _need(ids, "ids", torch.int32, (N,), dev)
+    _need(table, "table", table.dtype, (V, C), dev)
+    if out is None:
+        out = torch.empty((N, C), dtype=table.dtype, device=dev)
+    else:
+        _like(out, "out", table.dtype, (N, C), dev)
+    _call("cgtp_embed_fwd", dev, d, N, V, C, ids.data_ptr(), table.data_ptr(), scale, out.data_ptr(),
+          _rows(out, "out"))
+    return out
+
+
+def embed_bwd_workspace_size(dtype, n_rows: int, table_rows: int, channels: int) -> int:
+    return _bytes("cgtp_embed_bwd_workspace_size", _DTYPES[dtype], n_rows, table_rows, channels)
+
+
+def embed_bwd(ids, grad_out, table_rows: int, scale: float = 1.0, grad_table=None, ws=None) -> torch.Tensor:
+    """grad_table[v] = scale * sum of grad_out[n] over the n with ids[n] = v
+    (zeros for rows that no id names; ids outside the table are ignored), of
+    <grad_out, embed_fwd(ids, table, scale)>.  grad_out [N][C] may have a row
+    stride; every row of grad_table [table_rows][C] is written."""
+    d = _dtype(grad_out, "grad_out")
+    if grad_out.dim() != 2:
+        raise ValueError("grad_out must be [N][C]")
+    N, C, dev = grad_out.shape[0], grad_out.shape[1], grad_out.device
+    _need(ids, "ids", torch.int32, (N,), dev)
+    ld = _rows(grad_out, "grad_out")
+    nbytes = _bytes("cgtp_embed_bwd_workspace_size", d, N, table_rows, C)
+    if grad_table is None:
+        grad_table = torch.empty((table_rows, C), dtype=grad_out.dtype, device=dev)
+    else:
+        _need(grad_table, "grad_table", grad_out.dtype, (table_rows, C), dev)
+    ws = _workspace(ws, nbytes, dev)
+    _call("cgtp_embed_bwd", dev, d, N, table_rows, C, ids.data_ptr(), grad_out.data_ptr(), ld, scale,
+          grad_table.data_ptr(), ws.data_ptr(), ws.numel())
+    return grad_table
+
+
+# ---- group normalisation with an activation ------------------------------------------
+def _norm_shape(x, groups, seg_ptr):
+    """(N, B, C) of [N][C] rows (one segment, or seg_ptr's) or [B][S][C] rows
+    (B segments of S rows)."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [N][C] or [B][S][C]")
+    C = x.shape[-1]
+    if groups < 1 or C % groups:
+        raise ValueError(f"groups = {groups} does not divide the {C} channels")
+    if seg_ptr is None:
+        return (x.shape[0], 1, C) if x.dim() == 2 else (x.shape[0] * x.shape[1], x.shape[0], C)
+    if x.dim() != 2:
+        raise ValueError("seg_ptr needs x as [N][C]")
+    if not isinstance(seg_ptr, torch.Tensor) or seg_ptr.dim() != 1 or seg_ptr.shape[0] < 1:
+        raise TypeError("seg_ptr must be a torch.Tensor [segments + 1]")
+    _need(seg_ptr, "seg_ptr", torch.int32, seg_ptr.shape, x.device)
+    return x.shape[0], seg_ptr.shape[0] - 1, C
+
+
+def _act(act):
+    a = _ACTS.get(act)
+    if a is None:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return a
+
+
+def _channel(t, name, C, dev):
+    if t is None:
+        return None
+    _need(t, name, torch.float32, (C,), dev)
+    return t.data_ptr()
+
+
+def norm_act_workspace_size(dtype, n_rows: int, n_segments: int, channels: int, groups: int) -> int:
+    return _bytes("cgtp_norm_act_workspace_size", _DTYPES[dtype], n_rows, n_segments, channels, groups)
+
+
+def norm_act_fwd(x, gamma, beta, groups: int, seg_ptr=None, eps: float = 1e-5, act: str = "silu", out=None, ws=None):
+    """(y, mean, rstd): y = act((x - mean) * rstd * gamma + beta) with the mean
+    and deviation of each segment's groups of channels.
+
+    x: [N][C] rows cut into segments by ``seg_ptr`` [B+1] int32 (the atoms of
+    each structure of a batch; one segment without it), or [B][S][C] equal
+    segments; rows may have a stride (``features[:, 0, :]``).  gamma, beta [C]
+    float32 or None (ones, zeros).  act: "none", "silu" or "tanh".  mean and
+    rstd are [B][groups] float32."""
+    d = _dtype(x, "x")
+    N, B, C = _norm_shape(x, groups, seg_ptr)
+    dev = x.device
+    ldx = _rows(x, "x")
+    g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
+    nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _like(out, "out", x.dtype, x.shape, dev)
+    stats = torch.empty((2, B, groups), dtype=torch.float32, device=dev)
+    mean, rstd = stats.unbind(0)
+    ws = _workspace(ws, nbytes, dev)
+    _call("cgtp_norm_act_fwd", dev, d, _act(act), N, B, C, groups, None if seg_ptr is None else seg_ptr.data_ptr(),
+          eps, x.data_ptr(), ldx, g, b, out.data_ptr(), _rows(out, "out"), mean.data_ptr(), rstd.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return out, mean, rstd
+
+
+def norm_act_bwd(x, mean, rstd, gamma, beta, grad_y, groups: int, seg_ptr=None, act: str = "silu",
+                 want=("x", "gamma", "beta"), ws=None):
+    """(grad_x, grad_gamma, grad_beta) of <grad_y, y> for norm_act_fwd's y on
+    the same arguments and its mean and rstd; a gradient not in ``want`` comes
+    back as None."""
+    d = _dtype(x, "x")
+    N, B, C = _norm_shape(x, groups, seg_ptr)
+    dev = x.device
+    _like(grad_y, "grad_y", x.dtype, x.shape, dev)
+    _need(mean, "mean", torch.float32, (B, groups), dev)
+    _need(rstd, "rstd", torch.float32, (B, groups), dev)
+    g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
+    ldx, ldy = _rows(x, "x"), _rows(grad_y, "grad_y")
+    nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups)
+    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if "x" in want else None
+    gg = torch.empty(C, dtype=torch.float32, device=dev) if "gamma" in want else None
+    gb = torch.empty(C, dtype=torch.float32, device=dev) if "beta" in want else None
+    ws = _workspace(ws, nbytes, dev)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call("cgtp_norm_act_bwd", dev, d, _act(act), N, B, C, groups, ptr(seg_ptr), x.data_ptr(), ldx, mean.data_ptr(),
+          rstd.data_ptr(), g, b, grad_y.data_ptr(), ldy, ptr(gx), C, ptr(gg), ptr(gb), ws.data_ptr(), ws.numel())
+    return gx, gg, gb

@@ -1,0 +1,244 @@
+"""GPU parity of the group normalisation with an activation, forward and
+backward, against the oracle in 64 bits.
+
+Tolerances, in units u = 2^-24.  mean and rstd are fp64 sums rounded once:
+mean within 2 u |mean| (+ 2 u), rstd within 2 u rstd plus the fp64
+cancellation.  An element passes through x - mean (the rounded mean is off by
+u |mean|), two products, an addition and an activation with slope at most 1.1
+whose own evaluation is good to about 8 u max(1, |z|): in all at most
+16 u (|gamma| (1 + |xhat| + |mean| rstd) + |beta| + 1).  dx goes through the
+same chain times |dy| and rstd, plus the group means: 32 u rstd (|h| + |s1| +
+|xhat s2| + the mean term).  The channel sums add n such terms in fp64.  bf16
+results carry 2^-9 relative on top.
+"""
+import numpy as np
+import pytest
+
+from tests import train_oracle as T
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def tt():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch, torch.device("cuda:0")
+
+
+def lengths(rng, kind, N, B):
+    if kind == "equal":
+        assert N % B == 0
+        return np.full(B, N // B)
+    if kind == "one":
+        v = np.zeros(B, np.int64)
+        v[B // 2] = N
+        return v
+    w = rng.random(B) ** 4 + 1e-9
+    w[rng.random(B) < 0.3] = 0
+    w[0] += 1e-9
+    cut = np.floor(np.cumsum(w) / w.sum() * N).astype(np.int64)
+    cut[-1] = N
+    return np.diff(np.concatenate([[0], cut]))
+
+
+def bounds(x, gamma, beta, grad, ptr, G, eps, kind):
+    """(tolerances of y, of dx, of dgamma and of dbeta before rounding to bf16)"""
+    C = x.shape[1]
+    mean, rstd = T.norm_stats(x, ptr, G, eps)
+    mu, rs = T._spread(mean, ptr, C), T._spread(rstd, ptr, C)
+    xhat = np.abs((x - mu) * rs)
+    off = 1 + xhat + np.abs(mu) * rs
+    ty = 16 * U * (np.abs(gamma) * off + np.abs(beta) + 1)
+    e = np.abs(grad) * (1 + ty / U / 16)     # |dz| and what an error of z does to it
+    h = e * np.abs(gamma)
+    s = np.zeros_like(h)
+    for i, j in zip(ptr, ptr[1:]):
+        if j > i:
+            hs, xs = (v[i:j].reshape(j - i, G, C // G) for v in (h, off))
+            s[i:j] = (hs.mean((0, 2), keepdims=True) + xs * (hs * xs).mean((0, 2), keepdims=True)).reshape(j - i, C)
+    return ty, 32 * U * rs * (h * off + s), 32 * U * (e * off).sum(0), 32 * U * e.sum(0)
+
+
+CASES = [("equal", 1, 1, 1, 1, 1), ("equal", 4, 4, 8, 2, 1), ("equal", 6, 2, 128, 8, 1), ("one", 2000, 1, 128, 8, 9),
+         ("ragged", 2500, 100, 128, 8, 1), ("ragged", 777, 300, 96, 32, 4), ("ragged", 3000, 3, 40, 8, 1),
+         ("ragged", 500, 7, 6, 2, 1), ("ragged", 401, 5, 30, 10, 2), ("equal", 35000, 5, 16, 1, 1),
+         ("ragged", 300, 4, 1536, 3, 1), ("ragged", 200, 3, 2050, 2, 1), ("ragged", 90, 2, 4104, 1, 1),
+         ("one", 70, 2000, 24, 4, 1), ("ragged", 1, 3, 8, 8, 1), ("ragged", 65000, 30, 8, 8, 1),
+         ("ragged", 2048, 1500, 64, 64, 1), ("equal", 300, 3, 333, 9, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("k", range(len(CASES)))
+def test_norm(tt, k, dtype):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    kind, N, B, C, G, pitch = CASES[k]
+    act, eps = ("none", "silu", "tanh")[k % 3], 1e-5
+    print(f"[norm] {kind} N={N} B={B} C={C} G={G} pitch={pitch} {act} {dtype}", flush=True)
+    rng = np.random.default_rng(k)
+    ptr = np.concatenate([[0], np.cumsum(lengths(rng, kind, N, B))])
+    q = T.bf16 if dtype == "bf16" else (lambda v: v.astype(np.float32))
+    x = q(rng.standard_normal((N, C)) * (0.5 + rng.random(C)) + 2 * rng.standard_normal(C))
+    grad = q(rng.standard_normal((N, C)))
+    gamma, beta = ((1 + 0.3 * rng.standard_normal(C)).astype(np.float32), rng.standard_normal(C).astype(np.float32))
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+
+    def rows(v):        # every pitch-th row of a wider array
+        t = torch.full((N, pitch, C), float("nan"), dtype=dt, device=dev)
+        t[:, 0, :] = torch.from_numpy(v).to(dev)
+        return t[:, 0, :]
+
+    tx, tg = rows(x), rows(grad)
+    seg = torch.from_numpy(ptr.astype(np.int32)).to(dev)
+    if kind == "equal":
+        tx, tg, seg = tx.view(B, N // B, C), tg.view(B, N // B, C), None
+    tgm, tbt = torch.from_numpy(gamma).to(dev), torch.from_numpy(beta).to(dev)
+    y, mean, rstd = cg.norm_act_fwd(tx, tgm, tbt, G, seg, eps, act)
+    dx, dg, db = cg.norm_act_bwd(tx, mean, rstd, tgm, tbt, tg, G, seg, act)
+    wy, wm, wr = T.norm_fwd(x, gamma, beta, ptr, G, eps, act)
+    wdx, wdg, wdb = T.norm_bwd(x, gamma, beta, grad, ptr, G, eps, act)
+    ty, tdx, tdg, tdb = bounds(x.astype(np.float64), gamma, beta, grad, ptr, G, eps, act)
+    r = 2.0 ** -8 if dtype == "bf16" else 2 * U
+    for name, got, want, tol in (("mean", mean, wm, 2 * U * np.abs(wm) + 2 * U), ("rstd", rstd, wr, 4 * U * wr),
+                                 ("y", y, wy, ty + r * np.abs(wy)), ("dx", dx, wdx, tdx + r * np.abs(wdx)),
+                                 ("dgamma", dg, wdg, tdg + 2 * U * np.abs(wdg)),
+                                 ("dbeta", db, wdb, tdb + 2 * U * np.abs(wdb))):
+        g = got.float().cpu().numpy().astype(np.float64).reshape(want.shape)
+        err = np.abs(g - want)
+        assert np.all(err <= tol), (name, float((err / np.maximum(tol, 1e-300)).max()))
+    again = cg.norm_act_bwd(tx, mean, rstd, tgm, tbt, tg, G, seg, act)
+    assert torch.equal(y, cg.norm_act_fwd(tx, tgm, tbt, G, seg, eps, act)[0])
+    assert all(torch.equal(u, v) for u, v in zip((dx, dg, db), again))
+
+
+def test_norm_without_affine_and_partial_gradients(tt):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x, g = torch.randn(300, 64, device=dev), torch.randn(300, 64, device=dev)
+    one, zero = torch.ones(64, device=dev), torch.zeros(64, device=dev)
+    y, m, r = cg.norm_act_fwd(x, None, None, 4)
+    assert torch.equal(y, cg.norm_act_fwd(x, one, zero, 4)[0])
+    full = cg.norm_act_bwd(x, m, r, one, zero, g, 4)
+    for want in (("x",), ("gamma",), ("beta",), ("x", "beta"), ()):
+        got = cg.norm_act_bwd(x, m, r, None, None, g, 4, want=want)
+        for name, a, b in zip(("x", "gamma", "beta"), got, full):
+            assert (a is None) == (name not in want)
+            assert a is None or torch.equal(a, b), name
+
+
+def test_norm_of_no_rows(tt):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x, w = torch.zeros(0, 16, device=dev), torch.ones(16, device=dev)
+    seg = torch.zeros(4, dtype=torch.int32, device=dev)
+    y, m, r = cg.norm_act_fwd(x, w, w, 2, seg, eps=0.25)
+    assert y.shape == (0, 16) and (m == 0).all() and (r == 2).all()
+    dx, dg, db = cg.norm_act_bwd(x, m, r, w, w, x, 2, seg)
+    assert dx.shape == (0, 16) and (dg == 0).all() and (db == 0).all()
+    y, m, r = cg.norm_act_fwd(x, w, w, 2, seg[:1])
+    assert y.shape == (0, 16) and m.shape == (0, 2)
+    assert all((t == 0).all() for t in cg.norm_act_bwd(x, m, r, w, w, x, 2, seg[:1])[1:])
+
+
+def test_norm_keeps_nonfinite_values_in_their_group(tt):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x = torch.randn(90, 32, device=dev)
+    seg = torch.tensor([0, 30, 60, 90], dtype=torch.int32, device=dev)
+    w = torch.ones(32, device=dev)
+    ref, rm, rr = cg.norm_act_fwd(x, w, w, 4, seg)
+    x[40, 9], x[70, 31] = float("nan"), float("inf")
+    y, m, r = cg.norm_act_fwd(x, w, w, 4, seg)
+    hit = torch.zeros(90, 32, dtype=torch.bool, device=dev)
+    hit[30:60, 8:16] = True
+    hit[60:90, 24:32] = True
+    assert torch.equal(y[~hit], ref[~hit]) and torch.isnan(y[30:60, 8:16]).all() and torch.isnan(y[60:90, 24:32]).all()
+    bad = torch.zeros(3, 4, dtype=torch.bool, device=dev)
+    bad[1, 1] = bad[2, 3] = True
+    assert torch.equal(m[~bad], rm[~bad]) and torch.equal(r[~bad], rr[~bad])
+
+
+def test_norm_large_offset(tt):
+    """Values far from zero beside their spread: the variance is formed in 64
+    bits, so only the mean's own rounding is lost."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    rng = np.random.default_rng(8)
+    x = (1000 + 0.01 * rng.standard_normal((512, 16))).astype(np.float32)
+    one = np.ones(16)
+    y, m, r = cg.norm_act_fwd(torch.from_numpy(x).to(dev), None, None, 2, act="none", eps=1e-8)
+    wy, wm, wr = T.norm_fwd(x, one, 0 * one, np.array([0, 512]), 2, 1e-8, "none")
+    assert np.abs(r.cpu().numpy() / wr - 1).max() <= 4 * U + 512 * 8 * 2.0 ** -53 * 1e6 / 1e-4
+    err = np.abs(y.cpu().numpy() - wy)
+    assert np.all(err <= 16 * U * (2 + np.abs(wy) + np.abs(wm).max() * wr.max()))
+
+
+def test_norm_malformed_offsets_stay_in_bounds(tt):
+    """Offsets that break the precondition (unsorted, beyond the rows,
+    negative): every index is clamped, the call returns."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x, w = torch.randn(200, 32, device=dev), torch.ones(32, device=dev)
+    for bad in ([0, 150, 50, 200], [0, 500, 700, 900], [-5, -3, 10, 2000], [200, 200, 200, 200], [0, 0, 0, 0]):
+        seg = torch.tensor(bad, dtype=torch.int32, device=dev)
+        y, m, r = cg.norm_act_fwd(x, w, w, 4, seg)
+        cg.norm_act_bwd(x, torch.zeros(3, 4, device=dev), torch.ones(3, 4, device=dev), w, w, x, 4, seg)
+        torch.cuda.synchronize()
+        assert y.shape == x.shape
+
+
+def test_norm_gradient_against_differences(tt):
+    """The GPU gradients' product with a direction is the difference quotient
+    of the oracle's forward along it (step 1e-5 in 64 bits: error about 1e-9)."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    rng = np.random.default_rng(21)
+    ptr, G, C = np.array([0, 50, 50, 51, 140]), 4, 32
+    x, g = (rng.standard_normal((140, C)).astype(np.float32) for _ in range(2))
+    gamma, beta = (rng.standard_normal(C).astype(np.float32) for _ in range(2))
+    t = [torch.from_numpy(v).to(dev) for v in (x, gamma, beta, g, ptr.astype(np.int32))]
+    y, m, r = cg.norm_act_fwd(t[0], t[1], t[2], G, t[4], 1e-3, "silu")
+    grads = cg.norm_act_bwd(t[0], m, r, t[1], t[2], t[3], G, t[4], "silu")
+    _, tdx, tdg, tdb = bounds(x.astype(np.float64), gamma, beta, g, ptr, G, 1e-3, "silu")
+    for k, (got, tol) in enumerate(zip(grads, (tdx, tdg, tdb))):
+        args = [v.astype(np.float64) for v in (x, gamma, beta)]
+        d, at, h = rng.standard_normal(args[k].shape), args[k], 1e-5
+
+        def f(v):
+            args[k] = v
+            return (g.astype(np.float64) * T.norm_fwd(*args, ptr, G, 1e-3, "silu")[0]).sum()
+
+        want = (f(at + h * d) - f(at - h * d)) / (2 * h)
+        assert abs((got.double().cpu().numpy() * d).sum() - want) <= (tol * np.abs(d)).sum() + 1e-6 * abs(want), k
+
+
+def test_norm_on_another_stream_and_in_a_graph(tt):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x, g = torch.randn(1000, 64, device=dev), torch.randn(1000, 64, device=dev)
+    w = torch.randn(64, device=dev)
+    seg = torch.tensor([0, 10, 10, 700, 1000], dtype=torch.int32, device=dev)
+    step = lambda: (lambda y, m, r: (y, m, r) + cg.norm_act_bwd(x, m, r, w, w, g, 8, seg))(  # noqa: E731
+        *cg.norm_act_fwd(x, w, w, 8, seg))
+    want = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for k in range(3):
+        x.copy_(torch.randn(1000, 64, device=dev) + k)
+        seg.copy_(torch.tensor([0, 300 * k, 900, 900, 1000], dtype=torch.int32, device=dev))
+        for o in outs:
+            o.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, step())), k
