@@ -6,7 +6,7 @@ node-side operators of a training step (include/cgtp_train.h) are the functions
 of ``train``.  The library is loaded on first use and its absence raises.
 """
 _TRAIN = ("embed_fwd", "embed_bwd", "embed_bwd_workspace_size", "norm_act_fwd", "norm_act_bwd",
-          "norm_act_workspace_size")
+          "norm_act_workspace_size", "orthogonalize", "orthogonalize_workspace_size")
 
 
 def __getattr__(name):

@@ -78,6 +78,9 @@ SIGNATURES = {
                                                               _vp, _vp, _size, _vp]),
     "cgtp_norm_act_bwd": (_int, [_int, _int] + [_c_i64] * 4 + [_vp, _vp, _c_i64] + [_vp] * 5 +
                           [_c_i64, _vp, _c_i64, _vp, _vp, _vp, _size, _vp]),
+    "cgtp_orthogonalize_workspace_size": (_int, [_int] + [_c_i64] * 3 + [_sp]),
+    "cgtp_orthogonalize": (_int, [_int] + [_c_i64] * 3 + [_int] + [ctypes.c_double] * 3 + [_f32, _f32, _vp, _vp, _vp,
+                                                                                        _size, _vp]),
     "cgtp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

@@ -1,0 +1,453 @@
+// cgtp_ortho.hip -- orthogonalised updates by Newton-Schulz products on the
+// fp16 matrix cores.
+//
+//   X = G / (||G||_F + eps), then `steps` times
+//   A = X X^T,  B = b A + c A A,  X <- a X + B X
+// on the orientation whose rows are the shorter side (s <= t), so that every
+// singular value x of X becomes a x + b x^3 + c x^5.
+//
+// Precision.  Each operand v is kept as two fp16 numbers, h = fp16(v k) and
+// l = fp16(v k - h), with a power of two k that places the operand's bound at
+// 2^14..2^15: the spectral norm is at most ||X||_F = ||G||_F / (||G||_F + eps) at
+// the start and follows the polynomial's maximum from step to step.  h + l holds 24
+// bits of every value down to 2^-16 of the bound, as fp32 does, and
+//   u v = (hu hv + hu lv + lu hv) / k^2
+// leaves out lu lv only, 2^-24 of the product.  Three fp16 products with fp32
+// accumulation so give what an fp32 product gives, at a third of the fp16 rate
+// instead of the sixteenth that fp32 matrix instructions reach.
+//
+// Layout.  An operand row of K values is cut into blocks of 32: 32 h, then
+// their 32 l, one 128-byte line.  All products are "rows times rows": D[i][j] =
+// sum_k P[i][k] Q[j][k] with k contiguous in both; A and B are symmetric, and X
+// is kept as it is and transposed.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "cgtp_internal.h"
+#include "cgtp_train_internal.h"
+#include "cgtp_vec.h"
+
+namespace cgtp {
+namespace {
+
+constexpr int kThreads = 256;
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// offset of element k of a split row (its low half is 32 further on)
+__device__ __forceinline__ int64_t split_at(int64_t k) { return (k >> 5) * 64 + (k & 31); }
+
+__device__ __forceinline__ void split(float v, _Float16& h, _Float16& l)
+{
+    h = (_Float16)v;
+    l = (_Float16)(v - (float)h);
+}
+
+// ---- units ------------------------------------------------------------------------------
+// Bounds of a step: |x| <= M for every singular value gives |a x + b x^3 + c x^5|
+// <= next, and |b y + c y^2| <= poly for y = x^2.
+struct Bounds {
+    double next, poly;
+};
+
+__host__ __device__ inline Bounds step_bounds(double a, double b, double c, double M)
+{
+    auto p = [&](double x) { return fabs(x * (a + x * x * (b + c * x * x))); };
+    auto q = [&](double y) { return fabs(y * (b + c * y)); };
+    Bounds r{p(M), q(M * M)};
+    // p' = a + 3 b y + 5 c y^2 at y = x^2; q' = b + 2 c y
+    auto at = [&](double y) {
+        if (y > 0.0 && y < M * M) r.next = fmax(r.next, p(sqrt(y)));
+    };
+    if (c != 0.0) {
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        if (disc >= 0.0) {
+            at((-3.0 * b + sqrt(disc)) / (10.0 * c));
+            at((-3.0 * b - sqrt(disc)) / (10.0 * c));
+        }
+        const double y = -b / (2.0 * c);
+        if (y > 0.0 && y < M * M) r.poly = fmax(r.poly, q(y));
+    } else if (b != 0.0) {
+        at(-a / (3.0 * b));
+    }
+    return r;
+}
+
+// the power of two that takes `bound` to 2^14 .. 2^15 (1 for a zero or NaN bound)
+__host__ __device__ inline double unit_of(double bound)
+{
+    if (!(bound > 0.0) || !(bound < 1e300)) return 1.0;
+    int e;
+    frexp(bound, &e);  // bound = f 2^e, f in [0.5, 1)
+    return ldexp(1.0, 15 - e);
+}
+
+// Factors of one step's three products, from its operands' units to its results':
+// A = gram * XX, B = sq * AA + lin * A, X' = mul * BX + add * X.
+struct Units {
+    float gram, sq, lin, mul, add;
+};
+
+// The steps' factors for a matrix whose first iterate has Frobenius norm r (at
+// most 1; far below it where eps exceeds the norm).
+__device__ inline void step_units(const OrthoPoly& p, double r, Units* __restrict__ u)
+{
+    double M = r, kx = unit_of(r);
+    for (int k = 0; k < p.steps; ++k) {
+        const Bounds bd = step_bounds(p.a, p.b, p.c, M);
+        const double ka = unit_of(M * M), kb = unit_of(bd.poly);
+        const double kn = k + 1 < p.steps ? unit_of(bd.next) : (double)p.scale;
+        u[k] = Units{(float)(ka / kx / kx), (float)(p.c * kb / ka / ka), (float)(p.b * kb / ka),
+                     (float)(kn / kb / kx), (float)(p.a * kn / kx)};
+        M = bd.next;
+        kx = kn;
+    }
+}
+
+
+// ---- norms and the first X ---------------------------------------------------------------
+constexpr int kNormBlocks = 64;  // partial sums per matrix, at most
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_ortho_norm(int64_t size, int32_t per, const T* __restrict__ G,
+                                                         double* __restrict__ part)
+{
+    __shared__ double s[kThreads];
+    const int64_t b = blockIdx.x / per, k = blockIdx.x % per;
+    const int64_t each = (size + per - 1) / per;
+    const int64_t i0 = k * each, i1 = i0 + each < size ? i0 + each : size;
+    const T* p = G + b * size;
+    double t = 0.0;
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+        const double v = (double)to_f32(p[i]);
+        t += v * v;
+    }
+    s[threadIdx.x] = t;
+    __syncthreads();
+    for (int d = kThreads / 2; d > 0; d /= 2) {
+        if ((int)threadIdx.x < d) s[threadIdx.x] += s[threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) part[blockIdx.x] = s[0];
+}
+
+// X and X^T of one 64 x 64 tile, split, zero outside the matrix; the first tile
+// of a matrix leaves its steps' factors
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly poly, int32_t per,
+                                                          const double* __restrict__ part, const T* __restrict__ G,
+                                                          _Float16* __restrict__ X, _Float16* __restrict__ Xt,
+                                                          Units* __restrict__ units)
+{
+    __shared__ float tile[64][65];
+    const int64_t ti = d.sp / 64, tj = d.tp / 64;
+    const int64_t b = blockIdx.x / (ti * tj), r = blockIdx.x % (ti * tj);
+    const int64_t i0 = r / tj * 64, j0 = r % tj * 64;
+    double sum = 0.0;
+    for (int32_t q = 0; q < per; ++q) sum += part[b * per + q];
+    const double norm = sqrt(sum), den = norm + (double)poly.eps;
+    const double inv = unit_of(norm / den) / den;
+    if (r == 0 && threadIdx.x == 0) step_units(poly, norm / den, units + b * poly.steps);
+    const T* g = G + b * d.s * d.t;
+    for (int q = threadIdx.x; q < 64 * 64; q += kThreads) {
+        const int a = q / 64, c = q % 64;  // c runs along G's rows
+        const int64_t i = i0 + (d.tall ? c : a), j = j0 + (d.tall ? a : c);
+        float v = 0.0f;
+        if (i < d.s && j < d.t) v = (float)((double)to_f32(g[d.tall ? j * d.s + i : i * d.t + j]) * inv);
+        tile[d.tall ? c : a][d.tall ? a : c] = v;
+    }
+    __syncthreads();
+    X += b * d.sp * d.tp * 2;
+    Xt += b * d.sp * d.tp * 2;
+    for (int q = threadIdx.x; q < 64 * 64; q += kThreads) {
+        const int a = q / 64, c = q % 64;
+        _Float16 h, l;
+        split(tile[a][c], h, l);
+        _Float16* p = X + (i0 + a) * d.tp * 2 + split_at(j0 + c);
+        p[0] = h;
+        p[32] = l;
+        split(tile[c][a], h, l);
+        p = Xt + (j0 + a) * d.sp * 2 + split_at(i0 + c);
+        p[0] = h;
+        p[32] = l;
+    }
+}
+
+// ---- products ----------------------------------------------------------------------------
+enum : int { kGram = 0, kPoly = 1, kNext = 2, kLast = 3 };
+
+struct ProdArgs {
+    OrthoDims d;
+    int64_t K;          // contraction length (padded)
+    int64_t ti, tj;     // tiles along i and j; tj = 0: the upper triangle of ti x ti
+    const _Float16 *P, *Q;
+    const _Float16* E;  // kPoly: A; kNext, kLast: X^T (rows j)
+    _Float16 *R, *Rt;   // results, [i][j] and [j][i]
+    void* out;          // kLast: O in G's layout
+    const Units* units; // this step's factors, `steps` apart for each matrix
+    int32_t steps;
+};
+
+// One TILE x TILE tile of D = P Q^T, four waves of (TILE/2)^2 each, 32 k at a
+// time through two LDS buffers.
+template <int TILE, int KIND, class T>
+__global__ void __launch_bounds__(kThreads) k_ortho_prod(ProdArgs a)
+{
+    constexpr int W = TILE / 64;  // 32 x 32 tiles per wave and side
+    constexpr int kRowHalves = 64;
+    __shared__ __attribute__((aligned(16))) _Float16 lds[2][2][TILE * kRowHalves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const bool upper = a.tj == 0;
+    const int64_t tiles = upper ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
+    const int64_t b = blockIdx.x / tiles;
+    int64_t r = blockIdx.x % tiles, bi, bj;
+    if (upper) {  // r counts the tiles (bi, bj), bi <= bj, column by column
+        bj = 0;
+        while (r > bj) r -= ++bj;
+        bi = r;
+    } else {
+        bi = r % a.ti;
+        bj = r / a.ti;
+    }
+    const OrthoDims& d = a.d;
+    const int64_t rowsP = d.sp, rowsQ = KIND == kNext || KIND == kLast ? d.tp : d.sp;
+    const _Float16* P = a.P + (b * rowsP + bi * TILE) * a.K * 2;
+    const _Float16* Q = a.Q + (b * rowsQ + bj * TILE) * a.K * 2;
+
+    f16v acc[W][W];
+#pragma unroll
+    for (int x = 0; x < W; ++x)
+#pragma unroll
+        for (int y = 0; y < W; ++y)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[x][y][q] = 0.0f;
+
+    // 16-byte piece c of row r sits at piece c ^ (r & 7), so that the reads of
+    // eight rows at one k spread over all banks
+    constexpr int kPieces = TILE * 8 / kThreads;
+    uint4 ra[kPieces], rb[kPieces];
+    auto load = [&](int64_t kb) {
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            const int p = q * kThreads + tid, row = p / 8, c = p % 8;
+            ra[q] = *reinterpret_cast<const uint4*>(P + row * a.K * 2 + kb * 64 + c * 8);
+            rb[q] = *reinterpret_cast<const uint4*>(Q + row * a.K * 2 + kb * 64 + c * 8);
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            const int p = q * kThreads + tid, row = p / 8, c = p % 8;
+            const int at = row * kRowHalves + ((c ^ (row & 7)) * 8);
+            *reinterpret_cast<uint4*>(&lds[buf][0][at]) = ra[q];
+            *reinterpret_cast<uint4*>(&lds[buf][1][at]) = rb[q];
+        }
+    };
+    const int wi = (wave >> 1) * 32 * W, wj = (wave & 1) * 32 * W;
+    auto read = [&](int buf, int op, int row, int piece) {
+        return *reinterpret_cast<const h8*>(&lds[buf][op][row * kRowHalves + ((piece ^ (row & 7)) * 8)]);
+    };
+    const int64_t nk = a.K / 32;
+    load(0);
+    for (int64_t kb = 0; kb < nk; ++kb) {
+        const int buf = (int)(kb & 1);
+        // this buffer was last read two blocks ago, before the last barrier
+        put(buf);
+        __syncthreads();
+        if (kb + 1 < nk) load(kb + 1);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            h8 ph[W], pl[W], qh[W], ql[W];
+            const int piece = ks * 2 + (lane >> 5);
+#pragma unroll
+            for (int x = 0; x < W; ++x) {
+                const int ri = wi + 32 * x + (lane & 31), rj = wj + 32 * x + (lane & 31);
+                ph[x] = read(buf, 0, ri, piece);
+                pl[x] = read(buf, 0, ri, piece + 4);
+                qh[x] = read(buf, 1, rj, piece);
+                ql[x] = read(buf, 1, rj, piece + 4);
+            }
+#pragma unroll
+            for (int x = 0; x < W; ++x)
+#pragma unroll
+                for (int y = 0; y < W; ++y) {
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql[y], acc[x][y], 0, 0, 0);
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh[y], acc[x][y], 0, 0, 0);
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh[y], acc[x][y], 0, 0, 0);
+                }
+        }
+    }
+
+    const Units u = a.units[b * a.steps];
+    const float alpha = KIND == kGram ? u.gram : KIND == kPoly ? u.sq : u.mul;
+    const float beta = KIND == kPoly ? u.lin : u.add;
+    // lane: column j = lane % 32, rows 8 (q / 4) + 4 (lane / 32) + q % 4
+    const int64_t i0 = bi * TILE + wi + 4 * (lane >> 5), j0 = bj * TILE + wj + (lane & 31);
+    const int64_t ldR = rowsQ * 2, ldT = rowsP * 2;  // halves per row of R and Rt
+#pragma unroll
+    for (int x = 0; x < W; ++x)
+#pragma unroll
+        for (int y = 0; y < W; ++y)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t i = i0 + 32 * x + 8 * g, j = j0 + 32 * y;  // rows i .. i+3
+                float v[4];
+                typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+                if constexpr (KIND == kGram) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = alpha * acc[x][y][4 * g + q];
+                } else {
+                    const _Float16* e = a.E + (b * rowsQ + j) * ldT + split_at(i);
+                    const h4 eh = *reinterpret_cast<const h4*>(e), el = *reinterpret_cast<const h4*>(e + 32);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = alpha * acc[x][y][4 * g + q] + beta * ((float)eh[q] + (float)el[q]);
+                }
+                if constexpr (KIND == kLast) {
+                    T* o = (T*)a.out + b * d.s * d.t;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (i + q < d.s && j < d.t) o[d.tall ? j * d.s + i + q : (i + q) * d.t + j] = from_f32<T>(v[q]);
+                } else {
+                    h4 vh, vl;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        _Float16 h, l;
+                        split(v[q], h, l);
+                        vh[q] = h;
+                        vl[q] = l;
+                        _Float16* p = a.R + (b * rowsP + i + q) * ldR + split_at(j);
+                        // a diagonal tile is its own mirror: its entries are written once, from above
+                        if (KIND == kNext || !(bi == bj) || i + q <= j) {
+                            p[0] = h;
+                            p[32] = l;
+                        }
+                    }
+                    _Float16* p = a.Rt + (b * rowsQ + j) * ldT + split_at(i);
+                    if (KIND == kNext || bi != bj) {
+                        *reinterpret_cast<h4*>(p) = vh;
+                        *reinterpret_cast<h4*>(p + 32) = vl;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (i + q < j) {
+                                p[q] = vh[q];
+                                p[q + 32] = vl[q];
+                            }
+                    }
+                }
+            }
+}
+
+// ---- host ----------------------------------------------------------------------------------
+struct OrthoLayout {
+    OrthoDims d;
+    int tile;
+    int32_t per;
+    size_t part, units, X, Xt[2], A, B, bytes;
+};
+
+OrthoLayout ortho_layout(const OrthoShape& o)
+{
+    OrthoLayout w{};
+    w.d.tall = o.m > o.n;
+    w.d.s = w.d.tall ? o.n : o.m;
+    w.d.t = w.d.tall ? o.m : o.n;
+    w.tile = w.d.s > 1024 ? 128 : 64;
+    w.d.sp = cdiv64(w.d.s, w.tile) * w.tile;
+    w.d.tp = cdiv64(w.d.t, w.tile) * w.tile;
+    const int64_t size = o.m * o.n;
+    w.per = (int32_t)(size / 16384 < 1 ? 1 : size / 16384 < kNormBlocks ? size / 16384 : kNormBlocks);
+    size_t off = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t at = off;
+        off += align256((size_t)bytes);
+        return at;
+    };
+    w.part = take(8 * o.batch * w.per);
+    w.units = take((int64_t)sizeof(Units) * o.batch * kMaxOrthoSteps);
+    w.X = take(4 * o.batch * w.d.sp * w.d.tp);
+    for (int k = 0; k < 2; ++k) w.Xt[k] = take(4 * o.batch * w.d.sp * w.d.tp);
+    w.A = take(4 * o.batch * w.d.sp * w.d.sp);
+    w.B = take(4 * o.batch * w.d.sp * w.d.sp);
+    w.bytes = off;
+    return w;
+}
+
+template <int KIND, class T>
+void prod(const OrthoLayout& w, const OrthoShape& o, const ProdArgs& a, hipStream_t s)
+{
+    const int64_t tiles = a.tj == 0 ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
+    const dim3 grid((unsigned)(tiles * o.batch));
+    if (w.tile == 128)
+        hipLaunchKernelGGL((k_ortho_prod<128, KIND, T>), grid, dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_ortho_prod<64, KIND, T>), grid, dim3(kThreads), 0, s, a);
+}
+
+template <class T>
+hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s)
+{
+    const OrthoLayout w = ortho_layout(o);
+    char* base = (char*)ws;
+    double* part = (double*)(base + w.part);
+    _Float16 *X = (_Float16*)(base + w.X), *Xt[2] = {(_Float16*)(base + w.Xt[0]), (_Float16*)(base + w.Xt[1])};
+    _Float16 *A = (_Float16*)(base + w.A), *B = (_Float16*)(base + w.B);
+    Units* units = (Units*)(base + w.units);
+    const OrthoPoly poly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
+    hipLaunchKernelGGL(k_ortho_norm<T>, dim3((unsigned)(o.batch * w.per)), dim3(kThreads), 0, s, o.m * o.n, w.per,
+                       (const T*)G, part);
+    hipLaunchKernelGGL(k_ortho_first<T>, dim3((unsigned)(o.batch * (w.d.sp / 64) * (w.d.tp / 64))), dim3(kThreads), 0,
+                       s, w.d, poly, w.per, part, (const T*)G, X, Xt[0], units);
+    for (int step = 0; step < o.steps; ++step) {
+        ProdArgs a{};
+        a.d = w.d;
+        a.units = units + step;
+        a.steps = o.steps;
+        a.ti = w.d.sp / w.tile;
+        a.K = w.d.tp;
+        a.P = a.Q = X;
+        a.R = a.Rt = A;
+        prod<kGram, T>(w, o, a, s);
+        a.K = w.d.sp;
+        a.P = a.Q = a.E = A;
+        a.R = a.Rt = B;
+        prod<kPoly, T>(w, o, a, s);
+        a.tj = w.d.tp / w.tile;
+        a.P = B;
+        a.Q = a.E = Xt[step & 1];
+        a.R = X;
+        a.Rt = Xt[(step & 1) ^ 1];
+        a.out = out;
+        if (step + 1 == o.steps) prod<kLast, T>(w, o, a, s);
+        else prod<kNext, T>(w, o, a, s);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool ortho_bounded(double a, double b, double c, int steps)
+{
+    double M = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        const Bounds r = step_bounds(a, b, c, M);
+        // no product at all, or beyond what the fp32 factors hold
+        if (!(r.next >= 1e-6) || !(r.next <= 1e6) || !(r.poly >= 1e-6) || !(r.poly <= 1e6)) return false;
+        M = r.next;
+    }
+    return true;
+}
+
+size_t ortho_workspace_bytes(const OrthoShape& o) { return ortho_layout(o).bytes; }
+
+hipError_t launch_orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s)
+{
+    return o.dtype == kF32 ? orthogonalize<float>(o, G, out, ws, s) : orthogonalize<bf16_t>(o, G, out, ws, s);
+}
+
+}  // namespace cgtp

@@ -71,6 +71,28 @@ bool bad_rows(const void* p, int64_t rows, int64_t ld, int64_t width, int64_t al
     return bad(p, align) || ld < width || too_long(rows, ld);
 }
 
+constexpr int64_t kMaxSide = 1 << 16, kMaxMatrixElems = int64_t(1) << 31, kMaxStack = int64_t(1) << 33;
+
+cgtp_status_t check_ortho(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols)
+{
+    if (!type_ok(dtype) || batch < 0 || rows < 1 || cols < 1) return CGTP_ERR_INVALID_ARG;
+    if (rows > kMaxSide || cols > kMaxSide || rows * cols > kMaxMatrixElems) return CGTP_ERR_UNSUPPORTED;
+    // padded sides are at least 64: the launches stay below 2^32 threads
+    const int64_t padded = (rows + 127) / 128 * 128 * ((cols + 127) / 128 * 128);
+    if (batch > kMaxStack / padded) return CGTP_ERR_UNSUPPORTED;
+    return CGTP_OK;
+}
+
+cgtp::OrthoShape ortho_shape(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols)
+{
+    cgtp::OrthoShape o{};
+    o.dtype = dtype;
+    o.batch = batch;
+    o.m = rows;
+    o.n = cols;
+    return o;
+}
+
 }  // namespace
 
 extern "C" {
@@ -179,6 +201,42 @@ cgtp_status_t cgtp_norm_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_ro
     n.ldd = ld_dx;
     return hip_status(cgtp::launch_norm_bwd(n, x, mean, rstd, gamma, beta, grad_y, grad_x, grad_gamma, grad_beta, ws,
                                             stream));
+}
+
+// ---- orthogonalised update -------------------------------------------------------------
+cgtp_status_t cgtp_orthogonalize_workspace_size(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                                size_t* bytes)
+{
+    if (!bytes) return CGTP_ERR_INVALID_ARG;
+    const cgtp_status_t st = check_ortho(dtype, batch, rows, cols);
+    if (st != CGTP_OK) return st;
+    *bytes = cgtp::ortho_workspace_bytes(ortho_shape(dtype, batch, rows, cols));
+    return CGTP_OK;
+}
+
+cgtp_status_t cgtp_orthogonalize(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps, double a,
+                                 double b, double c, float eps, float scale, const void* G, void* out, void* ws,
+                                 size_t ws_bytes, hipStream_t stream)
+{
+    const cgtp_status_t st = check_ortho(dtype, batch, rows, cols);
+    if (st != CGTP_OK) return st;
+    if (steps < 1 || steps > cgtp::kMaxOrthoSteps || !(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(scale))
+        return CGTP_ERR_INVALID_ARG;
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !cgtp::ortho_bounded(a, b, c, steps))
+        return CGTP_ERR_INVALID_ARG;
+    if (batch == 0) return CGTP_OK;
+    const int64_t es = cgtp::dtype_size(dtype);
+    if (bad(G, es) || bad(out, es)) return CGTP_ERR_INVALID_ARG;
+    cgtp::OrthoShape o = ortho_shape(dtype, batch, rows, cols);
+    if (!ws || ws_bytes < cgtp::ortho_workspace_bytes(o)) return CGTP_ERR_WORKSPACE;
+    if (((uintptr_t)ws & 255u) != 0) return CGTP_ERR_INVALID_ARG;
+    o.steps = steps;
+    o.a = a;
+    o.b = b;
+    o.c = c;
+    o.eps = eps;
+    o.scale = scale;
+    return hip_status(cgtp::launch_orthogonalize(o, G, out, ws, stream));
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // cgtp_train_internal.h -- shapes, workspaces and launchers of the node-side operators
-// (kernels in cgtp_embed.hip and cgtp_norm.hip; entry points in
-// cgtp_train_api.cpp).
+// (kernels in cgtp_embed.hip, cgtp_norm.hip and cgtp_ortho.hip;
+// entry points in cgtp_train_api.cpp).
 #pragma once
 
 #include <stddef.h>
@@ -46,5 +46,36 @@ hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma
 hipError_t launch_norm_bwd(const NormShape& n, const void* x, const float* mean, const float* rstd,
                            const float* gamma, const float* beta, const void* dy, void* dx, float* dgamma,
                            float* dbeta, void* ws, hipStream_t s);
+
+// ---- orthogonalised update -------------------------------------------------------------
+struct OrthoShape {
+    int dtype;
+    int64_t batch, m, n;  // matrices [batch][m][n]
+    int steps;
+    double a, b, c;
+    float eps, scale;
+};
+
+constexpr int kMaxOrthoSteps = 64;
+
+struct OrthoPoly {
+    int32_t steps;
+    double a, b, c;
+    float eps, scale;
+};
+
+// The orientation that is worked on: s <= t, sp and tp padded to whole tiles;
+// tall: the stored matrices are [t][s].
+struct OrthoDims {
+    int64_t s, t, sp, tp;
+    int32_t tall;
+};
+
+// whether the iterates of these coefficients stay within the fixed-point units
+bool ortho_bounded(double a, double b, double c, int steps);
+
+size_t ortho_workspace_bytes(const OrthoShape& o);
+
+hipError_t launch_orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s);
 
 }  // namespace cgtp

@@ -1,6 +1,7 @@
 """The node-side operators of a training step, over the C ABI of
 include/cgtp_train.h: embedding of species (token) ids and its gradient, group
-normalisation with an activation over ragged segments and its gradient.
+normalisation with an activation over ragged segments and its gradient, the
+orthogonalised update of a stack of weight matrices.
 
 Each function checks types, devices and shapes, allocates outputs and
 workspace with torch (device memory only) unless they are given, and calls the
@@ -241,3 +242,35 @@ def norm_act_bwd(x, mean, rstd, gamma, beta, grad_y, groups: int, seg_ptr=None, 
     _call("cgtp_norm_act_bwd", dev, d, _act(act), N, B, C, groups, ptr(seg_ptr), x.data_ptr(), ldx, mean.data_ptr(),
           rstd.data_ptr(), g, b, grad_y.data_ptr(), ldy, ptr(gx), C, ptr(gg), ptr(gb), ws.data_ptr(), ws.numel())
     return gx, gg, gb
+
+
+# ---- orthogonalised update -------------------------------------------------------------
+def orthogonalize_workspace_size(dtype, batch: int, rows: int, cols: int) -> int:
+    return _bytes("cgtp_orthogonalize_workspace_size", _DTYPES[dtype], batch, rows, cols)
+
+
+def orthogonalize(grad, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0,
+                  out=None, ws=None) -> torch.Tensor:
+    """scale times ``steps`` Newton-Schulz steps of a x + b x^3 + c x^5
+    (``coeffs``) on the singular values of each matrix of ``grad`` [..., rows,
+    cols], taken first to grad / (Frobenius norm + eps): the update direction
+    of weight matrices such as path_mix_fwd's Wmix [P][C][C_out]."""
+    d = _dtype(grad, "grad")
+    if grad.dim() < 2:
+        raise ValueError("grad must be [..., rows, cols]")
+    dev = grad.device
+    _need(grad, "grad", grad.dtype, grad.shape, dev)
+    m, n = grad.shape[-2:]
+    if m < 1 or n < 1:
+        raise ValueError(f"grad has shape {tuple(grad.shape)}: rows and cols must be at least 1")
+    B = grad.numel() // (m * n)
+    a, b, c = coeffs
+    nbytes = _bytes("cgtp_orthogonalize_workspace_size", d, B, m, n)
+    if out is None:
+        out = torch.empty_like(grad)
+    else:
+        _need(out, "out", grad.dtype, grad.shape, dev)
+    ws = _workspace(ws, nbytes, dev)
+    _call("cgtp_orthogonalize", dev, d, B, m, n, steps, a, b, c, eps, scale, grad.data_ptr(), out.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return out

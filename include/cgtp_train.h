@@ -107,6 +107,30 @@ cgtp_status_t cgtp_norm_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_ro
                                 float* grad_gamma, float* grad_beta, void* ws, size_t ws_bytes,
                                 hipStream_t stream);
 
+/* ---- orthogonalised update ---------------------------------------------------------
+ * out = scale * Q(G) for each of `batch` matrices [rows][cols] (contiguous), by
+ * `steps` Newton-Schulz steps of the odd polynomial a x + b x^3 + c x^5:
+ *   X = G / (||G||_F + eps);   steps times: A = X X^T, X <- a X + (b A + c A A) X
+ * (A = X^T X, products from the other side, where rows > cols: the same
+ * result).  Every singular value x of X goes through the polynomial `steps`
+ * times and the singular vectors stay; with a = 3.4445, b = -4.7750,
+ * c = 2.0315 and five steps all but the smallest end near 1, so that the
+ * update of a weight matrix acts on all its directions alike.  A zero matrix
+ * gives zeros (eps > 0); a matrix with an infinity or NaN gives NaN throughout, and the
+ * others of the stack are not touched by it.
+ * 1 <= steps <= 64.  The coefficients must keep the iterates bounded: over
+ * singular values in [0, 1] the polynomial's maximum, followed from step to
+ * step, and that of b y + c y^2 must stay within 1e-6 .. 1e6
+ * (CGTP_ERR_INVALID_ARG otherwise; b = c = 0 is refused so). */
+
+/* Workspace bytes. */
+cgtp_status_t cgtp_orthogonalize_workspace_size(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                                size_t* bytes);
+
+cgtp_status_t cgtp_orthogonalize(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols, int steps, double a,
+                                 double b, double c, float eps, float scale, const void* G, void* out, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

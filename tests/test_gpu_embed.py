@@ -1,11 +1,11 @@
 """GPU parity of the embedding and of its table's gradient against the oracle
 in 64 bits.
 
-Tolerances.  Forward: one fp32 product, rounded once more to bf16: relative
-2^-24 (fp32), 2^-9 + 2^-24 (bf16).  Gradient: fp64 sums of the given values,
-one rounding to fp32 (the scaled sum) and one more to bf16, plus the fp64 sum's
-own error, at most n 2^-53 times the sum of the magnitudes.  Twice these bounds
-are allowed.
+Tolerances, with the unit roundoffs 2^-24 of fp32 and 2^-8 of bf16.  Forward:
+one fp32 product, rounded once more to bf16.  Gradient: fp64 sums of the given
+values, one rounding to fp32 (the scaled sum) and one more to bf16, plus the
+fp64 sum's own error, at most n 2^-53 times the sum of the magnitudes.  Two
+fp32 roundoffs and one of bf16 are allowed (2 EPS below), and twice the sum's.
 """
 import numpy as np
 import pytest

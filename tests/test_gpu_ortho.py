@@ -1,0 +1,138 @@
+"""GPU parity of the orthogonalised update against the singular-value form in
+64 bits.
+
+Tolerance.  A step's rounding (products that carry 24 bits, fp32 sums) disturbs
+its result by about u (|a| + |b| + |c|) ||X||_F, u = 2^-24, at the step's
+iterate X; the later steps magnify that by at most their largest slope, a each.
+Four times the sum over the steps is allowed, in the Frobenius norm (which also
+bounds every element), and bf16's unit roundoff, 2^-8 of the result's norm, for
+bf16 results.
+"""
+import numpy as np
+import pytest
+
+from tests import train_oracle as T
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+QUINTIC, CUBIC = (3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0)
+
+
+@pytest.fixture(scope="module")
+def tt():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch, torch.device("cuda:0")
+
+
+def tolerance(norms, coeffs, scale, dtype):
+    a, steps = abs(coeffs[0]), len(norms) - 1
+    size = sum(abs(v) for v in coeffs)
+    t = 4 * U * scale * size * sum(norms[k] * a ** (steps - 1 - k) for k in range(steps))
+    return t + (2.0 ** -8 if dtype == "bf16" else U) * scale * norms[-1]
+
+
+def gradient(rng, B, m, n, kind):
+    G = rng.standard_normal((B, m, n))
+    if kind == "spectrum":      # a few strong directions over noise
+        r = max(1, min(m, n) // 8)
+        G = 0.3 * G + (rng.standard_normal((B, m, r)) * np.exp(-3 * np.arange(r) / r)) @ rng.standard_normal((B, r, n))
+    if kind == "rank one":
+        G = rng.standard_normal((B, m, 1)) @ rng.standard_normal((B, 1, n))
+    return G.astype(np.float32)
+
+
+CASES = [(1, 1, 1, "noise"), (3, 1, 70, "noise"), (2, 70, 1, "noise"), (15, 128, 128, "spectrum"),
+         (4, 64, 200, "noise"), (3, 200, 64, "noise"), (5, 5, 7, "noise"), (2, 33, 31, "spectrum"),
+         (34, 64, 64, "noise"), (2, 127, 129, "spectrum"), (2, 130, 126, "noise"), (1, 128, 1024, "spectrum"),
+         (1, 257, 300, "spectrum"), (2, 300, 150, "noise"), (1, 8, 3000, "noise"), (1, 3000, 8, "noise"),
+         (1, 520, 520, "spectrum"), (2, 96, 96, "rank one"), (1, 1100, 1030, "noise"), (1, 1030, 2100, "spectrum")]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,m,n,kind", CASES)
+def test_orthogonalize(tt, B, m, n, kind, dtype):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[ortho] {B} x {m} x {n} {kind} {dtype}", flush=True)
+    rng = np.random.default_rng(m * 7 + n)
+    G = gradient(rng, B, m, n, kind)
+    G *= np.exp(rng.uniform(-8, 8, (B, 1, 1))).astype(np.float32)      # the matrices' own magnitudes do not matter
+    G = T.bf16(G) if dtype == "bf16" else G
+    coeffs, steps, scale = ((QUINTIC, 5, 1.0), (CUBIC, 4, 0.2), (QUINTIC, 1, 3.0))[(m + n) % 3]
+    t = torch.from_numpy(G).to(dev).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    out = cg.orthogonalize(t, steps, coeffs, 1e-7, scale)
+    assert out.dtype == t.dtype and out.shape == t.shape
+    got = out.double().cpu().numpy()
+    for b in range(B):
+        want, norms = T.orthogonalize(G[b], steps, coeffs, 1e-7, scale)
+        err, tol = np.linalg.norm(got[b] - want), tolerance(norms, coeffs, scale, dtype)
+        assert err <= tol, (b, float(err / tol))
+    assert torch.equal(out, cg.orthogonalize(t, steps, coeffs, 1e-7, scale))
+
+
+@pytest.mark.parametrize("m,n", [(40, 48), (128, 300), (200, 160)])
+def test_orthogonalize_special_matrices(tt, m, n):
+    """Zero, tiny, huge and non-finite matrices of one stack do not touch each
+    other."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    g = torch.randn(7, m, n, device=dev)
+    plain = cg.orthogonalize(g)
+    s = g.clone()
+    s[0] = 0.0
+    s[1, 3, 4] = float("nan")
+    s[2, m - 1, n - 1] = float("inf")
+    s[3] *= 1e30
+    s[4] *= 1e-30                       # far below eps: eps decides
+    s[5] = 0.0
+    s[5, 1, 2] = -4.0                   # one entry: one singular value
+    out = cg.orthogonalize(s)
+    assert (out[0] == 0).all() and torch.isnan(out[1]).all() and torch.isnan(out[2]).all()
+    assert torch.equal(out[6], plain[6])
+    for b in (3, 4, 5):
+        want, norms = T.orthogonalize(s[b].cpu().numpy(), 5, QUINTIC, 1e-7, 1.0)
+        err = np.linalg.norm(out[b].double().cpu().numpy() - want)
+        assert err <= tolerance(norms, QUINTIC, 1.0, "f32"), b
+
+
+def test_orthogonalize_makes_orthogonal_rows(tt):
+    """A convergent cubic ends at the nearest matrix with orthonormal rows."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    g = torch.randn(2, 60, 90, device=dev)
+    q = cg.orthogonalize(g, steps=30, coeffs=CUBIC).double()
+    eye = torch.eye(60, dtype=torch.float64, device=dev)
+    assert max((v @ v.t().contiguous() - eye).norm() for v in q) <= 30 * 4 * U * 2 * 60 ** 0.5
+
+
+def test_orthogonalize_empty_stack(tt):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    assert cg.orthogonalize(torch.zeros(0, 5, 6, device=dev)).shape == (0, 5, 6)
+
+
+@pytest.mark.parametrize("m,n", [(128, 128), (64, 500), (300, 260)])
+def test_orthogonalize_on_another_stream_and_in_a_graph(tt, m, n):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    g = torch.randn(3, m, n, device=dev)
+    want = cg.orthogonalize(g)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = cg.orthogonalize(g)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    out = torch.empty_like(g)
+    with torch.cuda.graph(graph):
+        cg.orthogonalize(g, out=out)
+    for k in range(3):
+        g.copy_(torch.randn(3, m, n, device=dev))
+        out.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, cg.orthogonalize(g)), k

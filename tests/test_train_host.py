@@ -97,6 +97,30 @@ def test_norm_refusals(L):
     assert bwd(n=64) == L.CGTP_ERR_WORKSPACE and bwd(ws=None) == L.CGTP_ERR_WORKSPACE
 
 
+def test_orthogonalize_refusals(L):
+    lib, bad, uns = L.lib(), L.CGTP_ERR_INVALID_ARG, L.CGTP_ERR_UNSUPPORTED
+    nan, inf = float("nan"), float("inf")
+
+    def call(d=0, B=2, m=4, n=6, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7, scale=1.0, G=FAKE, out=FAKE, ws=WS,
+             size=BIG):
+        return lib.cgtp_orthogonalize(d, B, m, n, steps, a, b, c, eps, scale, G, out, ws, size, None)
+
+    assert call(B=0, G=None, out=None, ws=None) == L.CGTP_OK
+    assert call(d=3) == bad and call(B=-1) == bad and call(m=0) == bad and call(n=0) == bad
+    assert call(m=(1 << 16) + 1) == uns and call(m=1 << 16, n=1 << 16) == uns and call(B=1 << 40) == uns
+    assert call(steps=0) == bad and call(steps=65) == bad and call(eps=-1e-7) == bad and call(eps=nan) == bad
+    assert call(scale=inf) == bad and call(a=nan) == bad and call(b=inf) == bad
+    assert call(a=30.0, b=0.0, c=20.0) == bad           # grows without bound
+    assert call(a=1.0, b=0.0, c=0.0) == bad             # no product at all
+    assert call(a=1.5, b=-0.5, c=0.0, ws=None) == L.CGTP_ERR_WORKSPACE      # the cubic is fine
+    assert call(G=None) == bad and call(out=None) == bad and call(G=ODD) == bad and call(out=ODD) == bad
+    assert call(ws=None) == L.CGTP_ERR_WORKSPACE and call(size=64) == L.CGTP_ERR_WORKSPACE and call(ws=WS_ODD) == bad
+    b = ctypes.c_size_t()
+    size = lambda *a: (lib.cgtp_orthogonalize_workspace_size(*a, ctypes.byref(b)), b.value)  # noqa: E731
+    assert size(0, 1, 128, 128)[1] < size(0, 15, 128, 128)[1] <= size(1, 15, 128, 1024)[1]
+    assert size(0, 1, 0, 8)[0] == bad and lib.cgtp_orthogonalize_workspace_size(0, 1, 8, 8, None) == bad
+
+
 def test_binding_refusals(L):
     import clebsch_gordan_tensor_cgtp_amd as cg
     ids, table = torch.zeros(4, dtype=torch.int32), torch.zeros(5, 8)
@@ -115,6 +139,14 @@ def test_binding_refusals(L):
     with pytest.raises(ValueError, match="overlap"):
         cg.embed_bwd(ids, torch.zeros(1, 8).expand(4, 8), 5)
     x, w = torch.zeros(6, 8), torch.ones(8)
+    with pytest.raises(ValueError, match="contiguous"):
+        cg.orthogonalize(torch.zeros(8, 4).t())
+    with pytest.raises(ValueError, match="rows, cols"):
+        cg.orthogonalize(torch.zeros(8))
+    with pytest.raises(ValueError, match="at least 1"):
+        cg.orthogonalize(torch.zeros(3, 0, 8))
+    with pytest.raises(ValueError, match="GPU"):
+        cg.orthogonalize(torch.zeros(3, 4, 8))
     with pytest.raises(ValueError, match="does not divide"):
         cg.norm_act_fwd(x, w, w, 3)
     with pytest.raises(ValueError, match="act must be"):

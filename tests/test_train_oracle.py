@@ -36,6 +36,23 @@ def test_norm_gradients_against_differences(kind):
         assert np.isclose((got * d).sum(), _directional(f, v, d), rtol=1e-6), k
 
 
+@pytest.mark.parametrize("shape", [(5, 9), (9, 5), (1, 4), (6, 6)])
+def test_orthogonalize_is_the_matrix_iteration(shape):
+    """The singular-value form equals the iteration by matrix products."""
+    rng = np.random.default_rng(4)
+    G, (a, b, c) = rng.standard_normal(shape), (3.4445, -4.7750, 2.0315)
+    X = G / (np.linalg.norm(G) + 1e-7)
+    for _ in range(5):
+        A = X @ X.T
+        X = a * X + (b * A + c * A @ A) @ X
+    got, norms = T.orthogonalize(G, 5, (a, b, c), 1e-7, 2.0)
+    assert np.allclose(got, 2.0 * X, rtol=1e-10, atol=1e-10)
+    assert np.isclose(norms[-1], np.linalg.norm(X))
+    # a cubic that converges gives the nearest orthogonal matrix
+    U, _, Vt = np.linalg.svd(G, full_matrices=False)
+    assert np.allclose(T.orthogonalize(G, 60, (1.5, -0.5, 0.0), 0.0, 1.0)[0], U @ Vt, atol=1e-9)
+
+
 def test_bf16_rounding():
     v = np.array([1.0, 1.00390625, 1.01171875, -3.14159, 0.0, 1e-30], np.float32)
     import torch

@@ -79,3 +79,16 @@ def norm_bwd(x, gamma, beta, grad, ptr, groups, eps, kind):
             one, two = hs.mean((0, 2), keepdims=True), (hs * xs).mean((0, 2), keepdims=True)
             dx[i:j] = (rstd[b][None, :, None] * (hs - one - xs * two)).reshape(j - i, C)
     return dx, (dz * xhat).sum(0), dz.sum(0)
+
+
+def orthogonalize(G, steps, coeffs, eps, scale):
+    """By the singular values: x -> a x + b x^3 + c x^5, `steps` times.  Also
+    the Frobenius norm of every iterate."""
+    a, b, c = coeffs
+    G = np.asarray(G, np.float64)
+    U, x, Vt = np.linalg.svd(G / (np.linalg.norm(G) + eps), full_matrices=False)
+    norms = [np.linalg.norm(x)]
+    for _ in range(steps):
+        x = a * x + b * x ** 3 + c * x ** 5
+        norms.append(np.linalg.norm(x))
+    return scale * (U * x) @ Vt, norms
