@@ -110,22 +110,32 @@ __device__ inline void step_units(const OrthoPoly& p, double r, Units* __restric
 
 
 // ---- norms and the first X ---------------------------------------------------------------
-constexpr int kNormBlocks = 64;  // partial sums per matrix, at most
+constexpr int kNormBlocks = 256;    // partial sums per matrix, at most
+constexpr int kNormElems = 8192;    // elements per partial sum, about
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_ortho_norm(int64_t size, int32_t per, const T* __restrict__ G,
-                                                         double* __restrict__ part)
+__global__ void __launch_bounds__(kThreads) k_ortho_norm(int64_t size, int32_t per, bool wide,
+                                                         const T* __restrict__ G, double* __restrict__ part)
 {
     __shared__ double s[kThreads];
+    constexpr int V = kWide<T>;
     const int64_t b = blockIdx.x / per, k = blockIdx.x % per;
-    const int64_t each = (size + per - 1) / per;
+    const int64_t each = ((size + per - 1) / per + V - 1) / V * V;
     const int64_t i0 = k * each, i1 = i0 + each < size ? i0 + each : size;
     const T* p = G + b * size;
     double t = 0.0;
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-        const double v = (double)to_f32(p[i]);
-        t += v * v;
+    int64_t i = i0 + threadIdx.x * V;
+    if (wide) {
+#pragma unroll 4
+        for (; i + V <= i1; i += kThreads * V) {
+            float v[V];
+            load_vec<T, V>(v, p + i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) t += (double)v[j] * (double)v[j];
+        }
     }
+    for (; i < i1; i += kThreads * V)
+        for (int64_t j = i; j < i + V && j < i1; ++j) t += (double)to_f32(p[j]) * (double)to_f32(p[j]);
     s[threadIdx.x] = t;
     __syncthreads();
     for (int d = kThreads / 2; d > 0; d /= 2) {
@@ -133,6 +143,16 @@ __global__ void __launch_bounds__(kThreads) k_ortho_norm(int64_t size, int32_t p
         __syncthreads();
     }
     if (threadIdx.x == 0) part[blockIdx.x] = s[0];
+}
+
+// Frobenius norm of matrix b, by every wave
+__device__ __forceinline__ double norm_of(const double* __restrict__ part, int64_t b, int32_t per)
+{
+    double t = 0.0;
+    for (int32_t q = threadIdx.x & 63; q < per; q += 64) t += part[b * per + q];
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) t += __shfl_xor(t, d, 64);
+    return sqrt(t);
 }
 
 // X and X^T of one 64 x 64 tile, split, zero outside the matrix; the first tile
@@ -147,9 +167,7 @@ __global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly
     const int64_t ti = d.sp / 64, tj = d.tp / 64;
     const int64_t b = blockIdx.x / (ti * tj), r = blockIdx.x % (ti * tj);
     const int64_t i0 = r / tj * 64, j0 = r % tj * 64;
-    double sum = 0.0;
-    for (int32_t q = 0; q < per; ++q) sum += part[b * per + q];
-    const double norm = sqrt(sum), den = norm + (double)poly.eps;
+    const double norm = norm_of(part, b, per), den = norm + (double)poly.eps;
     const double inv = unit_of(norm / den) / den;
     if (r == 0 && threadIdx.x == 0) step_units(poly, norm / den, units + b * poly.steps);
     const T* g = G + b * d.s * d.t;
@@ -192,27 +210,67 @@ struct ProdArgs {
     int32_t steps;
 };
 
+// Tile `r` of a product of ti x tj tiles (tj = 0: the upper triangle, bi <= bj),
+// counted through bands of four columns, row by row within a band, so that
+// consecutive tiles share operands.
+__device__ __forceinline__ void tile_at(int64_t r, int64_t ti, int64_t tj, int64_t& bi, int64_t& bj)
+{
+    constexpr int64_t kBand = 4;
+    const bool upper = tj == 0;
+    const int64_t cols = upper ? ti : tj;
+    int64_t c0 = 0, w = 0, n = 0;
+    for (;; c0 += kBand, r -= n) {
+        w = cols - c0 < kBand ? cols - c0 : kBand;
+        n = upper ? w * c0 + w * (w + 1) / 2 : w * ti;
+        if (r < n) break;
+    }
+    const int64_t full = upper ? c0 : ti;  // rows with all w columns
+    if (r < full * w) {
+        bi = r / w;
+        bj = c0 + r % w;
+        return;
+    }
+    r -= full * w;  // the band's own triangle
+    bi = c0;
+    while (r >= c0 + w - bi) {
+        r -= c0 + w - bi;
+        ++bi;
+    }
+    bj = bi + r;
+}
+
+// Blocks go to the XCDs in turn: block x works on tile (x % kXcds) * (n / kXcds)
+// + x / kXcds (the first n % kXcds XCDs one more), so that an XCD's tiles are
+// neighbours and share its L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t x, int64_t n)
+{
+    const int64_t q = n / kXcds, rest = n % kXcds, c = x % kXcds;
+    return c * q + (c < rest ? c : rest) + x / kXcds;
+}
+
+// all but the last N of this wave's loads have arrived, its LDS reads are done,
+// and every wave of the block is here
+template <int N>
+__device__ __forceinline__ void wait_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // One TILE x TILE tile of D = P Q^T, four waves of (TILE/2)^2 each, 32 k at a
-// time through two LDS buffers.
+// time through a ring of kStages LDS buffers that loads fill directly, kStages - 1
+// blocks of k ahead.
 template <int TILE, int KIND, class T>
 __global__ void __launch_bounds__(kThreads) k_ortho_prod(ProdArgs a)
 {
     constexpr int W = TILE / 64;  // 32 x 32 tiles per wave and side
-    constexpr int kRowHalves = 64;
-    __shared__ __attribute__((aligned(16))) _Float16 lds[2][2][TILE * kRowHalves];
+    constexpr int kRowHalves = 64, kStages = 4;
+    constexpr int kPieces = TILE * 8 / kThreads;  // 16-byte pieces per thread, operand and stage
+    __shared__ __attribute__((aligned(16))) _Float16 lds[kStages][2][TILE * kRowHalves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const bool upper = a.tj == 0;
-    const int64_t tiles = upper ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
-    const int64_t b = blockIdx.x / tiles;
-    int64_t r = blockIdx.x % tiles, bi, bj;
-    if (upper) {  // r counts the tiles (bi, bj), bi <= bj, column by column
-        bj = 0;
-        while (r > bj) r -= ++bj;
-        bi = r;
-    } else {
-        bi = r % a.ti;
-        bj = r / a.ti;
-    }
+    const int64_t tiles = a.tj == 0 ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
+    const int64_t x = xcd_order(blockIdx.x, gridDim.x), b = x / tiles;
+    int64_t bi, bj;
+    tile_at(x % tiles, a.ti, a.tj, bi, bj);
     const OrthoDims& d = a.d;
     const int64_t rowsP = d.sp, rowsQ = KIND == kNext || KIND == kLast ? d.tp : d.sp;
     const _Float16* P = a.P + (b * rowsP + bi * TILE) * a.K * 2;
@@ -226,39 +284,33 @@ __global__ void __launch_bounds__(kThreads) k_ortho_prod(ProdArgs a)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][y][q] = 0.0f;
 
-    // 16-byte piece c of row r sits at piece c ^ (r & 7), so that the reads of
-    // eight rows at one k spread over all banks
-    constexpr int kPieces = TILE * 8 / kThreads;
-    uint4 ra[kPieces], rb[kPieces];
-    auto load = [&](int64_t kb) {
+    // Thread p of a stage fills piece p % 8 of row p / 8, with the row's piece
+    // (p % 8) ^ (row % 8): a wave's LDS destination is one run of 1 KB, and the
+    // reads of eight rows at one k spread over all banks.
+    const int row0 = tid / 8, piece0 = (tid % 8) ^ (row0 & 7);
+    const _Float16* gp = P + (int64_t)row0 * a.K * 2 + piece0 * 8;
+    const _Float16* gq = Q + (int64_t)row0 * a.K * 2 + piece0 * 8;
+    const int64_t step = (int64_t)(kThreads / 8) * a.K * 2;
+    auto fill = [&](int64_t kb) {
+        _Float16(*to)[TILE * kRowHalves] = lds[kb % kStages];
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
-            const int p = q * kThreads + tid, row = p / 8, c = p % 8;
-            ra[q] = *reinterpret_cast<const uint4*>(P + row * a.K * 2 + kb * 64 + c * 8);
-            rb[q] = *reinterpret_cast<const uint4*>(Q + row * a.K * 2 + kb * 64 + c * 8);
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            const int p = q * kThreads + tid, row = p / 8, c = p % 8;
-            const int at = row * kRowHalves + ((c ^ (row & 7)) * 8);
-            *reinterpret_cast<uint4*>(&lds[buf][0][at]) = ra[q];
-            *reinterpret_cast<uint4*>(&lds[buf][1][at]) = rb[q];
+            const int at = (q * kThreads + (tid & ~63)) * 8;
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(gp + q * step + kb * 64),
+                (__attribute__((address_space(3))) void*)&to[0][at], 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(gq + q * step + kb * 64),
+                (__attribute__((address_space(3))) void*)&to[1][at], 16, 0, 0);
         }
     };
     const int wi = (wave >> 1) * 32 * W, wj = (wave & 1) * 32 * W;
-    auto read = [&](int buf, int op, int row, int piece) {
-        return *reinterpret_cast<const h8*>(&lds[buf][op][row * kRowHalves + ((piece ^ (row & 7)) * 8)]);
-    };
     const int64_t nk = a.K / 32;
-    load(0);
-    for (int64_t kb = 0; kb < nk; ++kb) {
-        const int buf = (int)(kb & 1);
-        // this buffer was last read two blocks ago, before the last barrier
-        put(buf);
-        __syncthreads();
-        if (kb + 1 < nk) load(kb + 1);
+    auto block = [&](int64_t kb) {
+        const _Float16(*from)[TILE * kRowHalves] = lds[kb % kStages];
+        auto read = [&](int op, int row, int piece) {
+            return *reinterpret_cast<const h8*>(&from[op][row * kRowHalves + ((piece ^ (row & 7)) * 8)]);
+        };
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             h8 ph[W], pl[W], qh[W], ql[W];
@@ -266,20 +318,41 @@ __global__ void __launch_bounds__(kThreads) k_ortho_prod(ProdArgs a)
 #pragma unroll
             for (int x = 0; x < W; ++x) {
                 const int ri = wi + 32 * x + (lane & 31), rj = wj + 32 * x + (lane & 31);
-                ph[x] = read(buf, 0, ri, piece);
-                pl[x] = read(buf, 0, ri, piece + 4);
-                qh[x] = read(buf, 1, rj, piece);
-                ql[x] = read(buf, 1, rj, piece + 4);
+                ph[x] = read(0, ri, piece);
+                pl[x] = read(0, ri, piece + 4);
+                qh[x] = read(1, rj, piece);
+                ql[x] = read(1, rj, piece + 4);
             }
 #pragma unroll
             for (int x = 0; x < W; ++x)
 #pragma unroll
-                for (int y = 0; y < W; ++y) {
+                for (int y = 0; y < W; ++y)
                     acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql[y], acc[x][y], 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < W; ++x)
+#pragma unroll
+                for (int y = 0; y < W; ++y)
                     acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh[y], acc[x][y], 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < W; ++x)
+#pragma unroll
+                for (int y = 0; y < W; ++y)
                     acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh[y], acc[x][y], 0, 0, 0);
-                }
         }
+    };
+    // Block kb is in when at most the loads of the kStages - 2 blocks after it
+    // are out; behind the barrier every wave has read block kb - 1, whose buffer
+    // block kb + kStages - 1 then takes.
+    int64_t kb = 0;
+    for (; kb < kStages - 1 && kb < nk; ++kb) fill(kb);
+    for (kb = 0; kb + kStages - 1 < nk; ++kb) {
+        wait_barrier<2 * kPieces*(kStages - 2)>();
+        fill(kb + kStages - 1);
+        block(kb);
+    }
+    for (; kb < nk; ++kb) {
+        wait_barrier<0>();
+        block(kb);
     }
 
     const Units u = a.units[b * a.steps];
@@ -361,7 +434,8 @@ OrthoLayout ortho_layout(const OrthoShape& o)
     w.d.sp = cdiv64(w.d.s, w.tile) * w.tile;
     w.d.tp = cdiv64(w.d.t, w.tile) * w.tile;
     const int64_t size = o.m * o.n;
-    w.per = (int32_t)(size / 16384 < 1 ? 1 : size / 16384 < kNormBlocks ? size / 16384 : kNormBlocks);
+    const int64_t sums = cdiv64(size, kNormElems);
+    w.per = (int32_t)(sums < kNormBlocks ? sums : kNormBlocks);
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t at = off;
@@ -400,7 +474,7 @@ hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws
     Units* units = (Units*)(base + w.units);
     const OrthoPoly poly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
     hipLaunchKernelGGL(k_ortho_norm<T>, dim3((unsigned)(o.batch * w.per)), dim3(kThreads), 0, s, o.m * o.n, w.per,
-                       (const T*)G, part);
+                       o.m * o.n % kWide<T> == 0 && ((uintptr_t)G & 15u) == 0, (const T*)G, part);
     hipLaunchKernelGGL(k_ortho_first<T>, dim3((unsigned)(o.batch * (w.d.sp / 64) * (w.d.tp / 64))), dim3(kThreads), 0,
                        s, w.d, poly, w.per, part, (const T*)G, X, Xt[0], units);
     for (int step = 0; step < o.steps; ++step) {
