@@ -16,8 +16,11 @@
 // accumulation so give what an fp32 product gives, at a third of the fp16 rate
 // instead of the sixteenth that fp32 matrix instructions reach.
 //
-// Layout.  An operand row of K values is cut into blocks of 32: 32 h, then
-// their 32 l, one 128-byte line.  All products are "rows times rows": D[i][j] =
+// Layout.  An operand of `rows` rows is cut along k into blocks of 32: a row's
+// piece of a block is 32 h, then their 32 l, one 128-byte line, and a block's
+// lines lie one after the other, so that what a tile loads for one block of k
+// is one run of memory (rows K apart would meet in a few cache channels: 62 us
+// where this takes XX us at 2048).  All products are "rows times rows": D[i][j] =
 // sum_k P[i][k] Q[j][k] with k contiguous in both; A and B are symmetric, and X
 // is kept as it is and transposed.
 #include <hip/hip_runtime.h>
@@ -38,8 +41,11 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// offset of element k of a split row (its low half is 32 further on)
-__device__ __forceinline__ int64_t split_at(int64_t k) { return (k >> 5) * 64 + (k & 31); }
+// offset of element (row, k) of a split operand (its low half is 32 further on)
+__device__ __forceinline__ int64_t split_at(int64_t row, int64_t k, int64_t rows)
+{
+    return ((k >> 5) * rows + row) * 64 + (k & 31);
+}
 
 __device__ __forceinline__ void split(float v, _Float16& h, _Float16& l)
 {
@@ -185,11 +191,11 @@ __global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly
         const int a = q / 64, c = q % 64;
         _Float16 h, l;
         split(tile[a][c], h, l);
-        _Float16* p = X + (i0 + a) * d.tp * 2 + split_at(j0 + c);
+        _Float16* p = X + split_at(i0 + a, j0 + c, d.sp);
         p[0] = h;
         p[32] = l;
         split(tile[c][a], h, l);
-        p = Xt + (j0 + a) * d.sp * 2 + split_at(i0 + c);
+        p = Xt + split_at(j0 + a, i0 + c, d.tp);
         p[0] = h;
         p[32] = l;
     }
@@ -248,178 +254,268 @@ __device__ __forceinline__ int64_t xcd_order(int64_t x, int64_t n)
     return c * q + (c < rest ? c : rest) + x / kXcds;
 }
 
-// all but the last N of this wave's loads have arrived, its LDS reads are done,
-// and every wave of the block is here
+// All but the last N of this wave's loads have arrived, its LDS reads are done,
+// and every wave of the block is here.  (The counters' wait as a builtin, so that
+// the compiler knows of it; the barrier holds memory accesses on their side.)
 template <int N>
 __device__ __forceinline__ void wait_barrier()
 {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
 }
 
-// One TILE x TILE tile of D = P Q^T, four waves of (TILE/2)^2 each, 32 k at a
-// time through a ring of kStages LDS buffers that loads fill directly, kStages - 1
-// blocks of k ahead.
+// One TILE x TILE tile of D = P Q^T, each wave WX x WY tiles of 32 x 32, 32 k at
+// a time through a ring of kStages LDS buffers that loads fill directly, kStages
+// blocks of k ahead.  Two waves per SIMD (TILE 128) keep the matrix cores busy
+// across the barriers of a block of k.
+template <int TILE>
+struct TileShape;
+template <>
+struct TileShape<128> {
+    static constexpr int WX = 2, WY = 1;
+};
+template <>
+struct TileShape<64> {
+    static constexpr int WX = 1, WY = 1;
+};
+template <int TILE>
+constexpr int kProdThreads = 64 * (TILE / 32 / TileShape<TILE>::WX) * (TILE / 32 / TileShape<TILE>::WY);
+
 template <int TILE, int KIND, class T>
-__global__ void __launch_bounds__(kThreads) k_ortho_prod(ProdArgs a)
+__global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
 {
-    constexpr int W = TILE / 64;  // 32 x 32 tiles per wave and side
+    constexpr int WX = TileShape<TILE>::WX, WY = TileShape<TILE>::WY, kThr = kProdThreads<TILE>;
     constexpr int kRowHalves = 64, kStages = 4;
-    constexpr int kPieces = TILE * 8 / kThreads;  // 16-byte pieces per thread, operand and stage
-    __shared__ __attribute__((aligned(16))) _Float16 lds[kStages][2][TILE * kRowHalves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int kPieces = TILE * 8 / kThr;  // 16-byte pieces per thread, operand and stage
+    constexpr int kLd = TILE + 4;             // row stride of the result in LDS
+    constexpr int kRing = kStages * 2 * TILE * kRowHalves * 2, kResult = TILE * kLd * 4;
+    __shared__ __attribute__((aligned(16))) char mem[kRing > kResult ? kRing : kResult];
+    auto lds = reinterpret_cast<_Float16(*)[2][TILE * kRowHalves]>(mem);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t tiles = a.tj == 0 ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
     const int64_t x = xcd_order(blockIdx.x, gridDim.x), b = x / tiles;
     int64_t bi, bj;
     tile_at(x % tiles, a.ti, a.tj, bi, bj);
     const OrthoDims& d = a.d;
     const int64_t rowsP = d.sp, rowsQ = KIND == kNext || KIND == kLast ? d.tp : d.sp;
-    const _Float16* P = a.P + (b * rowsP + bi * TILE) * a.K * 2;
-    const _Float16* Q = a.Q + (b * rowsQ + bj * TILE) * a.K * 2;
+    const _Float16* P = a.P + b * rowsP * a.K * 2 + bi * TILE * kRowHalves;
+    const _Float16* Q = a.Q + b * rowsQ * a.K * 2 + bj * TILE * kRowHalves;
 
-    f16v acc[W][W];
+    f16v acc[WX][WY];
 #pragma unroll
-    for (int x = 0; x < W; ++x)
+    for (int x = 0; x < WX; ++x)
 #pragma unroll
-        for (int y = 0; y < W; ++y)
+        for (int y = 0; y < WY; ++y)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][y][q] = 0.0f;
 
     // Thread p of a stage fills piece p % 8 of row p / 8, with the row's piece
-    // (p % 8) ^ (row % 8): a wave's LDS destination is one run of 1 KB, and the
-    // reads of eight rows at one k spread over all banks.
-    const int row0 = tid / 8, piece0 = (tid % 8) ^ (row0 & 7);
-    const _Float16* gp = P + (int64_t)row0 * a.K * 2 + piece0 * 8;
-    const _Float16* gq = Q + (int64_t)row0 * a.K * 2 + piece0 * 8;
-    const int64_t step = (int64_t)(kThreads / 8) * a.K * 2;
+    // (p % 8) ^ (row / 2 % 8): a wave's LDS destination is one run of 1 KB, and
+    // the reads of sixteen rows at one k spread over all 64 banks.
+    const uint32_t mine = (uint32_t)((tid / 8) * 128 + (((tid % 8) ^ ((tid / 16) & 7)) * 16));
     auto fill = [&](int64_t kb) {
         _Float16(*to)[TILE * kRowHalves] = lds[kb % kStages];
+        const char* pp = (const char*)(P + kb * rowsP * kRowHalves);
+        const char* qq = (const char*)(Q + kb * rowsQ * kRowHalves);
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
-            const int at = (q * kThreads + (tid & ~63)) * 8;
+            const int at = (q * kThr + wave * 64) * 8;
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(gp + q * step + kb * 64),
+                (const __attribute__((address_space(1))) void*)(pp + (uint32_t)(mine + q * kThr * 16)),
                 (__attribute__((address_space(3))) void*)&to[0][at], 16, 0, 0);
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(gq + q * step + kb * 64),
+                (const __attribute__((address_space(1))) void*)(qq + (uint32_t)(mine + q * kThr * 16)),
                 (__attribute__((address_space(3))) void*)&to[1][at], 16, 0, 0);
         }
     };
-    const int wi = (wave >> 1) * 32 * W, wj = (wave & 1) * 32 * W;
+    constexpr int kAcross = TILE / 32 / WY;  // waves along j
+    const int wi = wave / kAcross * 32 * WX, wj = wave % kAcross * 32 * WY;
     const int64_t nk = a.K / 32;
-    auto block = [&](int64_t kb) {
+    // operands of one block of k in registers
+    struct Frag {
+        h8 ph[2][WX], pl[2][WX], qh[2][WY], ql[2][WY];
+    };
+    auto read = [&](Frag& f, int64_t kb) {
         const _Float16(*from)[TILE * kRowHalves] = lds[kb % kStages];
-        auto read = [&](int op, int row, int piece) {
-            return *reinterpret_cast<const h8*>(&from[op][row * kRowHalves + ((piece ^ (row & 7)) * 8)]);
+        auto at = [&](int op, int row, int piece) {
+            return *reinterpret_cast<const h8*>(&from[op][row * kRowHalves + ((piece ^ ((row >> 1) & 7)) * 8)]);
         };
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            h8 ph[W], pl[W], qh[W], ql[W];
             const int piece = ks * 2 + (lane >> 5);
 #pragma unroll
-            for (int x = 0; x < W; ++x) {
-                const int ri = wi + 32 * x + (lane & 31), rj = wj + 32 * x + (lane & 31);
-                ph[x] = read(0, ri, piece);
-                pl[x] = read(0, ri, piece + 4);
-                qh[x] = read(1, rj, piece);
-                ql[x] = read(1, rj, piece + 4);
-            }
+            for (int x = 0; x < WX; ++x) f.ph[ks][x] = at(0, wi + 32 * x + (lane & 31), piece);
 #pragma unroll
-            for (int x = 0; x < W; ++x)
+            for (int y = 0; y < WY; ++y) f.ql[ks][y] = at(1, wj + 32 * y + (lane & 31), piece + 4);
 #pragma unroll
-                for (int y = 0; y < W; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql[y], acc[x][y], 0, 0, 0);
+            for (int x = 0; x < WX; ++x) f.pl[ks][x] = at(0, wi + 32 * x + (lane & 31), piece + 4);
 #pragma unroll
-            for (int x = 0; x < W; ++x)
-#pragma unroll
-                for (int y = 0; y < W; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh[y], acc[x][y], 0, 0, 0);
-#pragma unroll
-            for (int x = 0; x < W; ++x)
-#pragma unroll
-                for (int y = 0; y < W; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh[y], acc[x][y], 0, 0, 0);
+            for (int y = 0; y < WY; ++y) f.qh[ks][y] = at(1, wj + 32 * y + (lane & 31), piece);
         }
     };
-    // Block kb is in when at most the loads of the kStages - 2 blocks after it
-    // are out; behind the barrier every wave has read block kb - 1, whose buffer
-    // block kb + kStages - 1 then takes.
-    int64_t kb = 0;
-    for (; kb < kStages - 1 && kb < nk; ++kb) fill(kb);
-    for (kb = 0; kb + kStages - 1 < nk; ++kb) {
+    auto multiply = [&](const Frag& f) {
+        auto add = [&](const h8(&p)[WX], const h8(&q)[WY]) {
+#pragma unroll
+            for (int x = 0; x < WX; ++x)
+#pragma unroll
+                for (int y = 0; y < WY; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[x], q[y], acc[x][y], 0, 0, 0);
+        };
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            add(f.ph[ks], f.ql[ks]);
+            add(f.pl[ks], f.qh[ks]);
+            add(f.ph[ks], f.qh[ks]);
+        }
+        // first the next block's LDS reads, then the loads, between the products
+        constexpr int kReads = 4 * (WX + WY), kMul = 6 * WX * WY;
+#pragma unroll
+        for (int g = 0; g < kMul / 2; ++g) {
+            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMul / 2 - 1) / (kMul / 2), 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+#pragma unroll
+        for (int g = 0; g < kMul / 2; ++g) {
+            __builtin_amdgcn_sched_group_barrier(0x010, (2 * kPieces + kMul / 2 - 1) / (kMul / 2), 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+    };
+    // Step kb multiplies block kb, already in registers, while it reads block
+    // kb + 1 from LDS and starts the loads of block kb + kStages into the buffer
+    // that block kb has left.  Block kb + 1 is in when at most the kStages - 2
+    // blocks after it are out; behind the barrier every wave has read block kb.
+    auto main_step = [&](int64_t kb, const Frag& cur, Frag& next) {
         wait_barrier<2 * kPieces*(kStages - 2)>();
-        fill(kb + kStages - 1);
-        block(kb);
+        read(next, kb + 1);
+        fill(kb + kStages);
+        multiply(cur);
+    };
+    auto tail_step = [&](int64_t kb, const Frag& cur, Frag& next) {
+        if (kb + 1 < nk) {
+            wait_barrier<0>();
+            read(next, kb + 1);
+            if (kb + kStages < nk) fill(kb + kStages);
+        }
+        multiply(cur);
+    };
+    Frag f0, f1;
+    for (int64_t kb = 0; kb < kStages && kb < nk; ++kb) fill(kb);
+    wait_barrier<0>();
+    read(f0, 0);
+    int64_t kb = 0;
+    for (; kb + 1 + kStages < nk; kb += 2) {
+        main_step(kb, f0, f1);
+        main_step(kb + 1, f1, f0);
     }
-    for (; kb < nk; ++kb) {
-        wait_barrier<0>();
-        block(kb);
+    for (; kb < nk; kb += 2) {
+        tail_step(kb, f0, f1);
+        if (kb + 1 < nk) tail_step(kb + 1, f1, f0);
     }
 
+    // The result goes through LDS as s[j][i], so that both orientations leave in
+    // whole lines.  A lane holds column j = lane % 32, rows 8 (q / 4) + 4 (lane /
+    // 32) + q % 4 of each tile of 32.
     const Units u = a.units[b * a.steps];
     const float alpha = KIND == kGram ? u.gram : KIND == kPoly ? u.sq : u.mul;
     const float beta = KIND == kPoly ? u.lin : u.add;
-    // lane: column j = lane % 32, rows 8 (q / 4) + 4 (lane / 32) + q % 4
-    const int64_t i0 = bi * TILE + wi + 4 * (lane >> 5), j0 = bj * TILE + wj + (lane & 31);
-    const int64_t ldR = rowsQ * 2, ldT = rowsP * 2;  // halves per row of R and Rt
+    float* s = reinterpret_cast<float*>(mem);
+    __syncthreads();
 #pragma unroll
-    for (int x = 0; x < W; ++x)
+    for (int x = 0; x < WX; ++x)
 #pragma unroll
-        for (int y = 0; y < W; ++y)
+        for (int y = 0; y < WY; ++y)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int64_t i = i0 + 32 * x + 8 * g, j = j0 + 32 * y;  // rows i .. i+3
-                float v[4];
-                typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-                if constexpr (KIND == kGram) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = alpha * acc[x][y][4 * g + q];
-                } else {
-                    const _Float16* e = a.E + (b * rowsQ + j) * ldT + split_at(i);
-                    const h4 eh = *reinterpret_cast<const h4*>(e), el = *reinterpret_cast<const h4*>(e + 32);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] = alpha * acc[x][y][4 * g + q] + beta * ((float)eh[q] + (float)el[q]);
-                }
-                if constexpr (KIND == kLast) {
-                    T* o = (T*)a.out + b * d.s * d.t;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (i + q < d.s && j < d.t) o[d.tall ? j * d.s + i + q : (i + q) * d.t + j] = from_f32<T>(v[q]);
-                } else {
-                    h4 vh, vl;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        _Float16 h, l;
-                        split(v[q], h, l);
-                        vh[q] = h;
-                        vl[q] = l;
-                        _Float16* p = a.R + (b * rowsP + i + q) * ldR + split_at(j);
-                        // a diagonal tile is its own mirror: its entries are written once, from above
-                        if (KIND == kNext || !(bi == bj) || i + q <= j) {
-                            p[0] = h;
-                            p[32] = l;
-                        }
-                    }
-                    _Float16* p = a.Rt + (b * rowsQ + j) * ldT + split_at(i);
-                    if (KIND == kNext || bi != bj) {
-                        *reinterpret_cast<h4*>(p) = vh;
-                        *reinterpret_cast<h4*>(p + 32) = vl;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (i + q < j) {
-                                p[q] = vh[q];
-                                p[q + 32] = vl[q];
-                            }
-                    }
-                }
+                float4 v;
+                v.x = alpha * acc[x][y][4 * g];
+                v.y = alpha * acc[x][y][4 * g + 1];
+                v.z = alpha * acc[x][y][4 * g + 2];
+                v.w = alpha * acc[x][y][4 * g + 3];
+                *reinterpret_cast<float4*>(
+                    &s[(wj + 32 * y + (lane & 31)) * kLd + wi + 32 * x + 8 * g + 4 * (lane >> 5)]) = v;
             }
+    __syncthreads();
+    const int64_t of = b * rowsP * rowsQ * 2;  // this matrix in E, R and Rt
+    constexpr int kEights = TILE * TILE / 8;
+    // rows j, eight i at a time: add E and write R^T
+    if constexpr (KIND != kGram) {
+        for (int q = tid; q < kEights; q += kThr) {
+            const int c = q % 4, j = q / 4 % TILE, i = q / (4 * TILE) * 32 + 8 * c;
+            float* v = &s[j * kLd + i];
+            const int64_t at = of + split_at(bj * TILE + j, bi * TILE + i, rowsQ);
+            const h8 eh = *reinterpret_cast<const h8*>(a.E + at), el = *reinterpret_cast<const h8*>(a.E + at + 32);
+            h8 vh, vl;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] += beta * ((float)eh[e] + (float)el[e]);
+                _Float16 h, l;
+                split(v[e], h, l);
+                vh[e] = h;
+                vl[e] = l;
+            }
+            // the diagonal tile of a symmetric result is written below
+            if (KIND == kNext || (KIND == kPoly && bi != bj)) {
+                *reinterpret_cast<h8*>(a.Rt + at) = vh;
+                *reinterpret_cast<h8*>(a.Rt + at + 32) = vl;
+            }
+        }
+        __syncthreads();
+    }
+    if constexpr (KIND == kLast) {
+        T* o = (T*)a.out + b * d.s * d.t;
+        for (int q = tid; q < TILE * TILE; q += kThr) {
+            // the output's own rows
+            const int i = d.tall ? q % TILE : q / TILE, j = d.tall ? q / TILE : q % TILE;
+            const int64_t gi = bi * TILE + i, gj = bj * TILE + j;
+            if (gi < d.s && gj < d.t) o[d.tall ? gj * d.s + gi : gi * d.t + gj] = from_f32<T>(s[j * kLd + i]);
+        }
+    } else {
+        // rows i, eight j at a time: write R; of a symmetric result's diagonal
+        // tile the upper triangle decides, and off the diagonal its mirror too
+        for (int q = tid; q < kEights; q += kThr) {
+            const int c = q % 4, i = q / 4 % TILE, j = q / (4 * TILE) * 32 + 8 * c;
+            h8 vh, vl;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool flip = KIND != kNext && bi == bj && i > j + e;
+                _Float16 h, l;
+                split(flip ? s[i * kLd + j + e] : s[(j + e) * kLd + i], h, l);
+                vh[e] = h;
+                vl[e] = l;
+            }
+            const int64_t at = of + split_at(bi * TILE + i, bj * TILE + j, rowsP);
+            *reinterpret_cast<h8*>(a.R + at) = vh;
+            *reinterpret_cast<h8*>(a.R + at + 32) = vl;
+        }
+        if constexpr (KIND == kGram) {
+            if (bi != bj)
+                for (int q = tid; q < kEights; q += kThr) {
+                    const int c = q % 4, j = q / 4 % TILE, i = q / (4 * TILE) * 32 + 8 * c;
+                    h8 vh, vl;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        _Float16 h, l;
+                        split(s[j * kLd + i + e], h, l);
+                        vh[e] = h;
+                        vl[e] = l;
+                    }
+                    const int64_t at = of + split_at(bj * TILE + j, bi * TILE + i, rowsQ);
+                    *reinterpret_cast<h8*>(a.Rt + at) = vh;
+                    *reinterpret_cast<h8*>(a.Rt + at + 32) = vl;
+                }
+        }
+    }
 }
 
 // ---- host ----------------------------------------------------------------------------------
+// Wide tiles read less of LDS per product, small ones fill the chip: wide ones
+// where there are at least kFill of them.
+constexpr int64_t kFill = 200;
+
 struct OrthoLayout {
     OrthoDims d;
-    int tile;
+    int pad;
     int32_t per;
     size_t part, units, X, Xt[2], A, B, bytes;
 };
@@ -430,9 +526,11 @@ OrthoLayout ortho_layout(const OrthoShape& o)
     w.d.tall = o.m > o.n;
     w.d.s = w.d.tall ? o.n : o.m;
     w.d.t = w.d.tall ? o.m : o.n;
-    w.tile = w.d.s > 1024 ? 128 : 64;
-    w.d.sp = cdiv64(w.d.s, w.tile) * w.tile;
-    w.d.tp = cdiv64(w.d.t, w.tile) * w.tile;
+    // whole wide tiles where there are enough of them and they add little padding
+    const int64_t s64 = cdiv64(w.d.s, 64), t64 = cdiv64(w.d.t, 64), s128 = cdiv64(s64, 2), t128 = cdiv64(t64, 2);
+    w.pad = s128 * t128 * o.batch >= kFill && 40 * s128 * t128 <= 11 * s64 * t64 ? 128 : 64;
+    w.d.sp = cdiv64(w.d.s, w.pad) * w.pad;
+    w.d.tp = cdiv64(w.d.t, w.pad) * w.pad;
     const int64_t size = o.m * o.n;
     const int64_t sums = cdiv64(size, kNormElems);
     w.per = (int32_t)(sums < kNormBlocks ? sums : kNormBlocks);
@@ -453,14 +551,19 @@ OrthoLayout ortho_layout(const OrthoShape& o)
 }
 
 template <int KIND, class T>
-void prod(const OrthoLayout& w, const OrthoShape& o, const ProdArgs& a, hipStream_t s)
+void prod(const OrthoLayout& w, const OrthoShape& o, ProdArgs a, hipStream_t s)
 {
-    const int64_t tiles = a.tj == 0 ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
-    const dim3 grid((unsigned)(tiles * o.batch));
-    if (w.tile == 128)
-        hipLaunchKernelGGL((k_ortho_prod<128, KIND, T>), grid, dim3(kThreads), 0, s, a);
+    constexpr bool upper = KIND == kGram || KIND == kPoly;
+    auto tiles = [&](int64_t tile) {
+        a.ti = w.d.sp / tile;
+        a.tj = upper ? 0 : w.d.tp / tile;
+        return (upper ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj) * o.batch;
+    };
+    if (w.pad == 128 && tiles(128) >= kFill)
+        hipLaunchKernelGGL((k_ortho_prod<128, KIND, T>), dim3((unsigned)tiles(128)), dim3(kProdThreads<128>), 0, s,
+                           a);
     else
-        hipLaunchKernelGGL((k_ortho_prod<64, KIND, T>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_ortho_prod<64, KIND, T>), dim3((unsigned)tiles(64)), dim3(kProdThreads<64>), 0, s, a);
 }
 
 template <class T>
@@ -482,7 +585,6 @@ hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws
         a.d = w.d;
         a.units = units + step;
         a.steps = o.steps;
-        a.ti = w.d.sp / w.tile;
         a.K = w.d.tp;
         a.P = a.Q = X;
         a.R = a.Rt = A;
@@ -491,7 +593,6 @@ hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws
         a.P = a.Q = a.E = A;
         a.R = a.Rt = B;
         prod<kPoly, T>(w, o, a, s);
-        a.tj = w.d.tp / w.tile;
         a.P = B;
         a.Q = a.E = Xt[step & 1];
         a.R = X;
