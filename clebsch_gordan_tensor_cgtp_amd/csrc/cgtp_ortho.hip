@@ -508,10 +508,294 @@ __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
     }
 }
 
+// ---- short sides of at most 128 ------------------------------------------------------------
+// One block holds a matrix (or its chunk of TP columns, s <= SP) in LDS through
+// all three products of a step: X split in 64 KB at most, A and then B in another
+// 64 KB.  A step is 3 x 2 SP^2 TP flops and five barriers instead of three launches.
+// The next X is formed transposed, D[t][s] = sum_k X[k][t] B[s][k], so that a
+// lane ends with four consecutive t of a row of X and writes them back at once;
+// X^T is read from X's rows by transposing LDS reads.
+template <int SP, int TP>
+struct Small {
+    static constexpr int WC = SP / 32, NW = SP == 128 ? 8 : 4, WR = NW / WC;  // waves along the columns and rows
+    static constexpr int GX = SP / 32 / WR, NX = TP / 32 / WR;               // 32 x 32 tiles per wave, A and X
+    static constexpr int kThr = 64 * NW;
+    static constexpr int kX = SP * TP * 2, kA = SP * SP * 2;  // halves
+    static constexpr int kTileFloats = GX * 16 * kThr;          // A by threads: SP * SP
+};
+
+struct SmallArgs {
+    OrthoDims d;  // sp, tp unused
+    OrthoPoly poly;
+    int64_t chunks;      // TP columns each
+    int32_t blocks;      // per matrix
+    int32_t per;         // norm partials per matrix
+    const void* G;
+    void* out;
+    const double* part;
+    Units* units;
+    _Float16* image;     // X of every chunk, as in LDS
+    const float* sums;   // partial A of the blocks, by threads
+    float* osums;
+    int32_t nsums;       // partial sums to add
+    int32_t step;
+};
+
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef _Float16 h4v __attribute__((ext_vector_type(4)));
+
+template <int SP, int TP>
+struct SmallOps {
+    using S = Small<SP, TP>;
+    _Float16 *X, *A;
+    int lane, wi, wj, wt;  // wave's first row of A, column, first t
+
+    __device__ __forceinline__ SmallOps(_Float16* x, _Float16* a) : X(x), A(a)
+    {
+        lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wi = wave / S::WC * 32 * S::GX;
+        wt = wave / S::WC * 32 * S::NX;
+        wj = wave % S::WC * 32;
+    }
+    // halves offset of 16-byte piece c (0..7) of row r in block kb; an operand of `rows` rows
+    static __device__ __forceinline__ int at(int rows, int kb, int r, int c)
+    {
+        return (kb * rows + r) * 64 + ((c ^ ((r >> 1) & 7)) * 8);
+    }
+    // acc[x] = sum_k p[row wi + 32 x ..][k] p[row wj ..][k], k over blocks of 32
+    template <int N>
+    __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N], int blocks) const
+    {
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
+        const int r = lane & 31, hf = lane >> 5;
+        for (int kb = 0; kb < blocks; ++kb)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const int c = ks * 2 + hf;
+                const h8 qh = *reinterpret_cast<const h8*>(p + at(SP, kb, wj + r, c));
+                const h8 ql = *reinterpret_cast<const h8*>(p + at(SP, kb, wj + r, c + 4));
+                h8 ph[N], pl[N];
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    ph[x] = *reinterpret_cast<const h8*>(p + at(SP, kb, wi + 32 * x + r, c));
+                    pl[x] = *reinterpret_cast<const h8*>(p + at(SP, kb, wi + 32 * x + r, c + 4));
+                }
+#pragma unroll
+                for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
+#pragma unroll
+                for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
+#pragma unroll
+                for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh, acc[x], 0, 0, 0);
+            }
+    }
+    // four values of X^T rows: lanes of 16 hold rows t0 + lane % 16, k .. k+3;
+    // each lane points at 8 bytes of row k + lane % 16 / 4 of X
+    __device__ __forceinline__ h4v transposed(int t0, int k, int low) const
+    {
+        const int l = lane & 15, t = t0 + 4 * (l & 3), row = k + (l >> 2);
+        const _Float16* p = X + at(SP, t >> 5, row, ((t & 31) >> 3) + low) + (t & 4);
+        const s4v v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4v*)const_cast<_Float16*>(p));
+        return __builtin_bit_cast(h4v, v);
+    }
+    // acc[x][..] = sum_k X[k][wt + 32 x ..] B[wj ..][k], B in A's place
+    __device__ __forceinline__ void next(f16v (&acc)[S::NX]) const
+    {
+#pragma unroll
+        for (int x = 0; x < S::NX; ++x)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
+        const int r = lane & 31, hf = lane >> 5, half16 = (lane >> 4) & 1;
+        for (int kb = 0; kb < SP / 32; ++kb)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const int c = ks * 2 + hf, k = kb * 32 + ks * 16 + 8 * hf;
+                const h8 qh = *reinterpret_cast<const h8*>(A + at(SP, kb, wj + r, c));
+                const h8 ql = *reinterpret_cast<const h8*>(A + at(SP, kb, wj + r, c + 4));
+                h8 ph[S::NX], pl[S::NX];
+#pragma unroll
+                for (int x = 0; x < S::NX; ++x) {
+                    const int t0 = wt + 32 * x + 16 * half16;
+                    const h4v a = transposed(t0, k, 0), b = transposed(t0, k + 4, 0);
+                    const h4v e = transposed(t0, k, 4), f = transposed(t0, k + 4, 4);
+                    ph[x] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+                    pl[x] = __builtin_shufflevector(e, f, 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+#pragma unroll
+                for (int x = 0; x < S::NX; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
+#pragma unroll
+                for (int x = 0; x < S::NX; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
+#pragma unroll
+                for (int x = 0; x < S::NX; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh, acc[x], 0, 0, 0);
+            }
+    }
+    // rows v[x][4 g .. 4 g + 3] at first + 32 x + 8 g + 4 (lane / 32) of column wj + lane % 32,
+    // written as that row of p
+    template <int N>
+    __device__ __forceinline__ void put(_Float16* p, const f16v (&v)[N], int first) const
+    {
+        const int r = wj + (lane & 31);
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                h4v h, l;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    _Float16 a, b;
+                    split(v[x][4 * g + q], a, b);
+                    h[q] = a;
+                    l[q] = b;
+                }
+                const int kb = (first >> 5) + x, off = 4 * (lane >> 5);
+                *reinterpret_cast<h4v*>(p + at(SP, kb, r, g) + off) = h;
+                *reinterpret_cast<h4v*>(p + at(SP, kb, r, g + 4) + off) = l;
+            }
+    }
+    // the lane's values of X, as put() left them
+    __device__ __forceinline__ void get(f16v (&v)[S::NX]) const
+    {
+        const int r = wj + (lane & 31);
+#pragma unroll
+        for (int x = 0; x < S::NX; ++x)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int kb = (wt >> 5) + x, off = 4 * (lane >> 5);
+                const h4v h = *reinterpret_cast<const h4v*>(X + at(SP, kb, r, g) + off);
+                const h4v l = *reinterpret_cast<const h4v*>(X + at(SP, kb, r, g + 4) + off);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[x][4 * g + q] = (float)h[q] + (float)l[q];
+            }
+    }
+    // A (its values in ar) to B in A's place; two barriers inside, one owed after
+    __device__ __forceinline__ void poly(f16v (&ar)[S::GX], const Units& u) const
+    {
+        put(A, ar, wi);
+        __syncthreads();
+        f16v acc[S::GX];
+        square(A, acc, SP / 32);
+#pragma unroll
+        for (int x = 0; x < S::GX; ++x)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) ar[x][q] = u.sq * acc[x][q] + u.lin * ar[x][q];
+        __syncthreads();
+        put(A, ar, wi);
+    }
+    // columns t0 .. t0 + TP of matrix g (zero outside) to X, times inv
+    template <class T>
+    __device__ __forceinline__ void load(const OrthoDims& d, const T* __restrict__ g, int64_t t0, double inv) const
+    {
+        for (int q = threadIdx.x; q < SP * TP / 8; q += S::kThr) {
+            // eight elements along G's rows
+            int64_t i, j;
+            if (!d.tall) {
+                i = q / (TP / 8);
+                j = t0 + q % (TP / 8) * 8;
+            } else {
+                i = q % (SP / 8) * 8;
+                j = t0 + q / (SP / 8);
+            }
+            const int64_t from = d.tall ? j * d.s + i : i * d.t + j;
+            const int64_t left = (d.tall ? j < d.t : i < d.s) ? (d.tall ? d.s - i : d.t - j) : 0;
+            const int tj = (int)(j - t0);
+            _Float16 h[8], l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = e < left ? (float)((double)to_f32(g[from + e]) * inv) : 0.0f;
+                split(v, h[e], l[e]);
+            }
+            if (!d.tall) {
+                _Float16* p = X + at(SP, tj >> 5, (int)i, (tj & 31) >> 3);
+                _Float16* o = X + at(SP, tj >> 5, (int)i, ((tj & 31) >> 3) + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = h[e];
+                    o[e] = l[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    X[at(SP, tj >> 5, (int)i + e, (tj & 31) >> 3) + (tj & 7)] = h[e];
+                    X[at(SP, tj >> 5, (int)i + e, ((tj & 31) >> 3) + 4) + (tj & 7)] = l[e];
+                }
+            }
+        }
+    }
+    // the lane's values of the last X to the output
+    template <class T>
+    __device__ __forceinline__ void store(const OrthoDims& d, T* __restrict__ o, int64_t t0, const f16v (&v)[S::NX]) const
+    {
+        const int64_t i = wj + (lane & 31);
+        if (i >= d.s) return;
+#pragma unroll
+        for (int x = 0; x < S::NX; ++x)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t j = t0 + wt + 32 * x + 8 * g + 4 * (lane >> 5) + q;
+                    if (j < d.t) o[d.tall ? j * d.s + i : i * d.t + j] = from_f32<T>(v[x][4 * g + q]);
+                }
+    }
+};
+
+// A whole matrix per block (t <= TP), norm to output.
+template <int SP, int TP, class T>
+__global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs a)
+{
+    using S = Small<SP, TP>;
+    __shared__ __attribute__((aligned(16))) _Float16 X[S::kX], A[S::kA];
+    __shared__ Units units[kMaxOrthoSteps];
+    __shared__ double norms[S::NW];
+    const SmallOps<SP, TP> ops(X, A);
+    const int64_t size = a.d.s * a.d.t;
+    const T* g = (const T*)a.G + blockIdx.x * size;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int64_t q = threadIdx.x; q < size; q += S::kThr) sum += (double)to_f32(g[q]) * (double)to_f32(g[q]);
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) sum += __shfl_xor(sum, d, 64);
+    if ((threadIdx.x & 63) == 0) norms[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < S::NW; ++w) sum += norms[w];
+    const double norm = sqrt(sum), den = norm + (double)a.poly.eps;
+    if (threadIdx.x == 0) step_units(a.poly, norm / den, units);
+    ops.load(a.d, g, 0, unit_of(norm / den) / den);
+    __syncthreads();
+    f16v xr[S::NX], ar[S::GX], acc[S::NX];
+    ops.get(xr);
+    for (int k = 0; k < a.poly.steps; ++k) {
+        const Units u = units[k];
+        ops.square(X, ar, TP / 32);
+#pragma unroll
+        for (int x = 0; x < S::GX; ++x)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) ar[x][q] *= u.gram;
+        ops.poly(ar, u);
+        __syncthreads();
+        ops.next(acc);
+#pragma unroll
+        for (int x = 0; x < S::NX; ++x)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) xr[x][q] = u.mul * acc[x][q] + u.add * xr[x][q];
+        if (k + 1 == a.poly.steps) break;
+        __syncthreads();
+        ops.put(X, xr, ops.wt);
+        __syncthreads();
+    }
+    ops.store(a.d, (T*)a.out + blockIdx.x * size, 0, xr);
+}
+
 // ---- host ----------------------------------------------------------------------------------
 // Wide tiles read less of LDS per product, small ones fill the chip: wide ones
 // where there are at least kFill of them.
-constexpr int64_t kFill = 200;
+constexpr int64_t kFill = 100;
 
 struct OrthoLayout {
     OrthoDims d;
@@ -566,10 +850,25 @@ void prod(const OrthoLayout& w, const OrthoShape& o, ProdArgs a, hipStream_t s)
         hipLaunchKernelGGL((k_ortho_prod<64, KIND, T>), dim3((unsigned)tiles(64)), dim3(kProdThreads<64>), 0, s, a);
 }
 
+template <int SP, int TP, class T>
+hipError_t small(const OrthoLayout& w, const OrthoShape& o, const void* G, void* out, hipStream_t s)
+{
+    SmallArgs a{};
+    a.d = w.d;
+    a.poly = OrthoPoly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
+    a.G = G;
+    a.out = out;
+    hipLaunchKernelGGL((k_ortho_small<SP, TP, T>), dim3((unsigned)o.batch), dim3(Small<SP, TP>::kThr), 0, s, a);
+    return hipGetLastError();
+}
+
 template <class T>
 hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s)
 {
     const OrthoLayout w = ortho_layout(o);
+    if (w.d.t <= 64) return small<64, 64, T>(w, o, G, out, s);
+    if (w.d.t <= 128 && w.d.s <= 64) return small<64, 128, T>(w, o, G, out, s);
+    if (w.d.t <= 128) return small<128, 128, T>(w, o, G, out, s);
     char* base = (char*)ws;
     double* part = (double*)(base + w.part);
     _Float16 *X = (_Float16*)(base + w.X), *Xt[2] = {(_Float16*)(base + w.Xt[0]), (_Float16*)(base + w.Xt[1])};
