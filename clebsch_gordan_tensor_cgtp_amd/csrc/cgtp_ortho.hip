@@ -98,9 +98,9 @@ struct Units {
     float gram, sq, lin, mul, add;
 };
 
-// The steps' factors for a matrix whose first iterate has Frobenius norm r (at
-// most 1; far below it where eps exceeds the norm).
-__device__ inline void step_units(const OrthoPoly& p, double r, Units* __restrict__ u)
+// The steps' factors for a matrix whose first iterate's norm is at most r
+// (below 1 only where eps exceeds the norm).
+__host__ __device__ inline void step_units(const OrthoPoly& p, double r, Units* __restrict__ u)
 {
     double M = r, kx = unit_of(r);
     for (int k = 0; k < p.steps; ++k) {
@@ -114,6 +114,15 @@ __device__ inline void step_units(const OrthoPoly& p, double r, Units* __restric
     }
 }
 
+// The factors for the bound 1, formed on the host: they serve every matrix
+// whose norm is not below eps, so that the kernels need not wait for the fp64
+// chain above (about 4 us).
+struct UnitTable {
+    Units u[kMaxOrthoSteps];
+};
+
+// the bound that a matrix of norm r, at most 1, goes by
+__device__ __forceinline__ double start_bound(double r) { return r > 0.5 ? 1.0 : r; }
 
 // ---- norms and the first X ---------------------------------------------------------------
 constexpr int kNormBlocks = 256;    // partial sums per matrix, at most
@@ -164,18 +173,24 @@ __device__ __forceinline__ double norm_of(const double* __restrict__ part, int64
 // X and X^T of one 64 x 64 tile, split, zero outside the matrix; the first tile
 // of a matrix leaves its steps' factors
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly poly, int32_t per,
-                                                          const double* __restrict__ part, const T* __restrict__ G,
-                                                          _Float16* __restrict__ X, _Float16* __restrict__ Xt,
-                                                          Units* __restrict__ units)
+__global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly poly, UnitTable table,
+                                                          int32_t per, const double* __restrict__ part,
+                                                          const T* __restrict__ G, _Float16* __restrict__ X,
+                                                          _Float16* __restrict__ Xt, Units* __restrict__ units)
 {
     __shared__ float tile[64][65];
     const int64_t ti = d.sp / 64, tj = d.tp / 64;
     const int64_t b = blockIdx.x / (ti * tj), r = blockIdx.x % (ti * tj);
     const int64_t i0 = r / tj * 64, j0 = r % tj * 64;
     const double norm = norm_of(part, b, per), den = norm + (double)poly.eps;
-    const double inv = unit_of(norm / den) / den;
-    if (r == 0 && threadIdx.x == 0) step_units(poly, norm / den, units + b * poly.steps);
+    const double bound = start_bound(norm / den), inv = unit_of(bound) / den;
+    if (r == 0) {
+        if (bound == 1.0) {
+            if ((int)threadIdx.x < poly.steps) units[b * poly.steps + threadIdx.x] = table.u[threadIdx.x];
+        } else if (threadIdx.x == 0) {
+            step_units(poly, bound, units + b * poly.steps);
+        }
+    }
     const T* g = G + b * d.s * d.t;
     for (int q = threadIdx.x; q < 64 * 64; q += kThreads) {
         const int a = q / 64, c = q % 64;  // c runs along G's rows
@@ -527,18 +542,10 @@ struct Small {
 struct SmallArgs {
     OrthoDims d;  // sp, tp unused
     OrthoPoly poly;
-    int64_t chunks;      // TP columns each
-    int32_t blocks;      // per matrix
-    int32_t per;         // norm partials per matrix
+    UnitTable table;
+    bool wide;
     const void* G;
     void* out;
-    const double* part;
-    Units* units;
-    _Float16* image;     // X of every chunk, as in LDS
-    const float* sums;   // partial A of the blocks, by threads
-    float* osums;
-    int32_t nsums;       // partial sums to add
-    int32_t step;
 };
 
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -564,15 +571,16 @@ struct SmallOps {
         return (kb * rows + r) * 64 + ((c ^ ((r >> 1) & 7)) * 8);
     }
     // acc[x] = sum_k p[row wi + 32 x ..][k] p[row wj ..][k], k over blocks of 32
-    template <int N>
-    __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N], int blocks) const
+    template <int BLOCKS, int N>
+    __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N]) const
     {
 #pragma unroll
         for (int x = 0; x < N; ++x)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
         const int r = lane & 31, hf = lane >> 5;
-        for (int kb = 0; kb < blocks; ++kb)
+#pragma unroll
+        for (int kb = 0; kb < BLOCKS; ++kb)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 const int c = ks * 2 + hf;
@@ -610,6 +618,7 @@ struct SmallOps {
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
         const int r = lane & 31, hf = lane >> 5, half16 = (lane >> 4) & 1;
+#pragma unroll
         for (int kb = 0; kb < SP / 32; ++kb)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -677,7 +686,7 @@ struct SmallOps {
         put(A, ar, wi);
         __syncthreads();
         f16v acc[S::GX];
-        square(A, acc, SP / 32);
+        square<SP / 32>(A, acc);
 #pragma unroll
         for (int x = 0; x < S::GX; ++x)
 #pragma unroll
@@ -685,61 +694,93 @@ struct SmallOps {
         __syncthreads();
         put(A, ar, wi);
     }
-    // columns t0 .. t0 + TP of matrix g (zero outside) to X, times inv
+    // columns t0 .. t0 + TP of matrix g, zero outside: the thread's elements,
+    // eight along G's rows each (wide: G's rows are whole 16-byte accesses)
+    static constexpr int kEights = SP * TP / 8 / S::kThr;
     template <class T>
-    __device__ __forceinline__ void load(const OrthoDims& d, const T* __restrict__ g, int64_t t0, double inv) const
+    __device__ __forceinline__ void fetch(const OrthoDims& d, const T* __restrict__ g, int64_t t0, bool wide,
+                                          float (&v)[kEights][8]) const
     {
-        for (int q = threadIdx.x; q < SP * TP / 8; q += S::kThr) {
-            // eight elements along G's rows
-            int64_t i, j;
-            if (!d.tall) {
-                i = q / (TP / 8);
-                j = t0 + q % (TP / 8) * 8;
-            } else {
-                i = q % (SP / 8) * 8;
-                j = t0 + q / (SP / 8);
-            }
-            const int64_t from = d.tall ? j * d.s + i : i * d.t + j;
+#pragma unroll
+        for (int k = 0; k < kEights; ++k) {
+            const int q = k * S::kThr + (int)threadIdx.x;
+            const int64_t i = d.tall ? q % (SP / 8) * 8 : q / (TP / 8);
+            const int64_t j = t0 + (d.tall ? q / (SP / 8) : q % (TP / 8) * 8);
+            const T* p = g + (d.tall ? j * d.s + i : i * d.t + j);
             const int64_t left = (d.tall ? j < d.t : i < d.s) ? (d.tall ? d.s - i : d.t - j) : 0;
-            const int tj = (int)(j - t0);
-            _Float16 h[8], l[8];
+            if (wide) {
+                constexpr int V = kWide<T>;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = e < left ? (float)((double)to_f32(g[from + e]) * inv) : 0.0f;
-                split(v, h[e], l[e]);
-            }
-            if (!d.tall) {
-                _Float16* p = X + at(SP, tj >> 5, (int)i, (tj & 31) >> 3);
-                _Float16* o = X + at(SP, tj >> 5, (int)i, ((tj & 31) >> 3) + 4);
+                for (int e = 0; e < 8; e += V) {
+                    float f[V];
+                    if (e < left) {
+                        load_vec<T, V>(f, p + e);
+                    } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[e] = h[e];
-                    o[e] = l[e];
+                        for (int c = 0; c < V; ++c) f[c] = 0.0f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < V; ++c) v[k][e + c] = f[c];
                 }
             } else {
 #pragma unroll
+                for (int e = 0; e < 8; ++e) v[k][e] = e < left ? to_f32(p[e]) : 0.0f;
+            }
+        }
+    }
+    // those elements times inv, split, to X
+    __device__ __forceinline__ void place(const OrthoDims& d, const float (&v)[kEights][8], double inv) const
+    {
+#pragma unroll
+        for (int k = 0; k < kEights; ++k) {
+            const int q = k * S::kThr + (int)threadIdx.x;
+            const int i = d.tall ? q % (SP / 8) * 8 : q / (TP / 8);
+            const int j = d.tall ? q / (SP / 8) : q % (TP / 8) * 8;
+            h8 h, l;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                _Float16 a, b;
+                split((float)((double)v[k][e] * inv), a, b);
+                h[e] = a;
+                l[e] = b;
+            }
+            if (!d.tall) {
+                *reinterpret_cast<h8*>(X + at(SP, j >> 5, i, (j & 31) >> 3)) = h;
+                *reinterpret_cast<h8*>(X + at(SP, j >> 5, i, ((j & 31) >> 3) + 4)) = l;
+            } else {
+#pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    X[at(SP, tj >> 5, (int)i + e, (tj & 31) >> 3) + (tj & 7)] = h[e];
-                    X[at(SP, tj >> 5, (int)i + e, ((tj & 31) >> 3) + 4) + (tj & 7)] = l[e];
+                    X[at(SP, j >> 5, i + e, (j & 31) >> 3) + (j & 7)] = h[e];
+                    X[at(SP, j >> 5, i + e, ((j & 31) >> 3) + 4) + (j & 7)] = l[e];
                 }
             }
         }
     }
     // the lane's values of the last X to the output
     template <class T>
-    __device__ __forceinline__ void store(const OrthoDims& d, T* __restrict__ o, int64_t t0, const f16v (&v)[S::NX]) const
+    __device__ __forceinline__ void store(const OrthoDims& d, T* __restrict__ o, int64_t t0, bool wide,
+                                          const f16v (&v)[S::NX]) const
     {
         const int64_t i = wj + (lane & 31);
         if (i >= d.s) return;
 #pragma unroll
         for (int x = 0; x < S::NX; ++x)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+            for (int g = 0; g < 4; ++g) {
+                const int64_t j = t0 + wt + 32 * x + 8 * g + 4 * (lane >> 5);
+                if (wide && !d.tall) {  // t is a multiple of four
+                    struct alignas(4 * sizeof(T)) Four {
+                        T e[4];
+                    } w;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t j = t0 + wt + 32 * x + 8 * g + 4 * (lane >> 5) + q;
-                    if (j < d.t) o[d.tall ? j * d.s + i : i * d.t + j] = from_f32<T>(v[x][4 * g + q]);
+                    for (int q = 0; q < 4; ++q) w.e[q] = from_f32<T>(v[x][4 * g + q]);
+                    if (j < d.t) *reinterpret_cast<Four*>(o + i * d.t + j) = w;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (j + q < d.t) o[d.tall ? (j + q) * d.s + i : i * d.t + j + q] = from_f32<T>(v[x][4 * g + q]);
                 }
+            }
     }
 };
 
@@ -754,25 +795,30 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
     const SmallOps<SP, TP> ops(X, A);
     const int64_t size = a.d.s * a.d.t;
     const T* g = (const T*)a.G + blockIdx.x * size;
+    float v[SmallOps<SP, TP>::kEights][8];
+    ops.fetch(a.d, g, 0, a.wide, v);
     double sum = 0.0;
-#pragma unroll 4
-    for (int64_t q = threadIdx.x; q < size; q += S::kThr) sum += (double)to_f32(g[q]) * (double)to_f32(g[q]);
+#pragma unroll
+    for (int k = 0; k < SmallOps<SP, TP>::kEights; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += (double)v[k][e] * (double)v[k][e];
 #pragma unroll
     for (int d = 32; d > 0; d /= 2) sum += __shfl_xor(sum, d, 64);
     if ((threadIdx.x & 63) == 0) norms[threadIdx.x >> 6] = sum;
+    if ((int)threadIdx.x < a.poly.steps) units[threadIdx.x] = a.table.u[threadIdx.x];
     __syncthreads();
     sum = 0.0;
 #pragma unroll
     for (int w = 0; w < S::NW; ++w) sum += norms[w];
-    const double norm = sqrt(sum), den = norm + (double)a.poly.eps;
-    if (threadIdx.x == 0) step_units(a.poly, norm / den, units);
-    ops.load(a.d, g, 0, unit_of(norm / den) / den);
+    const double norm = sqrt(sum), den = norm + (double)a.poly.eps, bound = start_bound(norm / den);
+    if (bound != 1.0 && threadIdx.x == 0) step_units(a.poly, bound, units);
+    ops.place(a.d, v, unit_of(bound) / den);
     __syncthreads();
     f16v xr[S::NX], ar[S::GX], acc[S::NX];
     ops.get(xr);
     for (int k = 0; k < a.poly.steps; ++k) {
         const Units u = units[k];
-        ops.square(X, ar, TP / 32);
+        ops.template square<TP / 32>(X, ar);
 #pragma unroll
         for (int x = 0; x < S::GX; ++x)
 #pragma unroll
@@ -789,7 +835,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
         ops.put(X, xr, ops.wt);
         __syncthreads();
     }
-    ops.store(a.d, (T*)a.out + blockIdx.x * size, 0, xr);
+    ops.store(a.d, (T*)a.out + blockIdx.x * size, 0, a.wide, xr);
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -856,6 +902,8 @@ hipError_t small(const OrthoLayout& w, const OrthoShape& o, const void* G, void*
     SmallArgs a{};
     a.d = w.d;
     a.poly = OrthoPoly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
+    step_units(a.poly, 1.0, a.table.u);
+    a.wide = (o.n * dtype_size(o.dtype)) % 16 == 0 && (((uintptr_t)G | (uintptr_t)out) & 15u) == 0;
     a.G = G;
     a.out = out;
     hipLaunchKernelGGL((k_ortho_small<SP, TP, T>), dim3((unsigned)o.batch), dim3(Small<SP, TP>::kThr), 0, s, a);
@@ -875,10 +923,12 @@ hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws
     _Float16 *A = (_Float16*)(base + w.A), *B = (_Float16*)(base + w.B);
     Units* units = (Units*)(base + w.units);
     const OrthoPoly poly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
+    UnitTable table{};
+    step_units(poly, 1.0, table.u);
     hipLaunchKernelGGL(k_ortho_norm<T>, dim3((unsigned)(o.batch * w.per)), dim3(kThreads), 0, s, o.m * o.n, w.per,
                        o.m * o.n % kWide<T> == 0 && ((uintptr_t)G & 15u) == 0, (const T*)G, part);
     hipLaunchKernelGGL(k_ortho_first<T>, dim3((unsigned)(o.batch * (w.d.sp / 64) * (w.d.tp / 64))), dim3(kThreads), 0,
-                       s, w.d, poly, w.per, part, (const T*)G, X, Xt[0], units);
+                       s, w.d, poly, table, w.per, part, (const T*)G, X, Xt[0], units);
     for (int step = 0; step < o.steps; ++step) {
         ProdArgs a{};
         a.d = w.d;
