@@ -570,14 +570,18 @@ struct SmallOps {
     {
         return (kb * rows + r) * 64 + ((c ^ ((r >> 1) & 7)) * 8);
     }
-    // acc[x] = sum_k p[row wi + 32 x ..][k] p[row wj ..][k], k over blocks of 32
-    template <int BLOCKS, int N>
-    __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N]) const
+    template <int N>
+    static __device__ __forceinline__ void clear(f16v (&acc)[N])
     {
 #pragma unroll
         for (int x = 0; x < N; ++x)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
+    }
+    // acc[x] += sum_k p[row wi + 32 x ..][k] p[row wj ..][k], k over blocks of 32
+    template <int BLOCKS, int N>
+    __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N]) const
+    {
         const int r = lane & 31, hf = lane >> 5;
 #pragma unroll
         for (int kb = 0; kb < BLOCKS; ++kb)
@@ -613,10 +617,7 @@ struct SmallOps {
     // acc[x][..] = sum_k X[k][wt + 32 x ..] B[wj ..][k], B in A's place
     __device__ __forceinline__ void next(f16v (&acc)[S::NX]) const
     {
-#pragma unroll
-        for (int x = 0; x < S::NX; ++x)
-#pragma unroll
-            for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
+        clear(acc);
         const int r = lane & 31, hf = lane >> 5, half16 = (lane >> 4) & 1;
 #pragma unroll
         for (int kb = 0; kb < SP / 32; ++kb)
@@ -686,6 +687,7 @@ struct SmallOps {
         put(A, ar, wi);
         __syncthreads();
         f16v acc[S::GX];
+        clear(acc);
         square<SP / 32>(A, acc);
 #pragma unroll
         for (int x = 0; x < S::GX; ++x)
@@ -818,6 +820,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
     ops.get(xr);
     for (int k = 0; k < a.poly.steps; ++k) {
         const Units u = units[k];
+        ops.clear(ar);
         ops.template square<TP / 32>(X, ar);
 #pragma unroll
         for (int x = 0; x < S::GX; ++x)
@@ -838,17 +841,199 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
     ops.store(a.d, (T*)a.out + blockIdx.x * size, 0, a.wide, xr);
 }
 
+// ---- a short side of at most 128, the other longer -------------------------------------------
+// A matrix's chunks of TP columns are dealt to `blocks` blocks.  One launch per
+// step: every block adds the partial A = X X^T of all blocks, forms B (the same
+// work in each, in parallel), takes its chunks of X, held in memory as they lie
+// in LDS, through X <- a X + B X, and leaves its partial A of the new X.
+struct WideArgs {
+    OrthoDims d;  // sp, tp unused
+    OrthoPoly poly;
+    int64_t chunks;     // of a matrix
+    int32_t blocks;     // per matrix
+    bool wide;
+    const void* G;
+    void* out;
+    Units* units;       // [batch][steps]
+    _Float16* image;    // [batch][chunks] X as in LDS
+    const float* sums;  // [batch][nsums] partial A, by threads
+    float* osums;       // [batch][blocks]
+    int32_t nsums, step;
+};
+
+// A's values by threads: four at a time, the block's threads in a row
+template <int SP, int TP>
+__device__ __forceinline__ void put_sums(float* __restrict__ p, const f16v (&v)[Small<SP, TP>::GX])
+{
+    using S = Small<SP, TP>;
+    float4* o = reinterpret_cast<float4*>(p) + threadIdx.x;
+#pragma unroll
+    for (int x = 0; x < S::GX; ++x)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            o[(x * 4 + g) * S::kThr] = make_float4(v[x][4 * g], v[x][4 * g + 1], v[x][4 * g + 2], v[x][4 * g + 3]);
+}
+
+template <int SP, int TP>
+__device__ __forceinline__ void add_sums(const float* __restrict__ p, f16v (&v)[Small<SP, TP>::GX])
+{
+    using S = Small<SP, TP>;
+    const float4* o = reinterpret_cast<const float4*>(p) + threadIdx.x;
+#pragma unroll
+    for (int x = 0; x < S::GX; ++x)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 f = o[(x * 4 + g) * S::kThr];
+            v[x][4 * g] += f.x;
+            v[x][4 * g + 1] += f.y;
+            v[x][4 * g + 2] += f.z;
+            v[x][4 * g + 3] += f.w;
+        }
+}
+
+template <int SP, int TP>
+__device__ __forceinline__ void put_image(_Float16* __restrict__ to, const _Float16* X)
+{
+    using S = Small<SP, TP>;
+#pragma unroll
+    for (int q = 0; q < S::kX / 8 / S::kThr; ++q) {
+        const int at = (q * S::kThr + (int)threadIdx.x) * 8;
+        *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(X + at);
+    }
+}
+
+// starts the loads of a chunk's image; in when vmcnt says so
+template <int SP, int TP>
+__device__ __forceinline__ void load_image(const _Float16* __restrict__ from, _Float16* X)
+{
+    using S = Small<SP, TP>;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int q = 0; q < S::kX / 8 / S::kThr; ++q)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(from + (q * S::kThr + (int)threadIdx.x) * 8),
+            (__attribute__((address_space(3))) void*)(X + (q * S::kThr + wave * 64) * 8), 16, 0, 0);
+}
+
+// the first X, split, and its partial A
+template <int SP, int TP, class T>
+__global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_wide_first(WideArgs a, UnitTable table, int32_t per,
+                                                                            const double* __restrict__ part)
+{
+    using S = Small<SP, TP>;
+    __shared__ __attribute__((aligned(16))) _Float16 X[S::kX];
+    const SmallOps<SP, TP> ops(X, nullptr);
+    const int64_t b = blockIdx.x / a.blocks, k = blockIdx.x % a.blocks;
+    const double norm = norm_of(part, b, per), den = norm + (double)a.poly.eps, bound = start_bound(norm / den);
+    if (k == 0) {
+        if (bound == 1.0) {
+            if ((int)threadIdx.x < a.poly.steps) a.units[b * a.poly.steps + threadIdx.x] = table.u[threadIdx.x];
+        } else if (threadIdx.x == 0) {
+            step_units(a.poly, bound, a.units + b * a.poly.steps);
+        }
+    }
+    const double inv = unit_of(bound) / den;
+    const T* g = (const T*)a.G + b * a.d.s * a.d.t;
+    f16v ar[S::GX];
+    ops.clear(ar);
+    for (int64_t c = k; c < a.chunks; c += a.blocks) {
+        float v[SmallOps<SP, TP>::kEights][8];
+        ops.fetch(a.d, g, c * TP, a.wide, v);
+        __syncthreads();  // the chunk before is read
+        ops.place(a.d, v, inv);
+        __syncthreads();
+        put_image<SP, TP>(a.image + (b * a.chunks + c) * S::kX, X);
+        ops.template square<TP / 32>(X, ar);
+    }
+    put_sums<SP, TP>(a.osums + blockIdx.x * (int64_t)(SP * SP), ar);
+}
+
+// one step; the last one writes the output
+template <int SP, int TP, class T>
+__global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_wide_step(WideArgs a)
+{
+    using S = Small<SP, TP>;
+    __shared__ __attribute__((aligned(16))) _Float16 X[S::kX], A[S::kA];
+    const SmallOps<SP, TP> ops(X, A);
+    const int64_t b = blockIdx.x / a.blocks, k = blockIdx.x % a.blocks;
+    const bool last = a.step + 1 == a.poly.steps;
+    const Units u = a.units[b * a.poly.steps + a.step];
+    _Float16* image = a.image + b * a.chunks * S::kX;
+    load_image<SP, TP>(image + k * S::kX, X);
+    f16v ar[S::GX];
+    ops.clear(ar);
+#pragma unroll 2
+    for (int32_t p = 0; p < a.nsums; ++p) add_sums<SP, TP>(a.sums + (b * a.nsums + p) * (int64_t)(SP * SP), ar);
+#pragma unroll
+    for (int x = 0; x < S::GX; ++x)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) ar[x][q] *= u.gram;
+    ops.poly(ar, u);
+    ops.clear(ar);
+    for (int64_t c = k; c < a.chunks; c += a.blocks) {
+        if (c != k) {
+            __syncthreads();  // the chunk before is read
+            load_image<SP, TP>(image + c * S::kX, X);
+        }
+        wait_barrier<0>();
+        f16v xr[S::NX], acc[S::NX];
+        ops.get(xr);
+        ops.next(acc);
+#pragma unroll
+        for (int x = 0; x < S::NX; ++x)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) xr[x][q] = u.mul * acc[x][q] + u.add * xr[x][q];
+        if (last) {
+            ops.store(a.d, (T*)a.out + b * a.d.s * a.d.t, c * TP, a.wide, xr);
+        } else {
+            __syncthreads();
+            ops.put(X, xr, ops.wt);
+            __syncthreads();
+            put_image<SP, TP>(image + c * S::kX, X);
+            ops.template square<TP / 32>(X, ar);
+        }
+    }
+    if (!last) put_sums<SP, TP>(a.osums + blockIdx.x * (int64_t)(SP * SP), ar);
+}
+
+// sums of the blocks' partial A, where they are many
+__global__ void __launch_bounds__(kThreads) k_ortho_add(int64_t size, int32_t n, const float4* __restrict__ p,
+                                                        float4* __restrict__ o)
+{
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y;
+    if (i >= size) return;
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int32_t k = 0; k < n; ++k) {
+        const float4 f = p[(b * n + k) * size + i];
+        t.x += f.x;
+        t.y += f.y;
+        t.z += f.z;
+        t.w += f.w;
+    }
+    o[b * size + i] = t;
+}
+
 // ---- host ----------------------------------------------------------------------------------
+
 // Wide tiles read less of LDS per product, small ones fill the chip: wide ones
 // where there are at least kFill of them.
 constexpr int64_t kFill = 100;
 
+// Forms: a whole matrix per block, chunks of columns per block, or tiles.
+enum : int { kWhole = 0, kChunks = 1, kTiles = 2 };
+
 struct OrthoLayout {
     OrthoDims d;
+    int form, side;  // side: the padded short side of the first two forms
     int pad;
-    int32_t per;
-    size_t part, units, X, Xt[2], A, B, bytes;
+    int32_t per, blocks;
+    int64_t chunks;
+    size_t part, units, image, sums[2], total, X, Xt[2], A, B, bytes;
 };
+
+constexpr int kChunk = 128;    // columns
+constexpr int kAddBlocks = 8;  // partial sums that every block adds by itself; more are added first
 
 OrthoLayout ortho_layout(const OrthoShape& o)
 {
@@ -856,26 +1041,41 @@ OrthoLayout ortho_layout(const OrthoShape& o)
     w.d.tall = o.m > o.n;
     w.d.s = w.d.tall ? o.n : o.m;
     w.d.t = w.d.tall ? o.m : o.n;
-    // whole wide tiles where there are enough of them and they add little padding
-    const int64_t s64 = cdiv64(w.d.s, 64), t64 = cdiv64(w.d.t, 64), s128 = cdiv64(s64, 2), t128 = cdiv64(t64, 2);
-    w.pad = s128 * t128 * o.batch >= kFill && 40 * s128 * t128 <= 11 * s64 * t64 ? 128 : 64;
-    w.d.sp = cdiv64(w.d.s, w.pad) * w.pad;
-    w.d.tp = cdiv64(w.d.t, w.pad) * w.pad;
-    const int64_t size = o.m * o.n;
-    const int64_t sums = cdiv64(size, kNormElems);
-    w.per = (int32_t)(sums < kNormBlocks ? sums : kNormBlocks);
+    w.form = w.d.t <= kChunk ? kWhole : w.d.s <= 128 ? kChunks : kTiles;
+    w.side = w.d.s <= 64 ? 64 : 128;
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t at = off;
         off += align256((size_t)bytes);
         return at;
     };
+    if (w.form == kWhole) {
+        w.bytes = 256;
+        return w;
+    }
+    const int64_t sums = cdiv64(o.m * o.n, kNormElems);
+    w.per = (int32_t)(sums < kNormBlocks ? sums : kNormBlocks);
     w.part = take(8 * o.batch * w.per);
     w.units = take((int64_t)sizeof(Units) * o.batch * kMaxOrthoSteps);
-    w.X = take(4 * o.batch * w.d.sp * w.d.tp);
-    for (int k = 0; k < 2; ++k) w.Xt[k] = take(4 * o.batch * w.d.sp * w.d.tp);
-    w.A = take(4 * o.batch * w.d.sp * w.d.sp);
-    w.B = take(4 * o.batch * w.d.sp * w.d.sp);
+    if (w.form == kChunks) {
+        // about one block per compute unit (two of the small ones)
+        w.chunks = cdiv64(w.d.t, kChunk);
+        const int64_t want = (w.side == 128 ? 256 : 512) / (o.batch > 0 ? o.batch : 1);
+        w.blocks = (int32_t)(want < 1 ? 1 : want < w.chunks ? want : w.chunks);
+        w.image = take(4 * o.batch * w.chunks * w.side * kChunk);
+        for (int k = 0; k < 2; ++k) w.sums[k] = take(4 * o.batch * w.blocks * w.side * w.side);
+        w.total = take(4 * o.batch * w.side * w.side);
+    } else {
+        // whole wide tiles where there are enough of them and they add little padding
+        const int64_t s64 = cdiv64(w.d.s, 64), t64 = cdiv64(w.d.t, 64), s128 = cdiv64(s64, 2), t128 = cdiv64(t64, 2);
+        w.pad = s128 * t128 * o.batch >= kFill && 40 * s128 * t128 <= 11 * s64 * t64 ? 128 : 64;
+        w.d.sp = cdiv64(w.d.s, w.pad) * w.pad;
+        w.d.tp = cdiv64(w.d.t, w.pad) * w.pad;
+        w.X = take(4 * o.batch * w.d.sp * w.d.tp);
+        for (int k = 0; k < 2; ++k) w.Xt[k] = take(4 * o.batch * w.d.sp * w.d.tp);
+        w.A = take(4 * o.batch * w.d.sp * w.d.sp);
+        w.B = take(4 * o.batch * w.d.sp * w.d.sp);
+    }
     w.bytes = off;
     return w;
 }
@@ -896,39 +1096,74 @@ void prod(const OrthoLayout& w, const OrthoShape& o, ProdArgs a, hipStream_t s)
         hipLaunchKernelGGL((k_ortho_prod<64, KIND, T>), dim3((unsigned)tiles(64)), dim3(kProdThreads<64>), 0, s, a);
 }
 
+bool wide_rows(const OrthoShape& o, const void* G, const void* out)
+{
+    return (o.n * dtype_size(o.dtype)) % 16 == 0 && (((uintptr_t)G | (uintptr_t)out) & 15u) == 0;
+}
+
 template <int SP, int TP, class T>
-hipError_t small(const OrthoLayout& w, const OrthoShape& o, const void* G, void* out, hipStream_t s)
+hipError_t whole(const OrthoLayout& w, const OrthoShape& o, const OrthoPoly& poly, const UnitTable& table,
+                 const void* G, void* out, hipStream_t s)
 {
     SmallArgs a{};
     a.d = w.d;
-    a.poly = OrthoPoly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
-    step_units(a.poly, 1.0, a.table.u);
-    a.wide = (o.n * dtype_size(o.dtype)) % 16 == 0 && (((uintptr_t)G | (uintptr_t)out) & 15u) == 0;
+    a.poly = poly;
+    a.table = table;
+    a.wide = wide_rows(o, G, out);
     a.G = G;
     a.out = out;
     hipLaunchKernelGGL((k_ortho_small<SP, TP, T>), dim3((unsigned)o.batch), dim3(Small<SP, TP>::kThr), 0, s, a);
     return hipGetLastError();
 }
 
-template <class T>
-hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s)
+template <int SP, class T>
+hipError_t chunks(const OrthoLayout& w, const OrthoShape& o, const OrthoPoly& poly, const UnitTable& table,
+                  const void* G, void* out, char* base, hipStream_t s)
 {
-    const OrthoLayout w = ortho_layout(o);
-    if (w.d.t <= 64) return small<64, 64, T>(w, o, G, out, s);
-    if (w.d.t <= 128 && w.d.s <= 64) return small<64, 128, T>(w, o, G, out, s);
-    if (w.d.t <= 128) return small<128, 128, T>(w, o, G, out, s);
-    char* base = (char*)ws;
-    double* part = (double*)(base + w.part);
+    constexpr int TP = kChunk;
+    using S = Small<SP, TP>;
+    const dim3 grid((unsigned)(o.batch * w.blocks)), thr(S::kThr);
+    float *sums[2] = {(float*)(base + w.sums[0]), (float*)(base + w.sums[1])}, *total = (float*)(base + w.total);
+    WideArgs a{};
+    a.d = w.d;
+    a.poly = poly;
+    a.chunks = w.chunks;
+    a.blocks = w.blocks;
+    a.wide = wide_rows(o, G, out);
+    a.G = G;
+    a.out = out;
+    a.units = (Units*)(base + w.units);
+    a.image = (_Float16*)(base + w.image);
+    a.osums = sums[0];
+    hipLaunchKernelGGL((k_ortho_wide_first<SP, TP, T>), grid, thr, 0, s, a, table, w.per,
+                       (const double*)(base + w.part));
+    const bool add = w.blocks > kAddBlocks;
+    for (int step = 0; step < o.steps; ++step) {
+        a.step = step;
+        a.sums = sums[step & 1];
+        a.osums = sums[(step & 1) ^ 1];
+        a.nsums = w.blocks;
+        if (add) {
+            const int64_t size = SP * SP / 4;
+            hipLaunchKernelGGL(k_ortho_add, dim3((unsigned)cdiv64(size, kThreads), (unsigned)o.batch), dim3(kThreads), 0,
+                               s, size, w.blocks, (const float4*)a.sums, (float4*)total);
+            a.sums = total;
+            a.nsums = 1;
+        }
+        hipLaunchKernelGGL((k_ortho_wide_step<SP, TP, T>), grid, thr, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t tiles(const OrthoLayout& w, const OrthoShape& o, const OrthoPoly& poly, const UnitTable& table,
+                 const void* G, void* out, char* base, hipStream_t s)
+{
     _Float16 *X = (_Float16*)(base + w.X), *Xt[2] = {(_Float16*)(base + w.Xt[0]), (_Float16*)(base + w.Xt[1])};
     _Float16 *A = (_Float16*)(base + w.A), *B = (_Float16*)(base + w.B);
     Units* units = (Units*)(base + w.units);
-    const OrthoPoly poly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
-    UnitTable table{};
-    step_units(poly, 1.0, table.u);
-    hipLaunchKernelGGL(k_ortho_norm<T>, dim3((unsigned)(o.batch * w.per)), dim3(kThreads), 0, s, o.m * o.n, w.per,
-                       o.m * o.n % kWide<T> == 0 && ((uintptr_t)G & 15u) == 0, (const T*)G, part);
     hipLaunchKernelGGL(k_ortho_first<T>, dim3((unsigned)(o.batch * (w.d.sp / 64) * (w.d.tp / 64))), dim3(kThreads), 0,
-                       s, w.d, poly, table, w.per, part, (const T*)G, X, Xt[0], units);
+                       s, w.d, poly, table, w.per, (const double*)(base + w.part), (const T*)G, X, Xt[0], units);
     for (int step = 0; step < o.steps; ++step) {
         ProdArgs a{};
         a.d = w.d;
@@ -951,6 +1186,26 @@ hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws
         else prod<kNext, T>(w, o, a, s);
     }
     return hipGetLastError();
+}
+
+template <class T>
+hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s)
+{
+    const OrthoLayout w = ortho_layout(o);
+    char* base = (char*)ws;
+    const OrthoPoly poly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
+    UnitTable table{};
+    step_units(poly, 1.0, table.u);
+    if (w.form == kWhole) {
+        if (w.d.t <= 64) return whole<64, 64, T>(w, o, poly, table, G, out, s);
+        if (w.side == 64) return whole<64, 128, T>(w, o, poly, table, G, out, s);
+        return whole<128, 128, T>(w, o, poly, table, G, out, s);
+    }
+    hipLaunchKernelGGL(k_ortho_norm<T>, dim3((unsigned)(o.batch * w.per)), dim3(kThreads), 0, s, o.m * o.n, w.per,
+                       o.m * o.n % kWide<T> == 0 && ((uintptr_t)G & 15u) == 0, (const T*)G, (double*)(base + w.part));
+    if (w.form == kTiles) return tiles<T>(w, o, poly, table, G, out, base, s);
+    return w.side == 64 ? chunks<64, T>(w, o, poly, table, G, out, base, s)
+                        : chunks<128, T>(w, o, poly, table, G, out, base, s);
 }
 
 }  // namespace
