@@ -121,6 +121,21 @@ struct UnitTable {
     Units u[kMaxOrthoSteps];
 };
 
+// A factor as a power of two and the rest, for elements whose magnitude and
+// factor together stay in fp32's range although the factor alone may not.
+struct Scale {
+    float two, rest;
+};
+
+__device__ __forceinline__ Scale scale_of(double f)
+{
+    int e;
+    frexp(f, &e);
+    e = e < -120 ? -120 : e > 120 ? 120 : e;
+    const double two = ldexp(1.0, e);
+    return Scale{(float)two, (float)(f / two)};
+}
+
 // the bound that a matrix of norm r, at most 1, goes by
 __device__ __forceinline__ double start_bound(double r) { return r > 0.5 ? 1.0 : r; }
 
@@ -183,7 +198,8 @@ __global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly
     const int64_t b = blockIdx.x / (ti * tj), r = blockIdx.x % (ti * tj);
     const int64_t i0 = r / tj * 64, j0 = r % tj * 64;
     const double norm = norm_of(part, b, per), den = norm + (double)poly.eps;
-    const double bound = start_bound(norm / den), inv = unit_of(bound) / den;
+    const double bound = start_bound(norm / den);
+    const Scale inv = scale_of(unit_of(bound) / den);
     if (r == 0) {
         if (bound == 1.0) {
             if ((int)threadIdx.x < poly.steps) units[b * poly.steps + threadIdx.x] = table.u[threadIdx.x];
@@ -196,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly
         const int a = q / 64, c = q % 64;  // c runs along G's rows
         const int64_t i = i0 + (d.tall ? c : a), j = j0 + (d.tall ? a : c);
         float v = 0.0f;
-        if (i < d.s && j < d.t) v = (float)((double)to_f32(g[d.tall ? j * d.s + i : i * d.t + j]) * inv);
+        if (i < d.s && j < d.t) v = to_f32(g[d.tall ? j * d.s + i : i * d.t + j]) * inv.two * inv.rest;
         tile[d.tall ? c : a][d.tall ? a : c] = v;
     }
     __syncthreads();
@@ -556,6 +572,10 @@ struct SmallOps {
     using S = Small<SP, TP>;
     _Float16 *X, *A;
     int lane, wi, wj, wt;  // wave's first row of A, column, first t
+    // The lane's offsets (halves), formed once: rows begin at multiples of 32, so
+    // that the swizzle depends on the lane alone.
+    int at[4];  // pieces 2 ks + lane / 32 (+ 4) of row lane % 32, by ks + 2 low
+    int tr[4];  // transposing reads, by first row 0 or 4, + 2 low
 
     __device__ __forceinline__ SmallOps(_Float16* x, _Float16* a) : X(x), A(a)
     {
@@ -564,9 +584,17 @@ struct SmallOps {
         wi = wave / S::WC * 32 * S::GX;
         wt = wave / S::WC * 32 * S::NX;
         wj = wave % S::WC * 32;
+        const int r = lane & 31, hf = lane >> 5, l = lane & 15, half16 = (lane >> 4) & 1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            at[q] = place_of(0, 0, r, ((q & 1) * 2 + hf) + (q >> 1) * 4);
+            // lanes of 16 hold rows t0 + lane % 16, four k each; each lane points
+            // at 8 bytes of row k + lane % 16 / 4 of X
+            tr[q] = place_of(0, 0, 8 * hf + 4 * (q & 1) + (l >> 2), 2 * half16 + ((l & 3) >> 1) + (q >> 1) * 4) + 4 * (l & 1);
+        }
     }
     // halves offset of 16-byte piece c (0..7) of row r in block kb; an operand of `rows` rows
-    static __device__ __forceinline__ int at(int rows, int kb, int r, int c)
+    static __device__ __forceinline__ int place_of(int rows, int kb, int r, int c)
     {
         return (kb * rows + r) * 64 + ((c ^ ((r >> 1) & 7)) * 8);
     }
@@ -578,38 +606,40 @@ struct SmallOps {
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
     }
+    // acc[x] += three products of p[x] and q
+    template <int N>
+    static __device__ __forceinline__ void multiply(const h8 (&ph)[N], const h8 (&pl)[N], h8 qh, h8 ql, f16v (&acc)[N])
+    {
+#pragma unroll
+        for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh, acc[x], 0, 0, 0);
+    }
     // acc[x] += sum_k p[row wi + 32 x ..][k] p[row wj ..][k], k over blocks of 32
     template <int BLOCKS, int N>
     __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N]) const
     {
-        const int r = lane & 31, hf = lane >> 5;
+        const _Float16 *pi = p + wi * 64, *pj = p + wj * 64;
 #pragma unroll
         for (int kb = 0; kb < BLOCKS; ++kb)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const int c = ks * 2 + hf;
-                const h8 qh = *reinterpret_cast<const h8*>(p + at(SP, kb, wj + r, c));
-                const h8 ql = *reinterpret_cast<const h8*>(p + at(SP, kb, wj + r, c + 4));
+                const h8 qh = *reinterpret_cast<const h8*>(pj + at[ks] + kb * SP * 64);
+                const h8 ql = *reinterpret_cast<const h8*>(pj + at[ks + 2] + kb * SP * 64);
                 h8 ph[N], pl[N];
 #pragma unroll
                 for (int x = 0; x < N; ++x) {
-                    ph[x] = *reinterpret_cast<const h8*>(p + at(SP, kb, wi + 32 * x + r, c));
-                    pl[x] = *reinterpret_cast<const h8*>(p + at(SP, kb, wi + 32 * x + r, c + 4));
+                    ph[x] = *reinterpret_cast<const h8*>(pi + at[ks] + (kb * SP + 32 * x) * 64);
+                    pl[x] = *reinterpret_cast<const h8*>(pi + at[ks + 2] + (kb * SP + 32 * x) * 64);
                 }
-#pragma unroll
-                for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
-#pragma unroll
-                for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
-#pragma unroll
-                for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh, acc[x], 0, 0, 0);
+                multiply(ph, pl, qh, ql, acc);
             }
     }
-    // four values of X^T rows: lanes of 16 hold rows t0 + lane % 16, k .. k+3;
-    // each lane points at 8 bytes of row k + lane % 16 / 4 of X
-    __device__ __forceinline__ h4v transposed(int t0, int k, int low) const
+    // four k of X^T's rows
+    __device__ __forceinline__ h4v transposed(const _Float16* p) const
     {
-        const int l = lane & 15, t = t0 + 4 * (l & 3), row = k + (l >> 2);
-        const _Float16* p = X + at(SP, t >> 5, row, ((t & 31) >> 3) + low) + (t & 4);
         const s4v v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s4v*)const_cast<_Float16*>(p));
         return __builtin_bit_cast(h4v, v);
@@ -618,37 +648,34 @@ struct SmallOps {
     __device__ __forceinline__ void next(f16v (&acc)[S::NX]) const
     {
         clear(acc);
-        const int r = lane & 31, hf = lane >> 5, half16 = (lane >> 4) & 1;
+        const _Float16 *pt = X + (wt >> 5) * SP * 64, *pj = A + wj * 64;
 #pragma unroll
         for (int kb = 0; kb < SP / 32; ++kb)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const int c = ks * 2 + hf, k = kb * 32 + ks * 16 + 8 * hf;
-                const h8 qh = *reinterpret_cast<const h8*>(A + at(SP, kb, wj + r, c));
-                const h8 ql = *reinterpret_cast<const h8*>(A + at(SP, kb, wj + r, c + 4));
+                const h8 qh = *reinterpret_cast<const h8*>(pj + at[ks] + kb * SP * 64);
+                const h8 ql = *reinterpret_cast<const h8*>(pj + at[ks + 2] + kb * SP * 64);
                 h8 ph[S::NX], pl[S::NX];
 #pragma unroll
                 for (int x = 0; x < S::NX; ++x) {
-                    const int t0 = wt + 32 * x + 16 * half16;
-                    const h4v a = transposed(t0, k, 0), b = transposed(t0, k + 4, 0);
-                    const h4v e = transposed(t0, k, 4), f = transposed(t0, k + 4, 4);
-                    ph[x] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-                    pl[x] = __builtin_shufflevector(e, f, 0, 1, 2, 3, 4, 5, 6, 7);
+                    const _Float16* p = pt + (x * SP + kb * 32 + ks * 16) * 64;
+                    ph[x] = __builtin_shufflevector(transposed(p + tr[0]), transposed(p + tr[1]), 0, 1, 2, 3, 4, 5, 6, 7);
+                    pl[x] = __builtin_shufflevector(transposed(p + tr[2]), transposed(p + tr[3]), 0, 1, 2, 3, 4, 5, 6, 7);
                 }
-#pragma unroll
-                for (int x = 0; x < S::NX; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
-#pragma unroll
-                for (int x = 0; x < S::NX; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
-#pragma unroll
-                for (int x = 0; x < S::NX; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh, acc[x], 0, 0, 0);
+                multiply(ph, pl, qh, ql, acc);
             }
+    }
+    // the lane's four values g of block kb (low half: + 4) in row wj + lane % 32
+    __device__ __forceinline__ int four_at(int kb, int g) const
+    {
+        return place_of(SP, kb, lane & 31, g) + 4 * (lane >> 5);
     }
     // rows v[x][4 g .. 4 g + 3] at first + 32 x + 8 g + 4 (lane / 32) of column wj + lane % 32,
     // written as that row of p
     template <int N>
     __device__ __forceinline__ void put(_Float16* p, const f16v (&v)[N], int first) const
     {
-        const int r = wj + (lane & 31);
+        p += (wj + (first >> 5) * SP) * 64;
 #pragma unroll
         for (int x = 0; x < N; ++x)
 #pragma unroll
@@ -661,22 +688,20 @@ struct SmallOps {
                     h[q] = a;
                     l[q] = b;
                 }
-                const int kb = (first >> 5) + x, off = 4 * (lane >> 5);
-                *reinterpret_cast<h4v*>(p + at(SP, kb, r, g) + off) = h;
-                *reinterpret_cast<h4v*>(p + at(SP, kb, r, g + 4) + off) = l;
+                *reinterpret_cast<h4v*>(p + four_at(x, g)) = h;
+                *reinterpret_cast<h4v*>(p + four_at(x, g + 4)) = l;
             }
     }
     // the lane's values of X, as put() left them
     __device__ __forceinline__ void get(f16v (&v)[S::NX]) const
     {
-        const int r = wj + (lane & 31);
+        const _Float16* p = X + (wj + (wt >> 5) * SP) * 64;
 #pragma unroll
         for (int x = 0; x < S::NX; ++x)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int kb = (wt >> 5) + x, off = 4 * (lane >> 5);
-                const h4v h = *reinterpret_cast<const h4v*>(X + at(SP, kb, r, g) + off);
-                const h4v l = *reinterpret_cast<const h4v*>(X + at(SP, kb, r, g + 4) + off);
+                const h4v h = *reinterpret_cast<const h4v*>(p + four_at(x, g));
+                const h4v l = *reinterpret_cast<const h4v*>(p + four_at(x, g + 4));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[x][4 * g + q] = (float)h[q] + (float)l[q];
             }
@@ -699,61 +724,79 @@ struct SmallOps {
     // columns t0 .. t0 + TP of matrix g, zero outside: the thread's elements,
     // eight along G's rows each (wide: G's rows are whole 16-byte accesses)
     static constexpr int kEights = SP * TP / 8 / S::kThr;
+    // row i of X and column j of the thread's k-th eight's first element
+    static __device__ __forceinline__ int row_of(const OrthoDims& d, int k)
+    {
+        const int q = k * S::kThr + (int)threadIdx.x;
+        return d.tall ? q % (SP / 8) * 8 : q / (TP / 8);
+    }
+    static __device__ __forceinline__ int col_of(const OrthoDims& d, int k)
+    {
+        const int q = k * S::kThr + (int)threadIdx.x;
+        return d.tall ? q / (SP / 8) : q % (TP / 8) * 8;
+    }
+    static __device__ __forceinline__ int64_t offset(const OrthoDims& d, int64_t t0, int k)
+    {
+        const int64_t i = row_of(d, k), j = t0 + col_of(d, k);
+        return d.tall ? j * d.s + i : i * d.t + j;
+    }
+    // whether the eight's element e is in the matrix
+    static __device__ __forceinline__ bool inside(const OrthoDims& d, int64_t t0, int k, int e)
+    {
+        const int64_t i = row_of(d, k), j = t0 + col_of(d, k);
+        return d.tall ? j < d.t && i + e < d.s : i < d.s && j + e < d.t;
+    }
     template <class T>
     __device__ __forceinline__ void fetch(const OrthoDims& d, const T* __restrict__ g, int64_t t0, bool wide,
                                           float (&v)[kEights][8]) const
     {
+        // loads stand outside any condition (outside the matrix at its first
+        // element), so that all of them are in flight together
+        if (wide) {
+            constexpr int V = kWide<T>;
+            float f[kEights][8 / V][V];
 #pragma unroll
-        for (int k = 0; k < kEights; ++k) {
-            const int q = k * S::kThr + (int)threadIdx.x;
-            const int64_t i = d.tall ? q % (SP / 8) * 8 : q / (TP / 8);
-            const int64_t j = t0 + (d.tall ? q / (SP / 8) : q % (TP / 8) * 8);
-            const T* p = g + (d.tall ? j * d.s + i : i * d.t + j);
-            const int64_t left = (d.tall ? j < d.t : i < d.s) ? (d.tall ? d.s - i : d.t - j) : 0;
-            if (wide) {
-                constexpr int V = kWide<T>;
+            for (int k = 0; k < kEights; ++k)
 #pragma unroll
-                for (int e = 0; e < 8; e += V) {
-                    float f[V];
-                    if (e < left) {
-                        load_vec<T, V>(f, p + e);
-                    } else {
+                for (int e = 0; e < 8 / V; ++e)
+                    load_vec<T, V>(f[k][e], g + (inside(d, t0, k, e * V) ? offset(d, t0, k) + e * V : 0));
 #pragma unroll
-                        for (int c = 0; c < V; ++c) f[c] = 0.0f;
-                    }
+            for (int k = 0; k < kEights; ++k)
 #pragma unroll
-                    for (int c = 0; c < V; ++c) v[k][e + c] = f[c];
-                }
-            } else {
+                for (int e = 0; e < 8; ++e) v[k][e] = inside(d, t0, k, e / V * V) ? f[k][e / V][e % V] : 0.0f;
+        } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[k][e] = e < left ? to_f32(p[e]) : 0.0f;
-            }
+            for (int k = 0; k < kEights; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[k][e] = to_f32(g[inside(d, t0, k, e) ? offset(d, t0, k) + e : 0]);
+#pragma unroll
+            for (int k = 0; k < kEights; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[k][e] = inside(d, t0, k, e) ? v[k][e] : 0.0f;
         }
     }
-    // those elements times inv, split, to X
-    __device__ __forceinline__ void place(const OrthoDims& d, const float (&v)[kEights][8], double inv) const
+    // those elements times the scale, split, to X
+    __device__ __forceinline__ void place(const OrthoDims& d, const float (&v)[kEights][8], Scale k) const
     {
 #pragma unroll
-        for (int k = 0; k < kEights; ++k) {
-            const int q = k * S::kThr + (int)threadIdx.x;
-            const int i = d.tall ? q % (SP / 8) * 8 : q / (TP / 8);
-            const int j = d.tall ? q / (SP / 8) : q % (TP / 8) * 8;
+        for (int e8 = 0; e8 < kEights; ++e8) {
+            const int i = row_of(d, e8), j = col_of(d, e8);
             h8 h, l;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 _Float16 a, b;
-                split((float)((double)v[k][e] * inv), a, b);
+                split(v[e8][e] * k.two * k.rest, a, b);
                 h[e] = a;
                 l[e] = b;
             }
             if (!d.tall) {
-                *reinterpret_cast<h8*>(X + at(SP, j >> 5, i, (j & 31) >> 3)) = h;
-                *reinterpret_cast<h8*>(X + at(SP, j >> 5, i, ((j & 31) >> 3) + 4)) = l;
+                *reinterpret_cast<h8*>(X + place_of(SP, j >> 5, i, (j & 31) >> 3)) = h;
+                *reinterpret_cast<h8*>(X + place_of(SP, j >> 5, i, ((j & 31) >> 3) + 4)) = l;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    X[at(SP, j >> 5, i + e, (j & 31) >> 3) + (j & 7)] = h[e];
-                    X[at(SP, j >> 5, i + e, ((j & 31) >> 3) + 4) + (j & 7)] = l[e];
+                    X[place_of(SP, j >> 5, i + e, (j & 31) >> 3) + (j & 7)] = h[e];
+                    X[place_of(SP, j >> 5, i + e, ((j & 31) >> 3) + 4) + (j & 7)] = l[e];
                 }
             }
         }
@@ -814,7 +857,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
     for (int w = 0; w < S::NW; ++w) sum += norms[w];
     const double norm = sqrt(sum), den = norm + (double)a.poly.eps, bound = start_bound(norm / den);
     if (bound != 1.0 && threadIdx.x == 0) step_units(a.poly, bound, units);
-    ops.place(a.d, v, unit_of(bound) / den);
+    ops.place(a.d, v, scale_of(unit_of(bound) / den));
     __syncthreads();
     f16v xr[S::NX], ar[S::GX], acc[S::NX];
     ops.get(xr);
@@ -932,7 +975,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_wide_first(Wide
             step_units(a.poly, bound, a.units + b * a.poly.steps);
         }
     }
-    const double inv = unit_of(bound) / den;
+    const Scale inv = scale_of(unit_of(bound) / den);
     const T* g = (const T*)a.G + b * a.d.s * a.d.t;
     f16v ar[S::GX];
     ops.clear(ar);
@@ -1033,7 +1076,7 @@ struct OrthoLayout {
 };
 
 constexpr int kChunk = 128;    // columns
-constexpr int kAddBlocks = 8;  // partial sums that every block adds by itself; more are added first
+constexpr int kAddBlocks = 2;  // partial sums that every block adds by itself; more are added first
 
 OrthoLayout ortho_layout(const OrthoShape& o)
 {
