@@ -9,16 +9,26 @@
 //   dx = rstd (h - sum h / M - xhat sum(h xhat) / M)   sums over the group
 //
 // Bound by memory: the forward has to read x and write y, the backward reads x
-// and dy and writes dx.  A block takes a run of consecutive rows with the
-// lanes along the channels, so every access is a contiguous row.  A run may
-// hold the end of one segment and the beginning of others; each (run, segment)
-// piece leaves its sums at the place run + segment of a list, which is unique
-// because every new piece moves on by a run or a segment, and a second kernel
-// adds the pieces of a segment in order.  Sums are fp64: var comes from the sum
-// of squares, and the fp64 adds are hidden behind the loads.
+// and dy and writes dx.  The lanes of a block run along the channels, so every
+// access is a contiguous row.  Two forms:
+//   - a block per segment (and slice of whole groups), its rows kept in registers
+//     between the statistics and the result: one pass over memory, one launch;
+//   - for segments too long for that, blocks take runs of consecutive rows of
+//     equal length.  A run may hold the end of one segment and the beginning of
+//     others; each (run, segment) piece leaves its sums at the place run + segment
+//     of a list, which is unique because every new piece moves on by a run or a
+//     segment, a second kernel adds the pieces of a segment in order, and a third
+//     reads the rows again.
+// The lengths of ragged segments are known on the device only: where their mean
+// is short but the total is large enough that one long segment would hold up the
+// chip, both forms are launched and each takes the segments on its side of a
+// length.  Statistics of the forward are fp64 sums of x and x^2; the backward
+// adds four rows in fp32 and those in fp64.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "cgtp_internal.h"
 #include "cgtp_train_internal.h"
@@ -42,16 +52,17 @@ struct Slices {
 
 struct NormArgs {
     int64_t N, B, R, runs, ldx, ldy, ldd;
+    int64_t longest;  // rows of a segment that a block takes whole; the runs take the longer ones
     int32_t C, G, cpg;
     Slices sl;
     float eps;
-    int act;
     const int32_t* seg;
     const float *gamma, *beta, *mean, *rstd;
     float *omean, *orstd;
     double* part;  // [runs + B][G][parts][2]
-    double* chan;  // backward: [runs][2][C]
-    double* coef;  // backward: [B][G][2], the group means of h and h xhat
+    double* chan;  // backward: [runs, then the whole segments' blocks][2][C]
+    int64_t nchan;
+    float* coef;   // backward: [B][G][2], the group means of h and h xhat
 };
 
 struct Slice {
@@ -102,8 +113,9 @@ __device__ __forceinline__ int64_t find_segment(const NormArgs& a, int64_t r)
     return lo;
 }
 
-// f(segment, first row, end row) for every piece of rows [r0, r1), the same for
-// the whole block.  Stops where offsets break the precondition.
+// f(segment, first row, end row) for every piece of rows [r0, r1) of a segment of
+// more than `longest` rows, the same for the whole block.  Stops where offsets
+// break the precondition.
 template <class F>
 __device__ __forceinline__ void for_pieces(const NormArgs& a, int64_t r0, int64_t r1, F&& f)
 {
@@ -115,8 +127,9 @@ __device__ __forceinline__ void for_pieces(const NormArgs& a, int64_t r0, int64_
             e = seg_at(a, b + 1);
             if (e <= r) return;
         }
+        const bool take = e - seg_at(a, b) > a.longest;
         if (e > r1) e = r1;
-        f(b, r, e);
+        if (take) f(b, r, e);
         r = e;
         if (++b >= a.B) return;
     }
@@ -129,27 +142,29 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 // tanh from exp(2|z|): 1 - 2 / (e + 1), by its series where that would cancel
 __device__ __forceinline__ float tanh_f(float z)
 {
-    const float t = fabsf(z);
-    if (t < 0.3f) {
-        const float u = z * z;
-        // z (1 - u/3 + 2u^2/15 - 17u^3/315 + 62u^4/2835 - 1382u^5/155925)
-        return z * (1.0f + u * (-0.33333334f + u * (0.13333334f + u * (-0.053968254f + u * (0.021869488f + u * -0.0088632355f)))));
-    }
-    const float e = __expf(2.0f * t);
-    return copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f), z);
+    const float t = fabsf(z), u = z * z;
+    // z (1 - u/3 + 2u^2/15 - 17u^3/315 + 62u^4/2835 - 1382u^5/155925)
+    const float near = z * (1.0f + u * (-0.33333334f + u * (0.13333334f + u * (-0.053968254f + u * (0.021869488f + u * -0.0088632355f)))));
+    const float far = copysignf(1.0f - 2.0f * __builtin_amdgcn_rcpf(__expf(2.0f * t) + 1.0f), z);
+    return t < 0.3f ? near : far;
 }
 
-__device__ __forceinline__ float act_of(int act, float z)
+enum : int { kNone = 0, kSilu = 1, kTanh = 2 };  // values of cgtp_act_t
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z)
 {
-    if (act == 0) return z;
-    return act == 1 ? z * sigmoid(z) : tanh_f(z);
+    if constexpr (ACT == kNone) return z;
+    if constexpr (ACT == kSilu) return z * sigmoid(z);
+    return tanh_f(z);
 }
 
 // act'(z)
-__device__ __forceinline__ float act_slope(int act, float z)
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
 {
-    if (act == 0) return 1.0f;
-    if (act == 1) {
+    if constexpr (ACT == kNone) return 1.0f;
+    if constexpr (ACT == kSilu) {
         const float s = sigmoid(z);
         return s * (1.0f + z * (1.0f - s));
     }
@@ -159,14 +174,14 @@ __device__ __forceinline__ float act_slope(int act, float z)
 
 // ---- lanes ---------------------------------------------------------------------------
 // The block's place in its slice: L lanes along the channels, RL rows at a time.
-template <int VEC>
+template <int VEC, int THR = kThreads>
 struct Lanes {
     int32_t L, RL, rl, c;  // c: the lane's first channel
     bool on;
     __device__ __forceinline__ Lanes(const Slice& s)
     {
         L = (s.c1 - s.c0) / VEC;
-        RL = kThreads / L;
+        RL = THR / L;
         rl = (int32_t)threadIdx.x / L;
         c = s.c0 + ((int32_t)threadIdx.x - rl * L) * VEC;
         on = rl < RL;
@@ -180,10 +195,22 @@ __device__ __forceinline__ void load_chan(float (&v)[VEC], const float* __restri
     for (int j = 0; j < VEC; ++j) v[j] = p ? p[c + j] : none;
 }
 
+// LDS of a block: doubles for the sums (a pair per lane, or per channel where a
+// group's channels are no whole accesses; one per lane and channel for the
+// backward's channel sums), then the groups' two results.
+extern __shared__ __attribute__((aligned(16))) char norm_lds[];
+
+__host__ __device__ inline int sum_doubles(int32_t cpg, int vec, int threads, bool channels)
+{
+    const int pairs = 2 * (cpg % vec == 0 ? threads : threads * vec);
+    return channels && pairs < threads * vec ? threads * vec : pairs;
+}
+
 // out[(group)] = sums over the block of two values per (lane, channel) for each group of the slice, written by the
-// group's first thread to dst(g)[0..1].  s: kThreads * VEC * 2 doubles.
-template <int VEC, class Dst>
-__device__ __forceinline__ void group_sums(const NormArgs& a, const Slice& sl, const Lanes<VEC>& ln,
+// group's first thread by dst(g, sum, sum).  s: THR * VEC * 2 doubles (THR * 2
+// where a group's channels are whole accesses).
+template <int VEC, int THR, class Dst>
+__device__ __forceinline__ void group_sums(const NormArgs& a, const Slice& sl, const Lanes<VEC, THR>& ln,
                                            const double (&u)[VEC], const double (&v)[VEC], double* s, Dst&& dst)
 {
     // channels of one access in one group: one pair per lane, else one per channel
@@ -213,9 +240,9 @@ __device__ __forceinline__ void group_sums(const NormArgs& a, const Slice& sl, c
     // teams of up to 64 threads, one group each
     const int32_t groups = sl.g1 - sl.g0, each = w / groups;  // pairs of a group per row lane
     int32_t team = 64;
-    while (team > 1 && team * groups > kThreads) team /= 2;
+    while (team > 1 && team * groups > THR) team /= 2;
     const int32_t m = (int32_t)threadIdx.x & (team - 1);
-    for (int32_t g = (int32_t)threadIdx.x / team; g - (int32_t)threadIdx.x / team < groups; g += kThreads / team) {
+    for (int32_t g = (int32_t)threadIdx.x / team; g - (int32_t)threadIdx.x / team < groups; g += THR / team) {
         double x = 0.0, y = 0.0;
         if (g < groups)
             for (int32_t k = m; k < each * ln.RL; k += team) {
@@ -227,17 +254,16 @@ __device__ __forceinline__ void group_sums(const NormArgs& a, const Slice& sl, c
             x += __shfl_down(x, d, team);
             y += __shfl_down(y, d, team);
         }
-        if (m == 0 && g < groups) {
-            double* o = dst(sl.g0 + g);
-            o[0] = x;
-            o[1] = y;
-        }
+        if (m == 0 && g < groups) dst(sl.g0 + g, x, y);
     }
 }
 
-__device__ __forceinline__ double* piece_sums(const NormArgs& a, int64_t run, int64_t b, int32_t g, int32_t part)
+__device__ __forceinline__ void put_piece(const NormArgs& a, int64_t run, int64_t b, int32_t g, int32_t part, double x,
+                                          double y)
 {
-    return a.part + (((run + b) * a.G + g) * a.sl.parts + part) * 2;
+    double* o = a.part + (((run + b) * a.G + g) * a.sl.parts + part) * 2;
+    o[0] = x;
+    o[1] = y;
 }
 
 // ---- forward -------------------------------------------------------------------------
@@ -245,7 +271,7 @@ __device__ __forceinline__ double* piece_sums(const NormArgs& a, int64_t run, in
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_norm_sums(NormArgs a, const T* __restrict__ x)
 {
-    __shared__ double s[kThreads * VEC * 2];
+    double* s = reinterpret_cast<double*>(norm_lds);
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
     const Lanes<VEC> ln(sl);
     for (int64_t run = blockIdx.x; run < a.runs; run += gridDim.x) {
@@ -267,7 +293,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_sums(NormArgs a, const T* __r
                     }
                 }
             }
-            group_sums<VEC>(a, sl, ln, u, v, s, [&](int32_t g) { return piece_sums(a, run, b, g, sl.part); });
+            group_sums(a, sl, ln, u, v, s,
+                       [&](int32_t g, double x, double y) { put_piece(a, run, b, g, sl.part, x, y); });
         });
     }
 }
@@ -310,6 +337,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(NormArgs a)
     const int64_t n = a.B * a.G, step = (int64_t)gridDim.x * (kThreads / 64);
     for (int64_t i = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64; i < n; i += step) {
         double x, y, M;
+        if (a.longest > 0 && seg_at(a, i / a.G + 1) - seg_at(a, i / a.G) <= a.longest) continue;
         sum_pieces(a, i / a.G, (int32_t)(i % a.G), x, y, M);
         if ((threadIdx.x & 63) == 0) finish_stats(a, x, y, M, a.omean[i], a.orstd[i]);
     }
@@ -331,7 +359,7 @@ __device__ __forceinline__ void load_group(S (&o)[VEC], const S* __restrict__ v,
     }
 }
 
-template <class T, int VEC>
+template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __restrict__ x, T* __restrict__ y)
 {
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
@@ -353,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __
                 float f[VEC];
                 load_vec<T, VEC>(f, x + r * a.ldx + ln.c);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) f[j] = act_of(a.act, (f[j] - mu[j]) * rs[j] * gm[j] + bt[j]);
+                for (int j = 0; j < VEC; ++j) f[j] = act_of<ACT>((f[j] - mu[j]) * rs[j] * gm[j] + bt[j]);
                 store_vec<T, VEC>(y + r * a.ldy + ln.c, f);
             }
         });
@@ -362,11 +390,81 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __
 
 // ---- backward ------------------------------------------------------------------------
 // sums of h and h xhat of every piece, and of dz xhat and dz of every run
-template <class T, int VEC>
+// u += dz xhat, v += dz over rows p + rl, p + rl + RL, .. below e: four rows in
+// fp32, then in fp64
+template <class T, int VEC, int ACT, class Ln>
+__device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const T* __restrict__ x,
+                                         const T* __restrict__ dy, int64_t p, int64_t e, const float (&mu)[VEC],
+                                         const float (&rs)[VEC], const float (&gm)[VEC], const float (&bt)[VEC],
+                                         double (&u)[VEC], double (&v)[VEC])
+{
+    constexpr int kAt = 4;
+    for (int64_t r = p + ln.rl; r < e; r += kAt * ln.RL) {
+        float f[kAt][VEC], d[kAt][VEC], us[VEC], vs[VEC];
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+            const int64_t q = r + k * ln.RL, at = q < e ? q : r;  // loads outside any condition: all in flight
+            load_vec<T, VEC>(f[k], x + at * a.ldx + ln.c);
+            load_vec<T, VEC>(d[k], dy + at * a.ldy + ln.c);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+            const bool in = r + k * ln.RL < e;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float xh = (f[k][j] - mu[j]) * rs[j];
+                const float dz = in ? d[k][j] * act_slope<ACT>(xh * gm[j] + bt[j]) : 0.0f;
+                us[j] += dz * xh;
+                vs[j] += dz;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            u[j] += (double)us[j];
+            v[j] += (double)vs[j];
+        }
+    }
+}
+
+// dx of one element.  h is rounded as the group sums' terms are, so that a group
+// of one value gives exactly zero.
+template <int ACT>
+__device__ __forceinline__ float dx_of(float x, float dy, float mu, float rs, float gm, float bt, float s1, float s2)
+{
+    const float xh = (x - mu) * rs;
+    const float h = __fmul_rn(dy * act_slope<ACT>(xh * gm + bt), gm);
+    return rs * (h - s1 - xh * s2);
+}
+
+// the run's sums per channel: dz xhat, then dz.  s: THR * VEC doubles
+template <int VEC, int THR>
+__device__ __forceinline__ void channel_sums(const NormArgs& a, const Slice& sl, const Lanes<VEC, THR>& ln,
+                                             const double (&tu)[VEC], const double (&tv)[VEC], double* s, int64_t row)
+{
+    const int32_t w = ln.L * VEC;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+        if (ln.on)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[ln.rl * w + ln.c - sl.c0 + j] = which == 0 ? tu[j] : tv[j];
+        __syncthreads();
+        for (int32_t k = threadIdx.x; k < w; k += THR) {
+            double t = 0.0;
+            for (int32_t r = 0; r < ln.RL; ++r) t += s[r * w + k];
+            a.chan[(row * 2 + which) * a.C + sl.c0 + k] = t;
+        }
+    }
+    __syncthreads();
+}
+
+template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T* __restrict__ x,
                                                             const T* __restrict__ dy)
 {
-    __shared__ double s[kThreads * VEC * 2];
+    double* s = reinterpret_cast<double*>(norm_lds);
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
     const Lanes<VEC> ln(sl);
     float gm[VEC], bt[VEC];
@@ -387,19 +485,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
                 float mu[VEC], rs[VEC];
                 load_group(mu, a.mean, a, b, ln.c, 1, 0);
                 load_group(rs, a.rstd, a, b, ln.c, 1, 0);
-#pragma unroll 2
-                for (int64_t r = p + ln.rl; r < e; r += ln.RL) {
-                    float f[VEC], d[VEC];
-                    load_vec<T, VEC>(f, x + r * a.ldx + ln.c);
-                    load_vec<T, VEC>(d, dy + r * a.ldy + ln.c);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float xh = (f[j] - mu[j]) * rs[j];
-                        const double dz = (double)(d[j] * act_slope(a.act, xh * gm[j] + bt[j]));
-                        u[j] += dz * (double)xh;
-                        v[j] += dz;
-                    }
-                }
+                bwd_rows<T, VEC, ACT>(a, ln, x, dy, p, e, mu, rs, gm, bt, u, v);
             }
             double hu[VEC], hv[VEC];
 #pragma unroll
@@ -410,67 +496,53 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
                 hv[j] = ln.on ? u[j] * (double)gm[j] : 0.0;
             }
             if (a.coef)
-                group_sums<VEC>(a, sl, ln, hu, hv, s, [&](int32_t g) { return piece_sums(a, run, b, g, sl.part); });
+                group_sums(a, sl, ln, hu, hv, s,
+                           [&](int32_t g, double x, double y) { put_piece(a, run, b, g, sl.part, x, y); });
         });
-        if (!a.chan) continue;
-        // the run's sums per channel
-        const int32_t w = ln.L * VEC;
-        __syncthreads();
-        if (ln.on) {
-            double* d = s + ((int64_t)ln.rl * w + (ln.c - sl.c0)) * 2;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                d[2 * j] = tu[j];
-                d[2 * j + 1] = tv[j];
-            }
-        }
-        __syncthreads();
-        for (int32_t k = threadIdx.x; k < 2 * w; k += kThreads) {
-            double t = 0.0;
-            for (int32_t r = 0; r < ln.RL; ++r) t += s[(int64_t)r * w * 2 + k];
-            a.chan[(run * 2 + (k & 1)) * a.C + sl.c0 + k / 2] = t;
-        }
-        __syncthreads();
+        if (a.chan) channel_sums(a, sl, ln, tu, tv, s, run);
     }
 }
 
 // blocks [0, cblocks): dgamma and dbeta of kChan channels each, from the runs;
 // the others: the two group means of dx, one wave per (segment, group)
-constexpr int kChan = 8;
-__global__ void __launch_bounds__(kThreads) k_norm_bwd_join(NormArgs a, int32_t cblocks, float* __restrict__ dgamma,
-                                                            float* __restrict__ dbeta)
+constexpr int kChan = 4, kJoin = 1024;
+__global__ void __launch_bounds__(kJoin) k_norm_bwd_join(NormArgs a, int32_t cblocks, float* __restrict__ dgamma,
+                                                         float* __restrict__ dbeta)
 {
     if ((int32_t)blockIdx.x < cblocks) {
-        __shared__ double s[kThreads];
-        constexpr int kW = 2 * kChan, kR = kThreads / kW;  // 16 sums, 16 rows of runs at a time
+        __shared__ double s[kJoin];
+        constexpr int kW = 2 * kChan, kR = kJoin / kW;  // 8 sums, 128 rows of runs at a time
         const int32_t col = (int32_t)threadIdx.x % kW, row = (int32_t)threadIdx.x / kW;
         const int32_t which = col / kChan, c = (int32_t)blockIdx.x * kChan + col % kChan;
         double t = 0.0;
         if (c < a.C)
-#pragma unroll 4
-            for (int64_t r = row; r < a.runs; r += kR) t += a.chan[(r * 2 + which) * a.C + c];
+#pragma unroll 8
+            for (int64_t r = row; r < a.nchan; r += kR) t += a.chan[(r * 2 + which) * a.C + c];
         s[threadIdx.x] = t;
         __syncthreads();
+        for (int d = kR / 2; d > 0; d /= 2) {
+            if (row < d) s[threadIdx.x] += s[threadIdx.x + d * kW];
+            __syncthreads();
+        }
         if (row == 0 && c < a.C) {
-            double v = 0.0;
-            for (int k = 0; k < kR; ++k) v += s[k * kW + col];
             float* o = which == 0 ? dgamma : dbeta;
-            if (o) o[c] = (float)v;
+            if (o) o[c] = (float)s[col];
         }
         return;
     }
-    const int64_t n = a.B * a.G, step = (int64_t)(gridDim.x - cblocks) * (kThreads / 64);
-    for (int64_t i = (int64_t)((int32_t)blockIdx.x - cblocks) * (kThreads / 64) + threadIdx.x / 64; i < n; i += step) {
+    const int64_t n = a.B * a.G, step = (int64_t)(gridDim.x - cblocks) * (kJoin / 64);
+    for (int64_t i = (int64_t)((int32_t)blockIdx.x - cblocks) * (kJoin / 64) + threadIdx.x / 64; i < n; i += step) {
         double x, y, M;
+        if (a.longest > 0 && seg_at(a, i / a.G + 1) - seg_at(a, i / a.G) <= a.longest) continue;
         sum_pieces(a, i / a.G, (int32_t)(i % a.G), x, y, M);
         if ((threadIdx.x & 63) == 0) {
-            a.coef[2 * i] = M > 0.0 ? x / M : 0.0;
-            a.coef[2 * i + 1] = M > 0.0 ? y / M : 0.0;
+            a.coef[2 * i] = M > 0.0 ? (float)(x / M) : 0.0f;
+            a.coef[2 * i + 1] = M > 0.0 ? (float)(y / M) : 0.0f;
         }
     }
 }
 
-template <class T, int VEC>
+template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T* __restrict__ x,
                                                              const T* __restrict__ dy, T* __restrict__ dx)
 {
@@ -485,8 +557,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
         const int64_t r0 = run * a.R, r1 = r0 + a.R < a.N ? r0 + a.R : a.N;
         for_pieces(a, r0, r1, [&](int64_t b, int64_t p, int64_t e) {
             if (!ln.on) return;
-            float mu[VEC], rs[VEC];
-            double s1[VEC], s2[VEC];
+            float mu[VEC], rs[VEC], s1[VEC], s2[VEC];
             load_group(mu, a.mean, a, b, ln.c, 1, 0);
             load_group(rs, a.rstd, a, b, ln.c, 1, 0);
             load_group(s1, a.coef, a, b, ln.c, 2, 0);
@@ -498,10 +569,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
                 load_vec<T, VEC>(d, dy + r * a.ldy + ln.c);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float xh = (f[j] - mu[j]) * rs[j];
-                    const float dz = d[j] * act_slope(a.act, xh * gm[j] + bt[j]);
-                    // fp64: the three terms cancel where a group holds few values
-                    f[j] = rs[j] * (float)((double)dz * (double)gm[j] - s1[j] - (double)xh * s2[j]);
+                    f[j] = dx_of<ACT>(f[j], d[j], mu[j], rs[j], gm[j], bt[j], s1[j], s2[j]);
                 }
                 store_vec<T, VEC>(dx + r * a.ldd + ln.c, f);
             }
@@ -509,7 +577,208 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
     }
 }
 
-// ---- layout --------------------------------------------------------------------------
+// ---- a block per segment -----------------------------------------------------------------
+// Rows of a lane that stay in registers between the two passes; the rows of a
+// longer segment are read again.
+constexpr int kKeep = 8, kKeepBwd = 4;
+
+// values of the lane's channels from v[group of the slice]
+template <int VEC>
+__device__ __forceinline__ void slice_group(float (&o)[VEC], const float* v, const NormArgs& a, const Slice& sl,
+                                            int32_t c)
+{
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = v[(c + j) / a.cpg - sl.g0];
+}
+
+template <class T, int VEC, int THR, int ACT>
+__global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restrict__ x, T* __restrict__ y)
+{
+    const Slice sl = slice_of(a, (int32_t)blockIdx.y);
+    double* s = reinterpret_cast<double*>(norm_lds);
+    float* st[2];
+    st[0] = reinterpret_cast<float*>(s + sum_doubles(a.cpg, VEC, THR, false));
+    st[1] = st[0] + a.sl.groups;
+    const Lanes<VEC, THR> ln(sl);
+    float gm[VEC], bt[VEC];
+    if (ln.on) {
+        load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
+        load_chan<VEC>(bt, a.beta, ln.c, 0.0f);
+    }
+    for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const int64_t p = seg_at(a, b), e = seg_at(a, b + 1);
+        if (e - p > a.longest) continue;
+        const double M = (double)(e > p ? e - p : 0) * a.cpg;
+        float f[kKeep][VEC];
+        double u[VEC], v[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
+        const bool on = ln.on && p + ln.rl < e;
+        if (on) {
+#pragma unroll
+            for (int k = 0; k < kKeep; ++k) {
+                const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
+                load_vec<T, VEC>(f[k], x + (r < e ? r : p) * a.ldx + ln.c);
+            }
+#pragma unroll
+            for (int k = 0; k < kKeep; ++k)
+                if (p + ln.rl + (int64_t)k * ln.RL < e)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const double d = (double)f[k][j];
+                        u[j] += d;
+                        v[j] += d * d;
+                    }
+#pragma unroll 4
+            for (int64_t r = p + ln.rl + (int64_t)kKeep * ln.RL; r < e; r += ln.RL) {
+                float g[VEC];
+                load_vec<T, VEC>(g, x + r * a.ldx + ln.c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const double d = (double)g[j];
+                    u[j] += d;
+                    v[j] += d * d;
+                }
+            }
+        }
+        group_sums(a, sl, ln, u, v, s, [&](int32_t g, double x, double y) {
+            float m, r;
+            finish_stats(a, x, y, M, m, r);
+            st[0][g - sl.g0] = m;
+            st[1][g - sl.g0] = r;
+            a.omean[b * a.G + g] = m;
+            a.orstd[b * a.G + g] = r;
+        });
+        __syncthreads();
+        if (on) {
+            float mu[VEC], rs[VEC];
+            slice_group<VEC>(mu, st[0], a, sl, ln.c);
+            slice_group<VEC>(rs, st[1], a, sl, ln.c);
+#pragma unroll
+            for (int k = 0; k < kKeep; ++k) {
+                const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
+                if (r < e) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) f[k][j] = act_of<ACT>((f[k][j] - mu[j]) * rs[j] * gm[j] + bt[j]);
+                    store_vec<T, VEC>(y + r * a.ldy + ln.c, f[k]);
+                }
+            }
+#pragma unroll 4
+            for (int64_t r = p + ln.rl + (int64_t)kKeep * ln.RL; r < e; r += ln.RL) {
+                float g[VEC];
+                load_vec<T, VEC>(g, x + r * a.ldx + ln.c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) g[j] = act_of<ACT>((g[j] - mu[j]) * rs[j] * gm[j] + bt[j]);
+                store_vec<T, VEC>(y + r * a.ldy + ln.c, g);
+            }
+        }
+        __syncthreads();  // st
+    }
+}
+
+template <class T, int VEC, int THR, int ACT>
+__global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
+                                                      T* __restrict__ dx)
+{
+    const Slice sl = slice_of(a, (int32_t)blockIdx.y);
+    double* s = reinterpret_cast<double*>(norm_lds);
+    float* st[2];
+    st[0] = reinterpret_cast<float*>(s + sum_doubles(a.cpg, VEC, THR, true));
+    st[1] = st[0] + a.sl.groups;
+    const Lanes<VEC, THR> ln(sl);
+    float gm[VEC], bt[VEC];
+    if (ln.on) {
+        load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
+        load_chan<VEC>(bt, a.beta, ln.c, 0.0f);
+    }
+    double tu[VEC], tv[VEC];  // dz xhat and dz of this block's segments
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) tu[j] = tv[j] = 0.0;
+    // consecutive segments to a block
+    const int64_t each = (a.B + gridDim.x - 1) / gridDim.x, b0 = blockIdx.x * each;
+    const int64_t b1 = b0 + each < a.B ? b0 + each : a.B;
+    for (int64_t b = b0; b < b1; ++b) {
+        const int64_t p = seg_at(a, b), e = seg_at(a, b + 1);
+        if (e <= p || e - p > a.longest) continue;
+        const double M = (double)(e - p) * a.cpg;
+        float f[kKeepBwd][VEC], d[kKeepBwd][VEC], mu[VEC], rs[VEC];
+        double u[VEC], v[VEC], hu[VEC], hv[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
+        const bool on = ln.on && p + ln.rl < e;
+        if (on) {
+            load_group(mu, a.mean, a, b, ln.c, 1, 0);
+            load_group(rs, a.rstd, a, b, ln.c, 1, 0);
+            float us[VEC], vs[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kKeepBwd; ++k) {
+                const int64_t q = p + ln.rl + (int64_t)k * ln.RL, r = q < e ? q : p;
+                load_vec<T, VEC>(f[k], x + r * a.ldx + ln.c);
+                load_vec<T, VEC>(d[k], dy + r * a.ldy + ln.c);
+            }
+#pragma unroll
+            for (int k = 0; k < kKeepBwd; ++k)
+                if (p + ln.rl + (int64_t)k * ln.RL < e)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        // kept: xhat and dz
+                        f[k][j] = (f[k][j] - mu[j]) * rs[j];
+                        d[k][j] *= act_slope<ACT>(f[k][j] * gm[j] + bt[j]);
+                        us[j] += d[k][j] * f[k][j];
+                        vs[j] += d[k][j];
+                    }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                u[j] = (double)us[j];
+                v[j] = (double)vs[j];
+            }
+            bwd_rows<T, VEC, ACT>(a, ln, x, dy, p + (int64_t)kKeepBwd * ln.RL, e, mu, rs, gm, bt, u, v);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            tu[j] += u[j];
+            tv[j] += v[j];
+            hu[j] = on ? v[j] * (double)gm[j] : 0.0;
+            hv[j] = on ? u[j] * (double)gm[j] : 0.0;
+        }
+        if (!dx) continue;
+        group_sums(a, sl, ln, hu, hv, s, [&](int32_t g, double x, double y) {
+            st[0][g - sl.g0] = (float)(x / M);
+            st[1][g - sl.g0] = (float)(y / M);
+        });
+        __syncthreads();
+        if (on) {
+            float s1[VEC], s2[VEC];
+            slice_group<VEC>(s1, st[0], a, sl, ln.c);
+            slice_group<VEC>(s2, st[1], a, sl, ln.c);
+#pragma unroll
+            for (int k = 0; k < kKeepBwd; ++k) {
+                const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
+                if (r < e) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        f[k][j] = rs[j] * (__fmul_rn(d[k][j], gm[j]) - s1[j] - f[k][j] * s2[j]);
+                    store_vec<T, VEC>(dx + r * a.ldd + ln.c, f[k]);
+                }
+            }
+#pragma unroll 2
+            for (int64_t r = p + ln.rl + (int64_t)kKeepBwd * ln.RL; r < e; r += ln.RL) {
+                float g[VEC], h[VEC];
+                load_vec<T, VEC>(g, x + r * a.ldx + ln.c);
+                load_vec<T, VEC>(h, dy + r * a.ldy + ln.c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) g[j] = dx_of<ACT>(g[j], h[j], mu[j], rs[j], gm[j], bt[j], s1[j], s2[j]);
+                store_vec<T, VEC>(dx + r * a.ldd + ln.c, g);
+            }
+        }
+        __syncthreads();  // st
+    }
+    if (a.chan) channel_sums(a, sl, ln, tu, tv, s, a.nchan - gridDim.x + blockIdx.x);
+}
+
+// ---- layout and form -----------------------------------------------------------------------
 // Rows per run: about 2048 blocks over the rows, at least 16 rows, so that the
 // sums of a run are a small share of its rows.
 int64_t rows_per_run(int64_t N)
@@ -517,6 +786,11 @@ int64_t rows_per_run(int64_t N)
     const int64_t r = cdiv64(N, 2048);
     return r < 16 ? 16 : r;
 }
+
+constexpr int64_t kSegBlocks = 512;   // blocks of the whole segments' backward, each with one row of channel sums
+constexpr int64_t kLong = 256 << 10;  // bytes of a segment's slice that one block takes
+constexpr int64_t kTotal = 32 << 20;  // bytes that one block could be left with, if one segment held all rows
+constexpr int64_t kFill = 256;        // blocks that fill the chip
 
 struct NormLayout {
     int64_t R, runs, parts;
@@ -537,19 +811,25 @@ NormLayout norm_layout(const NormShape& n)
         return at;
     };
     w.part = take((w.runs + n.B) * n.G * w.parts * 2 * (int64_t)sizeof(double));
-    w.chan = take(w.runs * 2 * n.C * (int64_t)sizeof(double));
-    w.coef = take(n.B * n.G * 2 * (int64_t)sizeof(double));
+    w.chan = take((w.runs + kSegBlocks) * 2 * n.C * (int64_t)sizeof(double));
+    w.coef = take(n.B * n.G * 2 * (int64_t)sizeof(float));
     w.bytes = o > 0 ? o : 256;  // never none, so that a workspace always has an address
     return w;
 }
 
-Slices slices_of(const NormShape& n, int vec)
+// at least `want` slices, if groups and whole 64-byte pieces allow
+Slices slices_of(const NormShape& n, int vec, int threads, int64_t want)
 {
     Slices s{};
-    const int32_t cpg = n.C / n.G, most = kThreads * vec;
+    const int32_t cpg = n.C / n.G, most = threads * vec;
     if (cpg <= most) {
         s.parts = 1;
-        s.groups = most / cpg < n.G ? most / cpg : n.G;
+        int64_t groups = n.G / (want < n.G ? want : n.G);
+        const int64_t least = cdiv64(64, cpg * dtype_size(n.dtype));
+        if (groups < least) groups = least;
+        while (groups * cpg % vec != 0 && groups < n.G) ++groups;
+        if (groups > n.G) groups = n.G;
+        s.groups = (int32_t)(groups * cpg <= most ? groups : most / cpg);
         s.width = s.groups * cpg;
         s.n = (n.G + s.groups - 1) / s.groups;
     } else {
@@ -568,10 +848,21 @@ bool wide_ok(const NormShape& n, int vec)
     return n.C <= kThreads * vec || (n.C / n.G) % vec == 0;
 }
 
-NormArgs norm_args(const NormShape& n, int vec, void* ws)
+struct NormPlan {
+    NormArgs a;      // slices of the runs
+    Slices seg;      // slices of the whole segments
+    bool whole, runs;
+    int threads;     // of the whole segments' blocks
+};
+
+// Which forms run (the header comment says why): whole segments where their mean
+// length leaves a block at most kLong bytes; beside the runs where the segments
+// are ragged and all rows together exceed kTotal.  `arrays`: rows read per row.
+NormPlan norm_plan(const NormShape& n, int vec, int arrays, void* ws)
 {
     const NormLayout w = norm_layout(n);
-    NormArgs a{};
+    NormPlan p{};
+    NormArgs& a = p.a;
     a.N = n.N;
     a.B = n.B;
     a.R = w.R;
@@ -582,42 +873,112 @@ NormArgs norm_args(const NormShape& n, int vec, void* ws)
     a.C = n.C;
     a.G = n.G;
     a.cpg = n.C / n.G;
-    a.sl = slices_of(n, vec);
     a.eps = n.eps;
-    a.act = n.act;
     a.seg = n.seg;
     a.part = (double*)((char*)ws + w.part);
     a.chan = (double*)((char*)ws + w.chan);
-    a.coef = (double*)((char*)ws + w.coef);
-    return a;
+    a.coef = (float*)((char*)ws + w.coef);
+    a.sl = slices_of(n, vec, kThreads, 1);
+    const int64_t mean = n.B > 0 ? cdiv64(n.N, n.B) : 0, es = dtype_size(n.dtype);
+    // a block of 1024 threads where 256 could not keep the rows, if its group sums fit in LDS
+    p.threads = kThreads;
+    p.seg = slices_of(n, vec, p.threads, n.B > 0 ? cdiv64(kFill, n.B) : 1);
+    const int64_t lanes = p.seg.width / vec;
+    const int keep = arrays == 1 ? kKeep : kKeepBwd;
+    if (p.seg.parts == 1 && mean > keep * (kThreads / (lanes > 0 ? lanes : 1)) && a.cpg % vec == 0) p.threads = 1024;
+    p.whole = p.seg.parts == 1 && mean * p.seg.width * es * arrays <= kLong;
+    const bool safe = !n.seg || n.N * p.seg.width * es * arrays <= kTotal;
+    p.runs = n.N > 0 && (!p.whole || !safe);
+    if (!p.whole) a.longest = 0;
+    else if (!p.runs) a.longest = n.N;
+    else a.longest = kLong * 4 / (p.seg.width * es * arrays);
+    a.nchan = (p.runs ? w.runs : 0);
+    return p;
 }
 
-inline unsigned stat_blocks(const NormArgs& a) { return grid_of(cdiv64(a.B * a.G, kThreads / 64)); }
-
-template <class T, int VEC>
-hipError_t norm_fwd(const NormArgs& a, const void* x, void* y, hipStream_t s)
+inline unsigned lds_bytes(const NormArgs& a, int vec, int threads, bool channels, bool groups)
 {
-    const dim3 grid(grid_of(a.runs), (unsigned)a.sl.n);
-    if (a.N > 0) hipLaunchKernelGGL((k_norm_sums<T, VEC>), grid, dim3(kThreads), 0, s, a, (const T*)x);
-    hipLaunchKernelGGL(k_norm_stats, dim3(stat_blocks(a)), dim3(kThreads), 0, s, a);
-    if (a.N > 0) hipLaunchKernelGGL((k_norm_apply<T, VEC>), grid, dim3(kThreads), 0, s, a, (const T*)x, (T*)y);
+    return (unsigned)(sum_doubles(a.cpg, vec, threads, channels) * (int)sizeof(double) + (groups ? 8 * a.sl.groups : 0));
+}
+
+inline unsigned stat_blocks(const NormArgs& a, int threads) { return grid_of(cdiv64(a.B * a.G, threads / 64)); }
+
+template <class T, int VEC, int ACT>
+hipError_t norm_fwd(const NormPlan& p, const void* x, void* y, hipStream_t s)
+{
+    if (p.whole) {
+        NormArgs a = p.a;
+        a.sl = p.seg;
+        const dim3 grid(grid_of(a.B), (unsigned)a.sl.n);
+        const unsigned lds = lds_bytes(a, VEC, p.threads, false, true);
+        if (p.threads == 1024)
+            hipLaunchKernelGGL((k_norm_seg<T, VEC, 1024, ACT>), grid, dim3(1024), lds, s, a, (const T*)x, (T*)y);
+        else
+            hipLaunchKernelGGL((k_norm_seg<T, VEC, kThreads, ACT>), grid, dim3(kThreads), lds, s, a, (const T*)x,
+                               (T*)y);
+    }
+    if (p.runs || !p.whole) {
+        const NormArgs& a = p.a;
+        const dim3 grid(grid_of(a.runs), (unsigned)a.sl.n);
+        if (a.N > 0) 
+            hipLaunchKernelGGL((k_norm_sums<T, VEC>), grid, dim3(kThreads), lds_bytes(a, VEC, kThreads, false, false), s,
+                               a, (const T*)x);
+        hipLaunchKernelGGL(k_norm_stats, dim3(stat_blocks(a, kThreads)), dim3(kThreads), 0, s, a);
+        if (a.N > 0)
+            hipLaunchKernelGGL((k_norm_apply<T, VEC, ACT>), grid, dim3(kThreads), 0, s, a, (const T*)x, (T*)y);
+    }
     return hipGetLastError();
 }
 
-template <class T, int VEC>
-hipError_t norm_bwd(const NormArgs& a, const void* x, const void* dy, void* dx, float* dgamma, float* dbeta,
-                    hipStream_t s)
+template <class T, int VEC, int ACT>
+hipError_t norm_bwd(NormPlan& p, const void* x, const void* dy, void* dx, float* dgamma, float* dbeta, hipStream_t s)
 {
+    const bool chan = dgamma || dbeta;
+    NormArgs a = p.a;
+    if (!dx) a.coef = nullptr;
+    if (!chan) a.chan = nullptr;
+    if (p.whole && a.N > 0) {
+        const int64_t blocks = a.B < kSegBlocks ? a.B : kSegBlocks;
+        a.nchan += blocks;
+        NormArgs w = a;
+        w.sl = p.seg;
+        const dim3 grid((unsigned)blocks, (unsigned)w.sl.n);
+        const unsigned lds = lds_bytes(w, VEC, p.threads, true, true);
+        if (p.threads == 1024)
+            hipLaunchKernelGGL((k_norm_bwd_seg<T, VEC, 1024, ACT>), grid, dim3(1024), lds, s, w, (const T*)x,
+                               (const T*)dy, (T*)dx);
+        else
+            hipLaunchKernelGGL((k_norm_bwd_seg<T, VEC, kThreads, ACT>), grid, dim3(kThreads), lds, s, w, (const T*)x,
+                               (const T*)dy, (T*)dx);
+    }
     const dim3 grid(grid_of(a.runs), (unsigned)a.sl.n);
-    if (a.N > 0)
-        hipLaunchKernelGGL((k_norm_bwd_sums<T, VEC>), grid, dim3(kThreads), 0, s, a, (const T*)x, (const T*)dy);
-    const unsigned cb = a.chan ? (unsigned)cdiv64(a.C, kChan) : 0, sb = a.coef ? stat_blocks(a) : 0;
-    if (cb + sb > 0)
-        hipLaunchKernelGGL(k_norm_bwd_join, dim3(cb + sb), dim3(kThreads), 0, s, a, (int32_t)cb, dgamma, dbeta);
-    if (a.N > 0 && dx)
-        hipLaunchKernelGGL((k_norm_bwd_apply<T, VEC>), grid, dim3(kThreads), 0, s, a, (const T*)x, (const T*)dy,
+    if (p.runs)
+        hipLaunchKernelGGL((k_norm_bwd_sums<T, VEC, ACT>), grid, dim3(kThreads), lds_bytes(a, VEC, kThreads, true, false),
+                           s, a, (const T*)x, (const T*)dy);
+    const unsigned cb = chan ? (unsigned)cdiv64(a.C, kChan) : 0, sb = dx && p.runs ? stat_blocks(a, kJoin) : 0;
+    if (cb + sb > 0) hipLaunchKernelGGL(k_norm_bwd_join, dim3(cb + sb), dim3(kJoin), 0, s, a, (int32_t)cb, dgamma, dbeta);
+    if (p.runs && dx)
+        hipLaunchKernelGGL((k_norm_bwd_apply<T, VEC, ACT>), grid, dim3(kThreads), 0, s, a, (const T*)x, (const T*)dy,
                            (T*)dx);
     return hipGetLastError();
+}
+
+// f(element type, accesses, activation) as constants
+template <class F>
+hipError_t with_form(const NormShape& n, bool wide, F&& f)
+{
+    auto act = [&](auto t, auto vec) {
+        switch (n.act) {
+            case kNone: return f(t, vec, std::integral_constant<int, kNone>{});
+            case kSilu: return f(t, vec, std::integral_constant<int, kSilu>{});
+            default: return f(t, vec, std::integral_constant<int, kTanh>{});
+        }
+    };
+    if (n.dtype == kF32)
+        return wide ? act(float{}, std::integral_constant<int, kWide<float>>{})
+                    : act(float{}, std::integral_constant<int, 1>{});
+    return wide ? act(bf16_t{}, std::integral_constant<int, kWide<bf16_t>>{})
+                : act(bf16_t{}, std::integral_constant<int, 1>{});
 }
 
 }  // namespace
@@ -631,14 +992,14 @@ hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma
     const int64_t es = dtype_size(n.dtype);
     const int vec = (int)(16 / es);
     const bool wide = wide_ok(n, vec) && aligned_rows(x, n.ldx, es) && aligned_rows(y, n.ldy, es);
-    NormArgs a = norm_args(n, wide ? vec : 1, ws);
-    a.gamma = gamma;
-    a.beta = beta;
-    a.omean = mean;
-    a.orstd = rstd;
-    if (n.dtype == kF32)
-        return wide ? norm_fwd<float, kWide<float>>(a, x, y, s) : norm_fwd<float, 1>(a, x, y, s);
-    return wide ? norm_fwd<bf16_t, kWide<bf16_t>>(a, x, y, s) : norm_fwd<bf16_t, 1>(a, x, y, s);
+    NormPlan p = norm_plan(n, wide ? vec : 1, 1, ws);
+    p.a.gamma = gamma;
+    p.a.beta = beta;
+    p.a.omean = mean;
+    p.a.orstd = rstd;
+    return with_form(n, wide, [&](auto t, auto v, auto act) {
+        return norm_fwd<decltype(t), decltype(v)::value, decltype(act)::value>(p, x, y, s);
+    });
 }
 
 hipError_t launch_norm_bwd(const NormShape& n, const void* x, const float* mean, const float* rstd,
@@ -649,18 +1010,14 @@ hipError_t launch_norm_bwd(const NormShape& n, const void* x, const float* mean,
     const int vec = (int)(16 / es);
     const bool wide = wide_ok(n, vec) && aligned_rows(x, n.ldx, es) && aligned_rows(dy, n.ldy, es) &&
                       (!dx || aligned_rows(dx, n.ldd, es));
-    NormArgs a = norm_args(n, wide ? vec : 1, ws);
-    a.mean = mean;
-    a.rstd = rstd;
-    a.gamma = gamma;
-    a.beta = beta;
-    if (!dx) a.coef = nullptr;
-    if (!dgamma && !dbeta) a.chan = nullptr;
-    if (n.dtype == kF32)
-        return wide ? norm_bwd<float, kWide<float>>(a, x, dy, dx, dgamma, dbeta, s)
-                    : norm_bwd<float, 1>(a, x, dy, dx, dgamma, dbeta, s);
-    return wide ? norm_bwd<bf16_t, kWide<bf16_t>>(a, x, dy, dx, dgamma, dbeta, s)
-                : norm_bwd<bf16_t, 1>(a, x, dy, dx, dgamma, dbeta, s);
+    NormPlan p = norm_plan(n, wide ? vec : 1, 2, ws);
+    p.a.mean = mean;
+    p.a.rstd = rstd;
+    p.a.gamma = gamma;
+    p.a.beta = beta;
+    return with_form(n, wide, [&](auto t, auto v, auto act) {
+        return norm_bwd<decltype(t), decltype(v)::value, decltype(act)::value>(p, x, dy, dx, dgamma, dbeta, s);
+    });
 }
 
 }  // namespace cgtp
