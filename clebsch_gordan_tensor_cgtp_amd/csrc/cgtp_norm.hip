@@ -390,22 +390,22 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __
 
 // ---- backward ------------------------------------------------------------------------
 // sums of h and h xhat of every piece, and of dz xhat and dz of every run
-// u += dz xhat, v += dz over rows p + rl, p + rl + RL, .. below e: four rows in
+// u += dz xhat, v += dz over rows p + rl, p + rl + RL, .. below e: kAt rows in
 // fp32, then in fp64
-template <class T, int VEC, int ACT, class Ln>
+template <int kAt, class T, int VEC, int ACT, class Ln>
 __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const T* __restrict__ x,
                                          const T* __restrict__ dy, int64_t p, int64_t e, const float (&mu)[VEC],
                                          const float (&rs)[VEC], const float (&gm)[VEC], const float (&bt)[VEC],
                                          double (&u)[VEC], double (&v)[VEC])
 {
-    constexpr int kAt = 4;
     for (int64_t r = p + ln.rl; r < e; r += kAt * ln.RL) {
-        float f[kAt][VEC], d[kAt][VEC], us[VEC], vs[VEC];
+        Raw<T, VEC> f[kAt], d[kAt];
+        float us[VEC], vs[VEC];
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
             const int64_t q = r + k * ln.RL, at = q < e ? q : r;  // loads outside any condition: all in flight
-            load_vec<T, VEC>(f[k], x + at * a.ldx + ln.c);
-            load_vec<T, VEC>(d[k], dy + at * a.ldy + ln.c);
+            f[k].load(x + at * a.ldx + ln.c);
+            d[k].load(dy + at * a.ldy + ln.c);
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
                 float mu[VEC], rs[VEC];
                 load_group(mu, a.mean, a, b, ln.c, 1, 0);
                 load_group(rs, a.rstd, a, b, ln.c, 1, 0);
-                bwd_rows<T, VEC, ACT>(a, ln, x, dy, p, e, mu, rs, gm, bt, u, v);
+                bwd_rows<4, T, VEC, ACT>(a, ln, x, dy, p, e, mu, rs, gm, bt, u, v);
             }
             double hu[VEC], hv[VEC];
 #pragma unroll
@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
         load_chan<VEC>(bt, a.beta, ln.c, 0.0f);
     }
     for (int64_t run = blockIdx.x; run < a.runs; run += gridDim.x) {
-        const int64_t r0 = run * a.R, r1 = r0 + a.R < a.N ? r0 + a.R : a.N;
+        // the rows that were read last first: the cache may still hold them
+        const int64_t r0 = (a.runs - 1 - run) * a.R, r1 = r0 + a.R < a.N ? r0 + a.R : a.N;
         for_pieces(a, r0, r1, [&](int64_t b, int64_t p, int64_t e) {
             if (!ln.on) return;
             float mu[VEC], rs[VEC], s1[VEC], s2[VEC];
@@ -562,16 +563,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
             load_group(rs, a.rstd, a, b, ln.c, 1, 0);
             load_group(s1, a.coef, a, b, ln.c, 2, 0);
             load_group(s2, a.coef, a, b, ln.c, 2, 1);
-#pragma unroll 2
+#pragma unroll 4
             for (int64_t r = p + ln.rl; r < e; r += ln.RL) {
-                float f[VEC], d[VEC];
-                load_vec<T, VEC>(f, x + r * a.ldx + ln.c);
-                load_vec<T, VEC>(d, dy + r * a.ldy + ln.c);
+                Raw<T, VEC> f, d;
+                float g[VEC];
+                f.load(x + r * a.ldx + ln.c);
+                d.load(dy + r * a.ldy + ln.c);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    f[j] = dx_of<ACT>(f[j], d[j], mu[j], rs[j], gm[j], bt[j], s1[j], s2[j]);
-                }
-                store_vec<T, VEC>(dx + r * a.ldd + ln.c, f);
+                for (int j = 0; j < VEC; ++j) g[j] = dx_of<ACT>(f[j], d[j], mu[j], rs[j], gm[j], bt[j], s1[j], s2[j]);
+                store_vec<T, VEC>(dx + r * a.ldd + ln.c, g);
             }
         });
     }
@@ -580,7 +580,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
 // ---- a block per segment -----------------------------------------------------------------
 // Rows of a lane that stay in registers between the two passes; the rows of a
 // longer segment are read again.
-constexpr int kKeep = 8, kKeepBwd = 4;
+template <int THR>
+constexpr int kKeep = THR == kThreads ? 4 : 8;
+template <int THR>
+constexpr int kKeepBwd = 4;
 
 // values of the lane's channels from v[group of the slice]
 template <int VEC>
@@ -594,6 +597,7 @@ __device__ __forceinline__ void slice_group(float (&o)[VEC], const float* v, con
 template <class T, int VEC, int THR, int ACT>
 __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restrict__ x, T* __restrict__ y)
 {
+    constexpr int KEEP = kKeep<THR>;
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
     double* s = reinterpret_cast<double*>(norm_lds);
     float* st[2];
@@ -609,19 +613,19 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
         const int64_t p = seg_at(a, b), e = seg_at(a, b + 1);
         if (e - p > a.longest) continue;
         const double M = (double)(e > p ? e - p : 0) * a.cpg;
-        float f[kKeep][VEC];
+        Raw<T, VEC> f[KEEP];
         double u[VEC], v[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
         const bool on = ln.on && p + ln.rl < e;
         if (on) {
 #pragma unroll
-            for (int k = 0; k < kKeep; ++k) {
+            for (int k = 0; k < KEEP; ++k) {
                 const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
-                load_vec<T, VEC>(f[k], x + (r < e ? r : p) * a.ldx + ln.c);
+                f[k].load(x + (r < e ? r : p) * a.ldx + ln.c);
             }
 #pragma unroll
-            for (int k = 0; k < kKeep; ++k)
+            for (int k = 0; k < KEEP; ++k)
                 if (p + ln.rl + (int64_t)k * ln.RL < e)
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
@@ -630,7 +634,7 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
                         v[j] += d * d;
                     }
 #pragma unroll 4
-            for (int64_t r = p + ln.rl + (int64_t)kKeep * ln.RL; r < e; r += ln.RL) {
+            for (int64_t r = p + ln.rl + (int64_t)KEEP * ln.RL; r < e; r += ln.RL) {
                 float g[VEC];
                 load_vec<T, VEC>(g, x + r * a.ldx + ln.c);
 #pragma unroll
@@ -655,16 +659,17 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
             slice_group<VEC>(mu, st[0], a, sl, ln.c);
             slice_group<VEC>(rs, st[1], a, sl, ln.c);
 #pragma unroll
-            for (int k = 0; k < kKeep; ++k) {
+            for (int k = 0; k < KEEP; ++k) {
                 const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
                 if (r < e) {
+                    float g[VEC];
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) f[k][j] = act_of<ACT>((f[k][j] - mu[j]) * rs[j] * gm[j] + bt[j]);
-                    store_vec<T, VEC>(y + r * a.ldy + ln.c, f[k]);
+                    for (int j = 0; j < VEC; ++j) g[j] = act_of<ACT>((f[k][j] - mu[j]) * rs[j] * gm[j] + bt[j]);
+                    store_vec<T, VEC>(y + r * a.ldy + ln.c, g);
                 }
             }
 #pragma unroll 4
-            for (int64_t r = p + ln.rl + (int64_t)kKeep * ln.RL; r < e; r += ln.RL) {
+            for (int64_t r = p + ln.rl + (int64_t)KEEP * ln.RL; r < e; r += ln.RL) {
                 float g[VEC];
                 load_vec<T, VEC>(g, x + r * a.ldx + ln.c);
 #pragma unroll
@@ -680,6 +685,7 @@ template <class T, int VEC, int THR, int ACT>
 __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
                                                       T* __restrict__ dx)
 {
+    constexpr int KEEP = kKeepBwd<THR>;
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
     double* s = reinterpret_cast<double*>(norm_lds);
     float* st[2];
@@ -701,7 +707,8 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
         const int64_t p = seg_at(a, b), e = seg_at(a, b + 1);
         if (e <= p || e - p > a.longest) continue;
         const double M = (double)(e - p) * a.cpg;
-        float f[kKeepBwd][VEC], d[kKeepBwd][VEC], mu[VEC], rs[VEC];
+        Raw<T, VEC> f[KEEP], d[KEEP];
+        float mu[VEC], rs[VEC];
         double u[VEC], v[VEC], hu[VEC], hv[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
@@ -713,28 +720,27 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
 #pragma unroll
             for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kKeepBwd; ++k) {
+            for (int k = 0; k < KEEP; ++k) {
                 const int64_t q = p + ln.rl + (int64_t)k * ln.RL, r = q < e ? q : p;
-                load_vec<T, VEC>(f[k], x + r * a.ldx + ln.c);
-                load_vec<T, VEC>(d[k], dy + r * a.ldy + ln.c);
+                f[k].load(x + r * a.ldx + ln.c);
+                d[k].load(dy + r * a.ldy + ln.c);
             }
 #pragma unroll
-            for (int k = 0; k < kKeepBwd; ++k)
+            for (int k = 0; k < KEEP; ++k)
                 if (p + ln.rl + (int64_t)k * ln.RL < e)
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        // kept: xhat and dz
-                        f[k][j] = (f[k][j] - mu[j]) * rs[j];
-                        d[k][j] *= act_slope<ACT>(f[k][j] * gm[j] + bt[j]);
-                        us[j] += d[k][j] * f[k][j];
-                        vs[j] += d[k][j];
+                        const float xh = (f[k][j] - mu[j]) * rs[j];
+                        const float dz = d[k][j] * act_slope<ACT>(xh * gm[j] + bt[j]);
+                        us[j] += dz * xh;
+                        vs[j] += dz;
                     }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 u[j] = (double)us[j];
                 v[j] = (double)vs[j];
             }
-            bwd_rows<T, VEC, ACT>(a, ln, x, dy, p + (int64_t)kKeepBwd * ln.RL, e, mu, rs, gm, bt, u, v);
+            bwd_rows<2, T, VEC, ACT>(a, ln, x, dy, p + (int64_t)KEEP * ln.RL, e, mu, rs, gm, bt, u, v);
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
@@ -754,17 +760,18 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
             slice_group<VEC>(s1, st[0], a, sl, ln.c);
             slice_group<VEC>(s2, st[1], a, sl, ln.c);
 #pragma unroll
-            for (int k = 0; k < kKeepBwd; ++k) {
+            for (int k = 0; k < KEEP; ++k) {
                 const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
                 if (r < e) {
+                    float g[VEC];
 #pragma unroll
                     for (int j = 0; j < VEC; ++j)
-                        f[k][j] = rs[j] * (__fmul_rn(d[k][j], gm[j]) - s1[j] - f[k][j] * s2[j]);
-                    store_vec<T, VEC>(dx + r * a.ldd + ln.c, f[k]);
+                        g[j] = dx_of<ACT>(f[k][j], d[k][j], mu[j], rs[j], gm[j], bt[j], s1[j], s2[j]);
+                    store_vec<T, VEC>(dx + r * a.ldd + ln.c, g);
                 }
             }
 #pragma unroll 2
-            for (int64_t r = p + ln.rl + (int64_t)kKeepBwd * ln.RL; r < e; r += ln.RL) {
+            for (int64_t r = p + ln.rl + (int64_t)KEEP * ln.RL; r < e; r += ln.RL) {
                 float g[VEC], h[VEC];
                 load_vec<T, VEC>(g, x + r * a.ldx + ln.c);
                 load_vec<T, VEC>(h, dy + r * a.ldy + ln.c);
@@ -779,11 +786,12 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
 }
 
 // ---- layout and form -----------------------------------------------------------------------
-// Rows per run: about 2048 blocks over the rows, at least 16 rows, so that the
-// sums of a run are a small share of its rows.
+// Rows per run: about 1024 blocks over the rows (four to a compute unit, which
+// is what their registers allow), at least 16 rows, so that the sums of a run are
+// a small share of its rows.
 int64_t rows_per_run(int64_t N)
 {
-    const int64_t r = cdiv64(N, 2048);
+    const int64_t r = cdiv64(N, 1024);
     return r < 16 ? 16 : r;
 }
 
@@ -841,7 +849,7 @@ Slices slices_of(const NormShape& n, int vec, int threads, int64_t want)
     return s;
 }
 
-// 16-byte accesses need every slice to begin and end on them
+// wide accesses need every slice to begin and end on them
 bool wide_ok(const NormShape& n, int vec)
 {
     if (n.C % vec != 0) return false;
@@ -884,7 +892,7 @@ NormPlan norm_plan(const NormShape& n, int vec, int arrays, void* ws)
     p.threads = kThreads;
     p.seg = slices_of(n, vec, p.threads, n.B > 0 ? cdiv64(kFill, n.B) : 1);
     const int64_t lanes = p.seg.width / vec;
-    const int keep = arrays == 1 ? kKeep : kKeepBwd;
+    const int keep = arrays == 1 ? kKeep<kThreads> : kKeepBwd<kThreads>;
     if (p.seg.parts == 1 && mean > keep * (kThreads / (lanes > 0 ? lanes : 1)) && a.cpg % vec == 0) p.threads = 1024;
     p.whole = p.seg.parts == 1 && mean * p.seg.width * es * arrays <= kLong;
     const bool safe = !n.seg || n.N * p.seg.width * es * arrays <= kTotal;
@@ -963,8 +971,9 @@ hipError_t norm_bwd(NormPlan& p, const void* x, const void* dy, void* dx, float*
     return hipGetLastError();
 }
 
-// f(element type, accesses, activation) as constants
-template <class F>
+// f(element type, elements of an access, activation) as constants; BYTES of a
+// wide access
+template <int BYTES, class F>
 hipError_t with_form(const NormShape& n, bool wide, F&& f)
 {
     auto act = [&](auto t, auto vec) {
@@ -975,9 +984,8 @@ hipError_t with_form(const NormShape& n, bool wide, F&& f)
         }
     };
     if (n.dtype == kF32)
-        return wide ? act(float{}, std::integral_constant<int, kWide<float>>{})
-                    : act(float{}, std::integral_constant<int, 1>{});
-    return wide ? act(bf16_t{}, std::integral_constant<int, kWide<bf16_t>>{})
+        return wide ? act(float{}, std::integral_constant<int, 4>{}) : act(float{}, std::integral_constant<int, 1>{});
+    return wide ? act(bf16_t{}, std::integral_constant<int, BYTES / 2>{})
                 : act(bf16_t{}, std::integral_constant<int, 1>{});
 }
 
@@ -997,7 +1005,7 @@ hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma
     p.a.beta = beta;
     p.a.omean = mean;
     p.a.orstd = rstd;
-    return with_form(n, wide, [&](auto t, auto v, auto act) {
+    return with_form<16>(n, wide, [&](auto t, auto v, auto act) {
         return norm_fwd<decltype(t), decltype(v)::value, decltype(act)::value>(p, x, y, s);
     });
 }
@@ -1007,15 +1015,18 @@ hipError_t launch_norm_bwd(const NormShape& n, const void* x, const float* mean,
                            float* dbeta, void* ws, hipStream_t s)
 {
     const int64_t es = dtype_size(n.dtype);
-    const int vec = (int)(16 / es);
-    const bool wide = wide_ok(n, vec) && aligned_rows(x, n.ldx, es) && aligned_rows(dy, n.ldy, es) &&
-                      (!dx || aligned_rows(dx, n.ldd, es));
+    // four elements an access for either type: with eight of bf16 the sums of a
+    // lane's channels take so many registers that half the waves fit (119 us where
+    // this takes XX us for the sums of 400008 x 256)
+    const int vec = 4;
+    const bool wide = wide_ok(n, vec) && aligned_rows(x, n.ldx, es, vec * es) &&
+                      aligned_rows(dy, n.ldy, es, vec * es) && (!dx || aligned_rows(dx, n.ldd, es, vec * es));
     NormPlan p = norm_plan(n, wide ? vec : 1, 2, ws);
     p.a.mean = mean;
     p.a.rstd = rstd;
     p.a.gamma = gamma;
     p.a.beta = beta;
-    return with_form(n, wide, [&](auto t, auto v, auto act) {
+    return with_form<8>(n, wide, [&](auto t, auto v, auto act) {
         return norm_bwd<decltype(t), decltype(v)::value, decltype(act)::value>(p, x, dy, dx, dgamma, dbeta, s);
     });
 }

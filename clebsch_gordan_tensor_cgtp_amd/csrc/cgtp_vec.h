@@ -33,14 +33,14 @@ __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v)
 template <class T>
 constexpr int kWide = 16 / (int)sizeof(T);
 
-// VEC consecutive elements (VEC = kWide<T>: one 16-byte access; VEC = 1: one element)
+// VEC consecutive elements in one access, aligned to its size
 template <class T, int VEC>
 __device__ __forceinline__ void load_vec(float (&v)[VEC], const T* __restrict__ p)
 {
     if constexpr (VEC == 1) {
         v[0] = to_f32(p[0]);
     } else {
-        struct alignas(16) Pack {
+        struct alignas(VEC * sizeof(T)) Pack {
             T e[VEC];
         };
         const Pack q = *reinterpret_cast<const Pack*>(p);
@@ -55,7 +55,7 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[VE
     if constexpr (VEC == 1) {
         p[0] = from_f32<T>(v[0]);
     } else {
-        struct alignas(16) Pack {
+        struct alignas(VEC * sizeof(T)) Pack {
             T e[VEC];
         } q;
 #pragma unroll
@@ -64,9 +64,18 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[VE
     }
 }
 
-inline bool aligned_rows(const void* p, int64_t ld, int64_t elem)
+// the same as bits, converted where used: half the registers for bf16
+template <class T, int VEC>
+struct alignas(VEC * sizeof(T)) Raw {
+    T e[VEC];
+    __device__ __forceinline__ void load(const T* __restrict__ p) { *this = *reinterpret_cast<const Raw*>(p); }
+    __device__ __forceinline__ float operator[](int j) const { return to_f32(e[j]); }
+};
+
+// whether rows of `elem`-byte elements, ld apart, all begin on `bytes` bytes
+inline bool aligned_rows(const void* p, int64_t ld, int64_t elem, int64_t bytes = 16)
 {
-    return ((uintptr_t)p & 15u) == 0 && ld * elem % 16 == 0;
+    return (uintptr_t)p % (uintptr_t)bytes == 0 && ld * elem % bytes == 0;
 }
 
 }  // namespace cgtp
