@@ -177,14 +177,19 @@ __device__ __forceinline__ float act_slope(float z)
 template <int VEC, int THR = kThreads>
 struct Lanes {
     int32_t L, RL, rl, c;  // c: the lane's first channel
+    int32_t g[VEC];        // its channels' groups
     bool on;
-    __device__ __forceinline__ Lanes(const Slice& s)
+    __device__ __forceinline__ Lanes(const NormArgs& a, const Slice& s)
     {
         L = (s.c1 - s.c0) / VEC;
         RL = THR / L;
         rl = (int32_t)threadIdx.x / L;
         c = s.c0 + ((int32_t)threadIdx.x - rl * L) * VEC;
         on = rl < RL;
+        // the divisions are done here, once
+        const bool one = a.cpg % VEC == 0;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) g[j] = one && j > 0 ? g[0] : (c + j) / a.cpg;
     }
 };
 
@@ -195,15 +200,14 @@ __device__ __forceinline__ void load_chan(float (&v)[VEC], const float* __restri
     for (int j = 0; j < VEC; ++j) v[j] = p ? p[c + j] : none;
 }
 
-// LDS of a block: doubles for the sums (a pair per lane, or per channel where a
-// group's channels are no whole accesses; one per lane and channel for the
-// backward's channel sums), then the groups' two results.
+// LDS of a block: doubles for the group sums (a pair per lane, or per channel
+// where a group's channels are no whole accesses), for the backward those of dz
+// xhat and dz of every lane and channel, then the groups' two results.
 extern __shared__ __attribute__((aligned(16))) char norm_lds[];
 
 __host__ __device__ inline int sum_doubles(int32_t cpg, int vec, int threads, bool channels)
 {
-    const int pairs = 2 * (cpg % vec == 0 ? threads : threads * vec);
-    return channels && pairs < threads * vec ? threads * vec : pairs;
+    return 2 * (cpg % vec == 0 ? threads : threads * vec) + (channels ? 2 * threads * vec : 0);
 }
 
 // out[(group)] = sums over the block of two values per (lane, channel) for each group of the slice, written by the
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_sums(NormArgs a, const T* __r
 {
     double* s = reinterpret_cast<double*>(norm_lds);
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
-    const Lanes<VEC> ln(sl);
+    const Lanes<VEC> ln(a, sl);
     for (int64_t run = blockIdx.x; run < a.runs; run += gridDim.x) {
         const int64_t r0 = run * a.R, r1 = r0 + a.R < a.N ? r0 + a.R : a.N;
         for_pieces(a, r0, r1, [&](int64_t b, int64_t p, int64_t e) {
@@ -344,18 +348,18 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(NormArgs a)
 }
 
 // per-channel values of a lane: its groups' values v[b][g] (stride 1 or 2)
-template <int VEC, class S>
-__device__ __forceinline__ void load_group(S (&o)[VEC], const S* __restrict__ v, const NormArgs& a, int64_t b,
-                                           int32_t c, int32_t stride, int32_t off)
+template <int VEC, class Ln>
+__device__ __forceinline__ void load_group(float (&o)[VEC], const float* __restrict__ v, const NormArgs& a, int64_t b,
+                                           const Ln& ln, int32_t stride, int32_t off)
 {
-    const S* p = v + b * a.G * stride + off;
+    const float* p = v + b * a.G * stride + off;
     if (a.cpg % VEC == 0) {
-        const S w = p[c / a.cpg * stride];
+        const float w = p[ln.g[0] * stride];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o[j] = w;
     } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = p[(c + j) / a.cpg * stride];
+        for (int j = 0; j < VEC; ++j) o[j] = p[ln.g[j] * stride];
     }
 }
 
@@ -363,7 +367,7 @@ template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __restrict__ x, T* __restrict__ y)
 {
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
-    const Lanes<VEC> ln(sl);
+    const Lanes<VEC> ln(a, sl);
     float gm[VEC], bt[VEC];
     if (ln.on) {
         load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
@@ -374,8 +378,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __
         for_pieces(a, r0, r1, [&](int64_t b, int64_t p, int64_t e) {
             if (!ln.on) return;
             float mu[VEC], rs[VEC];
-            load_group(mu, a.omean, a, b, ln.c, 1, 0);
-            load_group(rs, a.orstd, a, b, ln.c, 1, 0);
+            load_group(mu, a.omean, a, b, ln, 1, 0);
+            load_group(rs, a.orstd, a, b, ln, 1, 0);
 #pragma unroll 4
             for (int64_t r = p + ln.rl; r < e; r += ln.RL) {
                 float f[VEC];
@@ -398,15 +402,20 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const 
                                          const float (&rs)[VEC], const float (&gm)[VEC], const float (&bt)[VEC],
                                          double (&u)[VEC], double (&v)[VEC])
 {
-    for (int64_t r = p + ln.rl; r < e; r += kAt * ln.RL) {
-        Raw<T, VEC> f[kAt], d[kAt];
-        float us[VEC], vs[VEC];
+    const int64_t first = p + ln.rl;
+    if (first >= e) return;
+    const T *xp = x + first * a.ldx + ln.c, *dp = dy + first * a.ldy + ln.c;
+    // loads stand outside any condition, the next rows' before the work on these
+    auto load = [&](int64_t r, Raw<T, VEC>(&f)[kAt], Raw<T, VEC>(&d)[kAt]) {
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
-            const int64_t q = r + k * ln.RL, at = q < e ? q : r;  // loads outside any condition: all in flight
-            f[k].load(x + at * a.ldx + ln.c);
-            d[k].load(dy + at * a.ldy + ln.c);
+            const bool in = r + k * ln.RL < e;
+            f[k].load(in ? xp + (r - first + k * ln.RL) * a.ldx : xp);
+            d[k].load(in ? dp + (r - first + k * ln.RL) * a.ldy : dp);
         }
+    };
+    auto work = [&](int64_t r, const Raw<T, VEC>(&f)[kAt], const Raw<T, VEC>(&d)[kAt]) {
+        float us[VEC], vs[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
 #pragma unroll
@@ -425,40 +434,65 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const 
             u[j] += (double)us[j];
             v[j] += (double)vs[j];
         }
+    };
+    int64_t r = first;
+    const int64_t step = (int64_t)kAt * ln.RL;
+    Raw<T, VEC> f0[kAt], d0[kAt], f1[kAt], d1[kAt];
+    load(r, f0, d0);
+    for (; r < e; r += 2 * step) {
+        load(r + step, f1, d1);
+        work(r, f0, d0);
+        load(r + 2 * step, f0, d0);
+        work(r + step, f1, d1);
     }
 }
 
 // dx of one element.  h is rounded as the group sums' terms are, so that a group
 // of one value gives exactly zero.
+__device__ __forceinline__ float dx_of(float xh, float dz, float rs, float gm, float s1, float s2)
+{
+    return rs * (__fmul_rn(dz, gm) - s1 - xh * s2);
+}
+
 template <int ACT>
 __device__ __forceinline__ float dx_of(float x, float dy, float mu, float rs, float gm, float bt, float s1, float s2)
 {
     const float xh = (x - mu) * rs;
-    const float h = __fmul_rn(dy * act_slope<ACT>(xh * gm + bt), gm);
-    return rs * (h - s1 - xh * s2);
+    return dx_of(xh, dy * act_slope<ACT>(xh * gm + bt), rs, gm, s1, s2);
 }
 
-// the run's sums per channel: dz xhat, then dz.  s: THR * VEC doubles
+// Sums over a block's pieces of dz xhat and of dz, kept in LDS (they change once a
+// piece): place j of lane t of the first at j THR + t, the second VEC THR further on.
 template <int VEC, int THR>
-__device__ __forceinline__ void channel_sums(const NormArgs& a, const Slice& sl, const Lanes<VEC, THR>& ln,
-                                             const double (&tu)[VEC], const double (&tv)[VEC], double* s, int64_t row)
-{
-    const int32_t w = ln.L * VEC;
+struct Totals {
+    double* t;
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
-        if (ln.on)
+        for (int j = 0; j < 2 * VEC; ++j) t[j * THR + threadIdx.x] = 0.0;
+    }
+    __device__ __forceinline__ void add(const double (&u)[VEC], const double (&v)[VEC])
+    {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) s[ln.rl * w + ln.c - sl.c0 + j] = which == 0 ? tu[j] : tv[j];
-        __syncthreads();
-        for (int32_t k = threadIdx.x; k < w; k += THR) {
-            double t = 0.0;
-            for (int32_t r = 0; r < ln.RL; ++r) t += s[r * w + k];
-            a.chan[(row * 2 + which) * a.C + sl.c0 + k] = t;
+        for (int j = 0; j < VEC; ++j) {
+            t[j * THR + threadIdx.x] += u[j];
+            t[(VEC + j) * THR + threadIdx.x] += v[j];
         }
     }
-    __syncthreads();
-}
+    // their sums over the rows' lanes to row `row` of a.chan
+    __device__ __forceinline__ void store(const NormArgs& a, const Slice& sl, const Lanes<VEC, THR>& ln, int64_t row)
+    {
+        const int32_t w = ln.L * VEC;
+        __syncthreads();
+        for (int32_t k = threadIdx.x; k < 2 * w; k += THR) {
+            const int32_t which = k / w, c = k - which * w;
+            double v = 0.0;
+            for (int32_t r = 0; r < ln.RL; ++r) v += t[(which * VEC + c % VEC) * THR + r * ln.L + c / VEC];
+            a.chan[(row * 2 + which) * a.C + sl.c0 + c] = v;
+        }
+        __syncthreads();
+    }
+};
 
 template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T* __restrict__ x,
@@ -466,7 +500,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
 {
     double* s = reinterpret_cast<double*>(norm_lds);
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
-    const Lanes<VEC> ln(sl);
+    const Lanes<VEC> ln(a, sl);
+    Totals<VEC, kThreads> total{s + sum_doubles(a.cpg, VEC, kThreads, false)};
     float gm[VEC], bt[VEC];
     if (ln.on) {
         load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
@@ -474,24 +509,21 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
     }
     for (int64_t run = blockIdx.x; run < a.runs; run += gridDim.x) {
         const int64_t r0 = run * a.R, r1 = r0 + a.R < a.N ? r0 + a.R : a.N;
-        double tu[VEC], tv[VEC];  // dz xhat and dz of the run
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) tu[j] = tv[j] = 0.0;
+        total.clear();
         for_pieces(a, r0, r1, [&](int64_t b, int64_t p, int64_t e) {
             double u[VEC], v[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
             if (ln.on) {
                 float mu[VEC], rs[VEC];
-                load_group(mu, a.mean, a, b, ln.c, 1, 0);
-                load_group(rs, a.rstd, a, b, ln.c, 1, 0);
+                load_group(mu, a.mean, a, b, ln, 1, 0);
+                load_group(rs, a.rstd, a, b, ln, 1, 0);
                 bwd_rows<4, T, VEC, ACT>(a, ln, x, dy, p, e, mu, rs, gm, bt, u, v);
             }
+            total.add(u, v);
             double hu[VEC], hv[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                tu[j] += u[j];
-                tv[j] += v[j];
                 hu[j] = ln.on ? v[j] * (double)gm[j] : 0.0;
                 hv[j] = ln.on ? u[j] * (double)gm[j] : 0.0;
             }
@@ -499,7 +531,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
                 group_sums(a, sl, ln, hu, hv, s,
                            [&](int32_t g, double x, double y) { put_piece(a, run, b, g, sl.part, x, y); });
         });
-        if (a.chan) channel_sums(a, sl, ln, tu, tv, s, run);
+        if (a.chan) total.store(a, sl, ln, run);
     }
 }
 
@@ -547,7 +579,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
                                                              const T* __restrict__ dy, T* __restrict__ dx)
 {
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
-    const Lanes<VEC> ln(sl);
+    const Lanes<VEC> ln(a, sl);
     float gm[VEC], bt[VEC];
     if (ln.on) {
         load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
@@ -559,10 +591,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
         for_pieces(a, r0, r1, [&](int64_t b, int64_t p, int64_t e) {
             if (!ln.on) return;
             float mu[VEC], rs[VEC], s1[VEC], s2[VEC];
-            load_group(mu, a.mean, a, b, ln.c, 1, 0);
-            load_group(rs, a.rstd, a, b, ln.c, 1, 0);
-            load_group(s1, a.coef, a, b, ln.c, 2, 0);
-            load_group(s2, a.coef, a, b, ln.c, 2, 1);
+            load_group(mu, a.mean, a, b, ln, 1, 0);
+            load_group(rs, a.rstd, a, b, ln, 1, 0);
+            load_group(s1, a.coef, a, b, ln, 2, 0);
+            load_group(s2, a.coef, a, b, ln, 2, 1);
 #pragma unroll 4
             for (int64_t r = p + ln.rl; r < e; r += ln.RL) {
                 Raw<T, VEC> f, d;
@@ -582,16 +614,14 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
 // longer segment are read again.
 template <int THR>
 constexpr int kKeep = THR == kThreads ? 4 : 8;
-template <int THR>
 constexpr int kKeepBwd = 4;
 
 // values of the lane's channels from v[group of the slice]
-template <int VEC>
-__device__ __forceinline__ void slice_group(float (&o)[VEC], const float* v, const NormArgs& a, const Slice& sl,
-                                            int32_t c)
+template <int VEC, class Ln>
+__device__ __forceinline__ void slice_group(float (&o)[VEC], const float* v, const Slice& sl, const Ln& ln)
 {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] = v[(c + j) / a.cpg - sl.g0];
+    for (int j = 0; j < VEC; ++j) o[j] = v[ln.g[j] - sl.g0];
 }
 
 template <class T, int VEC, int THR, int ACT>
@@ -603,7 +633,7 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
     float* st[2];
     st[0] = reinterpret_cast<float*>(s + sum_doubles(a.cpg, VEC, THR, false));
     st[1] = st[0] + a.sl.groups;
-    const Lanes<VEC, THR> ln(sl);
+    const Lanes<VEC, THR> ln(a, sl);
     float gm[VEC], bt[VEC];
     if (ln.on) {
         load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
@@ -618,11 +648,13 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
 #pragma unroll
         for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
         const bool on = ln.on && p + ln.rl < e;
+        const T* xp = x + (p + ln.rl) * a.ldx + ln.c;  // the lane's first row
+        T* yp = y + (p + ln.rl) * a.ldy + ln.c;
         if (on) {
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
                 const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
-                f[k].load(x + (r < e ? r : p) * a.ldx + ln.c);
+                f[k].load(xp + (r < e ? (int64_t)k * ln.RL * a.ldx : 0));
             }
 #pragma unroll
             for (int k = 0; k < KEEP; ++k)
@@ -656,8 +688,8 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
         __syncthreads();
         if (on) {
             float mu[VEC], rs[VEC];
-            slice_group<VEC>(mu, st[0], a, sl, ln.c);
-            slice_group<VEC>(rs, st[1], a, sl, ln.c);
+            slice_group(mu, st[0], sl, ln);
+            slice_group(rs, st[1], sl, ln);
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
                 const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
@@ -665,7 +697,7 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
                     float g[VEC];
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) g[j] = act_of<ACT>((f[k][j] - mu[j]) * rs[j] * gm[j] + bt[j]);
-                    store_vec<T, VEC>(y + r * a.ldy + ln.c, g);
+                    store_vec<T, VEC>(yp + (int64_t)k * ln.RL * a.ldy, g);
                 }
             }
 #pragma unroll 4
@@ -682,24 +714,23 @@ __global__ void __launch_bounds__(THR) k_norm_seg(NormArgs a, const T* __restric
 }
 
 template <class T, int VEC, int THR, int ACT>
-__global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
+__global__ void __launch_bounds__(THR, THR == 256 ? 4 : 1) k_norm_bwd_seg(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
                                                       T* __restrict__ dx)
 {
-    constexpr int KEEP = kKeepBwd<THR>;
+    constexpr int KEEP = kKeepBwd;
     const Slice sl = slice_of(a, (int32_t)blockIdx.y);
     double* s = reinterpret_cast<double*>(norm_lds);
     float* st[2];
     st[0] = reinterpret_cast<float*>(s + sum_doubles(a.cpg, VEC, THR, true));
     st[1] = st[0] + a.sl.groups;
-    const Lanes<VEC, THR> ln(sl);
+    const Lanes<VEC, THR> ln(a, sl);
     float gm[VEC], bt[VEC];
     if (ln.on) {
         load_chan<VEC>(gm, a.gamma, ln.c, 1.0f);
         load_chan<VEC>(bt, a.beta, ln.c, 0.0f);
     }
-    double tu[VEC], tv[VEC];  // dz xhat and dz of this block's segments
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) tu[j] = tv[j] = 0.0;
+    Totals<VEC, THR> total{s + sum_doubles(a.cpg, VEC, THR, false)};
+    total.clear();
     // consecutive segments to a block
     const int64_t each = (a.B + gridDim.x - 1) / gridDim.x, b0 = blockIdx.x * each;
     const int64_t b1 = b0 + each < a.B ? b0 + each : a.B;
@@ -707,45 +738,58 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
         const int64_t p = seg_at(a, b), e = seg_at(a, b + 1);
         if (e <= p || e - p > a.longest) continue;
         const double M = (double)(e - p) * a.cpg;
-        Raw<T, VEC> f[KEEP], d[KEEP];
+        float xh[KEEP][VEC], dz[KEEP][VEC];  // of the rows that are kept
         float mu[VEC], rs[VEC];
         double u[VEC], v[VEC], hu[VEC], hv[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
         const bool on = ln.on && p + ln.rl < e;
+        const T *xp = x + (p + ln.rl) * a.ldx + ln.c, *dp = dy + (p + ln.rl) * a.ldy + ln.c;  // the lane's first row
         if (on) {
-            load_group(mu, a.mean, a, b, ln.c, 1, 0);
-            load_group(rs, a.rstd, a, b, ln.c, 1, 0);
+            load_group(mu, a.mean, a, b, ln, 1, 0);
+            load_group(rs, a.rstd, a, b, ln, 1, 0);
             float us[VEC], vs[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
+            Raw<T, VEC> f[KEEP], d[KEEP];
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
-                const int64_t q = p + ln.rl + (int64_t)k * ln.RL, r = q < e ? q : p;
-                f[k].load(x + r * a.ldx + ln.c);
-                d[k].load(dy + r * a.ldy + ln.c);
+                const bool in = p + ln.rl + (int64_t)k * ln.RL < e;
+                f[k].load(xp + (in ? (int64_t)k * ln.RL * a.ldx : 0));
+                d[k].load(dp + (in ? (int64_t)k * ln.RL * a.ldy : 0));
             }
 #pragma unroll
             for (int k = 0; k < KEEP; ++k)
                 if (p + ln.rl + (int64_t)k * ln.RL < e)
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        const float xh = (f[k][j] - mu[j]) * rs[j];
-                        const float dz = d[k][j] * act_slope<ACT>(xh * gm[j] + bt[j]);
-                        us[j] += dz * xh;
-                        vs[j] += dz;
+                        xh[k][j] = (f[k][j] - mu[j]) * rs[j];
+                        dz[k][j] = d[k][j] * act_slope<ACT>(xh[k][j] * gm[j] + bt[j]);
+                        us[j] += dz[k][j] * xh[k][j];
+                        vs[j] += dz[k][j];
                     }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 u[j] = (double)us[j];
                 v[j] = (double)vs[j];
             }
-            bwd_rows<2, T, VEC, ACT>(a, ln, x, dy, p + (int64_t)KEEP * ln.RL, e, mu, rs, gm, bt, u, v);
+#pragma unroll 2
+            for (int64_t r = p + ln.rl + (int64_t)KEEP * ln.RL; r < e; r += ln.RL) {
+                Raw<T, VEC> g, h;
+                g.load(x + r * a.ldx + ln.c);
+                h.load(dy + r * a.ldy + ln.c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float xh = (g[j] - mu[j]) * rs[j];
+                    const float dz = h[j] * act_slope<ACT>(xh * gm[j] + bt[j]);
+                    u[j] += (double)(dz * xh);
+                    v[j] += (double)dz;
+                }
+            }
         }
+        total.add(u, v);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            tu[j] += u[j];
-            tv[j] += v[j];
             hu[j] = on ? v[j] * (double)gm[j] : 0.0;
             hv[j] = on ? u[j] * (double)gm[j] : 0.0;
         }
@@ -757,17 +801,16 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
         __syncthreads();
         if (on) {
             float s1[VEC], s2[VEC];
-            slice_group<VEC>(s1, st[0], a, sl, ln.c);
-            slice_group<VEC>(s2, st[1], a, sl, ln.c);
+            slice_group(s1, st[0], sl, ln);
+            slice_group(s2, st[1], sl, ln);
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
                 const int64_t r = p + ln.rl + (int64_t)k * ln.RL;
                 if (r < e) {
                     float g[VEC];
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        g[j] = dx_of<ACT>(f[k][j], d[k][j], mu[j], rs[j], gm[j], bt[j], s1[j], s2[j]);
-                    store_vec<T, VEC>(dx + r * a.ldd + ln.c, g);
+                    for (int j = 0; j < VEC; ++j) g[j] = dx_of(xh[k][j], dz[k][j], rs[j], gm[j], s1[j], s2[j]);
+                    store_vec<T, VEC>(dx + (p + ln.rl) * a.ldd + ln.c + (int64_t)k * ln.RL * a.ldd, g);
                 }
             }
 #pragma unroll 2
@@ -782,7 +825,7 @@ __global__ void __launch_bounds__(THR) k_norm_bwd_seg(NormArgs a, const T* __res
         }
         __syncthreads();  // st
     }
-    if (a.chan) channel_sums(a, sl, ln, tu, tv, s, a.nchan - gridDim.x + blockIdx.x);
+    if (a.chan) total.store(a, sl, ln, a.nchan - gridDim.x + blockIdx.x);
 }
 
 // ---- layout and form -----------------------------------------------------------------------
@@ -795,7 +838,7 @@ int64_t rows_per_run(int64_t N)
     return r < 16 ? 16 : r;
 }
 
-constexpr int64_t kSegBlocks = 512;   // blocks of the whole segments' backward, each with one row of channel sums
+constexpr int64_t kSegBlocks = 1024;   // blocks of the whole segments' backward, each with one row of channel sums
 constexpr int64_t kLong = 256 << 10;  // bytes of a segment's slice that one block takes
 constexpr int64_t kTotal = 32 << 20;  // bytes that one block could be left with, if one segment held all rows
 constexpr int64_t kFill = 256;        // blocks that fill the chip
@@ -849,6 +892,11 @@ Slices slices_of(const NormShape& n, int vec, int threads, int64_t want)
     return s;
 }
 
+// Elements of a wide access, for either type: with eight of bf16 the sums of a
+// lane's channels take so many registers that half the waves fit (119 us where
+// four take 100 us for the backward's sums of 400008 x 256).
+constexpr int kVec = 4;
+
 // wide accesses need every slice to begin and end on them
 bool wide_ok(const NormShape& n, int vec)
 {
@@ -861,6 +909,8 @@ struct NormPlan {
     Slices seg;      // slices of the whole segments
     bool whole, runs;
     int threads;     // of the whole segments' blocks
+    NormShape n;
+    bool wide16;     // backward: rows begin on 16 bytes
 };
 
 // Which forms run (the header comment says why): whole segments where their mean
@@ -888,12 +938,12 @@ NormPlan norm_plan(const NormShape& n, int vec, int arrays, void* ws)
     a.coef = (float*)((char*)ws + w.coef);
     a.sl = slices_of(n, vec, kThreads, 1);
     const int64_t mean = n.B > 0 ? cdiv64(n.N, n.B) : 0, es = dtype_size(n.dtype);
-    // a block of 1024 threads where 256 could not keep the rows, if its group sums fit in LDS
+    // 1024 threads where the registers of 256 could not keep the rows and the group
+    // sums fit in LDS
     p.threads = kThreads;
     p.seg = slices_of(n, vec, p.threads, n.B > 0 ? cdiv64(kFill, n.B) : 1);
-    const int64_t lanes = p.seg.width / vec;
-    const int keep = arrays == 1 ? kKeep<kThreads> : kKeepBwd<kThreads>;
-    if (p.seg.parts == 1 && mean > keep * (kThreads / (lanes > 0 ? lanes : 1)) && a.cpg % vec == 0) p.threads = 1024;
+    const int64_t lanes = p.seg.width / vec, keep = arrays == 1 ? kKeep<kThreads> : kKeepBwd;
+    if (p.seg.parts == 1 && mean > keep * (kThreads / lanes) && a.cpg % vec == 0) p.threads = 1024;
     p.whole = p.seg.parts == 1 && mean * p.seg.width * es * arrays <= kLong;
     const bool safe = !n.seg || n.N * p.seg.width * es * arrays <= kTotal;
     p.runs = n.N > 0 && (!p.whole || !safe);
@@ -965,15 +1015,25 @@ hipError_t norm_bwd(NormPlan& p, const void* x, const void* dy, void* dx, float*
                            s, a, (const T*)x, (const T*)dy);
     const unsigned cb = chan ? (unsigned)cdiv64(a.C, kChan) : 0, sb = dx && p.runs ? stat_blocks(a, kJoin) : 0;
     if (cb + sb > 0) hipLaunchKernelGGL(k_norm_bwd_join, dim3(cb + sb), dim3(kJoin), 0, s, a, (int32_t)cb, dgamma, dbeta);
-    if (p.runs && dx)
-        hipLaunchKernelGGL((k_norm_bwd_apply<T, VEC, ACT>), grid, dim3(kThreads), 0, s, a, (const T*)x, (const T*)dy,
-                           (T*)dx);
+    if (p.runs && dx) {
+        // no sums to keep: shorter runs, and the widest accesses where they fit
+        NormArgs w = a;
+        w.R = cdiv64(a.R, 2);
+        w.runs = cdiv64(a.N, w.R);
+        if (p.wide16) w.sl = slices_of(p.n, kWide<T>, kThreads, 1);
+        const dim3 g(grid_of(w.runs), (unsigned)w.sl.n);
+        if (p.wide16)
+            hipLaunchKernelGGL((k_norm_bwd_apply<T, kWide<T>, ACT>), g, dim3(kThreads), 0, s, w, (const T*)x,
+                               (const T*)dy, (T*)dx);
+        else
+            hipLaunchKernelGGL((k_norm_bwd_apply<T, VEC, ACT>), g, dim3(kThreads), 0, s, w, (const T*)x,
+                               (const T*)dy, (T*)dx);
+    }
     return hipGetLastError();
 }
 
-// f(element type, elements of an access, activation) as constants; BYTES of a
-// wide access
-template <int BYTES, class F>
+// f(element type, elements of an access, activation) as constants
+template <class F>
 hipError_t with_form(const NormShape& n, bool wide, F&& f)
 {
     auto act = [&](auto t, auto vec) {
@@ -984,8 +1044,8 @@ hipError_t with_form(const NormShape& n, bool wide, F&& f)
         }
     };
     if (n.dtype == kF32)
-        return wide ? act(float{}, std::integral_constant<int, 4>{}) : act(float{}, std::integral_constant<int, 1>{});
-    return wide ? act(bf16_t{}, std::integral_constant<int, BYTES / 2>{})
+        return wide ? act(float{}, std::integral_constant<int, kVec>{}) : act(float{}, std::integral_constant<int, 1>{});
+    return wide ? act(bf16_t{}, std::integral_constant<int, kVec>{})
                 : act(bf16_t{}, std::integral_constant<int, 1>{});
 }
 
@@ -998,14 +1058,13 @@ hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma
 {
     if (n.B == 0) return hipSuccess;
     const int64_t es = dtype_size(n.dtype);
-    const int vec = (int)(16 / es);
-    const bool wide = wide_ok(n, vec) && aligned_rows(x, n.ldx, es) && aligned_rows(y, n.ldy, es);
-    NormPlan p = norm_plan(n, wide ? vec : 1, 1, ws);
+    const bool wide = wide_ok(n, kVec) && aligned_rows(x, n.ldx, es, kVec * es) && aligned_rows(y, n.ldy, es, kVec * es);
+    NormPlan p = norm_plan(n, wide ? kVec : 1, 1, ws);
     p.a.gamma = gamma;
     p.a.beta = beta;
     p.a.omean = mean;
     p.a.orstd = rstd;
-    return with_form<16>(n, wide, [&](auto t, auto v, auto act) {
+    return with_form(n, wide, [&](auto t, auto v, auto act) {
         return norm_fwd<decltype(t), decltype(v)::value, decltype(act)::value>(p, x, y, s);
     });
 }
@@ -1015,18 +1074,17 @@ hipError_t launch_norm_bwd(const NormShape& n, const void* x, const float* mean,
                            float* dbeta, void* ws, hipStream_t s)
 {
     const int64_t es = dtype_size(n.dtype);
-    // four elements an access for either type: with eight of bf16 the sums of a
-    // lane's channels take so many registers that half the waves fit (119 us where
-    // this takes XX us for the sums of 400008 x 256)
-    const int vec = 4;
-    const bool wide = wide_ok(n, vec) && aligned_rows(x, n.ldx, es, vec * es) &&
-                      aligned_rows(dy, n.ldy, es, vec * es) && (!dx || aligned_rows(dx, n.ldd, es, vec * es));
-    NormPlan p = norm_plan(n, wide ? vec : 1, 2, ws);
+    const bool wide = wide_ok(n, kVec) && aligned_rows(x, n.ldx, es, kVec * es) &&
+                      aligned_rows(dy, n.ldy, es, kVec * es) && (!dx || aligned_rows(dx, n.ldd, es, kVec * es));
+    NormPlan p = norm_plan(n, wide ? kVec : 1, 2, ws);
     p.a.mean = mean;
     p.a.rstd = rstd;
     p.a.gamma = gamma;
     p.a.beta = beta;
-    return with_form<8>(n, wide, [&](auto t, auto v, auto act) {
+    p.n = n;
+    p.wide16 = wide_ok(n, (int)(16 / es)) && aligned_rows(x, n.ldx, es) && aligned_rows(dy, n.ldy, es) &&
+               (!dx || aligned_rows(dx, n.ldd, es));
+    return with_form(n, wide, [&](auto t, auto v, auto act) {
         return norm_bwd<decltype(t), decltype(v)::value, decltype(act)::value>(p, x, dy, dx, dgamma, dbeta, s);
     });
 }
