@@ -93,16 +93,19 @@ __global__ void __launch_bounds__(kThreads) k_clear(Clear c) { clear(c, blockIdx
 
 __device__ __forceinline__ int32_t key_of(int32_t id, int32_t V) { return id >= 0 && id < V ? id : V; }
 
-// Lanes of the wave (among `in`) whose digit equals this lane's.
+// Lanes of the wave (among `in`) whose digit equals this lane's: per bit the lanes
+// that have it as this one does, m where it is set and ~m where not.
 __device__ __forceinline__ uint64_t same_digit(int32_t d, int bits, bool in)
 {
-    uint64_t same = __ballot(in);
+    const uint64_t all = __ballot(in);
+    uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
     for (int b = 0; b < bits; ++b) {
-        const bool one = (d >> b) & 1;
-        const uint64_t m = __ballot(one);
-        same &= one ? m : ~m;
+        const int32_t one = (int32_t)((uint32_t)d << (31 - b)) >> 31;  // 0 or -1
+        const uint64_t m = __ballot(one != 0);
+        lo &= ~((uint32_t)m ^ (uint32_t)one);
+        hi &= ~((uint32_t)(m >> 32) ^ (uint32_t)one);
     }
-    return same;
+    return (uint64_t)hi << 32 | lo;
 }
 
 // The wave's LDS accesses before this come before those after it (the hardware
@@ -300,16 +303,17 @@ __global__ void __launch_bounds__(kThreads) k_sort_scatter(SortArgs a)
     constexpr int kEach = kDigits / kThreads;
     int32_t early[kEach], sum[kEach];
     if (a.tiles <= kFewTiles) {
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) early[e] = sum[e] = 0;
-#pragma unroll 8
-        for (int32_t t = 0; t < a.tiles; ++t)
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int32_t c = hist_at(a, kEach * tid + e, t);
-                sum[e] += c;
-                if (t < (int32_t)blockIdx.x) early[e] += c;
-            }
+        static_assert(kEach == 2, "two counts in one load");
+        early[0] = early[1] = sum[0] = sum[1] = 0;
+#pragma unroll 16
+        for (int32_t t = 0; t < a.tiles; ++t) {
+            const int2 c = *reinterpret_cast<const int2*>(&hist_at(a, 2 * tid, t));
+            const bool before = t < (int32_t)blockIdx.x;
+            sum[0] += c.x;
+            sum[1] += c.y;
+            early[0] += before ? c.x : 0;
+            early[1] += before ? c.y : 0;
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T* __re
 
 // Block (run, slice): if a stretch begins in this run and goes on after it, its
 // partial sums from here to its end.
-constexpr int kJoin = 512;
+constexpr int kJoin = 256;
 
 template <class T, int VEC>
 __global__ void __launch_bounds__(kJoin) k_embed_join(SumArgs a, T* __restrict__ gtab)
@@ -501,7 +505,7 @@ __global__ void __launch_bounds__(kJoin) k_embed_join(SumArgs a, T* __restrict__
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[j] = 0.0;
         if (ok) {
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t r = run + rl; r <= last; r += RL) {
                 const double* d = a.part + (r * 2 + (r == run ? 1 : 0)) * a.C + q * VEC;
 #pragma unroll
@@ -665,9 +669,14 @@ hipError_t launch_embed_bwd(const EmbedShape& e, const int32_t* ids, const void*
         a.oval = (int32_t*)(base + w.val[0]);
         a.c = clear_of(e, gtab, kOneThreads);
         const dim3 grid(1 + a.c.blocks), thr(kOneThreads);
-        if (e.N <= 2 * kOneThreads) hipLaunchKernelGGL(k_sort_one<2>, grid, thr, 0, s, a);
-        else if (e.N <= 8 * kOneThreads) hipLaunchKernelGGL(k_sort_one<8>, grid, thr, 0, s, a);
-        else hipLaunchKernelGGL(k_sort_one<kOnePer>, grid, thr, 0, s, a);
+        switch (cdiv64(e.N, 4 * kOneThreads)) {  // the time goes with the keys of a thread
+            case 1: hipLaunchKernelGGL(k_sort_one<4>, grid, thr, 0, s, a); break;
+            case 2: hipLaunchKernelGGL(k_sort_one<8>, grid, thr, 0, s, a); break;
+            case 3: hipLaunchKernelGGL(k_sort_one<12>, grid, thr, 0, s, a); break;
+            case 4: hipLaunchKernelGGL(k_sort_one<16>, grid, thr, 0, s, a); break;
+            case 5: hipLaunchKernelGGL(k_sort_one<20>, grid, thr, 0, s, a); break;
+            default: hipLaunchKernelGGL(k_sort_one<kOnePer>, grid, thr, 0, s, a); break;
+        }
         key = a.okey;
         val = a.oval;
     } else {
