@@ -73,7 +73,7 @@ SIGNATURES = {
     "cgtp_embed_fwd": (_int, [_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _f32, _vp, _c_i64, _vp]),
     "cgtp_embed_bwd_workspace_size": (_int, [_int, _c_i64, _c_i64, _c_i64, _sp]),
     "cgtp_embed_bwd": (_int, [_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64, _f32, _vp, _vp, _size, _vp]),
-    "cgtp_norm_act_workspace_size": (_int, [_int] + [_c_i64] * 4 + [_sp]),
+    "cgtp_norm_act_workspace_size": (_int, [_int] + [_c_i64] * 4 + [_int, _int, _sp]),
     "cgtp_norm_act_fwd": (_int, [_int, _int] + [_c_i64] * 4 + [_vp, _f32, _vp, _c_i64, _vp, _vp, _vp, _c_i64, _vp,
                                                               _vp, _vp, _size, _vp]),
     "cgtp_norm_act_bwd": (_int, [_int, _int] + [_c_i64] * 4 + [_vp, _vp, _c_i64] + [_vp] * 5 +

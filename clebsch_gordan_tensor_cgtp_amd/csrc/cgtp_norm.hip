@@ -1051,7 +1051,17 @@ hipError_t with_form(const NormShape& n, bool wide, F&& f)
 
 }  // namespace
 
-size_t norm_workspace_bytes(const NormShape& n) { return norm_layout(n).bytes; }
+size_t norm_workspace_bytes(const NormShape& n, bool ragged, bool backward)
+{
+    if (!backward) {
+        // none where whole segments take all rows, whichever accesses the arrays allow
+        NormShape m = n;
+        int32_t some = 0;
+        m.seg = ragged ? &some : nullptr;  // only whether there are offsets matters to the plan
+        if (!norm_plan(m, 1, 1, nullptr).runs && (!wide_ok(m, kVec) || !norm_plan(m, kVec, 1, nullptr).runs)) return 0;
+    }
+    return norm_layout(n).bytes;
+}
 
 hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma, const float* beta, void* y,
                            float* mean, float* rstd, void* ws, hipStream_t s)

@@ -1092,10 +1092,7 @@ OrthoLayout ortho_layout(const OrthoShape& o)
         off += align256((size_t)bytes);
         return at;
     };
-    if (w.form == kWhole) {
-        w.bytes = 256;
-        return w;
-    }
+    if (w.form == kWhole) return w;  // no workspace
     const int64_t sums = cdiv64(o.m * o.n, kNormElems);
     w.per = (int32_t)(sums < kNormBlocks ? sums : kNormBlocks);
     w.part = take(8 * o.batch * w.per);

@@ -20,6 +20,14 @@ cgtp_status_t hip_status(hipError_t e) { return e == hipSuccess ? CGTP_OK : CGTP
 
 bool type_ok(int t) { return t == CGTP_F32 || t == CGTP_BF16; }
 
+// a workspace of at least `need` bytes, none for none
+cgtp_status_t check_workspace(const void* ws, size_t ws_bytes, size_t need)
+{
+    if (need == 0) return CGTP_OK;
+    if (!ws || ws_bytes < need) return CGTP_ERR_WORKSPACE;
+    return ((uintptr_t)ws & 255u) != 0 ? CGTP_ERR_INVALID_ARG : CGTP_OK;
+}
+
 // a missing or misaligned array
 bool bad(const void* p, int64_t align) { return !p || ((uintptr_t)p % (uintptr_t)align) != 0; }
 
@@ -57,13 +65,11 @@ cgtp::NormShape norm_shape(cgtp_dtype_t dtype, int act, int64_t N, int64_t B, in
 
 // shared by both directions: sizes, offsets, activation, workspace
 cgtp_status_t check_norm_call(const cgtp::NormShape& n, cgtp_act_t act, const int32_t* seg_ptr, const void* ws,
-                              size_t ws_bytes)
+                              size_t ws_bytes, bool backward)
 {
     if (act != CGTP_ACT_NONE && act != CGTP_ACT_SILU && act != CGTP_ACT_TANH) return CGTP_ERR_INVALID_ARG;
     if (seg_ptr ? bad(seg_ptr, 4) : n.B > 0 && n.N % n.B != 0) return CGTP_ERR_INVALID_ARG;
-    if (!ws || ws_bytes < cgtp::norm_workspace_bytes(n)) return CGTP_ERR_WORKSPACE;
-    if (((uintptr_t)ws & 255u) != 0) return CGTP_ERR_INVALID_ARG;
-    return CGTP_OK;
+    return check_workspace(ws, ws_bytes, cgtp::norm_workspace_bytes(n, seg_ptr != nullptr, backward));
 }
 
 bool bad_rows(const void* p, int64_t rows, int64_t ld, int64_t width, int64_t align)
@@ -132,20 +138,21 @@ cgtp_status_t cgtp_embed_bwd(cgtp_dtype_t dtype, int64_t n_rows, int64_t table_r
     const cgtp::EmbedShape e{dtype, n_rows, table_rows, channels, ld_grad, scale};
     if (n_rows > 0) {
         if (bad(ids, 4) || bad_rows(grad_out, n_rows, ld_grad, channels, es)) return CGTP_ERR_INVALID_ARG;
-        if (!ws || ws_bytes < cgtp::embed_bwd_workspace_bytes(e)) return CGTP_ERR_WORKSPACE;
-        if (((uintptr_t)ws & 255u) != 0) return CGTP_ERR_INVALID_ARG;
+        const cgtp_status_t sw = check_workspace(ws, ws_bytes, cgtp::embed_bwd_workspace_bytes(e));
+        if (sw != CGTP_OK) return sw;
     }
     return hip_status(cgtp::launch_embed_bwd(e, ids, grad_out, grad_table, ws, stream));
 }
 
 // ---- group normalisation with an activation ------------------------------------------
 cgtp_status_t cgtp_norm_act_workspace_size(cgtp_dtype_t dtype, int64_t n_rows, int64_t n_segments,
-                                           int64_t channels, int64_t groups, size_t* bytes)
+                                           int64_t channels, int64_t groups, int ragged, int backward, size_t* bytes)
 {
     if (!bytes) return CGTP_ERR_INVALID_ARG;
     const cgtp_status_t st = check_norm(dtype, n_rows, n_segments, channels, groups);
     if (st != CGTP_OK) return st;
-    *bytes = cgtp::norm_workspace_bytes(norm_shape(dtype, 0, n_rows, n_segments, channels, groups));
+    *bytes = cgtp::norm_workspace_bytes(norm_shape(dtype, 0, n_rows, n_segments, channels, groups), ragged != 0,
+                                        backward != 0);
     return CGTP_OK;
 }
 
@@ -159,7 +166,7 @@ cgtp_status_t cgtp_norm_act_fwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_ro
     if (n_segments == 0) return CGTP_OK;
     if (!(eps > 0.0f) || !std::isfinite(eps)) return CGTP_ERR_INVALID_ARG;
     cgtp::NormShape n = norm_shape(dtype, act, n_rows, n_segments, channels, groups);
-    st = check_norm_call(n, act, seg_ptr, ws, ws_bytes);
+    st = check_norm_call(n, act, seg_ptr, ws, ws_bytes, false);
     if (st != CGTP_OK) return st;
     const int64_t es = cgtp::dtype_size(dtype);
     if (bad(mean, 4) || bad(rstd, 4) || (gamma && bad(gamma, 4)) || (beta && bad(beta, 4)))
@@ -184,7 +191,7 @@ cgtp_status_t cgtp_norm_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_ro
     if (st != CGTP_OK) return st;
     if (!grad_x && !grad_gamma && !grad_beta) return CGTP_OK;
     cgtp::NormShape n = norm_shape(dtype, act, n_rows, n_segments, channels, groups);
-    st = check_norm_call(n, act, seg_ptr, ws, ws_bytes);
+    st = check_norm_call(n, act, seg_ptr, ws, ws_bytes, true);
     if (st != CGTP_OK) return st;
     const int64_t es = cgtp::dtype_size(dtype);
     for (const float* p : {gamma, beta, (const float*)grad_gamma, (const float*)grad_beta})
@@ -228,8 +235,8 @@ cgtp_status_t cgtp_orthogonalize(cgtp_dtype_t dtype, int64_t batch, int64_t rows
     const int64_t es = cgtp::dtype_size(dtype);
     if (bad(G, es) || bad(out, es)) return CGTP_ERR_INVALID_ARG;
     cgtp::OrthoShape o = ortho_shape(dtype, batch, rows, cols);
-    if (!ws || ws_bytes < cgtp::ortho_workspace_bytes(o)) return CGTP_ERR_WORKSPACE;
-    if (((uintptr_t)ws & 255u) != 0) return CGTP_ERR_INVALID_ARG;
+    const cgtp_status_t sw = check_workspace(ws, ws_bytes, cgtp::ortho_workspace_bytes(o));
+    if (sw != CGTP_OK) return sw;
     o.steps = steps;
     o.a = a;
     o.b = b;

@@ -39,7 +39,8 @@ struct NormShape {
     float eps;
 };
 
-size_t norm_workspace_bytes(const NormShape& n);
+// of one direction; ragged: with offsets
+size_t norm_workspace_bytes(const NormShape& n, bool ragged, bool backward);
 
 hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma, const float* beta, void* y,
                            float* mean, float* rstd, void* ws, hipStream_t s);

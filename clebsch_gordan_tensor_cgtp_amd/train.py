@@ -12,6 +12,7 @@ indices int32.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -79,30 +80,49 @@ def _like(t, name, dtype, shape, device):
 
 
 def _workspace(ws, nbytes, device):
+    """(address, bytes, tensor) of the workspace, allocated here if not given."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), nbytes, ws
     if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise TypeError("ws must be a contiguous torch.uint8 tensor")
     if ws.device != device:
         raise ValueError(f"ws is on {ws.device}, expected {device}")
-    return ws
+    return ws.data_ptr(), ws.numel(), ws
+
+
+_functions = {}  # of the library, by name
+
+
+def _function(name):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(L.lib(), name)
+    return f
 
 
 def _call(name, device, *args):
-    """The library call `name` on the device's current stream."""
+    """The library call `name` on the device's current stream.  (These calls
+    can be a few microseconds long, so the stream's handle is asked for
+    directly: building a Stream object around it takes 2 us.)"""
     if device.type != "cuda":
         raise ValueError(f"{name} needs arrays on a GPU, got {device}")
-    f = getattr(L.lib(), name)
-    if device.index == torch.cuda.current_device():
-        L.check(name, f(*args, torch.cuda.current_stream(device).cuda_stream))
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = _function(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            L.check(name, f(*args, torch.cuda.current_stream(device).cuda_stream))
+            status = _function(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != L.CGTP_OK:
+        L.check(name, status)
 
 
+@functools.lru_cache(maxsize=256)  # of sizes alone
 def _bytes(name, *args):
     b = ctypes.c_size_t()
-    L.check(name, getattr(L.lib(), name)(*args, ctypes.byref(b)))
+    L.check(name, _function(name)(*args, ctypes.byref(b)))
     return b.value
 
 
@@ -149,9 +169,9 @@ def embed_bwd(ids, grad_out, table_rows: int, scale: float = 1.0, grad_table=Non
         grad_table = torch.empty((table_rows, C), dtype=grad_out.dtype, device=dev)
     else:
         _need(grad_table, "grad_table", grad_out.dtype, (table_rows, C), dev)
-    ws = _workspace(ws, nbytes, dev)
+    at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
     _call("cgtp_embed_bwd", dev, d, N, table_rows, C, ids.data_ptr(), grad_out.data_ptr(), ld, scale,
-          grad_table.data_ptr(), ws.data_ptr(), ws.numel())
+          grad_table.data_ptr(), at, room)
     return grad_table
 
 
@@ -188,8 +208,10 @@ def _channel(t, name, C, dev):
     return t.data_ptr()
 
 
-def norm_act_workspace_size(dtype, n_rows: int, n_segments: int, channels: int, groups: int) -> int:
-    return _bytes("cgtp_norm_act_workspace_size", _DTYPES[dtype], n_rows, n_segments, channels, groups)
+def norm_act_workspace_size(dtype, n_rows: int, n_segments: int, channels: int, groups: int, ragged: bool,
+                            backward: bool) -> int:
+    return _bytes("cgtp_norm_act_workspace_size", _DTYPES[dtype], n_rows, n_segments, channels, groups, int(ragged),
+                  int(backward))
 
 
 def norm_act_fwd(x, gamma, beta, groups: int, seg_ptr=None, eps: float = 1e-5, act: str = "silu", out=None, ws=None):
@@ -206,17 +228,17 @@ def norm_act_fwd(x, gamma, beta, groups: int, seg_ptr=None, eps: float = 1e-5, a
     dev = x.device
     ldx = _rows(x, "x")
     g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
-    nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups)
+    nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups, int(seg_ptr is not None), 0)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _like(out, "out", x.dtype, x.shape, dev)
     stats = torch.empty((2, B, groups), dtype=torch.float32, device=dev)
     mean, rstd = stats.unbind(0)
-    ws = _workspace(ws, nbytes, dev)
+    at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
     _call("cgtp_norm_act_fwd", dev, d, _act(act), N, B, C, groups, None if seg_ptr is None else seg_ptr.data_ptr(),
           eps, x.data_ptr(), ldx, g, b, out.data_ptr(), _rows(out, "out"), mean.data_ptr(), rstd.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          at, room)
     return out, mean, rstd
 
 
@@ -233,14 +255,14 @@ def norm_act_bwd(x, mean, rstd, gamma, beta, grad_y, groups: int, seg_ptr=None, 
     _need(rstd, "rstd", torch.float32, (B, groups), dev)
     g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
     ldx, ldy = _rows(x, "x"), _rows(grad_y, "grad_y")
-    nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups)
+    nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups, int(seg_ptr is not None), 1)
     gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if "x" in want else None
     gg = torch.empty(C, dtype=torch.float32, device=dev) if "gamma" in want else None
     gb = torch.empty(C, dtype=torch.float32, device=dev) if "beta" in want else None
-    ws = _workspace(ws, nbytes, dev)
+    at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _call("cgtp_norm_act_bwd", dev, d, _act(act), N, B, C, groups, ptr(seg_ptr), x.data_ptr(), ldx, mean.data_ptr(),
-          rstd.data_ptr(), g, b, grad_y.data_ptr(), ldy, ptr(gx), C, ptr(gg), ptr(gb), ws.data_ptr(), ws.numel())
+          rstd.data_ptr(), g, b, grad_y.data_ptr(), ldy, ptr(gx), C, ptr(gg), ptr(gb), at, room)
     return gx, gg, gb
 
 
@@ -270,7 +292,7 @@ def orthogonalize(grad, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: f
         out = torch.empty_like(grad)
     else:
         _need(out, "out", grad.dtype, grad.shape, dev)
-    ws = _workspace(ws, nbytes, dev)
+    at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
     _call("cgtp_orthogonalize", dev, d, B, m, n, steps, a, b, c, eps, scale, grad.data_ptr(), out.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          at, room)
     return out

@@ -22,7 +22,8 @@
  *   - arrays are aligned to their element type; rows that start on 16-byte
  *     boundaries (pointer, row stride and channel count) take the wide-load
  *     kernels.  Row strides count elements and are at least the row's width.
- *     Workspaces are aligned to 256 bytes and hold nothing between calls.
+ *     Workspaces are aligned to 256 bytes and hold nothing between calls; where
+ *     the size call says 0 none is needed (NULL).
  *   - an output must not overlap an input.
  */
 #ifndef CGTP_TRAIN_H
@@ -84,9 +85,10 @@ cgtp_status_t cgtp_embed_bwd(cgtp_dtype_t dtype, int64_t n_rows, int64_t table_r
  * Offsets that break the precondition give unspecified values but no access
  * out of bounds. */
 
-/* Workspace bytes of both directions. */
+/* Workspace bytes of one direction (backward 0 or 1), with offsets (ragged 1) or
+ * equal segments (0). */
 cgtp_status_t cgtp_norm_act_workspace_size(cgtp_dtype_t dtype, int64_t n_rows, int64_t n_segments,
-                                           int64_t channels, int64_t groups, size_t* bytes);
+                                           int64_t channels, int64_t groups, int ragged, int backward, size_t* bytes);
 
 cgtp_status_t cgtp_norm_act_fwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_rows, int64_t n_segments,
                                 int64_t channels, int64_t groups, const int32_t* seg_ptr, float eps, const void* x,

@@ -82,7 +82,14 @@ def test_norm_refusals(L):
     for k in ("seg", "gm", "bt"):
         assert fwd(**{k: ODD}) == bad, k
     assert fwd(ldx=7) == bad and fwd(ldy=7) == bad
-    assert fwd(ws=None) == L.CGTP_ERR_WORKSPACE and fwd(n=64) == L.CGTP_ERR_WORKSPACE and fwd(ws=WS_ODD) == bad
+    large = dict(N=400000, B=2)     # segments that no block takes whole: these need a workspace
+    assert fwd(**large, ws=None) == L.CGTP_ERR_WORKSPACE and fwd(**large, n=64) == L.CGTP_ERR_WORKSPACE
+    assert fwd(**large, ws=WS_ODD) == bad
+    b = ctypes.c_size_t()
+    size = lambda *a: (lib.cgtp_norm_act_workspace_size(*a, ctypes.byref(b)), b.value)  # noqa: E731
+    assert size(0, 6, 2, 8, 4, 1, 0) == (L.CGTP_OK, 0) and size(0, 6, 2, 8, 4, 1, 1)[1] > 0
+    assert size(0, 400000, 2, 8, 4, 1, 0)[1] > 0 and size(0, 6, 2, 8, 3, 1, 0)[0] == bad
+    assert lib.cgtp_norm_act_workspace_size(0, 6, 2, 8, 4, 1, 0, None) == bad
 
     def bwd(x=FAKE, mean=FAKE, rstd=FAKE, gm=FAKE, dy=FAKE, ldy=8, dx=FAKE, ldd=8, dg=FAKE, db=FAKE, ws=WS, n=BIG):
         return lib.cgtp_norm_act_bwd(0, 1, 6, 2, 8, 4, FAKE, x, 8, mean, rstd, gm, FAKE, dy, ldy, dx, ldd, dg, db, ws,
@@ -112,12 +119,15 @@ def test_orthogonalize_refusals(L):
     assert call(scale=inf) == bad and call(a=nan) == bad and call(b=inf) == bad
     assert call(a=30.0, b=0.0, c=20.0) == bad           # grows without bound
     assert call(a=1.0, b=0.0, c=0.0) == bad             # no product at all
-    assert call(a=1.5, b=-0.5, c=0.0, ws=None) == L.CGTP_ERR_WORKSPACE      # the cubic is fine
+    assert call(m=200, n=300, a=1.5, b=-0.5, c=0.0, ws=None) == L.CGTP_ERR_WORKSPACE      # the cubic is fine
     assert call(G=None) == bad and call(out=None) == bad and call(G=ODD) == bad and call(out=ODD) == bad
-    assert call(ws=None) == L.CGTP_ERR_WORKSPACE and call(size=64) == L.CGTP_ERR_WORKSPACE and call(ws=WS_ODD) == bad
+    large = dict(m=200, n=300)      # a matrix that no block holds: these need a workspace
+    assert call(**large, ws=None) == L.CGTP_ERR_WORKSPACE and call(**large, size=64) == L.CGTP_ERR_WORKSPACE
+    assert call(**large, ws=WS_ODD) == bad
     b = ctypes.c_size_t()
     size = lambda *a: (lib.cgtp_orthogonalize_workspace_size(*a, ctypes.byref(b)), b.value)  # noqa: E731
-    assert size(0, 1, 128, 128)[1] < size(0, 15, 128, 128)[1] <= size(1, 15, 128, 1024)[1]
+    assert size(0, 15, 128, 128) == (L.CGTP_OK, 0)
+    assert 0 < size(0, 1, 128, 1024)[1] < size(0, 15, 128, 1024)[1] < size(1, 15, 512, 1024)[1]
     assert size(0, 1, 0, 8)[0] == bad and lib.cgtp_orthogonalize_workspace_size(0, 1, 8, 8, None) == bad
 
 
