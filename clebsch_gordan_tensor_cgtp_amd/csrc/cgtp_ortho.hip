@@ -9,12 +9,16 @@
 // Precision.  Each operand v is kept as two fp16 numbers, h = fp16(v k) and
 // l = fp16(v k - h), with a power of two k that places the operand's bound at
 // 2^14..2^15: the spectral norm is at most ||X||_F = ||G||_F / (||G||_F + eps) at
-// the start and follows the polynomial's maximum from step to step.  h + l holds 24
-// bits of every value down to 2^-16 of the bound, as fp32 does, and
+// the start and follows the polynomial's maximum from step to step.  h + l holds 23
+// bits (eleven each and l's sign) of every value down to 2^-16 of the bound, one
+// fewer than fp32, and
 //   u v = (hu hv + hu lv + lu hv) / k^2
-// leaves out lu lv only, 2^-24 of the product.  Three fp16 products with fp32
-// accumulation so give what an fp32 product gives, at a third of the fp16 rate
-// instead of the sixteenth that fp32 matrix instructions reach.
+// leaves out lu lv only, at most 2^-22 of the product and of either sign.  Three fp16
+// products with fp32 accumulation so give what an fp32 product gives (the result of
+// five steps is off by 0.8 to 1.1 times what fp32 products give, from 20 rows up), at
+// a third of the fp16 rate instead of the sixteenth that fp32 matrix instructions
+// reach.  Below 17 rows sums are too short to hide the missing bit (up to twice the
+// fp32 error), and there is little to multiply: those matrices run in fp64.
 //
 // Layout.  An operand of `rows` rows is cut along k into blocks of 32: a row's
 // piece of a block is 32 h, then their 32 l, one 128-byte line, and a block's
@@ -536,6 +540,115 @@ __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
                     *reinterpret_cast<h8*>(a.Rt + at + 32) = vl;
                 }
         }
+    }
+}
+
+// ---- short sides of at most 16 -------------------------------------------------------------
+// A block holds a matrix as fp32 in LDS, s rows of `ld` elements, and works in fp64
+// (v_mfma_f64_16x16x4: A[i][k] in lane i + 16 k, B[k][j] in lane j + 16 k, D[i][j] in
+// element i / 4 of lane j + 16 (i % 4)).  A wave keeps to its own tiles of 16 columns:
+// the next X of a tile needs B and that tile alone, and the operand element m of a
+// lane, X[4 m + lane / 16][lane % 16], is the element that its D element m replaces.
+// Only the sum of A crosses waves.  No units: fp64 and fp32 hold every magnitude.
+constexpr int kTinySide = 16, kTinyWaves = 8, kTinyElems = 32768;
+typedef double d4 __attribute__((ext_vector_type(4)));
+
+struct TinyArgs {
+    OrthoDims d;  // sp, tp unused
+    OrthoPoly poly;
+    int32_t ld;
+    const void* G;
+    void* out;
+};
+
+extern __shared__ __attribute__((aligned(16))) float tiny_lds[];
+
+template <class T>
+__global__ void __launch_bounds__(64 * kTinyWaves) k_ortho_tiny(TinyArgs a)
+{
+    __shared__ double parts[kTinyWaves][256], A[256], norms[kTinyWaves];
+    float* X = tiny_lds;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int s = (int)a.d.s, t = (int)a.d.t, ld = a.ld, c = lane & 15, r4 = lane >> 4;
+    const T* g = (const T*)a.G + (int64_t)blockIdx.x * s * t;
+    double sum = 0.0;
+    for (int q = tid; q < s * t; q += 64 * kTinyWaves) {
+        const float v = to_f32(g[q]);
+        sum += (double)v * (double)v;
+        X[a.d.tall ? q % s * ld + q / s : q / t * ld + q % t] = v;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) sum += __shfl_xor(sum, d, 64);
+    if (lane == 0) norms[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kTinyWaves; ++w) sum += norms[w];
+    const double inv = 1.0 / (sqrt(sum) + (double)a.poly.eps);
+    // a row or column outside the matrix reads its first element and counts as zero
+    auto at = [&](int row, int col) { return (double)X[row < s && col < t ? row * ld + col : 0]; };
+    auto in = [&](int row, int col) { return row < s && col < t; };
+    for (int j0 = 16 * wave; j0 < t; j0 += 16 * kTinyWaves)  // the first X
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int row = 4 * m + r4, col = j0 + c;
+            const double v = at(row, col) * inv;
+            if (in(row, col)) X[row * ld + col] = (float)v;
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int k = 0; k < a.poly.steps; ++k) {
+        const bool last = k + 1 == a.poly.steps;
+        d4 acc = {0.0, 0.0, 0.0, 0.0};
+        for (int j0 = 16 * wave; j0 < t; j0 += 16 * kTinyWaves)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int col = j0 + 4 * m + r4;
+                const double v = in(c, col) ? at(c, col) : 0.0;
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(v, v, acc, 0, 0, 0);
+            }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) parts[wave][(4 * m + r4) * 16 + c] = acc[m];
+        __syncthreads();
+        if (tid < 256) {
+            double v = 0.0;
+#pragma unroll
+            for (int w = 0; w < kTinyWaves; ++w) v += parts[w][tid];
+            A[tid] = v;
+        }
+        __syncthreads();
+        // every wave forms B, each for itself: in D's layout, then as an operand by way of its part
+        acc = d4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(A[c * 16 + 4 * m + r4], A[(4 * m + r4) * 16 + c], acc, 0, 0, 0);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int e = (4 * m + r4) * 16 + c;
+            parts[wave][e] = a.poly.b * A[e] + a.poly.c * acc[m];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        double bk[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) bk[m] = parts[wave][c * 16 + 4 * m + r4];
+        T* o = (T*)a.out + (int64_t)blockIdx.x * s * t;
+        for (int j0 = 16 * wave; j0 < t; j0 += 16 * kTinyWaves) {
+            double x[4];
+            acc = d4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                x[m] = in(4 * m + r4, j0 + c) ? at(4 * m + r4, j0 + c) : 0.0;
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(bk[m], x[m], acc, 0, 0, 0);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int row = 4 * m + r4, col = j0 + c;
+                const double v = a.poly.a * x[m] + acc[m];
+                if (!in(row, col)) continue;
+                if (last) o[a.d.tall ? col * s + row : row * t + col] = from_f32<T>((float)(v * (double)a.poly.scale));
+                else X[row * ld + col] = (float)v;
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -1063,8 +1176,9 @@ __global__ void __launch_bounds__(kThreads) k_ortho_add(int64_t size, int32_t n,
 // where there are at least kFill of them.
 constexpr int64_t kFill = 100;
 
-// Forms: a whole matrix per block, chunks of columns per block, or tiles.
-enum : int { kWhole = 0, kChunks = 1, kTiles = 2 };
+// Forms: a whole matrix per block, chunks of columns per block, tiles, or a matrix
+// of few rows per block in fp64.
+enum : int { kWhole = 0, kChunks = 1, kTiles = 2, kTiny = 3 };
 
 struct OrthoLayout {
     OrthoDims d;
@@ -1092,7 +1206,8 @@ OrthoLayout ortho_layout(const OrthoShape& o)
         off += align256((size_t)bytes);
         return at;
     };
-    if (w.form == kWhole) return w;  // no workspace
+    if (w.d.s <= kTinySide && w.d.s * w.d.t <= kTinyElems) w.form = kTiny;
+    if (w.form == kWhole || w.form == kTiny) return w;  // no workspace
     const int64_t sums = cdiv64(o.m * o.n, kNormElems);
     w.per = (int32_t)(sums < kNormBlocks ? sums : kNormBlocks);
     w.part = take(8 * o.batch * w.per);
@@ -1229,11 +1344,27 @@ hipError_t tiles(const OrthoLayout& w, const OrthoShape& o, const OrthoPoly& pol
 }
 
 template <class T>
+hipError_t tiny(const OrthoLayout& w, const OrthoShape& o, const OrthoPoly& poly, const void* G, void* out,
+                hipStream_t s)
+{
+    TinyArgs a{};
+    a.d = w.d;
+    a.poly = poly;
+    // rows begin 4 modulo 16 banks apart: sixteen rows at four columns meet in no bank
+    a.ld = (int32_t)(cdiv64(w.d.t, 16) * 16 + 4);
+    a.G = G;
+    a.out = out;
+    hipLaunchKernelGGL(k_ortho_tiny<T>, dim3((unsigned)o.batch), dim3(64 * kTinyWaves), (unsigned)(w.d.s * a.ld * 4), s, a);
+    return hipGetLastError();
+}
+
+template <class T>
 hipError_t orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s)
 {
     const OrthoLayout w = ortho_layout(o);
     char* base = (char*)ws;
     const OrthoPoly poly{o.steps, o.a, o.b, o.c, o.eps, o.scale};
+    if (w.form == kTiny) return tiny<T>(w, o, poly, G, out, s);
     UnitTable table{};
     step_units(poly, 1.0, table.u);
     if (w.form == kWhole) {

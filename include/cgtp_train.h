@@ -17,8 +17,9 @@
  *   - no plan: sizes are arguments, and the element type of the large arrays
  *     is a cgtp_dtype_t.  Statistics, gamma and beta and their gradients are
  *     fp32 whatever the type.  Sums run in fp64, Newton-Schulz products as
- *     three fp16 products with fp32 accumulation, which together carry the 24
- *     bits of fp32 operands; each result is rounded once.
+ *     three fp16 products with fp32 accumulation, which together carry 23 bits
+ *     of their operands (fp64 for matrices of up to 16 rows or columns); each
+ *     result is rounded once.
  *   - arrays are aligned to their element type; rows that start on 16-byte
  *     boundaries (pointer, row stride and channel count) take the wide-load
  *     kernels.  Row strides count elements and are at least the row's width.

@@ -47,7 +47,8 @@ CASES = [(1, 1, 1, "noise"), (3, 1, 70, "noise"), (2, 70, 1, "noise"), (15, 128,
          (4, 64, 200, "noise"), (3, 200, 64, "noise"), (5, 5, 7, "noise"), (2, 33, 31, "spectrum"),
          (34, 64, 64, "noise"), (2, 127, 129, "spectrum"), (2, 130, 126, "noise"), (1, 128, 1024, "spectrum"),
          (1, 257, 300, "spectrum"), (2, 300, 150, "noise"), (1, 8, 3000, "noise"), (1, 3000, 8, "noise"),
-         (1, 520, 520, "spectrum"), (2, 96, 96, "rank one"), (1, 1100, 1030, "noise"), (1, 1030, 2100, "spectrum")]
+         (6, 10, 25, "spectrum"), (3, 16, 16, "noise"), (2, 16, 2048, "spectrum"), (2, 3900, 8, "noise"),
+         (1, 16, 2049, "noise"), (2, 17, 40, "noise"), (1, 520, 520, "spectrum"), (2, 96, 96, "rank one"), (1, 1100, 1030, "noise"), (1, 1030, 2100, "spectrum")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -72,7 +73,7 @@ def test_orthogonalize(tt, B, m, n, kind, dtype):
     assert torch.equal(out, cg.orthogonalize(t, steps, coeffs, 1e-7, scale))
 
 
-@pytest.mark.parametrize("m,n", [(40, 48), (128, 300), (200, 160)])
+@pytest.mark.parametrize("m,n", [(40, 48), (128, 300), (200, 160), (12, 31)])
 def test_orthogonalize_special_matrices(tt, m, n):
     """Zero, tiny, huge and non-finite matrices of one stack do not touch each
     other."""
@@ -113,7 +114,7 @@ def test_orthogonalize_empty_stack(tt):
     assert cg.orthogonalize(torch.zeros(0, 5, 6, device=dev)).shape == (0, 5, 6)
 
 
-@pytest.mark.parametrize("m,n", [(128, 128), (64, 500), (300, 260)])
+@pytest.mark.parametrize("m,n", [(128, 128), (64, 500), (300, 260), (9, 20)])
 def test_orthogonalize_on_another_stream_and_in_a_graph(tt, m, n):
     torch, dev = tt
     import clebsch_gordan_tensor_cgtp_amd as cg
