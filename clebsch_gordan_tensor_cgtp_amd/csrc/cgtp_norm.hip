@@ -22,8 +22,8 @@
 // The lengths of ragged segments are known on the device only: where their mean
 // is short but the total is large enough that one long segment would hold up the
 // chip, both forms are launched and each takes the segments on its side of a
-// length.  Statistics of the forward are fp64 sums of x and x^2; the backward
-// adds four rows in fp32 and those in fp64.
+// length.  Sums over the rows are fp64; in the runs two (backward) or four rows are
+// added in fp32 first.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -270,6 +270,83 @@ __device__ __forceinline__ void put_piece(const NormArgs& a, int64_t run, int64_
     o[1] = y;
 }
 
+// Rows first, first + RL, .. below e of a lane, kAt at a time and two such batches in
+// turn: load(row, batch) brings a batch (rows beyond e as the first), work(row, batch,
+// masked) takes it; the next loads are out before the work on these.
+template <int kAt, class Batch, class Load, class Work>
+__device__ __forceinline__ void row_batches(int64_t first, int64_t e, int32_t RL, Load&& load, Work&& work)
+{
+    if (first >= e) return;
+    const int64_t step = (int64_t)kAt * RL;
+    int64_t r = first;
+    Batch b0, b1;
+    load(r, b0);
+    for (; r + 2 * step - RL < e; r += 2 * step) {
+        load(r + step, b1);
+        work(r, b0, std::false_type{});
+        load(r + 2 * step, b0);
+        work(r + step, b1, std::false_type{});
+    }
+    if (r < e) {
+        load(r + step, b1);
+        work(r, b0, std::true_type{});
+        work(r + step, b1, std::true_type{});
+    }
+}
+
+// u += x, v += x^2 over the lane's rows below e.  Four rows in fp32, taken from the
+// lane's first value of each channel so that nothing cancels, then in fp64:
+// sum x = n ref + D, sum x^2 = n ref^2 + 2 ref D + Q with D = sum (x - ref) and
+// Q = sum (x - ref)^2.
+template <int kAt, class T, int VEC, class Ln>
+__device__ __forceinline__ void fwd_rows(const NormArgs& a, const Ln& ln, const T* __restrict__ x, int64_t p,
+                                         int64_t e, double (&u)[VEC], double (&v)[VEC])
+{
+    struct Batch {
+        Raw<T, VEC> f[kAt];
+    };
+    const int64_t first = p + ln.rl;
+    if (first >= e) return;
+    const T* xp = x + first * a.ldx + ln.c;
+    Raw<T, VEC> ref;
+    ref.load(xp);
+    double D[VEC], Q[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) D[j] = Q[j] = 0.0;
+    auto load = [&](int64_t r, Batch& b) {
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) b.f[k].load(r + k * ln.RL < e ? xp + (r - first + k * ln.RL) * a.ldx : xp);
+    };
+    auto work = [&](int64_t r, const Batch& b, auto masked) {
+        float ds[VEC], qs[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) ds[j] = qs[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+            // a row beyond e was loaded as the first: its difference is zero
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float d = b.f[k][j] - ref[j];
+                ds[j] += d;
+                qs[j] += d * d;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            D[j] += (double)ds[j];
+            Q[j] += (double)qs[j];
+        }
+    };
+    row_batches<kAt, Batch>(first, e, ln.RL, load, work);
+    const double n = (double)((e - first + ln.RL - 1) / ln.RL);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        const double w = (double)ref[j];
+        u[j] += n * w + D[j];
+        v[j] += w * (n * w + 2.0 * D[j]) + Q[j];
+    }
+}
+
 // ---- forward -------------------------------------------------------------------------
 // sums of x and x^2 of every piece
 template <class T, int VEC>
@@ -284,19 +361,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_sums(NormArgs a, const T* __r
             double u[VEC], v[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) u[j] = v[j] = 0.0;
-            if (ln.on) {
-#pragma unroll 4
-                for (int64_t r = p + ln.rl; r < e; r += ln.RL) {
-                    float f[VEC];
-                    load_vec<T, VEC>(f, x + r * a.ldx + ln.c);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const double d = (double)f[j];
-                        u[j] += d;
-                        v[j] += d * d;
-                    }
-                }
-            }
+            if (ln.on) fwd_rows<4, T, VEC>(a, ln, x, p, e, u, v);
             group_sums(a, sl, ln, u, v, s,
                        [&](int32_t g, double x, double y) { put_piece(a, run, b, g, sl.part, x, y); });
         });
@@ -382,11 +447,12 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __
             load_group(rs, a.orstd, a, b, ln, 1, 0);
 #pragma unroll 4
             for (int64_t r = p + ln.rl; r < e; r += ln.RL) {
-                float f[VEC];
-                load_vec<T, VEC>(f, x + r * a.ldx + ln.c);
+                Raw<T, VEC> f;
+                float g[VEC];
+                f.load(x + r * a.ldx + ln.c);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) f[j] = act_of<ACT>((f[j] - mu[j]) * rs[j] * gm[j] + bt[j]);
-                store_vec<T, VEC>(y + r * a.ldy + ln.c, f);
+                for (int j = 0; j < VEC; ++j) g[j] = act_of<ACT>((f[j] - mu[j]) * rs[j] * gm[j] + bt[j]);
+                store_vec<T, VEC>(y + r * a.ldy + ln.c, g);
             }
         });
     }
@@ -402,29 +468,30 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const 
                                          const float (&rs)[VEC], const float (&gm)[VEC], const float (&bt)[VEC],
                                          double (&u)[VEC], double (&v)[VEC])
 {
+    struct Batch {
+        Raw<T, VEC> f[kAt], d[kAt];
+    };
     const int64_t first = p + ln.rl;
-    if (first >= e) return;
     const T *xp = x + first * a.ldx + ln.c, *dp = dy + first * a.ldy + ln.c;
-    // loads stand outside any condition, the next rows' before the work on these
-    auto load = [&](int64_t r, Raw<T, VEC>(&f)[kAt], Raw<T, VEC>(&d)[kAt]) {
+    auto load = [&](int64_t r, Batch& b) {
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
             const bool in = r + k * ln.RL < e;
-            f[k].load(in ? xp + (r - first + k * ln.RL) * a.ldx : xp);
-            d[k].load(in ? dp + (r - first + k * ln.RL) * a.ldy : dp);
+            b.f[k].load(in ? xp + (r - first + k * ln.RL) * a.ldx : xp);
+            b.d[k].load(in ? dp + (r - first + k * ln.RL) * a.ldy : dp);
         }
     };
-    auto work = [&](int64_t r, const Raw<T, VEC>(&f)[kAt], const Raw<T, VEC>(&d)[kAt]) {
+    auto work = [&](int64_t r, const Batch& b, auto masked) {
         float us[VEC], vs[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
-            const bool in = r + k * ln.RL < e;
+            const bool in = !decltype(masked)::value || r + k * ln.RL < e;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float xh = (f[k][j] - mu[j]) * rs[j];
-                const float dz = in ? d[k][j] * act_slope<ACT>(xh * gm[j] + bt[j]) : 0.0f;
+                const float xh = (b.f[k][j] - mu[j]) * rs[j];
+                const float dz = in ? b.d[k][j] * act_slope<ACT>(xh * gm[j] + bt[j]) : 0.0f;
                 us[j] += dz * xh;
                 vs[j] += dz;
             }
@@ -435,16 +502,7 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const 
             v[j] += (double)vs[j];
         }
     };
-    int64_t r = first;
-    const int64_t step = (int64_t)kAt * ln.RL;
-    Raw<T, VEC> f0[kAt], d0[kAt], f1[kAt], d1[kAt];
-    load(r, f0, d0);
-    for (; r < e; r += 2 * step) {
-        load(r + step, f1, d1);
-        work(r, f0, d0);
-        load(r + 2 * step, f0, d0);
-        work(r + step, f1, d1);
-    }
+    row_batches<kAt, Batch>(first, e, ln.RL, load, work);
 }
 
 // dx of one element.  h is rounded as the group sums' terms are, so that a group
@@ -495,7 +553,7 @@ struct Totals {
 };
 
 template <class T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T* __restrict__ x,
+__global__ void __launch_bounds__(kThreads, 4) k_norm_bwd_sums(NormArgs a, const T* __restrict__ x,
                                                             const T* __restrict__ dy)
 {
     double* s = reinterpret_cast<double*>(norm_lds);
@@ -518,7 +576,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_sums(NormArgs a, const T*
                 float mu[VEC], rs[VEC];
                 load_group(mu, a.mean, a, b, ln, 1, 0);
                 load_group(rs, a.rstd, a, b, ln, 1, 0);
-                bwd_rows<4, T, VEC, ACT>(a, ln, x, dy, p, e, mu, rs, gm, bt, u, v);
+                bwd_rows<2, T, VEC, ACT>(a, ln, x, dy, p, e, mu, rs, gm, bt, u, v);
             }
             total.add(u, v);
             double hu[VEC], hv[VEC];
@@ -910,7 +968,7 @@ struct NormPlan {
     bool whole, runs;
     int threads;     // of the whole segments' blocks
     NormShape n;
-    bool wide16;     // backward: rows begin on 16 bytes
+    bool wide16;     // rows begin on 16 bytes
 };
 
 // Which forms run (the header comment says why): whole segments where their mean
@@ -982,8 +1040,14 @@ hipError_t norm_fwd(const NormPlan& p, const void* x, void* y, hipStream_t s)
             hipLaunchKernelGGL((k_norm_sums<T, VEC>), grid, dim3(kThreads), lds_bytes(a, VEC, kThreads, false, false), s,
                                a, (const T*)x);
         hipLaunchKernelGGL(k_norm_stats, dim3(stat_blocks(a, kThreads)), dim3(kThreads), 0, s, a);
-        if (a.N > 0)
+        if (a.N > 0 && p.wide16) {  // no sums to keep: the widest accesses where they fit
+            NormArgs w = a;
+            w.sl = slices_of(p.n, kWide<T>, kThreads, 1);
+            hipLaunchKernelGGL((k_norm_apply<T, kWide<T>, ACT>), dim3(grid_of(w.runs), (unsigned)w.sl.n), dim3(kThreads), 0,
+                               s, w, (const T*)x, (T*)y);
+        } else if (a.N > 0) {
             hipLaunchKernelGGL((k_norm_apply<T, VEC, ACT>), grid, dim3(kThreads), 0, s, a, (const T*)x, (T*)y);
+        }
     }
     return hipGetLastError();
 }
@@ -1072,6 +1136,8 @@ hipError_t launch_norm_fwd(const NormShape& n, const void* x, const float* gamma
     NormPlan p = norm_plan(n, wide ? kVec : 1, 1, ws);
     p.a.gamma = gamma;
     p.a.beta = beta;
+    p.n = n;
+    p.wide16 = wide_ok(n, (int)(16 / es)) && aligned_rows(x, n.ldx, es) && aligned_rows(y, n.ldy, es);
     p.a.omean = mean;
     p.a.orstd = rstd;
     return with_form(n, wide, [&](auto t, auto v, auto act) {
