@@ -47,8 +47,11 @@ def _need(t, name, dtype, shape, device):
 def _rows(t, name):
     """Row stride of an array of rows: [N][C], or [B][S][C] with one stride for
     all rows; the channels are contiguous."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     width = shape[-1]
+    if t.is_contiguous():
+        return width
+    stride = t.stride()
     if width > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: channels must be contiguous")
     n = t.numel() // width if width else 0
@@ -110,7 +113,7 @@ def _call(name, device, *args):
     if device.type != "cuda":
         raise ValueError(f"{name} needs arrays on a GPU, got {device}")
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = _function(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -141,11 +144,11 @@ def embed_fwd(ids, table, scale: float = 1.0, out=None) -> torch.Tensor:
     _need(ids, "ids", torch.int32, (N,), dev)
     _need(table, "table", table.dtype, (V, C), dev)
     if out is None:
-        out = torch.empty((N, C), dtype=table.dtype, device=dev)
+        out, ldo = table.new_empty((N, C)), C
     else:
         _like(out, "out", table.dtype, (N, C), dev)
-    _call("cgtp_embed_fwd", dev, d, N, V, C, ids.data_ptr(), table.data_ptr(), scale, out.data_ptr(),
-          _rows(out, "out"))
+        ldo = _rows(out, "out")
+    _call("cgtp_embed_fwd", dev, d, N, V, C, ids.data_ptr(), table.data_ptr(), scale, out.data_ptr(), ldo)
     return out
 
 
@@ -166,7 +169,7 @@ def embed_bwd(ids, grad_out, table_rows: int, scale: float = 1.0, grad_table=Non
     ld = _rows(grad_out, "grad_out")
     nbytes = _bytes("cgtp_embed_bwd_workspace_size", d, N, table_rows, C)
     if grad_table is None:
-        grad_table = torch.empty((table_rows, C), dtype=grad_out.dtype, device=dev)
+        grad_table = grad_out.new_empty((table_rows, C))
     else:
         _need(grad_table, "grad_table", grad_out.dtype, (table_rows, C), dev)
     at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
@@ -179,19 +182,21 @@ def embed_bwd(ids, grad_out, table_rows: int, scale: float = 1.0, grad_table=Non
 def _norm_shape(x, groups, seg_ptr):
     """(N, B, C) of [N][C] rows (one segment, or seg_ptr's) or [B][S][C] rows
     (B segments of S rows)."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    dim = len(shape)
+    if dim != 2 and dim != 3:
         raise ValueError("x must be [N][C] or [B][S][C]")
-    C = x.shape[-1]
+    C = shape[-1]
     if groups < 1 or C % groups:
         raise ValueError(f"groups = {groups} does not divide the {C} channels")
     if seg_ptr is None:
-        return (x.shape[0], 1, C) if x.dim() == 2 else (x.shape[0] * x.shape[1], x.shape[0], C)
-    if x.dim() != 2:
+        return (shape[0], 1, C) if dim == 2 else (shape[0] * shape[1], shape[0], C)
+    if dim != 2:
         raise ValueError("seg_ptr needs x as [N][C]")
     if not isinstance(seg_ptr, torch.Tensor) or seg_ptr.dim() != 1 or seg_ptr.shape[0] < 1:
         raise TypeError("seg_ptr must be a torch.Tensor [segments + 1]")
     _need(seg_ptr, "seg_ptr", torch.int32, seg_ptr.shape, x.device)
-    return x.shape[0], seg_ptr.shape[0] - 1, C
+    return shape[0], seg_ptr.shape[0] - 1, C
 
 
 def _act(act):
@@ -230,14 +235,15 @@ def norm_act_fwd(x, gamma, beta, groups: int, seg_ptr=None, eps: float = 1e-5, a
     g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
     nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups, int(seg_ptr is not None), 0)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out, ldo = x.new_empty(x.shape), C
     else:
         _like(out, "out", x.dtype, x.shape, dev)
+        ldo = _rows(out, "out")
     stats = torch.empty((2, B, groups), dtype=torch.float32, device=dev)
     mean, rstd = stats.unbind(0)
     at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
     _call("cgtp_norm_act_fwd", dev, d, _act(act), N, B, C, groups, None if seg_ptr is None else seg_ptr.data_ptr(),
-          eps, x.data_ptr(), ldx, g, b, out.data_ptr(), _rows(out, "out"), mean.data_ptr(), rstd.data_ptr(),
+          eps, x.data_ptr(), ldx, g, b, out.data_ptr(), ldo, mean.data_ptr(), rstd.data_ptr(),
           at, room)
     return out, mean, rstd
 
@@ -256,7 +262,7 @@ def norm_act_bwd(x, mean, rstd, gamma, beta, grad_y, groups: int, seg_ptr=None, 
     g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
     ldx, ldy = _rows(x, "x"), _rows(grad_y, "grad_y")
     nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups, int(seg_ptr is not None), 1)
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if "x" in want else None
+    gx = x.new_empty(x.shape) if "x" in want else None
     gg = torch.empty(C, dtype=torch.float32, device=dev) if "gamma" in want else None
     gb = torch.empty(C, dtype=torch.float32, device=dev) if "beta" in want else None
     at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
