@@ -160,27 +160,32 @@ struct OneArgs {
 };
 
 template <int PER>
-__global__ void __launch_bounds__(kOneThreads) k_sort_one(OneArgs a)
-{
+struct OneLds {
     // the exchanged words, and while ranks are formed the waves' masks
-    constexpr int kWords = kOneThreads * PER, kMasks = 2 * kOneWaves * kDigits;
-    __shared__ __attribute__((aligned(8))) uint32_t word[kWords > kMasks ? kWords : kMasks];
-    __shared__ int32_t cnt[kOneWaves][kDigits];
-    __shared__ int32_t s[kOneWaves];
-    if (blockIdx.x > 0) {
-        clear(a.c, blockIdx.x - 1);
-        return;
-    }
+    static constexpr int kWords = kOneThreads * PER, kMasks = 2 * kOneWaves * kDigits;
+    __attribute__((aligned(8))) uint32_t word[kWords > kMasks ? kWords : kMasks];
+    int32_t cnt[kOneWaves][kDigits];
+    int32_t s[kOneWaves];
+};
+
+// The words key << row_bits | position of N ids, sorted: in x.word by place (after a
+// barrier), and this thread's in w.
+template <int PER>
+__device__ __forceinline__ void sort_one(const int32_t* __restrict__ ids, int32_t N, int32_t V, int32_t key_bits,
+                                         int32_t row_bits, OneLds<PER>& x, uint32_t (&w)[PER])
+{
+    auto& word = x.word;
+    auto& cnt = x.cnt;
+    auto& s = x.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t first = wave * 64 * PER + lane;  // a wave owns 64 PER keys in a row
-    uint32_t w[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int32_t p = first + 64 * k;
-        w[k] = (uint32_t)key_of(a.ids[p < a.N ? p : 0], a.V) << a.row_bits | (uint32_t)p;
+        w[k] = (uint32_t)key_of(ids[p < N ? p : 0], V) << row_bits | (uint32_t)p;
     }
-    for (int shift = 0; shift < a.key_bits; shift += kBits) {
-        const int bits = a.key_bits - shift < kBits ? a.key_bits - shift : kBits;
+    for (int shift = 0; shift < key_bits; shift += kBits) {
+        const int bits = key_bits - shift < kBits ? key_bits - shift : kBits;
         unsigned long long* mask = reinterpret_cast<unsigned long long*>(word) + wave * kDigits;
         if (shift > 0) __syncthreads();  // the words of the pass before are read
         for (int d = lane; d < kDigits; d += 64) {
@@ -190,9 +195,10 @@ __global__ void __launch_bounds__(kOneThreads) k_sort_one(OneArgs a)
         wave_fence();
         int32_t rank[PER];
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
-            rank[k] = rank_in_wave((int32_t)(w[k] >> (a.row_bits + shift)) & ((1 << bits) - 1), first + 64 * k < a.N, mask,
-                                   cnt[wave]);
+        for (int k = 0; k < PER; ++k) {
+            const int32_t d = (int32_t)(w[k] >> (row_bits + shift)) & ((1 << bits) - 1);
+            rank[k] = rank_in_wave(d, first + 64 * k < N, mask, cnt[wave]);
+        }
         __syncthreads();
         // first place of each digit, then of each wave in it
         int32_t sum = 0, all;
@@ -208,17 +214,29 @@ __global__ void __launch_bounds__(kOneThreads) k_sort_one(OneArgs a)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k)
-            if (first + 64 * k < a.N)
-                word[cnt[wave][(int32_t)(w[k] >> (a.row_bits + shift)) & ((1 << bits) - 1)] + rank[k]] = w[k];
+            if (first + 64 * k < N)
+                word[cnt[wave][(int32_t)(w[k] >> (row_bits + shift)) & ((1 << bits) - 1)] + rank[k]] = w[k];
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k)
-            if (first + 64 * k < a.N) w[k] = word[first + 64 * k];
+            if (first + 64 * k < N) w[k] = word[first + 64 * k];
         // cnt is cleared by its own wave only, word written after two barriers
     }
+}
+
+template <int PER>
+__global__ void __launch_bounds__(kOneThreads) k_sort_one(OneArgs a)
+{
+    __shared__ OneLds<PER> x;
+    if (blockIdx.x > 0) {
+        clear(a.c, blockIdx.x - 1);
+        return;
+    }
+    uint32_t w[PER];
+    sort_one<PER>(a.ids, a.N, a.V, a.key_bits, a.row_bits, x, w);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int32_t p = first + 64 * k;
+        const int32_t p = ((int)threadIdx.x >> 6) * 64 * PER + ((int)threadIdx.x & 63) + 64 * k;
         if (p < a.N) {
             a.okey[p] = (int32_t)(w[k] >> a.row_bits);
             a.oval[p] = (int32_t)(w[k] & ((1u << a.row_bits) - 1));
@@ -373,7 +391,10 @@ struct SumArgs {
     double* part;              // [runs][2][C]
 };
 
-constexpr int kBatch = 8;  // rows in flight per lane
+constexpr int kBatch = 8;    // rows in flight per lane
+// Groups of a block, at most: a stretch adds its groups one by one (16385 x 8 in bf16:
+// sort, sum and join 45 us, where 256 groups joined by one of them took 125 us).
+constexpr int kGroups = 32;
 
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T* __restrict__ grad, T* __restrict__ gtab)
@@ -437,46 +458,168 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T* __re
             if (lane == 0) whole[rl] = first;
         }
         __syncthreads();
-        if (on && rl == 0) {
-            int32_t open = -1;   // the stretch under way
-            bool start = true;   // it began with the run
-            double acc[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) acc[j] = 0.0;
-            auto flush = [&](bool last) {
-                const bool from = start && open == before, to = last && open == after;
-                if (open >= 0 && open < a.V && (from || to)) {
+        // The group in which a stretch begins adds what the groups after it hold.
+        const int32_t head = on ? ids[0][rl] : -1;
+        if (head >= 0) {
+            auto flush = [&](int32_t id, const double (&acc)[VEC], bool from, bool to) {
+                if (id < a.V && (from || to)) {
                     double* d = a.part + (run * 2 + (from ? 0 : 1)) * a.C + q * VEC;
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) d[j] = acc[j];
-                } else if (open >= 0) {
-                    store(open, acc);
+                } else {
+                    store(id, acc);
                 }
             };
-            for (int32_t g = 0; g < a.RL; ++g) {
-                const int32_t id = ids[0][g];
-                if (id < 0) break;
-                if (id != open) {
-                    flush(false);
-                    start = g == 0;
-                    open = id;
+            const bool one = whole[rl];
+            const bool begins = rl == 0 || (whole[rl - 1] ? ids[0][rl - 1] : ids[1][rl - 1]) != head;
+            double acc[VEC];
+            if (begins && !one) {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) acc[j] = 0.0;
-                }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) acc[j] += ends[0][j][g * a.L + lane];
-                if (!whole[g]) {
-                    flush(false);
-                    start = false;
-                    open = ids[1][g];
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) acc[j] = ends[1][j][g * a.L + lane];
-                }
+                for (int j = 0; j < VEC; ++j) acc[j] = ends[0][j][threadIdx.x];
+                flush(head, acc, rl == 0 && head == before, false);
             }
-            flush(true);
+            if (begins || !one) {  // the last stretch
+                const int32_t id = one ? head : ids[1][rl];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) acc[j] = ends[one ? 0 : 1][j][threadIdx.x];
+                int32_t g = rl + 1;
+                bool goes = true;
+                for (; goes && g < a.RL && ids[0][g] == id; ++g) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[j] += ends[0][j][g * a.L + lane];
+                    goes = whole[g];
+                }
+                // it reaches the run's end if no group holds anything else
+                flush(id, acc, one && rl == 0 && id == before,
+                      goes && (g == a.RL || ids[0][g] < 0) && id == after);
+            }
         }
         __syncthreads();
     }
+}
+
+// ---- few ids and a small table: the whole gradient in one launch --------------------------
+// A small call is its launches: three of them take 13.7 us for 2000 x 128 of 10 ids, this
+// 8.7 us (4096 x 128 of 4096: 20.6 and 18.3 us; a table of 4096 x 1024 no longer gains: 23.4
+// and 25.5 us).  Every block sorts all ids for itself and sums kFewLanes accesses of each row.  Its groups
+// of kFewLanes lanes take equal shares of the sorted positions; a group stores the stretches
+// that lie inside its share, and a segmented sum over the groups (by shuffles in a wave,
+// through LDS across waves) finishes those that reach over shares.
+constexpr int kFewPer = 4, kFewLanes = 4, kFewGroups = kOneThreads / kFewLanes;
+constexpr int64_t kFewKeys = (int64_t)kOneThreads * kFewPer, kFewRows = 4096, kFewTable = 1 << 21;
+
+struct FewArgs {
+    int32_t N, V, key_bits, row_bits;
+    int64_t C, CV, ld;
+    float scale;
+    const int32_t* ids;
+};
+
+template <class T, int VEC>
+__global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* __restrict__ grad, T* __restrict__ gtab)
+{
+    __shared__ OneLds<kFewPer> x;
+    __shared__ double wsum[kOneWaves][kFewLanes][VEC];  // of a wave's last stretch
+    __shared__ bool wnew[kOneWaves];                    // it begins in that wave
+    const int tid = threadIdx.x, wave = tid >> 6, l = tid % kFewLanes, g = tid / kFewLanes;
+    const int64_t q = (int64_t)blockIdx.x * kFewLanes + l;
+    const bool on = q < a.CV;
+    T* const col = gtab + q * VEC;
+    if (on) {  // the sort's barriers put these stores before those of the sums
+        float zero[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) zero[j] = 0.0f;
+        for (int64_t v = g; v < a.V; v += kFewGroups) store_vec<T, VEC>(col + v * a.C, zero);
+    }
+    uint32_t w[kFewPer];
+    sort_one<kFewPer>(a.ids, a.N, a.V, a.key_bits, a.row_bits, x, w);
+    __syncthreads();
+    auto store = [&](int32_t id, const double (&sum)[VEC]) {
+        if (!on || id >= a.V) return;
+        float v[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = (float)(sum[j] * (double)a.scale);
+        store_vec<T, VEC>(col + (int64_t)id * a.C, v);
+    };
+    auto key = [&](int32_t p) { return (int32_t)(x.word[p] >> a.row_bits); };
+    const int32_t R = (a.N + kFewGroups - 1) / kFewGroups;
+    const int32_t p0 = g * R < a.N ? g * R : a.N, p1 = p0 + R < a.N ? p0 + R : a.N;
+    const int32_t before = p0 > 0 ? key(p0 - 1) : -1, after = p1 < a.N ? key(p1) : -1;
+    const T* const from = grad + (on ? q : 0) * VEC;
+    double head[VEC], sum[VEC];  // of the first stretch and of the last
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) head[j] = sum[j] = 0.0;
+    int32_t first = -1, cur = -1;  // their ids
+    bool whole = true;             // they are one
+    if (p0 < p1) first = cur = key(p0);
+    for (int32_t p = p0; p < p1; p += kBatch) {
+        int32_t k[kBatch];
+        Raw<T, VEC> v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t o = x.word[p + u < p1 ? p + u : p];
+            k[u] = (int32_t)(o >> a.row_bits);
+            v[u].load(from + (int64_t)(o & ((1u << a.row_bits) - 1)) * a.ld);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (p + u >= p1) continue;
+            if (k[u] != cur) {
+                if (!whole) store(cur, sum);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    if (whole) head[j] = sum[j];
+                    sum[j] = 0.0;
+                }
+                whole = false;
+                cur = k[u];
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[j] += (double)v[u][j];
+        }
+    }
+    // sums of the last stretches from where they begin (`begun`), or from the wave's first group
+    bool begun = p0 >= p1 || !whole || first != before;
+#pragma unroll
+    for (int d = kFewLanes; d < 64; d *= 2) {
+        const int b = __shfl_up((int)begun, d, 64);
+        double t[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) t[j] = __shfl_up(sum[j], d, 64);
+        if ((tid & 63) >= d && !begun) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum[j] += t[j];
+            begun = b != 0;
+        }
+    }
+    if ((tid & 63) >= 64 - kFewLanes) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) wsum[wave][l][j] = sum[j];
+        if (l == 0) wnew[wave] = begun;
+    }
+    __syncthreads();
+    double carry[VEC];  // of the stretch that enters this wave
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) carry[j] = 0.0;
+    for (int v = 0; v < wave; ++v) {
+        const bool fresh = wnew[v];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) carry[j] = (fresh ? 0.0 : carry[j]) + wsum[v][l][j];
+    }
+    double enters[VEC];  // of the stretch that enters this group
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        if (!begun) sum[j] += carry[j];
+        enters[j] = __shfl_up(sum[j], kFewLanes, 64);
+        if ((tid & 63) < kFewLanes) enters[j] = carry[j];
+    }
+    if (p0 >= p1) return;
+    if (!whole) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) head[j] += first == before ? enters[j] : 0.0;
+        store(first, head);
+    }
+    if (cur != after) store(cur, sum);
 }
 
 // Block (run, slice): if a stretch begins in this run and goes on after it, its
@@ -490,18 +633,22 @@ __global__ void __launch_bounds__(kJoin) k_embed_join(SumArgs a, T* __restrict__
     const int64_t rows = (int64_t)a.R * a.RL;
     for (int64_t run = blockIdx.x; run + 1 < a.runs; run += gridDim.x) {  // conditions are the same for the whole block
         const int64_t p0 = run * rows, p1 = p0 + rows;
-        const int32_t k = a.key[p1 - 1];
-        if (k >= a.V || a.key[p1] != k) continue;
-        if (a.key[p0] == k && p0 > 0 && a.key[p0 - 1] == k) continue;
         // the last run that begins with k: every round counts the probes that do
-        // among kJoin spread over what is left
-        int64_t last = run + 1, n = a.runs - last;
+        // among kJoin spread over what is left (the first round's loads go with
+        // the others, ahead of the conditions)
+        int64_t last = run + 1, n = a.runs - last, step = (n + kJoin - 1) / kJoin, at = threadIdx.x * step;
+        int32_t probe = a.key[(last + (at < n ? at : 0)) * rows];
+        const int32_t k = a.key[p1 - 1], next = a.key[p1], head = a.key[p0], before = a.key[p0 > 0 ? p0 - 1 : 0];
+        if (k >= a.V || next != k) continue;
+        if (head == k && p0 > 0 && before == k) continue;
         while (n > 1) {
-            const int64_t step = (n + kJoin - 1) / kJoin, at = threadIdx.x * step;
-            const int c = __syncthreads_count(at < n && a.key[(last + at) * rows] == k);
+            const int c = __syncthreads_count(at < n && probe == k);
             const int64_t left = n - (c - 1) * step;
             last += (c - 1) * step;
             n = step < left ? step : left;
+            step = (n + kJoin - 1) / kJoin;
+            at = threadIdx.x * step;
+            if (n > 1) probe = a.key[(last + (at < n ? at : 0)) * rows];
         }
         const int32_t rl = (int32_t)threadIdx.x / a.L, RL = kJoin / a.L;
         const int64_t q = (int64_t)blockIdx.y * a.L + ((int32_t)threadIdx.x - rl * a.L);
@@ -520,14 +667,19 @@ __global__ void __launch_bounds__(kJoin) k_embed_join(SumArgs a, T* __restrict__
 #pragma unroll
         for (int j = 0; j < VEC; ++j) s[j * kJoin + threadIdx.x] = acc[j];
         __syncthreads();
+        for (int32_t m = RL; m > 1;) {  // by halves
+            const int32_t up = (m + 1) / 2;
+            if (ok && rl < m / 2) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[j * kJoin + threadIdx.x] += s[j * kJoin + up * a.L + threadIdx.x];
+            }
+            m = up;
+            __syncthreads();
+        }
         if (ok && rl == 0) {
             float v[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                double t = 0.0;
-                for (int32_t r = 0; r < RL; ++r) t += s[j * kJoin + r * a.L + (int32_t)threadIdx.x];
-                v[j] = (float)(t * (double)a.scale);
-            }
+            for (int j = 0; j < VEC; ++j) v[j] = (float)(s[j * kJoin + threadIdx.x] * (double)a.scale);
             store_vec<T, VEC>(gtab + (int64_t)k * a.C + q * VEC, v);
         }
         __syncthreads();
@@ -547,7 +699,7 @@ EmbedLayout embed_layout(const EmbedShape& e, bool wide)
     w.wide = wide;
     const int64_t cv = wide ? e.C / (16 / dtype_size(e.dtype)) : e.C;
     w.L = cv < kThreads ? cv : kThreads;
-    w.RL = kThreads / w.L;
+    w.RL = kThreads / w.L < kGroups ? kThreads / w.L : kGroups;
     // Positions of a group: enough groups to fill the chip (about 2^18 lanes), and 16
     // at least where they are many, so that hot ids leave fewer partial sums (50000
     // x 128: sum and join 14.2 us, with 8 positions 15.8 us)
@@ -582,6 +734,31 @@ hipError_t embed_fwd(const EmbedShape& e, const int32_t* ids, const void* table,
     return hipGetLastError();
 }
 
+int bits_of(int64_t v)  // of 0 .. v
+{
+    int b = 0;
+    while ((v >> b) != 0) ++b;
+    return b;
+}
+
+template <class T, int VEC>
+hipError_t embed_few(const EmbedShape& e, const int32_t* ids, const void* grad, void* gtab, hipStream_t s)
+{
+    FewArgs a{};
+    a.N = (int32_t)e.N;
+    a.V = (int32_t)e.V;
+    a.key_bits = bits_of(e.V);
+    a.row_bits = bits_of(e.N - 1);
+    a.C = e.C;
+    a.CV = e.C / VEC;
+    a.ld = e.ld;
+    a.scale = e.scale;
+    a.ids = ids;
+    hipLaunchKernelGGL((k_embed_few<T, VEC>), dim3((unsigned)cdiv64(a.CV, kFewLanes)), dim3(kOneThreads), 0, s, a,
+                       (const T*)grad, (T*)gtab);
+    return hipGetLastError();
+}
+
 template <class T, int VEC>
 hipError_t embed_sum(const EmbedShape& e, const EmbedLayout& w, const int32_t* key, const int32_t* val,
                      const void* grad, void* gtab, double* part, hipStream_t s)
@@ -601,7 +778,8 @@ hipError_t embed_sum(const EmbedShape& e, const EmbedLayout& w, const int32_t* k
     a.val = val;
     a.part = part;
     const unsigned slices = (unsigned)cdiv64(a.CV, a.L);
-    hipLaunchKernelGGL((k_embed_sum<T, VEC>), dim3(grid_of(w.runs), slices), dim3(kThreads), 0, s, a, (const T*)grad,
+    const unsigned threads = (unsigned)(cdiv64(w.L * w.RL, 64) * 64);
+    hipLaunchKernelGGL((k_embed_sum<T, VEC>), dim3(grid_of(w.runs), slices), dim3(threads), 0, s, a, (const T*)grad,
                        (T*)gtab);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || w.runs < 2) return err;
@@ -621,13 +799,6 @@ Clear clear_of(const EmbedShape& e, void* gtab, int threads)
     const int64_t blocks = cdiv64(c.n16 > c.tail ? c.n16 : c.tail, (int64_t)threads * 4);
     c.blocks = (uint32_t)(blocks < 4096 ? blocks : 4096);
     return c;
-}
-
-int bits_of(int64_t v)  // of 0 .. v
-{
-    int b = 0;
-    while ((v >> b) != 0) ++b;
-    return b;
 }
 
 }  // namespace
@@ -661,6 +832,11 @@ hipError_t launch_embed_bwd(const EmbedShape& e, const int32_t* ids, const void*
     }
     const int64_t es = dtype_size(e.dtype);
     const bool wide = e.C * es % 16 == 0 && aligned_rows(grad, e.ld, es) && aligned_rows(gtab, e.C, es);
+    if (e.N <= kFewKeys && e.V <= kFewRows && e.V * e.C <= kFewTable) {
+        if (e.dtype == kF32)
+            return wide ? embed_few<float, kWide<float>>(e, ids, grad, gtab, s) : embed_few<float, 1>(e, ids, grad, gtab, s);
+        return wide ? embed_few<bf16_t, kWide<bf16_t>>(e, ids, grad, gtab, s) : embed_few<bf16_t, 1>(e, ids, grad, gtab, s);
+    }
     const EmbedLayout w = embed_layout(e, wide);
     char* base = (char*)ws;
     const int32_t *key, *val;

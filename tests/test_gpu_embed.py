@@ -56,7 +56,12 @@ CASES = [("uniform", 1, 1, 1, 1), ("uniform", 0, 7, 8, 1), ("uniform", 2, 300, 3
          ("few", 2000, 89, 128, 9), ("mixed", 2047, 89, 130, 1), ("mixed", 2049, 255, 64, 1),
          ("uniform", 4097, 256, 40, 1), ("one", 5000, 257, 17, 3), ("sorted", 3001, 65536, 33, 1),
          ("mixed", 16385, 70001, 96, 1), ("padding", 999, 50, 24, 1), ("uniform", 33, 2**24 + 3, 1, 1),
-         ("few", 300, 11, 2056, 1), ("mixed", 70, 9, 4100, 2), ("one", 100003, 3, 8, 1)]
+         ("few", 300, 11, 2056, 1), ("mixed", 70, 9, 4100, 2), ("one", 100003, 3, 8, 1),
+         # either side of what the gradient does in one launch; narrow rows, many groups to a block
+         ("mixed", 4096, 4096, 36, 1), ("mixed", 4097, 4096, 36, 1), ("uniform", 4096, 4097, 20, 1),
+         ("few", 3999, 4097, 128, 4), ("sorted", 4095, 700, 8, 1), ("one", 4096, 511, 7, 1), ("sorted", 257, 512, 16, 1),
+         ("few", 30000, 70000, 8, 1), ("mixed", 20000, 300, 4, 1), ("sorted", 9000, 5000, 3, 2),
+         ("sorted", 26001, 900, 12, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
