@@ -33,7 +33,9 @@ inline unsigned grid_of(int64_t n) { return (unsigned)(n < kMaxBlocks ? n : kMax
 // ---- forward ---------------------------------------------------------------------
 // L lanes per row (CV = C / VEC accesses per row, at most 256 lanes), the rest
 // of the block on further rows; kRows rows per lane so that the gathers of
-// several rows are in flight behind their ids.
+// several rows are in flight behind their ids.  16385 rows x 1024 bf16 of 65536: 9.8 us
+// (6.9 TB/s read and written); 10^6 rows x 128 fp32 of a table that L2 holds: 88 us
+// (5.8 TB/s written, what a plain fill reaches is 6.8); 2000 x 128: 3.5 us, a launch.
 constexpr int kRows = 4;
 
 template <class T, int VEC>
@@ -148,7 +150,10 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* s, int32_t* al
 }
 
 // -- up to kOneKeys keys: one block, key and row in one word, all passes in LDS, while
-// the launch's other blocks clear the table
+// the launch's other blocks clear the table.  One compute unit's LDS accesses bound it:
+// 16385 ids of 65536, two passes, 26.6 us, and 29 us beside a table of 134 MB (whose
+// clearing takes 20.7 us alone, 6.5 TB/s); with every other key ranked by votes on its
+// bits instead 28.3 us, not worth a second way.
 constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / 64, kOnePer = 24;
 constexpr int64_t kOneKeys = (int64_t)kOneThreads * kOnePer;
 
@@ -246,7 +251,8 @@ __global__ void __launch_bounds__(kOneThreads) k_sort_one(OneArgs a)
 
 // -- more keys: tiles of kTile keys, a block each; per pass the tiles' counts, their
 // sums over earlier tiles (by each scattering block where the tiles are few, else by a
-// launch of their own), and the scatter
+// launch of their own), and the scatter.  Latency and launches: 50000 ids, one pass, 3.9 +
+// 6.9 us; 10^6 ids 10.1 + 5.2 + 9.1 us.
 constexpr int kWaves = kThreads / 64, kPer = 4, kTile = kThreads * kPer, kFewTiles = 64;
 
 struct SortArgs {
@@ -378,6 +384,8 @@ __global__ void __launch_bounds__(kThreads) k_sort_scatter(SortArgs a)
 }
 
 // ---- sums over the sorted rows --------------------------------------------------------
+// Bound by the gathered rows: 10^6 rows x 128 fp32 100 us (5.1 TB/s), 50000 x 128 7.5 us
+// (3.4 TB/s), 16385 x 1024 bf16 13.7 us (2.4 TB/s, and the rows of some thousand ids written).
 // A block's run is RL R consecutive sorted positions, R for each group of L lanes.  A
 // group writes a stretch of equal ids that lies inside its positions to its table row;
 // the first and the last stretch, which may reach over the ends, meet those of the
@@ -623,7 +631,8 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
 }
 
 // Block (run, slice): if a stretch begins in this run and goes on after it, its
-// partial sums from here to its end.
+// partial sums from here to its end.  Latency: keys, one or two rounds of the search,
+// partial sums, in turn (391 runs 6.8 us, 7815 runs 18.6 us, x 128 fp32).
 constexpr int kJoin = 256;
 
 template <class T, int VEC>

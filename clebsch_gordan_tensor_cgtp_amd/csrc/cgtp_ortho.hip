@@ -27,10 +27,9 @@
 // Layout.  An operand of `rows` rows is cut along k into blocks of 32: a row's
 // piece of a block is 32 h, then their 32 l, one 128-byte line, and a block's
 // lines lie one after the other, so that what a tile loads for one block of k
-// is one run of memory (rows K apart would meet in a few cache channels: 62 us
-// where this takes XX us at 2048).  All products are "rows times rows": D[i][j] =
-// sum_k P[i][k] Q[j][k] with k contiguous in both; A and B are symmetric, and X
-// is kept as it is and transposed.
+// is one run of memory (plain rows measured the same).  All products are "rows times
+// rows": D[i][j] = sum_k P[i][k] Q[j][k] with k contiguous in both; A and B are
+// symmetric, and X is kept as it is and transposed.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -151,6 +150,7 @@ __device__ __forceinline__ double start_bound(double r) { return r > 0.5 ? 1.0 :
 constexpr int kNormBlocks = 256;    // partial sums per matrix, at most
 constexpr int kNormElems = 8192;    // elements per partial sum, about
 
+// 2048 x 2048 fp32 5.6 us (3 TB/s), 4096 x 4096 22 us: one pass over G
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_ortho_norm(int64_t size, int32_t per, bool wide,
                                                          const T* __restrict__ G, double* __restrict__ part)
@@ -194,7 +194,8 @@ __device__ __forceinline__ double norm_of(const double* __restrict__ part, int64
 }
 
 // X and X^T of one 64 x 64 tile, split, zero outside the matrix; the first tile
-// of a matrix leaves its steps' factors
+// of a matrix leaves its steps' factors.  4096 x 4096 fp32 35 us: 67 MB read, 134 MB
+// written (5.7 TB/s); 2048 x 2048 12.7 us
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_ortho_first(OrthoDims d, OrthoPoly poly, UnitTable table,
                                                           int32_t per, const double* __restrict__ part,
@@ -334,7 +335,14 @@ __device__ __forceinline__ void wait_barrier()
 // One TILE x TILE tile of D = P Q^T, each wave WX x WY tiles of 32 x 32, 32 k at
 // a time through a ring of kStages LDS buffers that loads fill directly, kStages
 // blocks of k ahead.  Two waves per SIMD (TILE 128) keep the matrix cores busy
-// across the barriers of a block of k.
+// across the barriers of a block of k.  Bound by the matrix cores: a full product of
+// 4096 x 4096 x 4096 (X') takes 404 us, 1.02 PFLOP/s of fp16 products where a library's
+// large fp16 product reaches 1.15; A and B, by their upper triangle, 255 and 260 us.
+// At 2048 X' fills the 256 compute units once (57 us, 0.90 PFLOP/s), and the 136 tiles
+// of A and B leave half of them idle (45 us): equal shares of all 136 tiles' blocks of k
+// for 256 blocks, joined by a tile's last to arrive, were slower all the same (five steps
+// 733 against 698 us, at 4096 4.72 against 4.32 ms).  Two stages instead of four: 477
+// against 382 us a product at 4096.
 template <int TILE>
 struct TileShape;
 template <>
@@ -593,6 +601,7 @@ __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
 // the next X of a tile needs B and that tile alone, and the operand element m of a
 // lane, X[4 m + lane / 16][lane % 16], is the element that its D element m replaces.
 // Only the sum of A crosses waves.  No units: fp64 and fp32 hold every magnitude.
+// Bound by the chain of dependent products and barriers: 200 of 12 x 50, five steps, 16 us.
 constexpr int kTinySide = 16, kTinyWaves = 8, kTinyElems = 32768;
 typedef double d4 __attribute__((ext_vector_type(4)));
 
@@ -701,7 +710,9 @@ __global__ void __launch_bounds__(64 * kTinyWaves) k_ortho_tiny(TinyArgs a)
 // 64 KB.  A step is 3 x 2 SP^2 TP flops and five barriers instead of three launches.
 // The next X is formed transposed, D[t][s] = sum_k X[k][t] B[s][k], so that a
 // lane ends with four consecutive t of a row of X and writes them back at once;
-// X^T is read from X's rows by transposing LDS reads.
+// X^T is read from X's rows by transposing LDS reads.  Bound by one compute unit's matrix
+// cores and its LDS: 15 of 128 x 128 fp32, five steps, 42.8 us (8.5 us a step, of which the
+// products take 3.9 us at the cores' peak); 100 of 64 x 64 15.4 us.
 template <int SP, int TP>
 struct Small {
     static constexpr int WC = SP / 32, NW = SP == 128 ? 8 : 4, WR = NW / WC;  // waves along the columns and rows
@@ -1043,8 +1054,10 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
 }
 
 // ---- a short side of at most 128, the other longer -------------------------------------------
-// A matrix's chunks of TP columns are dealt to `blocks` blocks.  One launch per
-// step: every block adds the partial A = X X^T of all blocks, forms B (the same
+// A matrix's chunks of TP columns are dealt to `blocks` blocks.  A launch per step, and
+// one that adds the partial A where they are many (15 of 128 x 1024 bf16: 15.4 and 4.2 us,
+// bound by launches and by each block's own three products; the first X with its A takes
+// 11.5 us): every block adds the partial A = X X^T of all blocks, forms B (the same
 // work in each, in parallel), takes its chunks of X, held in memory as they lie
 // in LDS, through X <- a X + B X, and leaves its partial A of the new X.
 struct WideArgs {
@@ -1217,9 +1230,11 @@ __global__ void __launch_bounds__(kThreads) k_ortho_add(int64_t size, int32_t n,
 
 // ---- host ----------------------------------------------------------------------------------
 
-// Wide tiles read less of LDS per product, small ones fill the chip: wide ones
-// where there are at least kFill of them.
-constexpr int64_t kFill = 100;
+// Wide tiles read less of LDS per product, small ones fill the chip: wide ones where
+// they are on more than half of the 256 compute units (five steps, wide from 100 and
+// from 129 tiles: 1408 x 1408, 121 and 66 tiles, 329 and 306 us; 1792 x 1792, 196 and 105,
+// 558 and 510; 2048 x 2048, 256 and 136, 687 us, and 726 with the 136 as small tiles).
+constexpr int64_t kFill = 129;
 
 // Forms: a whole matrix per block, chunks of columns per block, tiles, or a matrix
 // of few rows per block in fp64.
