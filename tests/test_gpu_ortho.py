@@ -48,7 +48,8 @@ CASES = [(1, 1, 1, "noise"), (3, 1, 70, "noise"), (2, 70, 1, "noise"), (15, 128,
          (34, 64, 64, "noise"), (2, 127, 129, "spectrum"), (2, 130, 126, "noise"), (1, 128, 1024, "spectrum"),
          (1, 257, 300, "spectrum"), (2, 300, 150, "noise"), (1, 8, 3000, "noise"), (1, 3000, 8, "noise"),
          (6, 10, 25, "spectrum"), (3, 16, 16, "noise"), (2, 16, 2048, "spectrum"), (2, 3900, 8, "noise"),
-         (1, 16, 2049, "noise"), (2, 17, 40, "noise"), (1, 520, 520, "spectrum"), (2, 96, 96, "rank one"), (1, 1100, 1030, "noise"), (1, 1030, 2100, "spectrum")]
+         (1, 16, 2049, "noise"), (2, 17, 40, "noise"), (1, 520, 520, "spectrum"), (2, 96, 96, "rank one"), (1, 1100, 1030, "noise"), (1, 1030, 2100, "spectrum"),
+         (3, 1100, 1030, "spectrum")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
