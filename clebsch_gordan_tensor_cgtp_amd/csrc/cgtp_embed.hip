@@ -108,18 +108,19 @@ __device__ __forceinline__ void wave_fence()
 // bits in mask[digit] (zero before and after): three LDS accesses, where comparing
 // bit by bit takes seven vector instructions for each bit (a scatter of 50000 ids
 // 7.0 us, bit by bit 7.8 us).
-__device__ __forceinline__ int32_t rank_in_wave(int32_t d, bool in, unsigned long long* mask, int32_t* cnt)
+__device__ __forceinline__ int32_t rank_in_wave(int32_t d, bool in, uint32_t (*mask)[2], int32_t* cnt)
 {
     const int lane = threadIdx.x & 63;
-    if (in) __hip_atomic_fetch_or(&mask[d], 1ull << lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+    if (in)
+        __hip_atomic_fetch_or(&mask[d][lane >> 5], 1u << (lane & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     wave_fence();
-    const unsigned long long same = in ? mask[d] : 0ull;
+    const unsigned long long same = in ? (unsigned long long)mask[d][1] << 32 | mask[d][0] : 0ull;
     const unsigned long long below = same & ((1ull << lane) - 1);
     const int32_t r = in ? cnt[d] + (int32_t)__popcll(below) : 0;
     wave_fence();
     if (in && below == 0) {
         cnt[d] += (int32_t)__popcll(same);
-        mask[d] = 0ull;
+        mask[d][0] = mask[d][1] = 0u;
     }
     wave_fence();
     return r;
@@ -151,9 +152,9 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* s, int32_t* al
 
 // -- up to kOneKeys keys: one block, key and row in one word, all passes in LDS, while
 // the launch's other blocks clear the table.  One compute unit's LDS accesses bound it:
-// 16385 ids of 65536, two passes, 26.6 us, and 29 us beside a table of 134 MB (whose
-// clearing takes 20.7 us alone, 6.5 TB/s); with every other key ranked by votes on its
-// bits instead 28.3 us, not worth a second way.
+// 16385 ids of 65536, two passes, beside a table of 134 MB 28 us (the clearing alone takes
+// 20.7 us, 6.5 TB/s).  Ranking every other key by votes on its bits gained 0.7 us, not
+// worth a second way; 64-bit masks instead of two halves cost as much.
 constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / 64, kOnePer = 24;
 constexpr int64_t kOneKeys = (int64_t)kOneThreads * kOnePer;
 
@@ -191,11 +192,11 @@ __device__ __forceinline__ void sort_one(const int32_t* __restrict__ ids, int32_
     }
     for (int shift = 0; shift < key_bits; shift += kBits) {
         const int bits = key_bits - shift < kBits ? key_bits - shift : kBits;
-        unsigned long long* mask = reinterpret_cast<unsigned long long*>(word) + wave * kDigits;
+        uint32_t(*mask)[2] = reinterpret_cast<uint32_t(*)[2]>(word) + wave * kDigits;
         if (shift > 0) __syncthreads();  // the words of the pass before are read
         for (int d = lane; d < kDigits; d += 64) {
             cnt[wave][d] = 0;
-            mask[d] = 0ull;
+            mask[d][0] = mask[d][1] = 0u;
         }
         wave_fence();
         int32_t rank[PER];
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) k_sort_scan(SortArgs a)
 __global__ void __launch_bounds__(kThreads) k_sort_scatter(SortArgs a)
 {
     __shared__ int32_t cnt[kWaves][kDigits];  // keys of each digit met by each wave so far
-    __shared__ unsigned long long mask[kWaves][kDigits];
+    __shared__ __attribute__((aligned(8))) uint32_t mask[kWaves][kDigits][2];
     __shared__ int32_t s[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t p0 = (int64_t)blockIdx.x * kTile + (int64_t)wave * (kTile / kWaves) + lane;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) k_sort_scatter(SortArgs a)
     }
     for (int d = lane; d < kDigits; d += 64) {
         cnt[wave][d] = 0;
-        mask[wave][d] = 0ull;
+        mask[wave][d][0] = mask[wave][d][1] = 0u;
     }
     wave_fence();
 #pragma unroll
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
 
 // Block (run, slice): if a stretch begins in this run and goes on after it, its
 // partial sums from here to its end.  Latency: keys, one or two rounds of the search,
-// partial sums, in turn (391 runs 6.8 us, 7815 runs 18.6 us, x 128 fp32).
+// partial sums, in turn (391 runs 6.5 us, 7815 runs 18.6 us, x 128 fp32).
 constexpr int kJoin = 256;
 
 template <class T, int VEC>
@@ -642,22 +643,23 @@ __global__ void __launch_bounds__(kJoin) k_embed_join(SumArgs a, T* __restrict__
     const int64_t rows = (int64_t)a.R * a.RL;
     for (int64_t run = blockIdx.x; run + 1 < a.runs; run += gridDim.x) {  // conditions are the same for the whole block
         const int64_t p0 = run * rows, p1 = p0 + rows;
-        // the last run that begins with k: every round counts the probes that do
-        // among kJoin spread over what is left (the first round's loads go with
-        // the others, ahead of the conditions)
-        int64_t last = run + 1, n = a.runs - last, step = (n + kJoin - 1) / kJoin, at = threadIdx.x * step;
-        int32_t probe = a.key[(last + (at < n ? at : 0)) * rows];
+        // the last run that begins with k: among the kJoin runs that follow (these
+        // loads go with the others, ahead of the conditions), and where that is not
+        // the end, by rounds that count probes spread over what is left
+        int64_t last = run + 1, n = a.runs - last;
+        const int32_t probe = a.key[(last + ((int64_t)threadIdx.x < n ? (int64_t)threadIdx.x : 0)) * rows];
         const int32_t k = a.key[p1 - 1], next = a.key[p1], head = a.key[p0], before = a.key[p0 > 0 ? p0 - 1 : 0];
         if (k >= a.V || next != k) continue;
         if (head == k && p0 > 0 && before == k) continue;
+        const int begin = __syncthreads_count((int64_t)threadIdx.x < n && probe == k);
+        last += begin - 1;
+        n = begin == kJoin ? n - (kJoin - 1) : 1;
         while (n > 1) {
-            const int c = __syncthreads_count(at < n && probe == k);
+            const int64_t step = (n + kJoin - 1) / kJoin, at = threadIdx.x * step;
+            const int c = __syncthreads_count(at < n && a.key[(last + at) * rows] == k);
             const int64_t left = n - (c - 1) * step;
             last += (c - 1) * step;
             n = step < left ? step : left;
-            step = (n + kJoin - 1) / kJoin;
-            at = threadIdx.x * step;
-            if (n > 1) probe = a.key[(last + (at < n ? at : 0)) * rows];
         }
         const int32_t rl = (int32_t)threadIdx.x / a.L, RL = kJoin / a.L;
         const int64_t q = (int64_t)blockIdx.y * a.L + ((int32_t)threadIdx.x - rl * a.L);

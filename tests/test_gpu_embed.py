@@ -61,7 +61,9 @@ CASES = [("uniform", 1, 1, 1, 1), ("uniform", 0, 7, 8, 1), ("uniform", 2, 300, 3
          ("mixed", 4096, 4096, 36, 1), ("mixed", 4097, 4096, 36, 1), ("uniform", 4096, 4097, 20, 1),
          ("few", 3999, 4097, 128, 4), ("sorted", 4095, 700, 8, 1), ("one", 4096, 511, 7, 1), ("sorted", 257, 512, 16, 1),
          ("few", 30000, 70000, 8, 1), ("mixed", 20000, 300, 4, 1), ("sorted", 9000, 5000, 3, 2),
-         ("sorted", 26001, 900, 12, 1)]
+         ("sorted", 26001, 900, 12, 1),
+         # ids that span some hundred runs
+         ("one", 6000, 5000, 1024, 1), ("few", 9000, 7, 1024, 1), ("sorted", 5000, 3, 1032, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
