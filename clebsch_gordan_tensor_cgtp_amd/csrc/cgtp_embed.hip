@@ -14,6 +14,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cgtp_internal.h"
 #include "cgtp_train_internal.h"
 #include "cgtp_vec.h"
@@ -510,11 +512,13 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T* __re
 // ---- few ids and a small table: the whole gradient in one launch --------------------------
 // A small call is its launches: three of them take 13.7 us for 2000 x 128 of 10 ids, this
 // 8.7 us (4096 x 128 of 4096: 20.6 and 18.3 us; a table of 4096 x 1024 no longer gains: 23.4
-// and 25.5 us).  Every block sorts all ids for itself and sums kFewLanes accesses of each row.  Its groups
-// of kFewLanes lanes take equal shares of the sorted positions; a group stores the stretches
+// and 25.5 us).  Every block sorts all ids for itself and sums LANES accesses of each row: 4,
+// or 16 where fours would be more blocks than compute units (409 x 1778 fp32 12.8 -> 7.3 us;
+// 4000 x 33, few blocks either way, 11.5 us with 4 and 16.5 with 16).  Its groups of LANES
+// lanes take equal shares of the sorted positions; a group stores the stretches
 // that lie inside its share, and a segmented sum over the groups (by shuffles in a wave,
 // through LDS across waves) finishes those that reach over shares.
-constexpr int kFewPer = 4, kFewLanes = 4, kFewGroups = kOneThreads / kFewLanes;
+constexpr int kFewPer = 4;
 constexpr int64_t kFewKeys = (int64_t)kOneThreads * kFewPer, kFewRows = 4096, kFewTable = 1 << 21;
 
 struct FewArgs {
@@ -524,21 +528,22 @@ struct FewArgs {
     const int32_t* ids;
 };
 
-template <class T, int VEC>
+template <class T, int VEC, int LANES>
 __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* __restrict__ grad, T* __restrict__ gtab)
 {
+    constexpr int kShares = kOneThreads / LANES;  // groups
     __shared__ OneLds<kFewPer> x;
-    __shared__ double wsum[kOneWaves][kFewLanes][VEC];  // of a wave's last stretch
+    __shared__ double wsum[kOneWaves][LANES][VEC];  // of a wave's last stretch
     __shared__ bool wnew[kOneWaves];                    // it begins in that wave
-    const int tid = threadIdx.x, wave = tid >> 6, l = tid % kFewLanes, g = tid / kFewLanes;
-    const int64_t q = (int64_t)blockIdx.x * kFewLanes + l;
+    const int tid = threadIdx.x, wave = tid >> 6, l = tid % LANES, g = tid / LANES;
+    const int64_t q = (int64_t)blockIdx.x * LANES + l;
     const bool on = q < a.CV;
     T* const col = gtab + q * VEC;
     if (on) {  // the sort's barriers put these stores before those of the sums
         float zero[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) zero[j] = 0.0f;
-        for (int64_t v = g; v < a.V; v += kFewGroups) store_vec<T, VEC>(col + v * a.C, zero);
+        for (int64_t v = g; v < a.V; v += kShares) store_vec<T, VEC>(col + v * a.C, zero);
     }
     uint32_t w[kFewPer];
     sort_one<kFewPer>(a.ids, a.N, a.V, a.key_bits, a.row_bits, x, w);
@@ -551,7 +556,7 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
         store_vec<T, VEC>(col + (int64_t)id * a.C, v);
     };
     auto key = [&](int32_t p) { return (int32_t)(x.word[p] >> a.row_bits); };
-    const int32_t R = (a.N + kFewGroups - 1) / kFewGroups;
+    const int32_t R = (a.N + kShares - 1) / kShares;
     const int32_t p0 = g * R < a.N ? g * R : a.N, p1 = p0 + R < a.N ? p0 + R : a.N;
     const int32_t before = p0 > 0 ? key(p0 - 1) : -1, after = p1 < a.N ? key(p1) : -1;
     const T* const from = grad + (on ? q : 0) * VEC;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
     // sums of the last stretches from where they begin (`begun`), or from the wave's first group
     bool begun = p0 >= p1 || !whole || first != before;
 #pragma unroll
-    for (int d = kFewLanes; d < 64; d *= 2) {
+    for (int d = LANES; d < 64; d *= 2) {
         const int b = __shfl_up((int)begun, d, 64);
         double t[VEC];
 #pragma unroll
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
             begun = b != 0;
         }
     }
-    if ((tid & 63) >= 64 - kFewLanes) {
+    if ((tid & 63) >= 64 - LANES) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) wsum[wave][l][j] = sum[j];
         if (l == 0) wnew[wave] = begun;
@@ -619,8 +624,8 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         if (!begun) sum[j] += carry[j];
-        enters[j] = __shfl_up(sum[j], kFewLanes, 64);
-        if ((tid & 63) < kFewLanes) enters[j] = carry[j];
+        enters[j] = __shfl_up(sum[j], LANES, 64);
+        if ((tid & 63) < LANES) enters[j] = carry[j];
     }
     if (p0 >= p1) return;
     if (!whole) {
@@ -765,8 +770,14 @@ hipError_t embed_few(const EmbedShape& e, const int32_t* ids, const void* grad, 
     a.ld = e.ld;
     a.scale = e.scale;
     a.ids = ids;
-    hipLaunchKernelGGL((k_embed_few<T, VEC>), dim3((unsigned)cdiv64(a.CV, kFewLanes)), dim3(kOneThreads), 0, s, a,
-                       (const T*)grad, (T*)gtab);
+    auto launch = [&](auto lanes) {
+        constexpr int kLanes = decltype(lanes)::value;
+        hipLaunchKernelGGL((k_embed_few<T, VEC, kLanes>), dim3((unsigned)cdiv64(a.CV, kLanes)), dim3(kOneThreads), 0, s,
+                           a, (const T*)grad, (T*)gtab);
+    };
+    // blocks of few accesses while there are no more of them than compute units (256)
+    if (a.CV <= 4 * 256) launch(std::integral_constant<int, 4>{});
+    else launch(std::integral_constant<int, 16>{});
     return hipGetLastError();
 }
 

@@ -63,7 +63,9 @@ CASES = [("uniform", 1, 1, 1, 1), ("uniform", 0, 7, 8, 1), ("uniform", 2, 300, 3
          ("few", 30000, 70000, 8, 1), ("mixed", 20000, 300, 4, 1), ("sorted", 9000, 5000, 3, 2),
          ("sorted", 26001, 900, 12, 1),
          # ids that span some hundred runs
-         ("one", 6000, 5000, 1024, 1), ("few", 9000, 7, 1024, 1), ("sorted", 5000, 3, 1032, 1)]
+         ("one", 6000, 5000, 1024, 1), ("few", 9000, 7, 1024, 1), ("sorted", 5000, 3, 1032, 1),
+         # few ids, wide rows of either access
+         ("few", 409, 138, 1778, 1), ("mixed", 3000, 60, 4104, 2), ("mixed", 1500, 200, 1027, 1), ("sorted", 4096, 40, 8200, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
