@@ -20,9 +20,9 @@
 // reach.  Below 17 rows sums are too short to hide the missing bit (up to twice the
 // fp32 error), and there is little to multiply: those matrices run in fp64.
 //
-// For bf16 results A = X X^T takes hu hv alone: its error (4e-4 to 8e-4 of the result)
-// stays well below the 1.65e-3 of rounding the result, where single products
-// elsewhere would not (up to 3e-3 in all).
+// bf16 matrices take the same three products.  A step carries the error of the steps
+// before on, and steeper coefficients magnify it: with hu hv alone in A = X X^T the
+// result was off by 4e-4 to 8e-4 after five steps of the usual quintic, 6e-3 after twenty.
 //
 // Layout.  An operand of `rows` rows is cut along k into blocks of 32: a row's
 // piece of a block is 32 h, then their 32 l, one 128-byte line, and a block's
@@ -356,22 +356,16 @@ struct TileShape<64> {
 template <int TILE>
 constexpr int kProdThreads = 64 * (TILE / 32 / TileShape<TILE>::WX) * (TILE / 32 / TileShape<TILE>::WY);
 
-// products of A = X X^T for results of type T (the header comment says why)
-template <class T>
-constexpr int kGramProducts = sizeof(T) == 2 ? 1 : 3;
-
 template <int TILE, int KIND, class T>
 __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
 {
     constexpr int WX = TileShape<TILE>::WX, WY = TileShape<TILE>::WY, kThr = kProdThreads<TILE>;
-    constexpr bool kHigh = KIND == kGram && kGramProducts<T> == 1;  // the high halves alone
     constexpr int kRowHalves = 64, kStages = 4;
-    constexpr int kLine = kHigh ? 32 : 64, kPer = kLine / 8;  // halves and 16-byte pieces of a row in LDS
-    constexpr int kPieces = TILE * kPer / kThr;               // pieces per thread, operand and stage
-    constexpr int kLd = TILE + 4;                             // row stride of the result in LDS
-    constexpr int kRing = kStages * 2 * TILE * kLine * 2, kResult = TILE * kLd * 4;
+    constexpr int kPieces = TILE * 8 / kThr;  // 16-byte pieces per thread, operand and stage
+    constexpr int kLd = TILE + 4;             // row stride of the result in LDS
+    constexpr int kRing = kStages * 2 * TILE * kRowHalves * 2, kResult = TILE * kLd * 4;
     __shared__ __attribute__((aligned(16))) char mem[kRing > kResult ? kRing : kResult];
-    auto lds = reinterpret_cast<_Float16(*)[2][TILE * kLine]>(mem);
+    auto lds = reinterpret_cast<_Float16(*)[2][TILE * kRowHalves]>(mem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t tiles = a.tj == 0 ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
     const int64_t x = xcd_order(blockIdx.x, gridDim.x), b = x / tiles;
@@ -392,22 +386,20 @@ __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
 
     // Thread p of a stage fills piece p % 8 of row p / 8, with the row's piece
     // (p % 8) ^ (row / 2 % 8): a wave's LDS destination is one run of 1 KB, and
-    // the reads of sixteen rows at one k spread over all 64 banks.  (High halves
-    // alone: four pieces a row, ^ (row / 4 % 4).)
-    auto swizzle = [](int row) { return kHigh ? (row >> 2) & 3 : (row >> 1) & 7; };
-    const uint32_t mine = (uint32_t)((tid / kPer) * 128 + (((tid % kPer) ^ swizzle(tid / kPer)) * 16));
+    // the reads of sixteen rows at one k spread over all 64 banks.
+    const uint32_t mine = (uint32_t)((tid / 8) * 128 + (((tid % 8) ^ ((tid / 16) & 7)) * 16));
     auto fill = [&](int64_t kb) {
-        _Float16(*to)[TILE * kLine] = lds[kb % kStages];
+        _Float16(*to)[TILE * kRowHalves] = lds[kb % kStages];
         const char* pp = (const char*)(P + kb * rowsP * kRowHalves);
         const char* qq = (const char*)(Q + kb * rowsQ * kRowHalves);
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
             const int at = (q * kThr + wave * 64) * 8;
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(pp + (uint32_t)(mine + q * (kThr / kPer) * 128)),
+                (const __attribute__((address_space(1))) void*)(pp + (uint32_t)(mine + q * kThr * 16)),
                 (__attribute__((address_space(3))) void*)&to[0][at], 16, 0, 0);
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(qq + (uint32_t)(mine + q * (kThr / kPer) * 128)),
+                (const __attribute__((address_space(1))) void*)(qq + (uint32_t)(mine + q * kThr * 16)),
                 (__attribute__((address_space(3))) void*)&to[1][at], 16, 0, 0);
         }
     };
@@ -419,21 +411,19 @@ __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
         h8 ph[2][WX], pl[2][WX], qh[2][WY], ql[2][WY];
     };
     auto read = [&](Frag& f, int64_t kb) {
-        const _Float16(*from)[TILE * kLine] = lds[kb % kStages];
+        const _Float16(*from)[TILE * kRowHalves] = lds[kb % kStages];
         auto at = [&](int op, int row, int piece) {
-            return *reinterpret_cast<const h8*>(&from[op][row * kLine + ((piece ^ swizzle(row)) * 8)]);
+            return *reinterpret_cast<const h8*>(&from[op][row * kRowHalves + ((piece ^ ((row >> 1) & 7)) * 8)]);
         };
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             const int piece = ks * 2 + (lane >> 5);
 #pragma unroll
             for (int x = 0; x < WX; ++x) f.ph[ks][x] = at(0, wi + 32 * x + (lane & 31), piece);
-            if constexpr (!kHigh) {
 #pragma unroll
-                for (int y = 0; y < WY; ++y) f.ql[ks][y] = at(1, wj + 32 * y + (lane & 31), piece + 4);
+            for (int y = 0; y < WY; ++y) f.ql[ks][y] = at(1, wj + 32 * y + (lane & 31), piece + 4);
 #pragma unroll
-                for (int x = 0; x < WX; ++x) f.pl[ks][x] = at(0, wi + 32 * x + (lane & 31), piece + 4);
-            }
+            for (int x = 0; x < WX; ++x) f.pl[ks][x] = at(0, wi + 32 * x + (lane & 31), piece + 4);
 #pragma unroll
             for (int y = 0; y < WY; ++y) f.qh[ks][y] = at(1, wj + 32 * y + (lane & 31), piece);
         }
@@ -448,14 +438,12 @@ __global__ void __launch_bounds__(kProdThreads<TILE>) k_ortho_prod(ProdArgs a)
         };
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            if constexpr (!kHigh) {
-                add(f.ph[ks], f.ql[ks]);
-                add(f.pl[ks], f.qh[ks]);
-            }
+            add(f.ph[ks], f.ql[ks]);
+            add(f.pl[ks], f.qh[ks]);
             add(f.ph[ks], f.qh[ks]);
         }
         // first the next block's LDS reads, then the loads, between the products
-        constexpr int kReads = (kHigh ? 2 : 4) * (WX + WY), kMul = (kHigh ? 2 : 6) * WX * WY;
+        constexpr int kReads = 4 * (WX + WY), kMul = 6 * WX * WY;
 #pragma unroll
         for (int g = 0; g < kMul / 2; ++g) {
             __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMul / 2 - 1) / (kMul / 2), 0);
@@ -773,21 +761,19 @@ struct SmallOps {
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[x][q] = 0.0f;
     }
-    // acc[x] += the products (three or one) of p[x] and q
-    template <int PRODUCTS, int N>
+    // acc[x] += three products of p[x] and q
+    template <int N>
     static __device__ __forceinline__ void multiply(const h8 (&ph)[N], const h8 (&pl)[N], h8 qh, h8 ql, f16v (&acc)[N])
     {
-        if constexpr (PRODUCTS == 3) {
 #pragma unroll
-            for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
+        for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], ql, acc[x], 0, 0, 0);
 #pragma unroll
-            for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
-        }
+        for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[x], qh, acc[x], 0, 0, 0);
 #pragma unroll
         for (int x = 0; x < N; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[x], qh, acc[x], 0, 0, 0);
     }
     // acc[x] += sum_k p[row wi + 32 x ..][k] p[row wj ..][k], k over blocks of 32
-    template <int BLOCKS, int PRODUCTS, int N>
+    template <int BLOCKS, int N>
     __device__ __forceinline__ void square(const _Float16* p, f16v (&acc)[N]) const
     {
         const _Float16 *pi = p + wi * 64, *pj = p + wj * 64;
@@ -803,7 +789,7 @@ struct SmallOps {
                     ph[x] = *reinterpret_cast<const h8*>(pi + at[ks] + (kb * SP + 32 * x) * 64);
                     pl[x] = *reinterpret_cast<const h8*>(pi + at[ks + 2] + (kb * SP + 32 * x) * 64);
                 }
-                multiply<PRODUCTS>(ph, pl, qh, ql, acc);
+                multiply(ph, pl, qh, ql, acc);
             }
     }
     // four k of X^T's rows
@@ -831,7 +817,7 @@ struct SmallOps {
                     ph[x] = __builtin_shufflevector(transposed(p + tr[0]), transposed(p + tr[1]), 0, 1, 2, 3, 4, 5, 6, 7);
                     pl[x] = __builtin_shufflevector(transposed(p + tr[2]), transposed(p + tr[3]), 0, 1, 2, 3, 4, 5, 6, 7);
                 }
-                multiply<3>(ph, pl, qh, ql, acc);
+                multiply(ph, pl, qh, ql, acc);
             }
     }
     // the lane's four values g of block kb (low half: + 4) in row wj + lane % 32
@@ -882,7 +868,7 @@ struct SmallOps {
         __syncthreads();
         f16v acc[S::GX];
         clear(acc);
-        square<SP / 32, 3>(A, acc);
+        square<SP / 32>(A, acc);
 #pragma unroll
         for (int x = 0; x < S::GX; ++x)
 #pragma unroll
@@ -1033,7 +1019,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
     for (int k = 0; k < a.poly.steps; ++k) {
         const Units u = units[k];
         ops.clear(ar);
-        ops.template square<TP / 32, kGramProducts<T>>(X, ar);
+        ops.template square<TP / 32>(X, ar);
 #pragma unroll
         for (int x = 0; x < S::GX; ++x)
 #pragma unroll
@@ -1157,7 +1143,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_wide_first(Wide
         ops.place(a.d, v, inv);
         __syncthreads();
         put_image<SP, TP>(a.image + (b * a.chunks + c) * S::kX, X);
-        ops.template square<TP / 32, kGramProducts<T>>(X, ar);
+        ops.template square<TP / 32>(X, ar);
     }
     put_sums<SP, TP>(a.osums + blockIdx.x * (int64_t)(SP * SP), ar);
 }
@@ -1204,7 +1190,7 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_wide_step(WideA
             ops.put(X, xr, ops.wt);
             __syncthreads();
             put_image<SP, TP>(image + c * S::kX, X);
-            ops.template square<TP / 32, kGramProducts<T>>(X, ar);
+            ops.template square<TP / 32>(X, ar);
         }
     }
     if (!last) put_sums<SP, TP>(a.osums + blockIdx.x * (int64_t)(SP * SP), ar);

@@ -138,3 +138,62 @@ def test_orthogonalize_on_another_stream_and_in_a_graph(tt, m, n):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, cg.orthogonalize(g)), k
+
+
+def products32(G, steps, coeffs, eps, scale):
+    """The iteration by plain fp32 products, on the CPU."""
+    import torch
+    a, b, c = coeffs
+    X = torch.from_numpy(np.ascontiguousarray(G, np.float32))
+    X = X / (X.norm() + eps)
+    tall = X.shape[0] > X.shape[1]
+    X = X.t().contiguous() if tall else X
+    for _ in range(steps):
+        A = X @ X.t().contiguous()
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return (scale * (X.t() if tall else X)).double().numpy()
+
+
+STEEP = (4.0848, -6.8946, 2.9270)   # a steeper quintic: a step's error grows faster
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("coeffs,steps", [(QUINTIC, 5), (QUINTIC, 10), (QUINTIC, 20), (STEEP, 5)])
+@pytest.mark.parametrize("B,m,n,kind", [(1, 64, 64, "noise"), (1, 128, 128, "spectrum"), (1, 300, 260, "noise"),
+                                        (1, 128, 1024, "spectrum"), (1, 500, 64, "noise"), (3, 1100, 1030, "noise"),
+                                        (1, 12, 400, "noise")])
+def test_orthogonalize_is_as_exact_as_fp32_products(tt, B, m, n, kind, coeffs, steps, dtype):
+    """Against the same iteration by fp32 products on the CPU, whose error in
+    the Frobenius norm is e32: within 4 e32, whatever the type, steps and
+    coefficients, for every form.  A bf16 result is rounded once: rounding is
+    an element's distance to a grid, which changes by at most what the element
+    changes, so the error is at most that of rounding the exact result plus
+    twice 4 e32."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[ortho] {B} x {m} x {n} {kind} {coeffs} x {steps} {dtype}", flush=True)
+    G = gradient(np.random.default_rng(m + n + steps), B, m, n, kind)
+    G = T.bf16(G) if dtype == "bf16" else G
+    t = torch.from_numpy(G).to(dev).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    got = cg.orthogonalize(t, steps, coeffs, 1e-7, 0.5)[0].double().cpu().numpy()
+    want, norms = T.orthogonalize(G[0], steps, coeffs, 1e-7, 0.5)
+    e32 = np.linalg.norm(products32(G[0], steps, coeffs, 1e-7, 0.5) - want)
+    err, tol = np.linalg.norm(got - want), 4 * e32
+    if dtype == "bf16":
+        tol = np.linalg.norm(T.bf16(want.astype(np.float32)) - want) + 2 * tol
+    print(f"[ortho] error {err / norms[-1]:.3e} of the result, allowed {tol / norms[-1]:.3e}", flush=True)
+    assert err <= tol, float(err / tol)
+
+
+@pytest.mark.parametrize("B,m,n,kind", [(2, 64, 64, "noise"), (15, 128, 128, "spectrum"), (3, 90, 120, "noise"),
+                                        (4, 128, 1000, "noise"), (2, 500, 64, "noise"), (1, 300, 260, "noise"),
+                                        (3, 1100, 1030, "noise")])
+def test_orthogonalize_bf16_is_the_fp32_result_rounded(tt, B, m, n, kind):
+    """bf16 matrices are fp32 matrices too, and take the same arithmetic: the
+    results differ by the last rounding alone (from 17 rows up; below, fp64
+    sums are rounded to either type)."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[ortho] {B} x {m} x {n} {kind}", flush=True)
+    t = torch.from_numpy(T.bf16(gradient(np.random.default_rng(m + 2 * n), B, m, n, kind))).to(dev)
+    assert torch.equal(cg.orthogonalize(t.bfloat16()), cg.orthogonalize(t).bfloat16())
