@@ -22,7 +22,7 @@
 // The lengths of ragged segments are known on the device only: where their mean
 // is short but the total is large enough that one long segment would hold up the
 // chip, both forms are launched and each takes the segments on its side of a
-// length.  Sums over the rows are fp64; in the runs two (backward) or four rows are
+// length.  Sums over the rows are fp64; in the backward two (runs) or four rows are
 // added in fp32 first.
 #include <hip/hip_runtime.h>
 
@@ -294,8 +294,8 @@ __device__ __forceinline__ void row_batches(int64_t first, int64_t e, int32_t RL
     }
 }
 
-// u += x, v += x^2 over the lane's rows below e.  Four rows in fp32, taken from the
-// lane's first value of each channel so that nothing cancels, then in fp64:
+// u += x, v += x^2 over the lane's rows below e, in fp64 (fp32 holds no squares beyond
+// 1.8e19).  Taken from the lane's first value of each channel, so that little cancels:
 // sum x = n ref + D, sum x^2 = n ref^2 + 2 ref D + Q with D = sum (x - ref) and
 // Q = sum (x - ref)^2.
 template <int kAt, class T, int VEC, class Ln>
@@ -308,42 +308,38 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Ln& ln, const 
     const int64_t first = p + ln.rl;
     if (first >= e) return;
     const T* xp = x + first * a.ldx + ln.c;
-    Raw<T, VEC> ref;
-    ref.load(xp);
-    double D[VEC], Q[VEC];
+    double ref[VEC], D[VEC], Q[VEC];
+    {
+        Raw<T, VEC> f;
+        f.load(xp);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) D[j] = Q[j] = 0.0;
+        for (int j = 0; j < VEC; ++j) {
+            ref[j] = (double)f[j];
+            D[j] = Q[j] = 0.0;
+        }
+    }
     auto load = [&](int64_t r, Batch& b) {
 #pragma unroll
         for (int k = 0; k < kAt; ++k) b.f[k].load(r + k * ln.RL < e ? xp + (r - first + k * ln.RL) * a.ldx : xp);
     };
     auto work = [&](int64_t r, const Batch& b, auto masked) {
-        float ds[VEC], qs[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) ds[j] = qs[j] = 0.0f;
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
             // a row beyond e was loaded as the first: its difference is zero
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float d = b.f[k][j] - ref[j];
-                ds[j] += d;
-                qs[j] += d * d;
+                const double d = (double)b.f[k][j] - ref[j];
+                D[j] += d;
+                Q[j] += d * d;
             }
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            D[j] += (double)ds[j];
-            Q[j] += (double)qs[j];
         }
     };
     row_batches<kAt, Batch>(first, e, ln.RL, load, work);
     const double n = (double)((e - first + ln.RL - 1) / ln.RL);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        const double w = (double)ref[j];
-        u[j] += n * w + D[j];
-        v[j] += w * (n * w + 2.0 * D[j]) + Q[j];
+        u[j] += n * ref[j] + D[j];
+        v[j] += ref[j] * (n * ref[j] + 2.0 * D[j]) + Q[j];
     }
 }
 

@@ -242,3 +242,48 @@ def test_norm_on_another_stream_and_in_a_graph(tt):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, step())), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,N,C,G", [(3, 60, 32, 4), (1, 2000, 128, 8), (2, 40000, 32, 4), (1, 30001, 24, 3)])
+def test_norm_of_values_whose_squares_leave_fp32(tt, B, N, C, G, dtype):
+    """Values of up to 1e20 or so, whose squares fp32 does not hold: statistics
+    and results as for any other magnitude, in segments that a block takes
+    whole and in those cut into runs.  (Tolerances as above; the mean, a sum
+    that nearly cancels, to fp64's roundoff of the deviation too.)"""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[norm] large values {B} {N} {C} {G} {dtype}", flush=True)
+    rng = np.random.default_rng(N)
+    q = T.bf16 if dtype == "bf16" else (lambda v: v.astype(np.float32))
+    x = q(3e19 * (rng.standard_normal((N, C)) + rng.standard_normal(C)))
+    gamma, beta = ((1 + 0.3 * rng.standard_normal(C)).astype(np.float32), rng.standard_normal(C).astype(np.float32))
+    t = torch.from_numpy(x).to(dev).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    y, mean, rstd = cg.norm_act_fwd(t.view(B, N // B, C), torch.from_numpy(gamma).to(dev),
+                                    torch.from_numpy(beta).to(dev), G, act="none")
+    ptr = np.arange(B + 1) * (N // B)
+    wy, wm, wr = T.norm_fwd(x, gamma, beta, ptr, G, 1e-5, "none")
+    ty = bounds(x.astype(np.float64), gamma, beta, np.zeros_like(x), ptr, G, 1e-5, "none")[0]
+    r = 2.0 ** -8 if dtype == "bf16" else 2 * U
+    host = lambda v: v.double().cpu().numpy()  # noqa: E731
+    assert np.all(np.abs(host(rstd) - wr) <= 4 * U * wr)
+    assert np.all(np.abs(host(mean) - wm) <= 2 * U * np.abs(wm) + 2.0 ** -40 / wr)
+    assert np.all(np.abs(host(y).reshape(N, C) - wy) <= ty + r * np.abs(wy))
+
+
+@pytest.mark.parametrize("N,C,G", [(20000, 16, 2), (30001, 30, 3)])
+def test_norm_large_offset_in_long_segments(tt, N, C, G):
+    """As test_norm_large_offset, in a segment that is cut into runs: at most 512
+    lane sums and 1024 runs' sums are added after a lane's own, each to fp64's
+    roundoff of the squared mean."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x = (1000 + 0.01 * np.random.default_rng(9).standard_normal((N, C))).astype(np.float32)
+    one = np.ones(C)
+    y, m, r = cg.norm_act_fwd(torch.from_numpy(x).to(dev), None, None, G, act="none", eps=1e-8)
+    wy, wm, wr = T.norm_fwd(x, one, 0 * one, np.array([0, N]), G, 1e-8, "none")
+    off = 1536 * 2.0 ** -53 * 1e6 / 1e-4
+    assert np.abs(r.cpu().numpy() / wr - 1).max() <= 4 * U + off
+    assert np.abs(m.cpu().numpy() / wm - 1).max() <= 2 * U
+    err = np.abs(y.cpu().numpy() - wy)
+    assert np.all(err <= 16 * U * (2 + np.abs(wy) + np.abs(wm).max() * wr.max()) + off * np.abs(wy))
