@@ -22,8 +22,7 @@
 // The lengths of ragged segments are known on the device only: where their mean
 // is short but the total is large enough that one long segment would hold up the
 // chip, both forms are launched and each takes the segments on its side of a
-// length.  Sums over the rows are fp64; in the backward two (runs) or four rows are
-// added in fp32 first.
+// length.  Sums over the rows are fp64.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -460,8 +459,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __
 
 // ---- backward ------------------------------------------------------------------------
 // sums of h and h xhat of every piece, and of dz xhat and dz of every run
-// u += dz xhat, v += dz over rows p + rl, p + rl + RL, .. below e: kAt rows in
-// fp32, then in fp64
+// u += dz xhat, v += dz over rows p + rl, p + rl + RL, .. below e, kAt rows' loads at
+// a time: fp32 terms, fp64 sums
 template <int kAt, class T, int VEC, int ACT, class Ln>
 __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const T* __restrict__ x,
                                          const T* __restrict__ dy, int64_t p, int64_t e, const float (&mu)[VEC],
@@ -482,9 +481,6 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const 
         }
     };
     auto work = [&](int64_t r, const Batch& b, auto masked) {
-        float us[VEC], vs[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
 #pragma unroll
         for (int k = 0; k < kAt; ++k) {
             const bool in = !decltype(masked)::value || r + k * ln.RL < e;
@@ -492,14 +488,9 @@ __device__ __forceinline__ void bwd_rows(const NormArgs& a, const Ln& ln, const 
             for (int j = 0; j < VEC; ++j) {
                 const float xh = (b.f[k][j] - mu[j]) * rs[j];
                 const float dz = in ? b.d[k][j] * act_slope<ACT>(xh * gm[j] + bt[j]) : 0.0f;
-                us[j] += dz * xh;
-                vs[j] += dz;
+                u[j] += (double)(dz * xh);
+                v[j] += (double)dz;
             }
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            u[j] += (double)us[j];
-            v[j] += (double)vs[j];
         }
     };
     row_batches<kAt, Batch>(first, e, ln.RL, load, work);
@@ -815,9 +806,6 @@ __global__ void __launch_bounds__(THR, THR == 256 ? 4 : 1) k_norm_bwd_seg(NormAr
         if (on) {
             load_group(mu, a.mean, a, b, ln, 1, 0);
             load_group(rs, a.rstd, a, b, ln, 1, 0);
-            float us[VEC], vs[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) us[j] = vs[j] = 0.0f;
             Raw<T, VEC> f[KEEP], d[KEEP];
 #pragma unroll
             for (int k = 0; k < KEEP; ++k) {
@@ -832,14 +820,9 @@ __global__ void __launch_bounds__(THR, THR == 256 ? 4 : 1) k_norm_bwd_seg(NormAr
                     for (int j = 0; j < VEC; ++j) {
                         xh[k][j] = (f[k][j] - mu[j]) * rs[j];
                         dz[k][j] = d[k][j] * act_slope<ACT>(xh[k][j] * gm[j] + bt[j]);
-                        us[j] += dz[k][j] * xh[k][j];
-                        vs[j] += dz[k][j];
+                        u[j] += (double)(dz[k][j] * xh[k][j]);
+                        v[j] += (double)dz[k][j];
                     }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                u[j] = (double)us[j];
-                v[j] = (double)vs[j];
-            }
 #pragma unroll 2
             for (int64_t r = p + ln.rl + (int64_t)KEEP * ln.RL; r < e; r += ln.RL) {
                 Raw<T, VEC> g, h;

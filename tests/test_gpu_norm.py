@@ -287,3 +287,35 @@ def test_norm_large_offset_in_long_segments(tt, N, C, G):
     assert np.abs(m.cpu().numpy() / wm - 1).max() <= 2 * U
     err = np.abs(y.cpu().numpy() - wy)
     assert np.all(err <= 16 * U * (2 + np.abs(wy) + np.abs(wm).max() * wr.max()) + off * np.abs(wy))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,N,C,G", [(3, 60, 32, 4), (40, 4000, 64, 8), (1, 2000, 128, 8), (1, 40000, 16, 2),
+                                     (2, 30002, 30, 3)])
+def test_norm_gradient_sums_are_64_bit(tt, B, N, C, G, dtype):
+    """Rows of 2^30, -2^30 and 1 in turn at random: fp64 holds every partial sum
+    exactly, so what is left is the number of ones, where fp32 would lose a
+    one beside a large row.  (mean 0 and rstd 1 are given and x is 1, so that
+    xhat is 1 and both sums have the same terms.)"""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[norm] sums {B} {N} {C} {G} {dtype}", flush=True)
+    rng = np.random.default_rng(N + C)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    ones = N // 5 + N % 2               # the others in pairs
+    ones += (N - ones) % 2
+    row = np.concatenate([np.ones(ones), np.repeat([2.0 ** 30, -2.0 ** 30], (N - ones) // 2)])
+    g = np.stack([rng.permutation(row) for _ in range(C)], axis=1)
+    tg = torch.from_numpy(g).to(dev).to(dt).view(B, N // B, C)
+    x = torch.ones(B, N // B, C, device=dev, dtype=dt)
+    mean, rstd = torch.zeros(B, G, device=dev), torch.ones(B, G, device=dev)
+    for want in (("x", "gamma", "beta"), ("gamma", "beta")):
+        _, dg, db = cg.norm_act_bwd(x, mean, rstd, None, None, tg, G, act="none", want=want)
+        assert (db == ones).all() and (dg == ones).all(), (want, db[:4].tolist(), ones)
+    # the group means of dx: of a row of ones, 1 - 2 mean
+    dx = cg.norm_act_bwd(x, mean, rstd, None, None, tg, G, act="none")[0].double().cpu().numpy().reshape(g.shape)
+    s = g.reshape(B, N // B, G, C // G).mean((1, 3), keepdims=True)
+    w = np.broadcast_to(1 - 2 * s, (B, N // B, G, C // G)).reshape(N, C)
+    at = g == 1
+    r = 2.0 ** -8 if dtype == "bf16" else 4 * U
+    assert np.all(np.abs(dx - w)[at] <= (r * np.abs(w) + 4 * U * np.abs(1 - w))[at])
