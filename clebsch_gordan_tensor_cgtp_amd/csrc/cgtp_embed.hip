@@ -421,9 +421,9 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T* __re
         const int32_t before = b0 > 0 ? a.key[b0 - 1] : -1, after = b1 < a.N ? a.key[b1] : -1;
         auto store = [&](int32_t id, const double (&acc)[VEC]) {
             if (id >= a.V) return;
-            float v[VEC];
+            double v[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = (float)(acc[j] * (double)a.scale);
+            for (int j = 0; j < VEC; ++j) v[j] = acc[j] * (double)a.scale;
             store_vec<T, VEC>(gtab + (int64_t)id * a.C + q * VEC, v);
         };
         const int64_t p0 = b0 + (int64_t)rl * a.R, p1 = p0 + a.R < b1 ? p0 + a.R : b1;
@@ -550,9 +550,9 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
     __syncthreads();
     auto store = [&](int32_t id, const double (&sum)[VEC]) {
         if (!on || id >= a.V) return;
-        float v[VEC];
+        double v[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = (float)(sum[j] * (double)a.scale);
+        for (int j = 0; j < VEC; ++j) v[j] = sum[j] * (double)a.scale;
         store_vec<T, VEC>(col + (int64_t)id * a.C, v);
     };
     auto key = [&](int32_t p) { return (int32_t)(x.word[p] >> a.row_bits); };
@@ -693,9 +693,9 @@ __global__ void __launch_bounds__(kJoin) k_embed_join(SumArgs a, T* __restrict__
             __syncthreads();
         }
         if (ok && rl == 0) {
-            float v[VEC];
+            double v[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = (float)(s[j * kJoin + threadIdx.x] * (double)a.scale);
+            for (int j = 0; j < VEC; ++j) v[j] = s[j * kJoin + threadIdx.x] * (double)a.scale;
             store_vec<T, VEC>(gtab + (int64_t)k * a.C + q * VEC, v);
         }
         __syncthreads();

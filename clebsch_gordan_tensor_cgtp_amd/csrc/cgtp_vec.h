@@ -29,6 +29,20 @@ __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v)
     return bf16_t{__builtin_bit_cast(uint16_t, (__bf16)v)};
 }
 
+// from fp64 in one rounding (through fp32 a bf16 could be off by the second)
+template <class T>
+__device__ __forceinline__ T from_f64(double v);
+template <>
+__device__ __forceinline__ float from_f64<float>(double v)
+{
+    return (float)v;
+}
+template <>
+__device__ __forceinline__ bf16_t from_f64<bf16_t>(double v)
+{
+    return bf16_t{__builtin_bit_cast(uint16_t, (__bf16)v)};
+}
+
 // elements of one 16-byte access
 template <class T>
 constexpr int kWide = 16 / (int)sizeof(T);
@@ -49,17 +63,22 @@ __device__ __forceinline__ void load_vec(float (&v)[VEC], const T* __restrict__ 
     }
 }
 
-template <class T, int VEC>
-__device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&v)[VEC])
+// V: float, or double for sums that are rounded here
+template <class T, int VEC, class V>
+__device__ __forceinline__ void store_vec(T* __restrict__ p, const V (&v)[VEC])
 {
+    auto round = [](V x) {
+        if constexpr (sizeof(V) == 8) return from_f64<T>(x);
+        else return from_f32<T>(x);
+    };
     if constexpr (VEC == 1) {
-        p[0] = from_f32<T>(v[0]);
+        p[0] = round(v[0]);
     } else {
         struct alignas(VEC * sizeof(T)) Pack {
             T e[VEC];
         } q;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) q.e[j] = from_f32<T>(v[j]);
+        for (int j = 0; j < VEC; ++j) q.e[j] = round(v[j]);
         *reinterpret_cast<Pack*>(p) = q;
     }
 }

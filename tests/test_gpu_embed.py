@@ -177,3 +177,29 @@ def test_embed_on_another_stream_and_in_a_graph(tt):
         torch.cuda.synchronize()
         assert torch.equal(out, cg.embed_fwd(ids, table, 2.0)), k
         assert torch.equal(gt, cg.embed_bwd(ids, g, V, 2.0)), k
+
+
+@pytest.mark.parametrize("N,V,C", [(3, 5, 8), (3000, 90, 24), (6000, 5000, 16), (6000, 5000, 1032), (30000, 70000, 3),
+                                   (70001, 70000, 8)])
+def test_embed_gradient_is_rounded_once(tt, N, V, C):
+    """1 + 2^-8 + 2^-30 lies just above the middle of two bf16 numbers: rounded
+    once it is 1 + 2^-7; through fp32, where it is the middle, it would be 1.
+    Mirrored below zero, and 1 + 2^-8 - 2^-30 the other way.  One id's rows lie
+    together, another's span the whole batch."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[embed] rounding {N} {V} {C}", flush=True)
+    g = np.zeros((N, C))
+    ids = np.full(N, V - 1, np.int32)       # a hot id
+    ids[:3] = 0                             # three rows of their own
+    terms = np.array([1.0, 2.0 ** -8, 2.0 ** -30])[:, None] * np.where(np.arange(C) % 2, -1.0, 1.0)
+    terms[2] *= np.where(np.arange(C) % 3 == 2, -1.0, 1.0)
+    g[:3] = terms
+    if N > 3:
+        g[[3, N // 2, N - 1]] = terms
+    want = np.where(np.arange(C) % 3 == 2, 1.0, 1 + 2.0 ** -7) * np.where(np.arange(C) % 2, -1.0, 1.0)
+    got = cg.embed_bwd(torch.from_numpy(ids).to(dev), torch.from_numpy(g).to(dev).bfloat16(), V).float().cpu().numpy()
+    assert np.array_equal(got[0], want) and (N == 3 or np.array_equal(got[V - 1], want))
+    big = torch.full((2, C), 3.38e38, device=dev).bfloat16()
+    got = cg.embed_bwd(torch.zeros(2, dtype=torch.int32, device=dev), big, 2)
+    assert torch.isinf(got[0]).all() and (got[1] == 0).all()     # beyond the type: infinity
