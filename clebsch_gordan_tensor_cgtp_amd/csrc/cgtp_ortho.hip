@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(64 * kTinyWaves) k_ortho_tiny(TinyArgs a)
                 const int row = 4 * m + r4, col = j0 + c;
                 const double v = a.poly.a * x[m] + acc[m];
                 if (!in(row, col)) continue;
-                if (last) o[a.d.tall ? col * s + row : row * t + col] = from_f32<T>((float)(v * (double)a.poly.scale));
+                if (last) o[a.d.tall ? col * s + row : row * t + col] = from_f64<T>(v * (double)a.poly.scale);
                 else X[row * ld + col] = (float)v;
             }
         }

@@ -197,3 +197,30 @@ def test_orthogonalize_bf16_is_the_fp32_result_rounded(tt, B, m, n, kind):
     print(f"[ortho] {B} x {m} x {n} {kind}", flush=True)
     t = torch.from_numpy(T.bf16(gradient(np.random.default_rng(m + 2 * n), B, m, n, kind))).to(dev)
     assert torch.equal(cg.orthogonalize(t.bfloat16()), cg.orthogonalize(t).bfloat16())
+
+
+def test_orthogonalize_short_rows_are_rounded_once(tt):
+    """Matrices of few rows in fp64, one step, bf16: the definition followed in
+    64 bits (X held as fp32, as the kernel does) and rounded once gives the same
+    bits, but where the exact value is within 2^-40 of the middle of two bf16
+    numbers.  Through fp32 about one element in 2^17 would differ, a dozen here."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    rng = np.random.default_rng(17)
+    a, b, c = QUINTIC
+    G = T.bf16(rng.standard_normal((100000, 1, 16)).astype(np.float32))
+    t = torch.from_numpy(G).to(dev).bfloat16()
+    got = cg.orthogonalize(t, 1, QUINTIC, 2.0, 0.75).float().cpu().numpy().ravel()
+    g = G.astype(np.float64)
+    inv = 1.0 / (np.sqrt((g * g).sum((1, 2), keepdims=True)) + 2.0)
+    x = (g * inv).astype(np.float32).astype(np.float64)
+    A = (x * x).sum(2, keepdims=True)
+    want = ((a * x + (b * A + c * A * A) * x) * 0.75).ravel()
+    # bf16 by its definition: 2^7 steps in each power of two
+    f, e = np.frexp(want)
+    n = np.ldexp(f, 8)
+    clear = np.abs(np.abs(n - np.floor(n)) - 0.5) > 2.0 ** -32
+    exact = np.ldexp(np.rint(n), e - 8)
+    assert clear.mean() > 0.999
+    wrong = (got != exact)[clear].sum()
+    assert wrong == 0, wrong
