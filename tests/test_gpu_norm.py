@@ -319,3 +319,72 @@ def test_norm_gradient_sums_are_64_bit(tt, B, N, C, G, dtype):
     at = g == 1
     r = 2.0 ** -8 if dtype == "bf16" else 4 * U
     assert np.all(np.abs(dx - w)[at] <= (r * np.abs(w) + 4 * U * np.abs(1 - w))[at])
+
+
+def mixed_lengths(rng, kind, N, B, longest):
+    """Lengths of B segments of N rows together, where blocks take segments of up
+    to `longest` rows (the backward; the forward twice that) and runs the others."""
+    run = max(16, -(-N // 1024))
+    v = rng.integers(1, 40, B)
+    v[rng.random(B) < 0.1] = 0
+    if kind == "one":                       # one long structure holds nearly all rows
+        v[B // 3] = 0
+        v[B // 3] = N - v.sum()
+    elif kind == "several":                 # from a run's first row, next to each other, either side of the limit
+        before = v[:3].sum()
+        v[3] = -before % run                # the next begins with a run
+        v[4:10] = longest + 1, longest, 5 * run, longest + 1 + run, 2 * longest, 2 * longest + 1
+        v[-1] = longest + 2
+        v[B // 2] = 0
+        v[B // 2] = N - v.sum()
+    else:                                   # none is long: the runs find nothing
+        v = np.full(B, N // B)
+        v[rng.permutation(B)[:N - v.sum()]] += 1
+    assert v.sum() == N and v.min() >= 0
+    return v
+
+
+# Rows of C channels that together pass 32 MB, so that whole segments and runs go out in one call: in both directions,
+# but the last two in the backward alone.  C = 250: no wide accesses.  B = 3000: short segments, several to a block.
+MIXED = [("one", 17000, 300, 512, 8, "silu", "f32"), ("several", 17000, 300, 512, 8, "tanh", "f32"),
+         ("none", 16500, 400, 512, 8, "silu", "f32"), ("several", 34000, 400, 250, 5, "silu", "f32"),
+         ("one", 70000, 3000, 128, 8, "silu", "f32"), ("several", 34000, 400, 512, 32, "silu", "bf16"),
+         ("one", 9000, 256, 512, 4, "none", "f32"), ("several", 18000, 300, 512, 8, "silu", "bf16")]
+
+
+@pytest.mark.parametrize("kind,N,B,C,G,act,dtype", MIXED)
+def test_norm_whole_segments_beside_runs(tt, kind, N, B, C, G, act, dtype):
+    """Ragged batches in which blocks take the short segments and runs the long
+    ones: every result against the oracle, each gradient asked for alone."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[norm] mixed {kind} N={N} B={B} C={C} G={G} {act} {dtype}", flush=True)
+    rng = np.random.default_rng(N + B + C)
+    es = 4 if dtype == "f32" else 2
+    lens = mixed_lengths(rng, kind, N, B, (1 << 20) // (C * es * 2))
+    ptr = np.concatenate([[0], np.cumsum(lens)])
+    q = T.bf16 if dtype == "bf16" else (lambda v: v.astype(np.float32))
+    x = q(rng.standard_normal((N, C)) * (0.5 + rng.random(C)) + 2 * rng.standard_normal(C))
+    grad = q(rng.standard_normal((N, C)))
+    gamma, beta = ((1 + 0.3 * rng.standard_normal(C)).astype(np.float32), rng.standard_normal(C).astype(np.float32))
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    tx, tg = (torch.from_numpy(v).to(dev).to(dt) for v in (x, grad))
+    tgm, tbt, seg = (torch.from_numpy(v).to(dev) for v in (gamma, beta, ptr.astype(np.int32)))
+    y, mean, rstd = cg.norm_act_fwd(tx, tgm, tbt, G, seg, act=act)
+    dx, dg, db = cg.norm_act_bwd(tx, mean, rstd, tgm, tbt, tg, G, seg, act)
+    wy, wm, wr = T.norm_fwd(x, gamma, beta, ptr, G, 1e-5, act)
+    wdx, wdg, wdb = T.norm_bwd(x, gamma, beta, grad, ptr, G, 1e-5, act)
+    ty, tdx, tdg, tdb = bounds(x.astype(np.float64), gamma, beta, grad, ptr, G, 1e-5, act)
+    r = 2.0 ** -8 if dtype == "bf16" else 2 * U
+    for name, got, want, tol in (("mean", mean, wm, 2 * U * np.abs(wm) + 2 * U), ("rstd", rstd, wr, 4 * U * wr),
+                                 ("y", y, wy, ty + r * np.abs(wy)), ("dx", dx, wdx, tdx + r * np.abs(wdx)),
+                                 ("dgamma", dg, wdg, tdg + 2 * U * np.abs(wdg)),
+                                 ("dbeta", db, wdb, tdb + 2 * U * np.abs(wdb))):
+        err = np.abs(got.float().cpu().numpy().astype(np.float64) - want)
+        assert np.all(err <= tol), (name, float((err / np.maximum(tol, 1e-300)).max()))
+    for want in (("x",), ("gamma", "beta"), ("beta",)):
+        for name, a, b in zip(("x", "gamma", "beta"), cg.norm_act_bwd(tx, mean, rstd, tgm, tbt, tg, G, seg, act, want),
+                              (dx, dg, db)):
+            assert torch.equal(a, b) if name in want else a is None, name
+    again = cg.norm_act_fwd(tx, tgm, tbt, G, seg, act=act)
+    assert all(torch.equal(a, b) for a, b in zip((y, mean, rstd), again))
