@@ -203,3 +203,26 @@ def test_embed_gradient_is_rounded_once(tt, N, V, C):
     big = torch.full((2, C), 3.38e38, device=dev).bfloat16()
     got = cg.embed_bwd(torch.zeros(2, dtype=torch.int32, device=dev), big, 2)
     assert torch.isinf(got[0]).all() and (got[1] == 0).all()     # beyond the type: infinity
+
+
+# Sorts by tiles of 1024 ids: up to 64 tiles (65536 ids) and more, more than 256 of them (262144 ids, whose counts are
+# summed in several rounds), one, two and three passes of 9 bits, and many digits in use in each.
+TILED = [("uniform", 65536, 300, 4, 1), ("uniform", 65537, 300, 4, 1), ("mixed", 70001, 70000, 8, 1),
+         ("uniform", 270000, 600, 8, 1), ("uniform", 300001, 100000, 4, 1), ("mixed", 270001, 400, 3, 2),
+         ("sorted", 262145, 511, 4, 1), ("few", 300000, 2 ** 20, 4, 1), ("uniform", 66000, 2 ** 19, 4, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,N,V,C,pitch", TILED)
+def test_embed_gradient_of_many_ids(tt, kind, N, V, C, pitch, dtype):
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[embed] many {kind} N={N} V={V} C={C} pitch={pitch} {dtype}", flush=True)
+    rng = np.random.default_rng(N + V)
+    ids = draw_ids(rng, kind, N, V)
+    ti = torch.from_numpy(ids).to(dev)
+    g = torch.randn(N, pitch, C, device=dev).to(_dt(torch, dtype))[:, pitch - 1, :]
+    got = cg.embed_bwd(ti, g, V, 0.5)
+    gh = g.float().cpu().numpy()
+    check(got, T.embed_bwd(ids, gh, V, 0.5), T.embed_bwd(ids, np.abs(gh), V, 0.5), N, dtype)
+    assert torch.equal(got, cg.embed_bwd(ti, g, V, 0.5))
