@@ -224,3 +224,27 @@ def test_orthogonalize_short_rows_are_rounded_once(tt):
     assert clear.mean() > 0.999
     wrong = (got != exact)[clear].sum()
     assert wrong == 0, wrong
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,m,n,steps", [(100, 128, 300, 5), (200, 300, 60, 2), (300, 40, 200, 5), (90, 100, 520, 1),
+                                         (2, 20, 65536, 3), (2, 128, 33000, 5)])
+def test_orthogonalize_several_chunks_to_a_block(tt, B, m, n, steps, dtype):
+    """Short sides of up to 128 with more chunks of 128 columns than blocks, so
+    that a block takes several chunks in turn."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[ortho] chunks {B} x {m} x {n} {dtype}", flush=True)
+    G = gradient(np.random.default_rng(B + m), B, m, n, "noise")
+    G = T.bf16(G) if dtype == "bf16" else G
+    t = torch.from_numpy(G).to(dev).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    out = cg.orthogonalize(t, steps)
+    got = out.double().cpu().numpy()
+    for b in (0, B // 2, B - 1):
+        want, norms = T.orthogonalize(G[b], steps, QUINTIC, 1e-7, 1.0)
+        err, tol = np.linalg.norm(got[b] - want), tolerance(norms, QUINTIC, 1.0, dtype)
+        assert err <= tol, (b, float(err / tol))
+    assert torch.equal(out, cg.orthogonalize(t, steps))
+    few = cg.orthogonalize(t[:1], steps)        # the same matrix by more blocks: the partial sums differ in order
+    want, norms = T.orthogonalize(G[0], steps, QUINTIC, 1e-7, 1.0)
+    assert np.linalg.norm(few[0].double().cpu().numpy() - want) <= tolerance(norms, QUINTIC, 1.0, dtype)
