@@ -249,10 +249,11 @@ def norm_act_fwd(x, gamma, beta, groups: int, seg_ptr=None, eps: float = 1e-5, a
 
 
 def norm_act_bwd(x, mean, rstd, gamma, beta, grad_y, groups: int, seg_ptr=None, act: str = "silu",
-                 want=("x", "gamma", "beta"), ws=None):
+                 want=("x", "gamma", "beta"), ws=None, grad_x=None):
     """(grad_x, grad_gamma, grad_beta) of <grad_y, y> for norm_act_fwd's y on
     the same arguments and its mean and rstd; a gradient not in ``want`` comes
-    back as None."""
+    back as None.  ``grad_x`` of x's shape may be a view with a row stride, such
+    as the l = 0 rows of a gradient of node features."""
     d = _dtype(x, "x")
     N, B, C = _norm_shape(x, groups, seg_ptr)
     dev = x.device
@@ -262,13 +263,19 @@ def norm_act_bwd(x, mean, rstd, gamma, beta, grad_y, groups: int, seg_ptr=None, 
     g, b = _channel(gamma, "gamma", C, dev), _channel(beta, "beta", C, dev)
     ldx, ldy = _rows(x, "x"), _rows(grad_y, "grad_y")
     nbytes = _bytes("cgtp_norm_act_workspace_size", d, N, B, C, groups, int(seg_ptr is not None), 1)
-    gx = x.new_empty(x.shape) if "x" in want else None
+    if "x" not in want:
+        gx, ldd = None, C
+    elif grad_x is None:
+        gx, ldd = x.new_empty(x.shape), C
+    else:
+        _like(grad_x, "grad_x", x.dtype, x.shape, dev)
+        gx, ldd = grad_x, _rows(grad_x, "grad_x")
     gg = torch.empty(C, dtype=torch.float32, device=dev) if "gamma" in want else None
     gb = torch.empty(C, dtype=torch.float32, device=dev) if "beta" in want else None
     at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _call("cgtp_norm_act_bwd", dev, d, _act(act), N, B, C, groups, ptr(seg_ptr), x.data_ptr(), ldx, mean.data_ptr(),
-          rstd.data_ptr(), g, b, grad_y.data_ptr(), ldy, ptr(gx), C, ptr(gg), ptr(gb), at, room)
+          rstd.data_ptr(), g, b, grad_y.data_ptr(), ldy, ptr(gx), ldd, ptr(gg), ptr(gb), at, room)
     return gx, gg, gb
 
 

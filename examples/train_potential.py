@@ -95,10 +95,9 @@ class Potential:
         counts = (b["seg"][1:] - b["seg"][:-1]).long()
         grad_atom = torch.repeat_interleave(grad_energy, counts, output_size=h.shape[0])
         grad_h = grad_atom[:, None] * p["w_out"]
-        grad_rows, grad_gamma, grad_beta = cg.norm_act_bwd(z[:, 0, :], mean, rstd, p["gamma"], p["beta"], grad_h,
-                                                           self.groups, b["seg"])
         grad_z = torch.zeros_like(z)
-        grad_z[:, 0, :] = grad_rows
+        _, grad_gamma, grad_beta = cg.norm_act_bwd(z[:, 0, :], mean, rstd, p["gamma"], p["beta"], grad_h, self.groups,
+                                                   b["seg"], grad_x=grad_z[:, 0, :])
         grad_mid, grad_Wmix = plan.path_mix_bwd(mid, p["Wmix"], grad_z)
         grad_x = plan.conv_bwd(b["row_ptr"], b["src"], x, Y, W, grad_mid, ws, want=("dx",))[0]
         grad_table = cg.embed_bwd(b["species"], grad_x[:, 0, :], SPECIES, self.channels ** -0.5)

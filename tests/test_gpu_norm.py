@@ -388,3 +388,32 @@ def test_norm_whole_segments_beside_runs(tt, kind, N, B, C, G, act, dtype):
             assert torch.equal(a, b) if name in want else a is None, name
     again = cg.norm_act_fwd(tx, tgm, tbt, G, seg, act=act)
     assert all(torch.equal(a, b) for a, b in zip((y, mean, rstd), again))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,B,C,pitch", [(300, 20, 64, 4), (2000, 1, 128, 9), (40000, 2, 64, 3), (17000, 300, 512, 2),
+                                         (500, 7, 30, 5)])
+def test_norm_gradient_into_rows_of_a_wider_array(tt, N, B, C, pitch, dtype):
+    """grad_x as every pitch-th row of an array: the same values as by itself,
+    the other rows left alone; whole segments, runs, and both (the rows of all
+    cases begin on the same boundaries as by themselves, so that the same
+    kernels run)."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[norm] grad_x {N} {B} {C} {pitch} {dtype}", flush=True)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    ptr = np.concatenate([[0], np.cumsum(lengths(np.random.default_rng(N), "ragged" if B > 1 else "one", N, B))])
+    seg = torch.from_numpy(ptr.astype(np.int32)).to(dev)
+    x, g = torch.randn(N, C, device=dev).to(dt), torch.randn(N, C, device=dev).to(dt)
+    w = torch.randn(C, device=dev)
+    y, m, r = cg.norm_act_fwd(x, w, w, 2, seg)
+    want = cg.norm_act_bwd(x, m, r, w, w, g, 2, seg)
+    full = torch.full((N, pitch, C), 7.0, device=dev, dtype=dt)
+    for k in range(pitch):
+        full.fill_(7.0)
+        got = cg.norm_act_bwd(x, m, r, w, w, g, 2, seg, grad_x=full[:, k, :])
+        assert got[0].data_ptr() == full[:, k, :].data_ptr()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+        assert (full[:, [q for q in range(pitch) if q != k], :] == 7.0).all(), k
+    none = cg.norm_act_bwd(x, m, r, w, w, g, 2, seg, want=("gamma",), grad_x=full[:, 0, :])
+    assert none[0] is None and (full[:, 0, :] == 7.0).all() and torch.equal(none[1], want[1])

@@ -169,3 +169,22 @@ def test_binding_refusals(L):
         cg.norm_act_fwd(torch.zeros(3, 5, 8)[:, :2], w, w, 4)
     with pytest.raises(ValueError, match="shape"):
         cg.norm_act_bwd(x, torch.zeros(2, 4), torch.zeros(1, 4), w, w, x, 4)
+
+
+def test_norm_gradient_output_refusals(L):
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    x, w, s = torch.zeros(6, 8), torch.ones(8), torch.zeros(1, 4)
+    call = lambda g: cg.norm_act_bwd(x, s, s, w, w, x, 4, grad_x=g)  # noqa: E731
+    for bad in (torch.zeros(5, 8), torch.zeros(6, 3, 8)):
+        with pytest.raises(ValueError, match="grad_x has shape"):
+            call(bad)
+    with pytest.raises(TypeError, match="grad_x must be torch.float32"):
+        call(torch.zeros(6, 8).bfloat16())
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        call([0.0])
+    with pytest.raises(ValueError, match="channels must be contiguous"):
+        call(torch.zeros(8, 6).t())
+    with pytest.raises(ValueError, match="overlap"):
+        call(torch.zeros(1, 8).expand(6, 8))
+    with pytest.raises(ValueError, match="GPU"):
+        call(torch.zeros(6, 2, 8)[:, 0])
