@@ -161,7 +161,8 @@ STEEP = (4.0848, -6.8946, 2.9270)   # a steeper quintic: a step's error grows fa
 @pytest.mark.parametrize("coeffs,steps", [(QUINTIC, 5), (QUINTIC, 10), (QUINTIC, 20), (STEEP, 5)])
 @pytest.mark.parametrize("B,m,n,kind", [(1, 64, 64, "noise"), (1, 128, 128, "spectrum"), (1, 300, 260, "noise"),
                                         (1, 128, 1024, "spectrum"), (1, 500, 64, "noise"), (3, 1100, 1030, "noise"),
-                                        (1, 12, 400, "noise")])
+                                        (1, 12, 400, "noise"), (1, 12, 2730, "noise"), (1, 12, 2740, "noise"),
+                                        (1, 9000, 5, "spectrum"), (1, 3, 20000, "noise")])
 def test_orthogonalize_is_as_exact_as_fp32_products(tt, B, m, n, kind, coeffs, steps, dtype):
     """Against the same iteration by fp32 products on the CPU, whose error in
     the Frobenius norm is e32: within 4 e32, whatever the type, steps and
