@@ -638,7 +638,9 @@ __global__ void __launch_bounds__(kOneThreads) k_embed_few(FewArgs a, const T* _
 
 // Block (run, slice): if a stretch begins in this run and goes on after it, its
 // partial sums from here to its end.  Latency: keys, one or two rounds of the search,
-// partial sums, in turn (391 runs 6.5 us, 7815 runs 18.6 us, x 128 fp32).
+// partial sums, in turn (391 runs 6.5 us, 7815 runs 18.6 us, x 128 fp32).  Where a row is
+// 256 accesses or more, each lane adds all of a hot id's runs by itself: 40000 x 1024 fp32 of
+// six ids, 1000 runs, 50 us beside 27 us of sums.
 constexpr int kJoin = 256;
 
 template <class T, int VEC>

@@ -344,8 +344,8 @@ __device__ __forceinline__ void fwd_rows(const NormArgs& a, const Ln& ln, const 
 
 // ---- forward -------------------------------------------------------------------------
 // Figures of the runs are for eight segments of 50001 x 256 rows (bf16 205 MB, fp32 410 MB).
-// sums of x and x^2 of every piece: bound by reading x, bf16 44 us (4.7 TB/s), fp32 107 us
-// (3.8 TB/s)
+// sums of x and x^2 of every piece: bound by reading x, bf16 46 us, fp32 92 us (4.5 TB/s).
+// The fp64 arithmetic hides behind it (four rows in fp32 first: the same within 1 %).
 template <class T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_norm_sums(NormArgs a, const T* __restrict__ x)
 {
@@ -398,7 +398,7 @@ __device__ __forceinline__ void finish_stats(const NormArgs& a, double x, double
     rstd = (float)(1.0 / sqrt(var + (double)a.eps));
 }
 
-// a wave per (segment, group): 5 us, a launch and the pieces' latency
+// a wave per (segment, group): 6 us, a launch and the pieces' latency
 __global__ void __launch_bounds__(kThreads) k_norm_stats(NormArgs a)
 {
     const int64_t n = a.B * a.G, step = (int64_t)gridDim.x * (kThreads / 64);
@@ -426,7 +426,7 @@ __device__ __forceinline__ void load_group(float (&o)[VEC], const float* __restr
     }
 }
 
-// Bound by memory: bf16 77 us (5.3 TB/s read and written), fp32 147 us (5.6 TB/s).
+// Bound by memory: bf16 79 us (5.2 TB/s read and written), fp32 146 us (5.6 TB/s).
 template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) k_norm_apply(NormArgs a, const T* __restrict__ x, T* __restrict__ y)
 {
@@ -543,7 +543,7 @@ struct Totals {
     }
 };
 
-// Bound by reading x and dy: bf16 90 us, fp32 177 us (4.6 TB/s).
+// Bound by reading x and dy: bf16 96 us, fp32 192 us (4.3 TB/s).
 template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads, 4) k_norm_bwd_sums(NormArgs a, const T* __restrict__ x,
                                                             const T* __restrict__ dy)
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kJoin) k_norm_bwd_join(NormArgs a, int32_t cbl
     }
 }
 
-// Bound by memory: bf16 114 us (5.4 TB/s), fp32 224 us (5.5 TB/s).  (Going through the
+// Bound by memory: bf16 115 us (5.3 TB/s), fp32 222 us (5.5 TB/s).  (Going through the
 // segments in parts small enough to stay in the last-level cache between the two passes
 // gained nothing: a part's launches cost what its cached reads save.)
 template <class T, int VEC, int ACT>
@@ -666,7 +666,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_apply(NormArgs a, const T
 // ---- a block per segment -----------------------------------------------------------------
 // Bound by a block's chain of a load, two sums over its lanes and a store: 1024 segments of
 // 25000 x 128 bf16 rows in all 11.1 us (1.2 TB/s), one segment of 2000 x 128 fp32 rows
-// 10.3 us; backward, 1024 segments, fp32, 17.8 us (2.2 TB/s).  A wave for each segment instead
+// 10.4 us; backward, 1024 segments, fp32, 20.1 us (1.9 TB/s; its fp64 sums are 2.3 us of that:
+// four rows in fp32 first lost small terms beside large ones).  A wave for each segment instead
 // of a block took longer: few rows were in flight.
 // Rows of a lane that stay in registers between the two passes; the rows of a
 // longer segment are read again.
@@ -890,8 +891,17 @@ int64_t rows_per_run(int64_t N)
 
 constexpr int64_t kSegBlocks = 1024;   // blocks of the whole segments' backward, each with one row of channel sums
 constexpr int64_t kLong = 256 << 10;  // bytes of a segment's slice that one block takes
-constexpr int64_t kTotal = 32 << 20;  // bytes that one block could be left with, if one segment held all rows
 constexpr int64_t kFill = 256;        // blocks that fill the chip
+// Bytes up to which ragged segments go out as whole ones alone, although one segment may hold
+// all rows.  The runs beside them cost launches that mostly find nothing; without them a long
+// segment is one block's work, bound by the few rows that it has in flight.  25000 x 128 in 1024
+// segments, fp32, whole alone and with runs beside: of equal lengths forward 13 and 23 us,
+// backward 21 and 40; one of 500 rows 30 and 43, 65 and 83; one of 2000 rows 120 and 133 (a
+// block takes that one whole in either), 200 and 44; one of 8000 rows 660 and 26, 820 and 44; one of
+// 24000 rows 1960 and 43, 2420 and 53.  Batches of structures of like sizes, the usual ones, are
+// served; a batch with one that is a hundred times longer is quicker with that one in a call of
+// its own.
+constexpr int64_t kTotal = 32 << 20;
 
 struct NormLayout {
     int64_t R, runs, parts;
@@ -944,7 +954,7 @@ Slices slices_of(const NormShape& n, int vec, int threads, int64_t want)
 
 // Elements of a wide access, for either type: with eight of bf16 the sums of a
 // lane's channels take so many registers that half the waves fit (backward's sums of
-// 400008 x 256: 119 us where four took 100 us, before the batches that make it 90 us).
+// 400008 x 256: 119 us where four took 100 us, before the batches that make it 96 us).
 constexpr int kVec = 4;
 
 // wide accesses need every slice to begin and end on them

@@ -18,7 +18,8 @@
 // five steps is off by 0.8 to 1.1 times what fp32 products give, from 20 rows up), at
 // a third of the fp16 rate instead of the sixteenth that fp32 matrix instructions
 // reach.  Below 17 rows sums are too short to hide the missing bit (up to twice the
-// fp32 error), and there is little to multiply: those matrices run in fp64.
+// fp32 error), and there is little to multiply: those matrices run in fp64, up to the
+// 32768 elements that a block holds.
 //
 // bf16 matrices take the same three products.  A step carries the error of the steps
 // before on, and steeper coefficients magnify it: with hu hv alone in A = X X^T the
@@ -1041,9 +1042,9 @@ __global__ void __launch_bounds__((Small<SP, TP>::kThr)) k_ortho_small(SmallArgs
 
 // ---- a short side of at most 128, the other longer -------------------------------------------
 // A matrix's chunks of TP columns are dealt to `blocks` blocks.  A launch per step, and
-// one that adds the partial A where they are many (15 of 128 x 1024 bf16: 15.4 and 4.2 us,
+// one that adds the partial A where they are many (15 of 128 x 1024 bf16: 16.3 and 4.3 us,
 // bound by launches and by each block's own three products; the first X with its A takes
-// 11.5 us): every block adds the partial A = X X^T of all blocks, forms B (the same
+// 12.2 us): every block adds the partial A = X X^T of all blocks, forms B (the same
 // work in each, in parallel), takes its chunks of X, held in memory as they lie
 // in LDS, through X <- a X + B X, and leaves its partial A of the new X.
 struct WideArgs {

@@ -16,10 +16,11 @@
  * abort, no allocation, capturable into a HIP graph):
  *   - no plan: sizes are arguments, and the element type of the large arrays
  *     is a cgtp_dtype_t.  Statistics, gamma and beta and their gradients are
- *     fp32 whatever the type.  Sums run in fp64, Newton-Schulz products as
- *     three fp16 products with fp32 accumulation, which together carry 23 bits
- *     of their operands (fp64 for matrices of up to 16 rows or columns); each
- *     result is rounded once.
+ *     fp32 whatever the type.  Sums over rows run in fp64, elementwise terms
+ *     in fp32; Newton-Schulz products run as three fp16 products with fp32
+ *     accumulation, which together carry 23 bits of their operands, for either
+ *     type (in fp64 for matrices of up to 16 rows or columns and 32768
+ *     elements); each result is rounded to its type once.
  *   - arrays are aligned to their element type; rows that start on 16-byte
  *     boundaries (pointer, row stride and channel count) take the wide-load
  *     kernels.  Row strides count elements and are at least the row's width.
