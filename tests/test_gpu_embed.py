@@ -226,3 +226,44 @@ def test_embed_gradient_of_many_ids(tt, kind, N, V, C, pitch, dtype):
     gh = g.float().cpu().numpy()
     check(got, T.embed_bwd(ids, gh, V, 0.5), T.embed_bwd(ids, np.abs(gh), V, 0.5), N, dtype)
     assert torch.equal(got, cg.embed_bwd(ti, g, V, 0.5))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_embed_offsets_beyond_32_bits(tt, dtype):
+    """Tables and rows of more than 2^31 elements: the last rows are read and
+    written at their own places."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[embed] beyond 32 bits {dtype}", flush=True)
+    V, C, N = (1 << 22) + 37, 520, 3000     # a table of 2.18e9 elements
+    rng = np.random.default_rng(1)
+    ids = np.concatenate([[0, V - 1, V, -1, V - 2, 1 << 21], rng.integers(V - 500, V, N - 6)]).astype(np.int32)
+    ti = torch.from_numpy(ids).to(dev)
+    table = torch.zeros(V, C, device=dev, dtype=_dt(torch, dtype))
+    table[V - 500:] = torch.randn(500, C, device=dev)
+    table[0], table[1 << 21] = 3.0, 5.0
+    rows = np.unique(ids[(ids >= 0) & (ids < V)])
+    at = {int(v): k for k, v in enumerate(rows)}
+    small = np.array([at.get(int(i), -1) for i in ids], np.int32)
+    tr = torch.from_numpy(rows).to(dev).long()
+    out = cg.embed_fwd(ti, table, 0.5)
+    check(out, T.embed_fwd(small, table[tr].float().cpu().numpy(), 0.5), 0.0, 0, dtype)
+    del table
+    g = torch.randn(N, C, device=dev).to(_dt(torch, dtype))
+    got = cg.embed_bwd(ti, g, V, 0.5)
+    gh = g.float().cpu().numpy()
+    check(got[tr], T.embed_bwd(small, gh, len(rows), 0.5), T.embed_bwd(small, np.abs(gh), len(rows), 0.5), N, dtype)
+    got[tr] = 0
+    assert not got.any()
+    del got
+    # rows of 2^23 elements apart
+    n = 300
+    wide = torch.full((n, 1 << 23), 7.0, device=dev, dtype=g.dtype)
+    few = torch.randn(9, 64, device=dev).to(g.dtype)
+    ids = rng.integers(0, 9, n).astype(np.int32)
+    cg.embed_fwd(torch.from_numpy(ids).to(dev), few, 2.0, out=wide[:, :64])
+    check(wide[:, :64], T.embed_fwd(ids, few.float().cpu().numpy(), 2.0), 0.0, 0, dtype)
+    assert (wide[:, 64:] == 7.0).all()
+    gh = wide[:, :64].float().cpu().numpy()
+    got = cg.embed_bwd(torch.from_numpy(ids).to(dev), wide[:, :64], 9, 1.0)
+    check(got, T.embed_bwd(ids, gh, 9, 1.0), T.embed_bwd(ids, np.abs(gh), 9, 1.0), n, dtype)

@@ -417,3 +417,48 @@ def test_norm_gradient_into_rows_of_a_wider_array(tt, N, B, C, pitch, dtype):
         assert (full[:, [q for q in range(pitch) if q != k], :] == 7.0).all(), k
     none = cg.norm_act_bwd(x, m, r, w, w, g, 2, seg, want=("gamma",), grad_x=full[:, 0, :])
     assert none[0] is None and (full[:, 0, :] == 7.0).all() and torch.equal(none[1], want[1])
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_norm_offsets_beyond_32_bits(tt, long):
+    """Rows that together pass 2^31 elements, short segments throughout or one
+    long one before them: the last segments against the oracle, and the sums
+    over all rows from rows that are alike."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[norm] beyond 32 bits, long {long}", flush=True)
+    C, G, S, tail = 128, 4, 40, 25
+    B = (1 << 24) // S + 2 * tail           # 2.15e9 elements
+    N, last = B * S, tail * S
+    rng = np.random.default_rng(3)
+    part, dpart = (T.bf16(rng.standard_normal((last, C)).astype(np.float32)) for _ in range(2))
+    x = torch.ones(N, C, device=dev, dtype=torch.bfloat16)
+    x[1::2] = -1.0                          # mean 0, deviation 1 in every even-sized segment
+    g = torch.zeros_like(x)
+    x[-last:] = torch.from_numpy(part).to(dev)
+    g[-last:] = torch.from_numpy(dpart).to(dev)
+    ptr = np.arange(B + 1, dtype=np.int64) * S
+    if long:
+        ptr = np.concatenate([[0], ptr[-tail - 1:]])
+    seg = torch.from_numpy(ptr.astype(np.int32)).to(dev)
+    gamma, beta = (rng.standard_normal(C).astype(np.float32) for _ in range(2))
+    tgm, tbt = torch.from_numpy(gamma).to(dev), torch.from_numpy(beta).to(dev)
+    y, m, r = cg.norm_act_fwd(x, tgm, tbt, G, seg, act="silu")
+    end = np.arange(tail + 1) * S
+    wy, wm, wr = T.norm_fwd(part, gamma, beta, end, G, 1e-5, "silu")
+    ty, tdx, tdg, tdb = bounds(part.astype(np.float64), gamma, beta, dpart, end, G, 1e-5, "silu")
+    host = lambda v: v.double().cpu().numpy()  # noqa: E731
+    assert np.all(np.abs(host(y[-last:]) - wy) <= ty + 2.0 ** -8 * np.abs(wy))
+    assert np.all(np.abs(host(m[-tail:]) - wm) <= 2 * U * np.abs(wm) + 2 * U)
+    assert np.all(np.abs(host(r[-tail:]) - wr) <= 4 * U * wr)
+    assert (m[:-tail] == 0).all() and (r[:-tail] == r[0]).all()
+    for k in (0, 1):                        # all rows alike are the same bits
+        rows = y[k:N - last:2]
+        assert (rows == rows[0]).all()
+    del y, rows
+    dx, dg, db = cg.norm_act_bwd(x, m, r, tgm, tbt, g, G, seg, act="silu")
+    wdx, wdg, wdb = T.norm_bwd(part, gamma, beta, dpart, end, G, 1e-5, "silu")
+    assert np.all(np.abs(host(dx[-last:]) - wdx) <= tdx + 2.0 ** -8 * np.abs(wdx))
+    assert np.all(np.abs(host(dg) - wdg) <= tdg + 2 * U * np.abs(wdg))
+    assert np.all(np.abs(host(db) - wdb) <= tdb + 2 * U * np.abs(wdb))
+    assert not dx[:-last].any()

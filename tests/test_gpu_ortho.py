@@ -249,3 +249,26 @@ def test_orthogonalize_several_chunks_to_a_block(tt, B, m, n, steps, dtype):
     few = cg.orthogonalize(t[:1], steps)        # the same matrix by more blocks: the partial sums differ in order
     want, norms = T.orthogonalize(G[0], steps, QUINTIC, 1e-7, 1.0)
     assert np.linalg.norm(few[0].double().cpu().numpy() - want) <= tolerance(norms, QUINTIC, 1.0, dtype)
+
+
+def test_orthogonalize_offsets_beyond_32_bits(tt):
+    """A stack of more than 2^31 elements (matrices by tiles, by chunks, and one
+    per block): the last matrix as by itself, from the same form, or within the
+    tolerance."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    for B, m, n in ((9, 15000, 16200), (260, 128, 1 << 16), (131500, 128, 128)):
+        print(f"[ortho] beyond 32 bits {B} x {m} x {n}", flush=True)
+        assert B * m * n > 1 << 31
+        t = torch.zeros(B, m, n, device=dev, dtype=torch.bfloat16)
+        last = gradient(np.random.default_rng(5), 1, min(m, 40), min(n, 300), "noise")[0]
+        t[-1, :last.shape[0], :last.shape[1]] = torch.from_numpy(last).to(dev)
+        last = t[-1, :last.shape[0], :last.shape[1]].float().cpu().numpy()
+        out = cg.orthogonalize(t, 1)
+        assert not out[:-1].any()
+        got = out[-1]
+        want, norms = T.orthogonalize(last, 1, QUINTIC, 1e-7, 1.0)     # zero rows and columns stay zero
+        err = np.linalg.norm(got[:last.shape[0], :last.shape[1]].double().cpu().numpy() - want)
+        assert err <= tolerance(norms, QUINTIC, 1.0, "bf16")
+        assert not got[last.shape[0]:].any() and not got[:, last.shape[1]:].any()
+        del t, out, got
