@@ -39,6 +39,7 @@ _c_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _ip = ctypes.POINTER(ctypes.c_int)
 _int, _f32, _size = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_drop = [ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p]  # p, seed, offset, step
 _sp = ctypes.POINTER(ctypes.c_size_t)
 
 # name -> (restype, argtypes); mirrors include/cgtp.h and include/cgtp_train.h
@@ -81,6 +82,12 @@ SIGNATURES = {
     "cgtp_orthogonalize_workspace_size": (_int, [_int] + [_c_i64] * 3 + [_sp]),
     "cgtp_orthogonalize": (_int, [_int] + [_c_i64] * 3 + [_int] + [ctypes.c_double] * 3 + [_f32, _f32, _vp, _vp, _vp,
                                                                                         _size, _vp]),
+    "cgtp_dropout": (_int, [_int, _c_i64, _c_i64] + _drop + [_vp, _c_i64] * 3 + [_vp]),
+    "cgtp_linear_act_workspace_size": (_int, [_int] + [_c_i64] * 3 + [_int, _sp]),
+    "cgtp_linear_act_fwd": (_int, [_int, _int] + [_c_i64] * 3 + [_vp, _c_i64, _vp, _vp, _vp, _c_i64] + _drop +
+                            [_vp, _vp, _c_i64, _vp, _size, _vp]),
+    "cgtp_linear_act_bwd": (_int, [_int, _int] + [_c_i64] * 3 + [_vp, _c_i64, _vp, _vp, _vp, _c_i64] + _drop +
+                            [_vp, _c_i64, _vp, _vp, _vp, _size, _vp]),
     "cgtp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

@@ -1,0 +1,656 @@
+// cgtp_linear.hip -- the product of rows with a weight matrix, with bias, activation,
+// dropout and residual in its epilogue, and its gradients, on the bf16 matrix cores:
+//
+//   z = x W + b,  y = r + drop(act(z))                  [N][K] times [K][M]
+//   dz = drop(g) act'(z),  dx = dz W^T,  dW = x^T dz,  db = sum of dz's rows
+//
+// Precision.  An fp32 operand v is cut into three bf16 numbers, h = bf16(v),
+// m = bf16(v - h), l = bf16(v - h - m), which together hold all 24 bits of every
+// normal value (bf16 has fp32's range, so no units are needed), and
+//   u v = hu hv + (hu mv + mu hv) + (hu lv + mu mv + lu hv)
+// leaves out terms of at most 2^-25 of the product.  Six bf16 products with fp32
+// accumulation run at a sixth of the bf16 rate where fp32 matrix instructions reach a
+// sixteenth.  An infinity leaves a NaN in its remainders, so that the results it reaches
+// are not finite (NaN, where an fp32 product might give an infinity).
+// bf16 operands are multiplied as they are; dz of a bf16 gradient is formed in fp32 and
+// rounded once to bf16 for the two products (not for db): its rounding is as large as
+// that of the result and independent of it.  The scale of the dropout multiplies the
+// fp32 results, so that without an activation dz is exact.
+//
+// Layout.  Tiles go through registers into LDS, as they lie in memory: a row of a tile is a
+// run of k (x, g, W in dx) or, where the contraction runs across the rows (W in y; x and g
+// in dW), a row of one k.  Operands of the first kind are read by 16 bytes along k, of the
+// second by the transposing LDS read (ds_read_b64_tr_b16: sixteen lanes read 4 rows of 16
+// elements, lane i gets column i).  The matrix instruction takes the weights' side first:
+// a lane then holds four outputs in a row of one of the N rows.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "cgtp_act.h"
+#include "cgtp_drop.h"
+#include "cgtp_internal.h"
+#include "cgtp_train_internal.h"
+#include "cgtp_vec.h"
+
+namespace cgtp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBK = 32;  // contraction per step
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef float f8 __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// block x of n works on tile `xcd_order`: blocks go to the XCDs in turn, so that an XCD's
+// tiles are neighbours and share its L2
+__device__ __forceinline__ int64_t xcd_order(int64_t x, int64_t n)
+{
+    const int64_t q = n / kXcds, rest = n % kXcds, c = x % kXcds;
+    return c * q + (c < rest ? c : rest) + x / kXcds;
+}
+
+enum : int { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct GemmArgs {
+    const void *A, *B;        // kFwd: x, W; kDx: g, W; kDw: x, g
+    const void* Z;            // z [N][M], or nullptr: act none
+    int64_t lda, ldb, ldz;
+    int64_t rows, cols, depth;  // of the result, of the contraction
+    int64_t tr, tc;           // tiles along rows and columns
+    int64_t splits, run;      // parts of the contraction and their length
+    int act;
+    Drop drop;
+    // epilogue
+    const float* bias;
+    const void* R;
+    void *out, *zout;
+    int64_t ldr, ldo;
+    float* part;       // [splits][rows][cols] where splits > 1
+    float* db;         // kDw: the gradient of the bias, or nullptr
+    double* db_part;   // [splits][cols]
+    bool want;         // kDw: the product itself is wanted
+};
+
+// eight elements of a row as they lie in memory
+template <class T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int j) const
+    {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+        return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = uint4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void load(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    // the first n elements, by elements
+    __device__ __forceinline__ void load_some(const T* p, int n)
+    {
+        clear();
+        T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) e[j] = p[j];
+    }
+};
+
+// planes that an operand of type T is cut into
+template <class T>
+constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+
+// v as kPlanes bf16 vectors
+template <int NP>
+__device__ __forceinline__ void cut(f8 v, b8 (&p)[NP])
+{
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        p[i] = __builtin_convertvector(v, b8);
+        if (i + 1 < NP) v -= __builtin_convertvector(p[i], f8);
+    }
+}
+
+// A tile of RUNS rows of WIDTH elements in LDS, kPlanes of them.  ALONG: the contraction
+// runs along the rows.  The pads put the rows that are read together on different banks.
+template <class T, int RUNS, int WIDTH, bool ALONG>
+struct Side {
+    static constexpr int NP = kPlanes<T>;
+    static constexpr int kLd = WIDTH + (ALONG ? 8 : 16);
+    static constexpr int kHalves = RUNS * kLd;  // of one plane
+    static constexpr int kPer = WIDTH / 8;                     // blocks of eight in a row
+    static constexpr int kEach = RUNS * WIDTH / 8 / kThreads;  // and per thread
+    static_assert(RUNS * WIDTH % (8 * kThreads) == 0 && kThreads % (WIDTH / 8) == 0, "whole blocks per thread");
+
+    // fragment of the 32 x 16 operand whose first row (of the matrix instruction's) is r0
+    // and whose first k is k0
+    __device__ static __forceinline__ b8 read(const uint16_t* s, int plane, int r0, int k0, int lane)
+    {
+        const uint16_t* p = s + plane * kHalves;
+        if constexpr (ALONG) {
+            return *reinterpret_cast<const b8*>(p + (r0 + (lane & 31)) * kLd + k0 + 8 * (lane >> 5));
+        } else {
+            const int l = lane & 15;
+            p += (k0 + 8 * (lane >> 5) + l / 4) * kLd + r0 + (lane & 16) + 4 * (l % 4);
+            auto tr = [](const uint16_t* q) {
+                return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s4*)(const __attribute__((address_space(3))) void*)q);
+            };
+            struct Two {
+                s4 a, b;
+            } t{tr(p), tr(p + 4 * kLd)};
+            return __builtin_bit_cast(b8, t);
+        }
+    }
+};
+
+// act'(z) and the mask of eight elements of g at (n, 8 q)
+__device__ __forceinline__ void slope8(const GemmArgs& a, uint64_t offset, f8& v, const float (&z)[8], int64_t n, int32_t q)
+{
+    if (a.Z) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= act_slope(a.act, z[j]);
+    }
+    if (a.drop.thr) {
+        const Drawn f = philox((uint32_t)q, (uint32_t)n, offset, a.drop.seed);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] : 0.0f;
+    }
+}
+
+// eight results of row n from channel c on, of which w are inside
+template <class T, int KIND, bool VEC>
+__device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, float (&v)[8], int64_t n, int32_t c, int w)
+{
+    constexpr int V = VEC ? kWide<T> : 1;
+    auto put = [&](T* p) {
+#pragma unroll
+        for (int j = 0; j < 8; j += V) {
+            float t[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[e] = v[j + e];
+            if (VEC || j < w) store_vec<T, V>(p + j, t);
+        }
+    };
+    if constexpr (KIND == kFwd) {
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += a.bias[j < w ? c + j : c];
+        }
+        if (a.zout) put((T*)a.zout + n * a.cols + c);
+        if (a.act != kNone) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = act_of(a.act, v[j]);
+        }
+        if (a.drop.thr) {
+            const Drawn f = philox((uint32_t)c / 8, (uint32_t)n, offset, a.drop.seed);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] * a.drop.scale : 0.0f;
+        }
+        if (a.R) {
+            const T* r = (const T*)a.R + n * a.ldr + c;
+#pragma unroll
+            for (int j = 0; j < 8; j += V) {
+                float t[V] = {};
+                if (VEC || j < w) load_vec<T, V>(t, r + j);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[j + e] += t[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= a.drop.scale;
+    }
+    put((T*)a.out + n * a.ldo + c);
+}
+
+// One BM x BN tile of the result (one part of its contraction).  VEC: every row of every
+// array begins on 16 bytes and is a multiple of eight elements long.
+template <class T, int KIND, int BM, int BN, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
+{
+    // rows' side P and columns' side Q
+    constexpr bool kAlongP = KIND != kDw, kAlongQ = KIND == kDx;
+    using P = Side<T, kAlongP ? BM : kBK, kAlongP ? kBK : BM, kAlongP>;
+    using Q = Side<T, kAlongQ ? BN : kBK, kAlongQ ? kBK : BN, kAlongQ>;
+    constexpr int NP = kPlanes<T>, WM = BM / 2, WN = BN / 2, FM = WM / 32, FN = WN / 32;
+    constexpr bool kSlopeP = KIND == kDx, kSlopeQ = KIND == kDw;
+    constexpr int kLdS = BN + 4, kHalf = BM / 2;  // the result leaves in two halves
+    constexpr int kTiles = (P::kHalves + Q::kHalves) * NP * 2, kOut = kHalf * kLdS * 4, kSums = kThreads * 64;
+    constexpr int kMem = kTiles > kOut ? kTiles : kOut;
+    __shared__ __attribute__((aligned(16))) char mem[KIND == kDw && kSums > kMem ? kSums : kMem];
+    uint16_t* sp = reinterpret_cast<uint16_t*>(mem);
+    uint16_t* sq = sp + P::kHalves * NP;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t at = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t tile = at / a.splits, part = at % a.splits;
+    const int64_t r0 = tile / a.tc * BM, c0 = tile % a.tc * BN;
+    const int64_t k0 = part * a.run, k1 = k0 + a.run < a.depth ? k0 + a.run : a.depth;
+    const uint64_t offset = drop_offset(a.drop);
+
+    // The thread's blocks of eight: row `run` of the tile, element 8 * c.
+    // Rows outside are taken as zero, elements outside too.
+    Raw8<T> rp[P::kEach], rq[Q::kEach], rz[kSlopeP ? P::kEach : kSlopeQ ? Q::kEach : 1];
+    auto fetch = [&](auto side, Raw8<T>* raw, const T* base, int64_t ld, int64_t n0, int64_t lim_n, int64_t e0,
+                     int64_t lim_e) {
+        using S = decltype(side);
+        constexpr int kPer = S::kPer;
+#pragma unroll
+        for (int i = 0; i < S::kEach; ++i) {
+            const int b = tid + i * kThreads;
+            const int64_t n = n0 + b / kPer, e = e0 + b % kPer * 8;
+            const bool in = n < lim_n && e < lim_e;
+            const T* p = base + (in ? n * ld + e : 0);
+            if constexpr (VEC) {
+                raw[i].load(p);
+                if (!in) raw[i].clear();
+            } else {
+                raw[i].load_some(p, !in ? 0 : lim_e - e < 8 ? (int)(lim_e - e) : 8);
+            }
+        }
+    };
+    const bool product = KIND != kDw || a.want;
+    auto load = [&](int64_t k) {
+        if constexpr (kAlongP) {
+            fetch(P{}, rp, (const T*)a.A, a.lda, r0, a.rows, k, k1);
+            if (kSlopeP && a.Z) fetch(P{}, rz, (const T*)a.Z, a.ldz, r0, a.rows, k, k1);
+        } else {
+            if (product) fetch(P{}, rp, (const T*)a.A, a.lda, k, k1, r0, a.rows);
+        }
+        if constexpr (kAlongQ) {
+            fetch(Q{}, rq, (const T*)a.B, a.ldb, c0, a.cols, k, k1);
+        } else {
+            fetch(Q{}, rq, (const T*)a.B, a.ldb, k, k1, c0, a.cols);
+            if (kSlopeQ && a.Z) fetch(Q{}, rz, (const T*)a.Z, a.ldz, k, k1, c0, a.cols);
+        }
+    };
+    double sum[8] = {};  // of dz's columns 8 (tid % kPer) .. + 7
+    const bool sums = KIND == kDw && a.db && r0 == 0;
+    auto put = [&](auto side, uint16_t* s, const Raw8<T>* raw, auto slope, int64_t n0, int64_t e0) {
+        using S = decltype(side);
+        constexpr int kPer = S::kPer;
+#pragma unroll
+        for (int i = 0; i < S::kEach; ++i) {
+            const int b = tid + i * kThreads;
+            b8 planes[NP];
+            if constexpr (decltype(slope)::value || NP > 1) {
+                f8 v;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = raw[i][j];
+                if constexpr (decltype(slope)::value) {
+                    float z[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] = rz[i][j];
+                    slope8(a, offset, v, z, n0 + b / kPer, (int32_t)((e0 + b % kPer * 8) / 8));
+                    if (sums) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
+                    }
+                }
+                cut(v, planes);
+            } else {
+                planes[0] = __builtin_bit_cast(b8, raw[i].v[0]);
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                *reinterpret_cast<b8*>(s + p * S::kHalves + b / kPer * S::kLd + b % kPer * 8) = planes[p];
+        }
+    };
+    auto store = [&](int64_t k) {
+        if constexpr (kSlopeP) put(P{}, sp, rp, std::true_type{}, r0, k);
+        else if (product) put(P{}, sp, rp, std::false_type{}, 0, 0);
+        if constexpr (kSlopeQ) put(Q{}, sq, rq, std::true_type{}, k, c0);
+        else put(Q{}, sq, rq, std::false_type{}, 0, 0);
+    };
+
+    f16v acc[FM][FN];
+#pragma unroll
+    for (int x = 0; x < FM; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[x][y][q] = 0.0f;
+    const int wm = wave / 2 * WM, wn = wave % 2 * WN;
+    auto multiply = [&]() {
+#pragma unroll
+        for (int ks = 0; ks < kBK; ks += 16) {
+            b8 fp[FM][NP], fq[FN][NP];
+#pragma unroll
+            for (int p = NP - 1; p >= 0; --p) {
+#pragma unroll
+                for (int x = 0; x < FM; ++x) fp[x][p] = P::read(sp, p, wm + 32 * x, ks, lane);
+#pragma unroll
+                for (int y = 0; y < FN; ++y) fq[y][p] = Q::read(sq, p, wn + 32 * y, ks, lane);
+            }
+            // the smallest terms first
+#pragma unroll
+            for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                for (int p = 0; p <= o; ++p)
+#pragma unroll
+                    for (int x = 0; x < FM; ++x)
+#pragma unroll
+                        for (int y = 0; y < FN; ++y)
+                            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[y][o - p], fp[x][p], acc[x][y], 0, 0, 0);
+        }
+    };
+
+    load(k0);
+    for (int64_t k = k0; k < k1; k += kBK) {
+        store(k);
+        __syncthreads();
+        if (k + kBK < k1) load(k + kBK);
+        if (product) multiply();
+        __syncthreads();
+    }
+
+    if (KIND == kDw && sums) {
+        // the threads of one column block, in order
+        constexpr int kPer = BN / 8;
+        double* s = reinterpret_cast<double*>(mem);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j * kThreads + tid] = sum[j];
+        __syncthreads();
+        if (tid < BN) {
+            double t = 0.0;
+            for (int i = 0; i < kThreads / kPer; ++i) t += s[tid % 8 * kThreads + i * kPer + tid / 8];
+            if (c0 + tid < a.cols) {
+                if (a.splits > 1) a.db_part[part * a.cols + c0 + tid] = t;
+                else a.db[c0 + tid] = (float)(t * (double)a.drop.scale);
+            }
+        }
+        __syncthreads();
+    }
+    if (!product) return;
+
+    // A lane holds row lane % 32 and columns 8 g + 4 (lane / 32) + 0 .. 3 of each tile of 32:
+    // through LDS, so that rows leave in whole lines.
+    float* s = reinterpret_cast<float*>(mem);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h) __syncthreads();
+        if (wave / 2 == h) {
+#pragma unroll
+            for (int x = 0; x < FM; ++x)
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float4 v{acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+                        *reinterpret_cast<float4*>(&s[(32 * x + (lane & 31)) * kLdS + wn + 32 * y + 8 * g + 4 * (lane >> 5)]) = v;
+                    }
+        }
+        __syncthreads();
+        for (int b = tid; b < kHalf * BN / 8; b += kThreads) {
+            const int i = b / (BN / 8), j = b % (BN / 8) * 8;
+            const int64_t n = r0 + h * kHalf + i, c = c0 + j;
+            if (n >= a.rows || c >= a.cols) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(&v[e]) = *reinterpret_cast<const float4*>(&s[i * kLdS + j + e]);
+            const int w = a.cols - c < 8 ? (int)(a.cols - c) : 8;
+            if (a.splits > 1) {
+                float* p = a.part + (part * a.rows + n) * a.cols + c;
+                if constexpr (VEC) {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(p + e) = *reinterpret_cast<const float4*>(&v[e]);
+                } else {
+                    for (int e = 0; e < w; ++e) p[e] = v[e];
+                }
+            } else {
+                finish8<T, KIND, VEC>(a, offset, v, n, (int32_t)c, w);
+            }
+        }
+    }
+}
+
+// The parts' sums, in order and in fp64, and the epilogue; the gradient of the bias by the
+// blocks behind the others.
+template <class T, int KIND, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_linear_join(GemmArgs a, int64_t blocks)
+{
+    const int64_t per = (a.cols + 7) / 8, q = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if ((int64_t)blockIdx.x >= blocks) {
+        const int64_t c = ((int64_t)blockIdx.x - blocks) * kThreads + threadIdx.x;
+        if (c >= a.cols) return;
+        double t = 0.0;
+        for (int64_t i = 0; i < a.splits; ++i) t += a.db_part[i * a.cols + c];
+        a.db[c] = (float)(t * (double)a.drop.scale);
+        return;
+    }
+    if (q >= a.rows * per) return;
+    const int64_t n = q / per, c = q % per * 8;
+    const int w = a.cols - c < 8 ? (int)(a.cols - c) : 8;
+    double t[8] = {};
+    const float* p = a.part + n * a.cols + c;
+    for (int64_t i = 0; i < a.splits; ++i, p += a.rows * a.cols) {
+        constexpr int V = VEC ? 4 : 1;
+#pragma unroll
+        for (int j = 0; j < 8; j += V) {
+            float v[V] = {};
+            if (VEC || j < w) load_vec<float, V>(v, p + j);
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[j + e] += (double)v[e];
+        }
+    }
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)t[j];
+    finish8<T, KIND, VEC>(a, drop_offset(a.drop), v, n, (int32_t)c, w);
+}
+
+// out[0 .. n) = 0, in 4-byte words (a kernel: a captured graph may hold it)
+__global__ void __launch_bounds__(kThreads) k_linear_zero(int64_t bytes, char* __restrict__ out)
+{
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 2;
+    for (int64_t q = i; q < bytes; q += (int64_t)gridDim.x * kThreads * 2) *reinterpret_cast<uint16_t*>(out + q) = 0;
+}
+
+// ---- choice of tiles and parts ------------------------------------------------------------
+struct Plan {
+    int bm, bn;
+    int64_t tr, tc, splits, run;
+};
+
+// Tiles of 128 where they fill the chip or the result is that wide; the contraction is cut
+// where tiles alone leave compute units idle, into parts of at least eight steps.
+Plan plan_of(int64_t rows, int64_t cols, int64_t depth)
+{
+    Plan p{};
+    auto side = [](int64_t n) { return n > 64 ? 128 : 64; };
+    p.bm = side(rows);
+    p.bn = side(cols);
+    auto tiles = [&]() { return cdiv64(rows, p.bm) * cdiv64(cols, p.bn); };
+    if (tiles() < 256) p.bm = 64;
+    if (tiles() < 256) p.bn = 64;
+    p.tr = cdiv64(rows, p.bm);
+    p.tc = cdiv64(cols, p.bn);
+    const int64_t n = p.tr * p.tc, most = cdiv64(depth, 8 * kBK);
+    int64_t s = n >= 256 ? 1 : 512 / n;
+    s = s < most ? s : most;
+    s = s < 1 ? 1 : s;
+    p.run = cdiv64(cdiv64(depth, s), kBK) * kBK;
+    p.splits = p.run > 0 ? cdiv64(depth, p.run) : 1;
+    return p;
+}
+
+size_t part_bytes(const Plan& p, int64_t rows, int64_t cols, bool bias)
+{
+    if (p.splits <= 1) return 0;
+    const size_t b = (size_t)(p.splits * rows * cols) * 4;
+    return (b + 255) / 256 * 256 + (bias ? (size_t)(p.splits * cols) * 8 : 0);
+}
+
+Plan plan_kind(const LinShape& n, int kind)
+{
+    return kind == kFwd ? plan_of(n.N, n.M, n.K) : kind == kDx ? plan_of(n.N, n.K, n.M) : plan_of(n.K, n.M, n.N);
+}
+
+template <class T, int KIND, bool VEC>
+hipError_t run(GemmArgs& a, const Plan& p, void* ws, hipStream_t s)
+{
+    a.tr = p.tr;
+    a.tc = p.tc;
+    a.splits = p.splits;
+    a.run = p.run;
+    if (p.splits > 1) {
+        a.part = (float*)ws;
+        a.db_part = (double*)((char*)ws + ((size_t)(p.splits * a.rows * a.cols) * 4 + 255) / 256 * 256);
+    }
+    const dim3 grid((unsigned)(p.tr * p.tc * p.splits)), block(kThreads);
+    if (p.bm == 128 && p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 128, VEC>), grid, block, 0, s, a);
+    else if (p.bm == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 64, VEC>), grid, block, 0, s, a);
+    else if (p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 64, 128, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_linear<T, KIND, 64, 64, VEC>), grid, block, 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits <= 1) return e;
+    const int64_t blocks = KIND != kDw || a.want ? cdiv64(a.rows * cdiv64(a.cols, 8), kThreads) : 0;
+    const int64_t more = KIND == kDw && a.db ? cdiv64(a.cols, kThreads) : 0;
+    hipLaunchKernelGGL((k_linear_join<T, KIND, VEC>), dim3((unsigned)(blocks + more)), block, 0, s, a, blocks);
+    return hipGetLastError();
+}
+
+template <class T, int KIND>
+hipError_t run(GemmArgs& a, const Plan& p, bool vec, void* ws, hipStream_t s)
+{
+    return vec ? run<T, KIND, true>(a, p, ws, s) : run<T, KIND, false>(a, p, ws, s);
+}
+
+template <class T>
+hipError_t fwd(const LinShape& n, const void* x, const void* W, const float* bias, const void* R, void* z, void* y,
+               void* ws, hipStream_t s)
+{
+    GemmArgs a{};
+    a.A = x;
+    a.B = W;
+    a.lda = n.ldx;
+    a.ldb = n.M;
+    a.rows = n.N;
+    a.cols = n.M;
+    a.depth = n.K;
+    a.act = n.act;
+    a.drop = n.drop;
+    a.bias = bias;
+    a.R = R;
+    a.out = y;
+    a.zout = z;
+    a.ldr = n.ldr;
+    a.ldo = n.ldy;
+    constexpr int64_t es = sizeof(T);
+    const bool vec = n.K % 8 == 0 && n.M % 8 == 0 && aligned_rows(x, n.ldx, es) && aligned_rows(W, n.M, es) &&
+                     aligned_rows(y, n.ldy, es) && (!z || aligned_rows(z, n.M, es)) &&
+                     (!R || aligned_rows(R, n.ldr, es));
+    return run<T, kFwd>(a, plan_kind(n, kFwd), vec, ws, s);
+}
+
+template <class T>
+hipError_t bwd(const LinShape& n, const void* x, const void* W, const void* z, const void* g, void* dx, void* dW,
+               float* db, void* ws, hipStream_t s)
+{
+    constexpr int64_t es = sizeof(T);
+    GemmArgs a{};
+    a.Z = n.act == kNone ? nullptr : z;
+    a.ldz = n.M;
+    a.act = n.act;
+    a.drop = n.drop;
+    const bool vec = n.K % 8 == 0 && n.M % 8 == 0 && aligned_rows(g, n.ldg, es) && (!a.Z || aligned_rows(z, n.M, es));
+    if (dx) {
+        GemmArgs b = a;
+        b.A = g;
+        b.B = W;
+        b.lda = n.ldg;
+        b.ldb = n.M;
+        b.rows = n.N;
+        b.cols = n.K;
+        b.depth = n.M;
+        b.out = dx;
+        b.ldo = n.ldd;
+        const hipError_t e = run<T, kDx>(b, plan_kind(n, kDx),
+                                         vec && aligned_rows(W, n.M, es) && aligned_rows(dx, n.ldd, es), ws, s);
+        if (e != hipSuccess) return e;
+    }
+    if (dW || db) {
+        a.A = x;  // not read where only the bias is wanted
+        a.B = g;
+        a.lda = n.ldx;
+        a.ldb = n.ldg;
+        a.rows = n.K;
+        a.cols = n.M;
+        a.depth = n.N;
+        a.out = dW;
+        a.ldo = n.M;
+        a.db = db;
+        a.want = dW != nullptr;
+        return run<T, kDw>(a, plan_kind(n, kDw),
+                           vec && (!dW || (aligned_rows(x, n.ldx, es) && aligned_rows(dW, n.M, es))), ws, s);
+    }
+    return hipSuccess;
+}
+
+hipError_t zero(void* p, int64_t bytes, hipStream_t s)
+{
+    int64_t blocks = cdiv64(bytes, kThreads * 8);
+    blocks = blocks < 4096 ? blocks : 4096;
+    hipLaunchKernelGGL(k_linear_zero, dim3((unsigned)blocks), dim3(kThreads), 0, s, bytes, (char*)p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool linear_fits(const LinShape& n)
+{
+    if (n.N == 0) return true;
+    for (int kind : {kFwd, kDx, kDw}) {
+        const Plan p = plan_kind(n, kind);
+        const double blocks = (double)p.tr * (double)p.tc * (double)p.splits;
+        const double rows = kind == kDw ? (double)n.K : (double)n.N, cols = kind == kDx ? (double)n.K : (double)n.M;
+        const double join = p.splits > 1 ? rows * (cols / 8 + 1) / kThreads : 0.0;
+        if (blocks >= 16777216.0 || join >= 16777216.0) return false;
+    }
+    return true;
+}
+
+size_t linear_workspace_bytes(const LinShape& n, bool backward)
+{
+    if (n.N == 0) return 0;
+    if (!backward) return part_bytes(plan_kind(n, kFwd), n.N, n.M, false);
+    const size_t dx = part_bytes(plan_kind(n, kDx), n.N, n.K, false), dw = part_bytes(plan_kind(n, kDw), n.K, n.M, true);
+    return dx > dw ? dx : dw;
+}
+
+hipError_t launch_linear_fwd(const LinShape& n, const void* x, const void* W, const float* bias, const void* residual,
+                             void* z, void* y, void* ws, hipStream_t s)
+{
+    if (n.N == 0) return hipSuccess;
+    return n.dtype == kF32 ? fwd<float>(n, x, W, bias, residual, z, y, ws, s)
+                           : fwd<bf16_t>(n, x, W, bias, residual, z, y, ws, s);
+}
+
+hipError_t launch_linear_bwd(const LinShape& n, const void* x, const void* W, const void* z, const void* grad_y,
+                             void* grad_x, void* grad_W, float* grad_bias, void* ws, hipStream_t s)
+{
+    if (n.N == 0) {
+        hipError_t e = hipSuccess;
+        if (grad_W) e = zero(grad_W, n.K * n.M * dtype_size(n.dtype), s);
+        if (e == hipSuccess && grad_bias) e = zero(grad_bias, n.M * 4, s);
+        return e;
+    }
+    return n.dtype == kF32 ? bwd<float>(n, x, W, z, grad_y, grad_x, grad_W, grad_bias, ws, s)
+                           : bwd<bf16_t>(n, x, W, z, grad_y, grad_x, grad_W, grad_bias, ws, s);
+}
+
+}  // namespace cgtp

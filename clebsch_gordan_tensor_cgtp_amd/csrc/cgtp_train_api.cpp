@@ -89,6 +89,35 @@ cgtp_status_t check_ortho(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64
     return CGTP_OK;
 }
 
+// the generator's arguments; thr = 65536 p, rounded
+cgtp_status_t check_drop(double p, uint64_t seed, uint64_t offset, const int64_t* step, cgtp::Drop* d)
+{
+    if (!(p >= 0.0 && p < 1.0) || (step && bad(step, 8))) return CGTP_ERR_INVALID_ARG;
+    const double t = std::floor(65536.0 * p + 0.5);
+    d->thr = t < 65535.0 ? (uint32_t)t : 65535u;
+    d->scale = (float)(1.0 / (1.0 - d->thr / 65536.0));
+    d->seed = seed;
+    d->offset = offset;
+    d->step = d->thr ? step : nullptr;
+    return CGTP_OK;
+}
+
+constexpr int64_t kMaxLinearRows = int64_t(1) << 30, kMaxLinearWidth = 1 << 16;
+
+cgtp_status_t check_linear(cgtp_dtype_t dtype, int64_t n_rows, int64_t in, int64_t out, cgtp::LinShape* n)
+{
+    if (!type_ok(dtype) || n_rows < 0 || in < 1 || out < 1) return CGTP_ERR_INVALID_ARG;
+    if (n_rows >= kMaxLinearRows || in > kMaxLinearWidth || out > kMaxLinearWidth) return CGTP_ERR_UNSUPPORTED;
+    *n = cgtp::LinShape{};
+    n->dtype = dtype;
+    n->N = n_rows;
+    n->K = in;
+    n->M = out;
+    return cgtp::linear_fits(*n) ? CGTP_OK : CGTP_ERR_UNSUPPORTED;
+}
+
+bool act_ok(int act) { return act == CGTP_ACT_NONE || act == CGTP_ACT_SILU || act == CGTP_ACT_TANH; }
+
 cgtp::OrthoShape ortho_shape(cgtp_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols)
 {
     cgtp::OrthoShape o{};
@@ -208,6 +237,99 @@ cgtp_status_t cgtp_norm_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_ro
     n.ldd = ld_dx;
     return hip_status(cgtp::launch_norm_bwd(n, x, mean, rstd, gamma, beta, grad_y, grad_x, grad_gamma, grad_beta, ws,
                                             stream));
+}
+
+// ---- dropout ---------------------------------------------------------------------------
+cgtp_status_t cgtp_dropout(cgtp_dtype_t dtype, int64_t n_rows, int64_t channels, double p, uint64_t seed,
+                           uint64_t offset, const int64_t* step, const void* x, int64_t ld_x, const void* residual,
+                           int64_t ld_r, void* out, int64_t ld_out, hipStream_t stream)
+{
+    if (!type_ok(dtype) || n_rows < 0 || channels < 1 || n_rows >= kMaxRows) return CGTP_ERR_INVALID_ARG;
+    if (channels > kMaxEmbedChannels) return CGTP_ERR_UNSUPPORTED;
+    cgtp::DropShape d{};
+    const cgtp_status_t st = check_drop(p, seed, offset, step, &d.drop);
+    if (st != CGTP_OK) return st;
+    if (n_rows == 0) return CGTP_OK;
+    const int64_t es = cgtp::dtype_size(dtype);
+    if (bad_rows(x, n_rows, ld_x, channels, es) || bad_rows(out, n_rows, ld_out, channels, es))
+        return CGTP_ERR_INVALID_ARG;
+    if (residual && bad_rows(residual, n_rows, ld_r, channels, es)) return CGTP_ERR_INVALID_ARG;
+    d.dtype = dtype;
+    d.N = n_rows;
+    d.C = channels;
+    d.ldx = ld_x;
+    d.ldr = ld_r;
+    d.ldo = ld_out;
+    return hip_status(cgtp::launch_dropout(d, x, residual, out, stream));
+}
+
+// ---- product with bias, activation, dropout and residual -------------------------------
+cgtp_status_t cgtp_linear_act_workspace_size(cgtp_dtype_t dtype, int64_t n_rows, int64_t in_channels,
+                                             int64_t out_channels, int backward, size_t* bytes)
+{
+    if (!bytes) return CGTP_ERR_INVALID_ARG;
+    cgtp::LinShape n;
+    const cgtp_status_t st = check_linear(dtype, n_rows, in_channels, out_channels, &n);
+    if (st != CGTP_OK) return st;
+    *bytes = cgtp::linear_workspace_bytes(n, backward != 0);
+    return CGTP_OK;
+}
+
+cgtp_status_t cgtp_linear_act_fwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_rows, int64_t in_channels,
+                                  int64_t out_channels, const void* x, int64_t ld_x, const void* W, const float* bias,
+                                  const void* residual, int64_t ld_r, double p, uint64_t seed, uint64_t offset,
+                                  const int64_t* step, void* z, void* y, int64_t ld_y, void* ws, size_t ws_bytes,
+                                  hipStream_t stream)
+{
+    cgtp::LinShape n;
+    cgtp_status_t st = check_linear(dtype, n_rows, in_channels, out_channels, &n);
+    if (st != CGTP_OK) return st;
+    if (!act_ok(act)) return CGTP_ERR_INVALID_ARG;
+    st = check_drop(p, seed, offset, step, &n.drop);
+    if (st != CGTP_OK) return st;
+    if (n_rows == 0) return CGTP_OK;
+    const int64_t es = cgtp::dtype_size(dtype);
+    if (bad_rows(x, n_rows, ld_x, in_channels, es) || bad(W, es) || bad_rows(y, n_rows, ld_y, out_channels, es))
+        return CGTP_ERR_INVALID_ARG;
+    if ((bias && bad(bias, 4)) || (z && bad(z, es))) return CGTP_ERR_INVALID_ARG;
+    if (residual && bad_rows(residual, n_rows, ld_r, out_channels, es)) return CGTP_ERR_INVALID_ARG;
+    st = check_workspace(ws, ws_bytes, cgtp::linear_workspace_bytes(n, false));
+    if (st != CGTP_OK) return st;
+    n.act = act;
+    n.ldx = ld_x;
+    n.ldr = ld_r;
+    n.ldy = ld_y;
+    return hip_status(cgtp::launch_linear_fwd(n, x, W, bias, residual, z, y, ws, stream));
+}
+
+cgtp_status_t cgtp_linear_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_rows, int64_t in_channels,
+                                  int64_t out_channels, const void* x, int64_t ld_x, const void* W, const void* z,
+                                  const void* grad_y, int64_t ld_dy, double p, uint64_t seed, uint64_t offset,
+                                  const int64_t* step, void* grad_x, int64_t ld_dx, void* grad_W, float* grad_bias,
+                                  void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    cgtp::LinShape n;
+    cgtp_status_t st = check_linear(dtype, n_rows, in_channels, out_channels, &n);
+    if (st != CGTP_OK) return st;
+    if (!act_ok(act)) return CGTP_ERR_INVALID_ARG;
+    st = check_drop(p, seed, offset, step, &n.drop);
+    if (st != CGTP_OK) return st;
+    if (!grad_x && !grad_W && !grad_bias) return CGTP_OK;
+    const int64_t es = cgtp::dtype_size(dtype);
+    if ((grad_W && bad(grad_W, es)) || (grad_bias && bad(grad_bias, 4))) return CGTP_ERR_INVALID_ARG;
+    if (n_rows > 0) {
+        if (bad_rows(grad_y, n_rows, ld_dy, out_channels, es)) return CGTP_ERR_INVALID_ARG;
+        if (act != CGTP_ACT_NONE && bad(z, es)) return CGTP_ERR_INVALID_ARG;
+        if (grad_x && (bad(W, es) || bad_rows(grad_x, n_rows, ld_dx, in_channels, es))) return CGTP_ERR_INVALID_ARG;
+        if (grad_W && bad_rows(x, n_rows, ld_x, in_channels, es)) return CGTP_ERR_INVALID_ARG;
+        st = check_workspace(ws, ws_bytes, cgtp::linear_workspace_bytes(n, true));
+        if (st != CGTP_OK) return st;
+    }
+    n.act = act;
+    n.ldx = ld_x;
+    n.ldg = ld_dy;
+    n.ldd = ld_dx;
+    return hip_status(cgtp::launch_linear_bwd(n, x, W, z, grad_y, grad_x, grad_W, grad_bias, ws, stream));
 }
 
 // ---- orthogonalised update -------------------------------------------------------------

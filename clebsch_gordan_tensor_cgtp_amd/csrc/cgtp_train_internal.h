@@ -1,6 +1,6 @@
 // cgtp_train_internal.h -- shapes, workspaces and launchers of the node-side operators
-// (kernels in cgtp_embed.hip, cgtp_norm.hip and cgtp_ortho.hip;
-// entry points in cgtp_train_api.cpp).
+// (kernels in cgtp_embed.hip, cgtp_norm.hip, cgtp_ortho.hip, cgtp_dropout.hip and
+// cgtp_linear.hip; entry points in cgtp_train_api.cpp).
 #pragma once
 
 #include <stddef.h>
@@ -78,5 +78,40 @@ bool ortho_bounded(double a, double b, double c, int steps);
 size_t ortho_workspace_bytes(const OrthoShape& o);
 
 hipError_t launch_orthogonalize(const OrthoShape& o, const void* G, void* out, void* ws, hipStream_t s);
+
+// ---- dropout ---------------------------------------------------------------------------
+struct Drop {
+    uint32_t thr;  // of 65536: fields below it are dropped; 0: none
+    float scale;   // 1 / (1 - thr / 65536)
+    uint64_t seed, offset;
+    const int64_t* step;  // on the device, added to the offset; or nullptr
+};
+
+struct DropShape {
+    int dtype;
+    int64_t N;  // rows (below 2^31)
+    int64_t C;
+    int64_t ldx, ldr, ldo;
+    Drop drop;
+};
+
+hipError_t launch_dropout(const DropShape& d, const void* x, const void* residual, void* out, hipStream_t s);
+
+// ---- product with bias, activation, dropout and residual -------------------------------
+struct LinShape {
+    int dtype, act;
+    int64_t N, K, M;  // rows (below 2^30), inputs, outputs
+    int64_t ldx, ldr, ldy, ldg, ldd;  // row strides of x, residual, y, grad_y, grad_x
+    Drop drop;
+};
+
+// whether the launches stay below 2^32 threads
+bool linear_fits(const LinShape& n);
+size_t linear_workspace_bytes(const LinShape& n, bool backward);
+
+hipError_t launch_linear_fwd(const LinShape& n, const void* x, const void* W, const float* bias, const void* residual,
+                             void* z, void* y, void* ws, hipStream_t s);
+hipError_t launch_linear_bwd(const LinShape& n, const void* x, const void* W, const void* z, const void* grad_y,
+                             void* grad_x, void* grad_W, float* grad_bias, void* ws, hipStream_t s);
 
 }  // namespace cgtp

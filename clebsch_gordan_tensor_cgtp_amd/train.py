@@ -1,7 +1,9 @@
 """The node-side operators of a training step, over the C ABI of
 include/cgtp_train.h: embedding of species (token) ids and its gradient, group
 normalisation with an activation over ragged segments and its gradient, the
-orthogonalised update of a stack of weight matrices.
+orthogonalised update of a stack of weight matrices, dropout from a
+counter-based generator, the product of rows with a weight matrix with bias,
+activation, dropout and residual in its epilogue and its gradients.
 
 Each function checks types, devices and shapes, allocates outputs and
 workspace with torch (device memory only) unless they are given, and calls the
@@ -309,3 +311,140 @@ def orthogonalize(grad, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: f
     _call("cgtp_orthogonalize", dev, d, B, m, n, steps, a, b, c, eps, scale, grad.data_ptr(), out.data_ptr(),
           at, room)
     return out
+
+
+# ---- dropout -------------------------------------------------------------------------
+def _generator(p, seed, offset, step, dev):
+    """The generator's arguments as the library takes them."""
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"the dropout probability must be in [0, 1), got {p}")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"seed and offset must be in [0, 2^64), got {seed} and {offset}")
+    if step is None:
+        return p, seed, offset, None
+    _need(step, "step", torch.int64, (1,), dev)
+    return p, seed, offset, step.data_ptr()
+
+
+def _row_shape(t, name):
+    """(N, C) of [N][C] or [B][S][C] rows."""
+    shape = t.shape
+    if len(shape) == 2:
+        return shape[0], shape[1]
+    if len(shape) == 3:
+        return shape[0] * shape[1], shape[2]
+    raise ValueError(f"{name} must be [N][C] or [B][S][C]")
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None, out=None) -> torch.Tensor:
+    """residual + (x / (1 - p) where an element is kept, else 0), the mask from
+    Philox4x32-10 by the seed, the offset, the element's row and its channel (as
+    include/cgtp_train.h says; p counts in steps of 1 / 65536): nothing is stored,
+    and the gradient of x is ``dropout(grad, p, seed, offset, step)``.
+
+    x: [N][C] or [B][S][C] rows (B S rows), which may have a stride, as
+    ``residual`` and ``out`` may.  Calls of one seed need offsets of their own;
+    ``step``, an int64 tensor [1] on the device, is added to the offset when the
+    kernel runs, so that the replays of a captured graph draw new masks."""
+    d = _dtype(x, "x")
+    N, C = _row_shape(x, "x")
+    dev = x.device
+    ldx = _rows(x, "x")
+    if residual is None:
+        r, ldr = None, C
+    else:
+        _like(residual, "residual", x.dtype, x.shape, dev)
+        r, ldr = residual.data_ptr(), _rows(residual, "residual")
+    if out is None:
+        out, ldo = x.new_empty(x.shape), C
+    else:
+        _like(out, "out", x.dtype, x.shape, dev)
+        ldo = _rows(out, "out")
+    _call("cgtp_dropout", dev, d, N, C, *_generator(p, seed, offset, step, dev), x.data_ptr(), ldx, r, ldr,
+          out.data_ptr(), ldo)
+    return out
+
+
+# ---- product with bias, activation, dropout and residual ---------------------------------
+def linear_act_workspace_size(dtype, n_rows: int, in_channels: int, out_channels: int, backward: bool) -> int:
+    return _bytes("cgtp_linear_act_workspace_size", _DTYPES[dtype], n_rows, in_channels, out_channels, int(backward))
+
+
+def _weights(W, K, x):
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise TypeError("W must be a torch.Tensor [in][out]")
+    M = W.shape[1]
+    _need(W, "W", x.dtype, (K, M), x.device)
+    return M
+
+
+def linear_act_fwd(x, W, bias=None, act: str = "silu", residual=None, p_drop: float = 0.0, seed: int = 0,
+                   offset: int = 0, step=None, save: bool = True, out=None, ws=None):
+    """(y, z): z = x W + bias, y = residual + dropout(act(z)).
+
+    x: [N][in] or [B][S][in] rows, which may have a stride (``features[:, 0, :]``),
+    as ``residual`` and ``out`` of y's shape may; W [in][out]; bias [out] float32 or
+    None.  act: "none", "silu" or "tanh".  p_drop, seed, offset and step are
+    ``dropout``'s, its mask by y's rows and channels.  z (contiguous, y's shape) is
+    what the backward needs: None where ``save`` is false or act is "none"."""
+    d = _dtype(x, "x")
+    N, K = _row_shape(x, "x")
+    dev = x.device
+    M = _weights(W, K, x)
+    ldx = _rows(x, "x")
+    b = _channel(bias, "bias", M, dev)
+    shape = x.shape[:-1] + (M,)
+    if residual is None:
+        r, ldr = None, M
+    else:
+        _like(residual, "residual", x.dtype, shape, dev)
+        r, ldr = residual.data_ptr(), _rows(residual, "residual")
+    if out is None:
+        out, ldo = x.new_empty(shape), M
+    else:
+        _like(out, "out", x.dtype, shape, dev)
+        ldo = _rows(out, "out")
+    a = _act(act)
+    z = x.new_empty(shape) if save and a != L.CGTP_ACT_NONE else None
+    nbytes = _bytes("cgtp_linear_act_workspace_size", d, N, K, M, 0)
+    at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
+    _call("cgtp_linear_act_fwd", dev, d, a, N, K, M, x.data_ptr(), ldx, W.data_ptr(), b, r, ldr,
+          *_generator(p_drop, seed, offset, step, dev), None if z is None else z.data_ptr(), out.data_ptr(), ldo, at,
+          room)
+    return out, z
+
+
+def linear_act_bwd(x, W, z, grad_y, act: str = "silu", p_drop: float = 0.0, seed: int = 0, offset: int = 0, step=None,
+                   want=("x", "W", "bias"), grad_x=None, ws=None):
+    """(grad_x, grad_W, grad_bias) of <grad_y, y> for linear_act_fwd's y on the
+    same arguments and its z (None for act "none"); the residual's gradient is
+    grad_y.  A gradient not in ``want`` comes back as None.  ``grad_x`` of x's shape
+    may be a view with a row stride; grad_W has W's type, grad_bias is float32."""
+    d = _dtype(x, "x")
+    N, K = _row_shape(x, "x")
+    dev = x.device
+    M = _weights(W, K, x)
+    shape = x.shape[:-1] + (M,)
+    _like(grad_y, "grad_y", x.dtype, shape, dev)
+    ldx, ldg = _rows(x, "x"), _rows(grad_y, "grad_y")
+    a = _act(act)
+    if a == L.CGTP_ACT_NONE:
+        zp = None
+    else:
+        _need(z, "z", x.dtype, shape, dev)
+        zp = z.data_ptr()
+    if "x" not in want:
+        gx, ldd = None, K
+    elif grad_x is None:
+        gx, ldd = x.new_empty(x.shape), K
+    else:
+        _like(grad_x, "grad_x", x.dtype, x.shape, dev)
+        gx, ldd = grad_x, _rows(grad_x, "grad_x")
+    gW = torch.empty_like(W) if "W" in want else None
+    gb = torch.empty(M, dtype=torch.float32, device=dev) if "bias" in want else None
+    nbytes = _bytes("cgtp_linear_act_workspace_size", d, N, K, M, 1)
+    at, room, ws = _workspace(ws, nbytes, dev)  # (held until the call is out)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _call("cgtp_linear_act_bwd", dev, d, a, N, K, M, x.data_ptr(), ldx, W.data_ptr(), zp, grad_y.data_ptr(), ldg,
+          *_generator(p_drop, seed, offset, step, dev), ptr(gx), ldd, ptr(gW), ptr(gb), at, room)
+    return gx, gW, gb

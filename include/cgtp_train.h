@@ -8,7 +8,11 @@
  *     channels-last rows (the invariant, l = 0, rows of the atoms of each
  *     structure of a batch), and its gradient;
  *   - the orthogonalised update of a stack of weight matrices (the mixing
- *     matrices of cgtp_path_mix_fwd, say) by Newton-Schulz products.
+ *     matrices of cgtp_path_mix_fwd, say) by Newton-Schulz products;
+ *   - dropout from a counter-based generator, with a mask that is never stored;
+ *   - the product of rows with a weight matrix with bias, activation, dropout and
+ *     residual in its epilogue (the layers of the radial network that makes the
+ *     convolution's edge weights, the update of the invariant rows), and its gradients.
  *
  * Conventions, beside those of cgtp.h (device pointers owned by the caller,
  * asynchronous on the given stream, outputs overwritten, every sum in a fixed
@@ -17,7 +21,7 @@
  *   - no plan: sizes are arguments, and the element type of the large arrays
  *     is a cgtp_dtype_t.  Statistics, gamma and beta and their gradients are
  *     fp32 whatever the type.  Sums over rows run in fp64, elementwise terms
- *     in fp32; Newton-Schulz products run as three fp16 products with fp32
+ *     in fp32 (products over channels or rows accumulate in fp32); Newton-Schulz products run as three fp16 products with fp32
  *     accumulation, which together carry 23 bits of their operands, for either
  *     type (in fp64 for matrices of up to 16 rows or columns and 32768
  *     elements); each result is rounded to its type once.
@@ -110,6 +114,57 @@ cgtp_status_t cgtp_norm_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_ro
                                 const float* beta, const void* grad_y, int64_t ld_dy, void* grad_x, int64_t ld_dx,
                                 float* grad_gamma, float* grad_beta, void* ws, size_t ws_bytes,
                                 hipStream_t stream);
+
+/* ---- dropout -----------------------------------------------------------------------
+ * out[n][c] = residual[n][c] + (kept(n, c) ? x[n][c] / (1 - t / 65536) : 0),
+ *   t = min(floor(65536 p + 1/2), 65535),  0 <= p < 1,
+ * residual NULL counting as zeros.  kept(n, c) holds where field c mod 8 (16 bits
+ * each, from the lowest) of the 128 bits of Philox4x32-10 at the counter
+ * (c div 8, n, offset low, offset high) and the key (seed low, seed high) is at
+ * least t.  So p counts in steps of 1/65536, the mean of the values is kept
+ * exactly, and the mask depends on the seed, the offset, n and c alone: the gradient
+ * of x is the same call on the gradient of out (the residual's is that gradient
+ * itself).  Calls of one seed need offsets of their own.  step: NULL, or a
+ * device int64 that is read when the kernel runs and added to the offset (modulo
+ * 2^64), so that the replays of a captured graph draw new masks when it is advanced.
+ * What is dropped is zero, whatever x holds there.  Rows are ld elements apart. */
+cgtp_status_t cgtp_dropout(cgtp_dtype_t dtype, int64_t n_rows, int64_t channels, double p, uint64_t seed,
+                           uint64_t offset, const int64_t* step, const void* x, int64_t ld_x, const void* residual,
+                           int64_t ld_r, void* out, int64_t ld_out, hipStream_t stream);
+
+/* ---- product with bias, activation, dropout and residual ---------------------------
+ *   z = x W + bias,   y = residual + drop(act(z))
+ * of n_rows rows x (in_channels values, ld_x elements apart), W [in_channels]
+ * [out_channels] and bias [out_channels] fp32 (NULL: zeros); residual and y have
+ * out_channels values to a row, ld_r and ld_y apart (residual NULL: zeros).  drop is
+ * cgtp_dropout's with p, seed, offset and step (p = 0: none), its mask by the rows and
+ * channels of y.  z [n_rows][out_channels] is what the backward needs (not for
+ * CGTP_ACT_NONE); NULL where it is not wanted.  y is formed from z before z is rounded.
+ * fp32 operands are multiplied as three bf16 numbers each, whose six products hold 24
+ * bits, with fp32 accumulation; where a row of x or a column of W holds an infinity or
+ * a NaN (or a value of 3.39e38 or more) the results it reaches are not finite.
+ * Up to 2^30 rows and 65536 channels. */
+
+/* Workspace bytes of one direction (backward 0 or 1). */
+cgtp_status_t cgtp_linear_act_workspace_size(cgtp_dtype_t dtype, int64_t n_rows, int64_t in_channels,
+                                             int64_t out_channels, int backward, size_t* bytes);
+
+cgtp_status_t cgtp_linear_act_fwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_rows, int64_t in_channels,
+                                  int64_t out_channels, const void* x, int64_t ld_x, const void* W, const float* bias,
+                                  const void* residual, int64_t ld_r, double p, uint64_t seed, uint64_t offset,
+                                  const int64_t* step, void* z, void* y, int64_t ld_y, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
+
+/* Backward of L = <grad_y, y>, with dz = drop(grad_y) * act'(z) from the forward's z
+ * and the same p, seed, offset and step:
+ *   grad_x = dz W^T,   grad_W = x^T dz,   grad_bias[c] = sum_n dz[n][c]
+ * (the residual's gradient is grad_y).  z is not read for CGTP_ACT_NONE, x only for
+ * grad_W and W only for grad_x.  Each gradient may be NULL. */
+cgtp_status_t cgtp_linear_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_rows, int64_t in_channels,
+                                  int64_t out_channels, const void* x, int64_t ld_x, const void* W, const void* z,
+                                  const void* grad_y, int64_t ld_dy, double p, uint64_t seed, uint64_t offset,
+                                  const int64_t* step, void* grad_x, int64_t ld_dx, void* grad_W, float* grad_bias,
+                                  void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---- orthogonalised update ---------------------------------------------------------
  * out = scale * Q(G) for each of `batch` matrices [rows][cols] (contiguous), by
