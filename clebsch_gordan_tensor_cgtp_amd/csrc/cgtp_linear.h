@@ -1,0 +1,161 @@
+// cgtp_linear.h -- what the kernels of the product with its epilogue share (device code;
+// cgtp_linear.hip and cgtp_linear_wide.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "cgtp_act.h"
+#include "cgtp_drop.h"
+#include "cgtp_internal.h"
+#include "cgtp_train_internal.h"
+#include "cgtp_vec.h"
+
+namespace cgtp {
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef float f8 __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// block x of n works on tile `xcd_order`: blocks go to the XCDs in turn, so that an XCD's
+// tiles are neighbours and share its L2
+__device__ __forceinline__ int64_t xcd_order(int64_t x, int64_t n)
+{
+    const int64_t q = n / kXcds, rest = n % kXcds, c = x % kXcds;
+    return c * q + (c < rest ? c : rest) + x / kXcds;
+}
+
+enum : int { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct GemmArgs {
+    const void *A, *B;        // kFwd: x, W; kDx: g, W; kDw: x, g
+    const void* Z;            // z [N][M], or nullptr: act none
+    int64_t lda, ldb, ldz;
+    int64_t rows, cols, depth;  // of the result, of the contraction
+    int64_t tr, tc;           // tiles along rows and columns
+    int64_t splits, run;      // parts of the contraction and their length
+    int act;
+    Drop drop;
+    // epilogue
+    const float* bias;
+    const void* R;
+    void *out, *zout;
+    int64_t ldr, ldo;
+    float* part;       // [splits][rows][cols] where splits > 1
+    float* db;         // kDw: the gradient of the bias, or nullptr
+    double* db_part;   // [db_splits][cols]
+    int64_t db_splits;
+    bool want;         // kDw: the product itself is wanted
+};
+
+// eight elements of a row as they lie in memory
+template <class T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ float operator[](int j) const
+    {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+        return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = uint4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void load(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    // the first n elements, by elements
+    __device__ __forceinline__ void load_some(const T* p, int n)
+    {
+        clear();
+        T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) e[j] = p[j];
+    }
+};
+
+// planes that an operand of type T is cut into
+template <class T>
+constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+
+// v as kPlanes bf16 vectors
+template <int NP>
+__device__ __forceinline__ void cut(f8 v, b8 (&p)[NP])
+{
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        p[i] = __builtin_convertvector(v, b8);
+        if (i + 1 < NP) v -= __builtin_convertvector(p[i], f8);
+    }
+}
+
+// act'(z) and the mask of eight elements of g at (n, 8 q)
+__device__ __forceinline__ void slope8(const GemmArgs& a, uint64_t offset, f8& v, const float (&z)[8], int64_t n, int32_t q)
+{
+    if (a.Z) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= act_slope(a.act, z[j]);
+    }
+    if (a.drop.thr) {
+        const Drawn f = philox((uint32_t)q, (uint32_t)n, offset, a.drop.seed);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] : 0.0f;
+    }
+}
+
+// eight results of row n from channel c on, of which w are inside
+template <class T, int KIND, bool VEC>
+__device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, float (&v)[8], int64_t n, int32_t c, int w)
+{
+    constexpr int V = VEC ? kWide<T> : 1;
+    auto put = [&](T* p) {
+#pragma unroll
+        for (int j = 0; j < 8; j += V) {
+            float t[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[e] = v[j + e];
+            if (VEC || j < w) store_vec<T, V>(p + j, t);
+        }
+    };
+    if constexpr (KIND == kFwd) {
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += a.bias[j < w ? c + j : c];
+        }
+        if (a.zout) put((T*)a.zout + n * a.cols + c);
+        if (a.act != kNone) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = act_of(a.act, v[j]);
+        }
+        if (a.drop.thr) {
+            const Drawn f = philox((uint32_t)c / 8, (uint32_t)n, offset, a.drop.seed);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] * a.drop.scale : 0.0f;
+        }
+        if (a.R) {
+            const T* r = (const T*)a.R + n * a.ldr + c;
+#pragma unroll
+            for (int j = 0; j < 8; j += V) {
+                float t[V] = {};
+                if (VEC || j < w) load_vec<T, V>(t, r + j);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[j + e] += t[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= a.drop.scale;
+    }
+    put((T*)a.out + n * a.ldo + c);
+}
+
+}  // namespace cgtp

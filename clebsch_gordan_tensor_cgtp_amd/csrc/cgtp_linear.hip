@@ -29,100 +29,14 @@
 
 #include <type_traits>
 
-#include "cgtp_act.h"
-#include "cgtp_drop.h"
-#include "cgtp_internal.h"
-#include "cgtp_train_internal.h"
-#include "cgtp_vec.h"
+#include "cgtp_linear.h"
+#include "cgtp_linear_wide.h"
 
 namespace cgtp {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBK = 32;  // contraction per step
-
-typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-typedef float f8 __attribute__((ext_vector_type(8)));
-typedef float f16v __attribute__((ext_vector_type(16)));
-typedef short s4 __attribute__((ext_vector_type(4)));
-
-inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// block x of n works on tile `xcd_order`: blocks go to the XCDs in turn, so that an XCD's
-// tiles are neighbours and share its L2
-__device__ __forceinline__ int64_t xcd_order(int64_t x, int64_t n)
-{
-    const int64_t q = n / kXcds, rest = n % kXcds, c = x % kXcds;
-    return c * q + (c < rest ? c : rest) + x / kXcds;
-}
-
-enum : int { kFwd = 0, kDx = 1, kDw = 2 };
-
-struct GemmArgs {
-    const void *A, *B;        // kFwd: x, W; kDx: g, W; kDw: x, g
-    const void* Z;            // z [N][M], or nullptr: act none
-    int64_t lda, ldb, ldz;
-    int64_t rows, cols, depth;  // of the result, of the contraction
-    int64_t tr, tc;           // tiles along rows and columns
-    int64_t splits, run;      // parts of the contraction and their length
-    int act;
-    Drop drop;
-    // epilogue
-    const float* bias;
-    const void* R;
-    void *out, *zout;
-    int64_t ldr, ldo;
-    float* part;       // [splits][rows][cols] where splits > 1
-    float* db;         // kDw: the gradient of the bias, or nullptr
-    double* db_part;   // [splits][cols]
-    bool want;         // kDw: the product itself is wanted
-};
-
-// eight elements of a row as they lie in memory
-template <class T>
-struct Raw8 {
-    uint4 v[sizeof(T) / 2];
-    __device__ __forceinline__ float operator[](int j) const
-    {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
-        return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
-    }
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = uint4{0, 0, 0, 0};
-    }
-    __device__ __forceinline__ void load(const T* p)
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-    }
-    // the first n elements, by elements
-    __device__ __forceinline__ void load_some(const T* p, int n)
-    {
-        clear();
-        T* e = reinterpret_cast<T*>(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) e[j] = p[j];
-    }
-};
-
-// planes that an operand of type T is cut into
-template <class T>
-constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-
-// v as kPlanes bf16 vectors
-template <int NP>
-__device__ __forceinline__ void cut(f8 v, b8 (&p)[NP])
-{
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        p[i] = __builtin_convertvector(v, b8);
-        if (i + 1 < NP) v -= __builtin_convertvector(p[i], f8);
-    }
-}
 
 // A tile of RUNS rows of WIDTH elements in LDS, kPlanes of them.  ALONG: the contraction
 // runs along the rows.  The pads put the rows that are read together on different banks.
@@ -156,66 +70,6 @@ struct Side {
         }
     }
 };
-
-// act'(z) and the mask of eight elements of g at (n, 8 q)
-__device__ __forceinline__ void slope8(const GemmArgs& a, uint64_t offset, f8& v, const float (&z)[8], int64_t n, int32_t q)
-{
-    if (a.Z) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= act_slope(a.act, z[j]);
-    }
-    if (a.drop.thr) {
-        const Drawn f = philox((uint32_t)q, (uint32_t)n, offset, a.drop.seed);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] : 0.0f;
-    }
-}
-
-// eight results of row n from channel c on, of which w are inside
-template <class T, int KIND, bool VEC>
-__device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, float (&v)[8], int64_t n, int32_t c, int w)
-{
-    constexpr int V = VEC ? kWide<T> : 1;
-    auto put = [&](T* p) {
-#pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            float t[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) t[e] = v[j + e];
-            if (VEC || j < w) store_vec<T, V>(p + j, t);
-        }
-    };
-    if constexpr (KIND == kFwd) {
-        if (a.bias) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += a.bias[j < w ? c + j : c];
-        }
-        if (a.zout) put((T*)a.zout + n * a.cols + c);
-        if (a.act != kNone) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = act_of(a.act, v[j]);
-        }
-        if (a.drop.thr) {
-            const Drawn f = philox((uint32_t)c / 8, (uint32_t)n, offset, a.drop.seed);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] * a.drop.scale : 0.0f;
-        }
-        if (a.R) {
-            const T* r = (const T*)a.R + n * a.ldr + c;
-#pragma unroll
-            for (int j = 0; j < 8; j += V) {
-                float t[V] = {};
-                if (VEC || j < w) load_vec<T, V>(t, r + j);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[j + e] += t[e];
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= a.drop.scale;
-    }
-    put((T*)a.out + n * a.ldo + c);
-}
 
 // One BM x BN tile of the result (one part of its contraction).  VEC: every row of every
 // array begins on 16 bytes and is a multiple of eight elements long.
@@ -418,35 +272,60 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
     }
 }
 
-// The parts' sums, in order and in fp64, and the epilogue; the gradient of the bias by the
-// blocks behind the others.
-template <class T, int KIND, bool VEC>
+// The parts' sums in fp64 and the epilogue: G threads share eight results, each adds every
+// G-th part in order (G = 8 where there are many: one thread's loads would wait for each
+// other, 128 parts of 128 x 128 34 us), then one adds the eight.  The gradient of the bias by
+// the blocks behind the others, eight threads to a column.
+template <class T, int KIND, bool VEC, int G>
 __global__ void __launch_bounds__(kThreads) k_linear_join(GemmArgs a, int64_t blocks)
 {
-    const int64_t per = (a.cols + 7) / 8, q = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    constexpr int kEach = kThreads / G;
+    __shared__ double s[G > 1 ? kThreads * 8 : kThreads];
+    const int tid = threadIdx.x, g = tid / kEach;
     if ((int64_t)blockIdx.x >= blocks) {
-        const int64_t c = ((int64_t)blockIdx.x - blocks) * kThreads + threadIdx.x;
-        if (c >= a.cols) return;
+        constexpr int kCols = kThreads / 8;
+        const int64_t c = ((int64_t)blockIdx.x - blocks) * kCols + tid % kCols;
         double t = 0.0;
-        for (int64_t i = 0; i < a.splits; ++i) t += a.db_part[i * a.cols + c];
+        if (c < a.cols) {
+#pragma unroll 4
+            for (int64_t i = tid / kCols; i < a.db_splits; i += 8) t += a.db_part[i * a.cols + c];
+        }
+        s[tid] = t;
+        __syncthreads();
+        if (tid >= kCols || c >= a.cols) return;
+        for (int i = 1; i < 8; ++i) t += s[i * kCols + tid];
         a.db[c] = (float)(t * (double)a.drop.scale);
         return;
     }
-    if (q >= a.rows * per) return;
-    const int64_t n = q / per, c = q % per * 8;
+    const int64_t per = (a.cols + 7) / 8, q = (int64_t)blockIdx.x * kEach + tid % kEach;
+    const bool on = q < a.rows * per;
+    const int64_t n = on ? q / per : 0, c = on ? q % per * 8 : 0;
     const int w = a.cols - c < 8 ? (int)(a.cols - c) : 8;
     double t[8] = {};
-    const float* p = a.part + n * a.cols + c;
-    for (int64_t i = 0; i < a.splits; ++i, p += a.rows * a.cols) {
-        constexpr int V = VEC ? 4 : 1;
+    if (on) {
+        const float* p = a.part + (g * a.rows + n) * a.cols + c;
+#pragma unroll 4
+        for (int64_t i = g; i < a.splits; i += G, p += G * a.rows * a.cols) {
+            constexpr int V = VEC ? 4 : 1;
 #pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            float v[V] = {};
-            if (VEC || j < w) load_vec<float, V>(v, p + j);
+            for (int j = 0; j < 8; j += V) {
+                float v[V] = {};
+                if (VEC || j < w) load_vec<float, V>(v, p + j);
 #pragma unroll
-            for (int e = 0; e < V; ++e) t[j + e] += (double)v[e];
+                for (int e = 0; e < V; ++e) t[j + e] += (double)v[e];
+            }
         }
     }
+    if constexpr (G > 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j * kThreads + tid] = t[j];
+        __syncthreads();
+        if (g) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            for (int i = 1; i < G; ++i) t[j] += s[j * kThreads + i * kEach + tid];
+    }
+    if (!on) return;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (float)t[j];
@@ -462,42 +341,129 @@ __global__ void __launch_bounds__(kThreads) k_linear_zero(int64_t bytes, char* _
 
 // ---- choice of tiles and parts ------------------------------------------------------------
 struct Plan {
+    bool wide;   // planes (cgtp_linear_wide.hip)
     int bm, bn;
     int64_t tr, tc, splits, run;
 };
 
+constexpr int64_t kManySplits = 16;  // eight threads to a result from here on
+
+// the three products' result and contraction
+struct Dims {
+    int64_t rows, cols, depth;
+};
+
+Dims dims_of(const LinShape& n, int kind)
+{
+    return kind == kFwd ? Dims{n.N, n.M, n.K} : kind == kDx ? Dims{n.N, n.K, n.M} : Dims{n.K, n.M, n.N};
+}
+
 // Tiles of 128 where they fill the chip or the result is that wide; the contraction is cut
 // where tiles alone leave compute units idle, into parts of at least eight steps.
-Plan plan_of(int64_t rows, int64_t cols, int64_t depth)
+Plan plan_tiles(const Dims& d)
 {
     Plan p{};
     auto side = [](int64_t n) { return n > 64 ? 128 : 64; };
-    p.bm = side(rows);
-    p.bn = side(cols);
-    auto tiles = [&]() { return cdiv64(rows, p.bm) * cdiv64(cols, p.bn); };
+    p.bm = side(d.rows);
+    p.bn = side(d.cols);
+    auto tiles = [&]() { return cdiv64(d.rows, p.bm) * cdiv64(d.cols, p.bn); };
     if (tiles() < 256) p.bm = 64;
     if (tiles() < 256) p.bn = 64;
-    p.tr = cdiv64(rows, p.bm);
-    p.tc = cdiv64(cols, p.bn);
-    const int64_t n = p.tr * p.tc, most = cdiv64(depth, 8 * kBK);
+    p.tr = cdiv64(d.rows, p.bm);
+    p.tc = cdiv64(d.cols, p.bn);
+    const int64_t n = p.tr * p.tc, most = cdiv64(d.depth, 8 * kBK);
     int64_t s = n >= 256 ? 1 : 512 / n;
     s = s < most ? s : most;
     s = s < 1 ? 1 : s;
-    p.run = cdiv64(cdiv64(depth, s), kBK) * kBK;
-    p.splits = p.run > 0 ? cdiv64(depth, p.run) : 1;
+    p.run = cdiv64(cdiv64(d.depth, s), kBK) * kBK;
+    p.splits = cdiv64(d.depth, p.run);
     return p;
 }
 
-size_t part_bytes(const Plan& p, int64_t rows, int64_t cols, bool bias)
+Plan plan_wide(const Dims& d)
 {
-    if (p.splits <= 1) return 0;
-    const size_t b = (size_t)(p.splits * rows * cols) * 4;
-    return (b + 255) / 256 * 256 + (bias ? (size_t)(p.splits * cols) * 8 : 0);
+    Plan p{};
+    p.wide = true;
+    p.bm = p.bn = 256;
+    auto tiles = [&]() { return cdiv64(d.rows, p.bm) * cdiv64(d.cols, p.bn); };
+    if (tiles() < 256 && tiles() * cdiv64(d.depth, 1024) < 256) p.bm = p.bn = 128;
+    p.tr = cdiv64(d.rows, p.bm);
+    p.tc = cdiv64(d.cols, p.bn);
+    const int64_t n = p.tr * p.tc, fill = p.bm == 256 ? 256 : 512, most = cdiv64(d.depth, 512);
+    int64_t s = fill / n;
+    s = s < most ? s : most;
+    s = s < 1 ? 1 : s;
+    p.run = cdiv64(cdiv64(d.depth, s), kBK) * kBK;
+    p.splits = cdiv64(d.depth, p.run);
+    return p;
 }
 
-Plan plan_kind(const LinShape& n, int kind)
+constexpr int64_t kMaxWideLd = int64_t(1) << 22;  // row strides: a tile's byte offsets stay in 32 bits
+
+// Planes where the products bound the call, not memory or launches.
+bool wide_shape(const LinShape& n)
 {
-    return kind == kFwd ? plan_of(n.N, n.M, n.K) : kind == kDx ? plan_of(n.N, n.K, n.M) : plan_of(n.K, n.M, n.N);
+    return n.K % 8 == 0 && n.M % 8 == 0 && n.N >= 256 && n.K >= 256 && n.M >= 256 &&
+           (double)n.N * (double)n.K * (double)n.M >= 1e9;
+}
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+size_t part_bytes(const Plan& p, const Dims& d, bool bias)
+{
+    if (p.splits <= 1) return 0;
+    return round256((size_t)(p.splits * d.rows * d.cols) * 4) + (bias ? (size_t)(p.splits * d.cols) * 8 : 0);
+}
+
+Plan plan_of(const LinShape& n, int kind) { return plan_tiles(dims_of(n, kind)); }
+
+// rows of a block that forms planes, and how many blocks that makes
+int64_t plane_run(int64_t rows, int64_t cols)
+{
+    const int64_t across = cdiv64(cols, 256);
+    int64_t run = cdiv64(rows * across, 2048);
+    run = cdiv64(run < 8 ? 8 : run, 8) * 8;
+    return run;
+}
+
+// workspace of the wide form, by arrays
+struct WideSpace {
+    size_t dz, x, W, db, part, bytes;
+    WideSpace(const LinShape& n, bool backward)
+    {
+        const int np = n.dtype == kF32 ? 3 : 1;
+        size_t at = 0;
+        auto take = [&](size_t b) {
+            const size_t was = at;
+            at += round256(b);
+            return was;
+        };
+        dz = take(backward ? (size_t)(np * n.N * n.M) * 2 : 0);
+        x = take(np > 1 ? (size_t)(np * n.N * n.K) * 2 : 0);
+        W = take(np > 1 ? (size_t)(np * n.K * n.M) * 2 : 0);
+        db = take(backward ? (size_t)(cdiv64(n.N, plane_run(n.N, n.M)) * n.M) * 8 : 0);
+        size_t most = 0;
+        for (int kind : {kFwd, kDx, kDw}) {
+            if ((kind != kFwd) != backward) continue;
+            const size_t b = part_bytes(plan_wide(dims_of(n, kind)), dims_of(n, kind), false);
+            most = most > b ? most : b;
+        }
+        part = take(most);
+        bytes = at;
+    }
+};
+
+template <class T, int KIND, bool VEC>
+hipError_t join(const GemmArgs& a, hipStream_t s)
+{
+    const dim3 block(kThreads);
+    const bool many = a.splits >= kManySplits;
+    const int64_t blocks = a.splits > 1 && (KIND != kDw || a.want) ? cdiv64(a.rows * cdiv64(a.cols, 8), many ? kThreads / 8 : kThreads) : 0;
+    const int64_t more = KIND == kDw && a.db ? cdiv64(a.cols, kThreads / 8) : 0;
+    const dim3 grid((unsigned)(blocks + more));
+    if (many) hipLaunchKernelGGL((k_linear_join<T, KIND, VEC, 8>), grid, block, 0, s, a, blocks);
+    else hipLaunchKernelGGL((k_linear_join<T, KIND, VEC, 1>), grid, block, 0, s, a, blocks);
+    return hipGetLastError();
 }
 
 template <class T, int KIND, bool VEC>
@@ -509,25 +475,73 @@ hipError_t run(GemmArgs& a, const Plan& p, void* ws, hipStream_t s)
     a.run = p.run;
     if (p.splits > 1) {
         a.part = (float*)ws;
-        a.db_part = (double*)((char*)ws + ((size_t)(p.splits * a.rows * a.cols) * 4 + 255) / 256 * 256);
+        a.db_part = (double*)((char*)ws + round256((size_t)(p.splits * a.rows * a.cols) * 4));
+        a.db_splits = p.splits;
     }
     const dim3 grid((unsigned)(p.tr * p.tc * p.splits)), block(kThreads);
     if (p.bm == 128 && p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 128, VEC>), grid, block, 0, s, a);
     else if (p.bm == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 64, VEC>), grid, block, 0, s, a);
     else if (p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 64, 128, VEC>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_linear<T, KIND, 64, 64, VEC>), grid, block, 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits <= 1) return e;
-    const int64_t blocks = KIND != kDw || a.want ? cdiv64(a.rows * cdiv64(a.cols, 8), kThreads) : 0;
-    const int64_t more = KIND == kDw && a.db ? cdiv64(a.cols, kThreads) : 0;
-    hipLaunchKernelGGL((k_linear_join<T, KIND, VEC>), dim3((unsigned)(blocks + more)), block, 0, s, a, blocks);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || p.splits <= 1 ? e : join<T, KIND, VEC>(a, s);
 }
 
 template <class T, int KIND>
 hipError_t run(GemmArgs& a, const Plan& p, bool vec, void* ws, hipStream_t s)
 {
     return vec ? run<T, KIND, true>(a, p, ws, s) : run<T, KIND, false>(a, p, ws, s);
+}
+
+// one product of planes
+template <class T, int KIND>
+hipError_t run_wide(const LinShape& n, GemmArgs a, const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq,
+                    float* part, hipStream_t s)
+{
+    const Dims d = dims_of(n, KIND);
+    const Plan p = plan_wide(d);
+    WideArgs w{};
+    a.rows = d.rows;
+    a.cols = d.cols;
+    a.depth = d.depth;
+    a.tr = p.tr;
+    a.tc = p.tc;
+    a.splits = p.splits;
+    a.run = p.run;
+    a.part = part;
+    w.g = a;
+    w.P = P;
+    w.Q = Q;
+    w.ldp = ldp;
+    w.ldq = ldq;
+    w.planeP = KIND == kDx ? n.N * n.M : n.N * n.K;
+    w.planeQ = KIND == kDw ? n.N * n.M : n.K * n.M;
+    w.passes = kPlanes<T> == 3 ? 6 : 1;
+    w.side = p.bm;
+    const hipError_t e = launch_linear_wide(n.dtype, KIND, w, s);
+    return e != hipSuccess || (p.splits <= 1 && !(KIND == kDw && a.db)) ? e : join<T, KIND, true>(w.g, s);
+}
+
+// x or W as planes: as it is for bf16, else formed at `to`
+template <class T>
+hipError_t planes_of(const void* v, int64_t ld, int64_t rows, int64_t cols, void* to, const uint16_t*& p, int64_t& ldp,
+                     hipStream_t s)
+{
+    if (kPlanes<T> == 1) {
+        p = (const uint16_t*)v;
+        ldp = ld;
+        return hipSuccess;
+    }
+    PlaneArgs a{};
+    a.x = v;
+    a.ld = ld;
+    a.rows = rows;
+    a.cols = cols;
+    a.run = plane_run(rows, cols);
+    a.out = (uint16_t*)to;
+    p = a.out;
+    ldp = cols;
+    return launch_linear_planes(kF32, false, a, s);
 }
 
 template <class T>
@@ -554,7 +568,69 @@ hipError_t fwd(const LinShape& n, const void* x, const void* W, const float* bia
     const bool vec = n.K % 8 == 0 && n.M % 8 == 0 && aligned_rows(x, n.ldx, es) && aligned_rows(W, n.M, es) &&
                      aligned_rows(y, n.ldy, es) && (!z || aligned_rows(z, n.M, es)) &&
                      (!R || aligned_rows(R, n.ldr, es));
-    return run<T, kFwd>(a, plan_kind(n, kFwd), vec, ws, s);
+    if (vec && wide_shape(n) && n.ldx < kMaxWideLd) {
+        const WideSpace at(n, false);
+        char* w = (char*)ws;
+        const uint16_t *P, *Q;
+        int64_t ldp, ldq;
+        hipError_t e = planes_of<T>(x, n.ldx, n.N, n.K, w + at.x, P, ldp, s);
+        if (e == hipSuccess) e = planes_of<T>(W, n.M, n.K, n.M, w + at.W, Q, ldq, s);
+        return e != hipSuccess ? e : run_wide<T, kFwd>(n, a, P, ldp, Q, ldq, (float*)(w + at.part), s);
+    }
+    return run<T, kFwd>(a, plan_of(n, kFwd), vec, ws, s);
+}
+
+template <class T>
+hipError_t bwd_wide(const LinShape& n, GemmArgs a, const void* x, const void* W, const void* g, void* dx, void* dW,
+                    float* db, void* ws, hipStream_t s)
+{
+    const WideSpace at(n, true);
+    char* w = (char*)ws;
+    // dz: g itself where it is a plane already
+    const bool plain = kPlanes<T> == 1 && a.act == kNone && a.drop.thr == 0 && n.ldg < kMaxWideLd;
+    const uint16_t* dz = plain ? (const uint16_t*)g : (const uint16_t*)(w + at.dz);
+    const int64_t ldz = plain ? n.ldg : n.M;
+    hipError_t e = hipSuccess;
+    a.db = db;
+    a.db_part = (double*)(w + at.db);
+    if (!plain || db) {
+        PlaneArgs p{};
+        p.g = a;
+        p.x = g;
+        p.ld = n.ldg;
+        p.rows = n.N;
+        p.cols = n.M;
+        p.run = plane_run(n.N, n.M);
+        p.out = plain || !(dx || dW) ? nullptr : (uint16_t*)(w + at.dz);
+        a.db_splits = cdiv64(p.rows, p.run);
+        e = launch_linear_planes(n.dtype, true, p, s);
+        if (e != hipSuccess) return e;
+    }
+    float* part = (float*)(w + at.part);
+    const uint16_t *P, *Q;
+    int64_t ldp, ldq;
+    if (dx) {
+        GemmArgs b = a;
+        b.out = dx;
+        b.ldo = n.ldd;
+        b.db = nullptr;
+        e = planes_of<T>(W, n.M, n.K, n.M, w + at.W, Q, ldq, s);
+        if (e == hipSuccess) e = run_wide<T, kDx>(n, b, dz, ldz, Q, ldq, part, s);
+        if (e != hipSuccess) return e;
+    }
+    a.out = dW;
+    a.ldo = n.M;
+    a.want = dW != nullptr;
+    if (dW) {
+        e = planes_of<T>(x, n.ldx, n.N, n.K, w + at.x, P, ldp, s);
+        return e != hipSuccess ? e : run_wide<T, kDw>(n, a, P, ldp, dz, ldz, part, s);
+    }
+    if (db) {
+        a.rows = n.K;
+        a.cols = n.M;
+        return join<T, kDw, true>(a, s);
+    }
+    return hipSuccess;
 }
 
 template <class T>
@@ -568,6 +644,10 @@ hipError_t bwd(const LinShape& n, const void* x, const void* W, const void* z, c
     a.act = n.act;
     a.drop = n.drop;
     const bool vec = n.K % 8 == 0 && n.M % 8 == 0 && aligned_rows(g, n.ldg, es) && (!a.Z || aligned_rows(z, n.M, es));
+    const bool vec_x = vec && aligned_rows(W, n.M, es) && aligned_rows(dx, n.ldd, es);
+    const bool vec_w = vec && aligned_rows(x, n.ldx, es) && aligned_rows(dW, n.M, es);
+    if ((!dx || vec_x) && (!dW || vec_w) && vec && wide_shape(n) && (!dW || n.ldx < kMaxWideLd))
+        return bwd_wide<T>(n, a, x, W, g, dx, dW, db, ws, s);
     if (dx) {
         GemmArgs b = a;
         b.A = g;
@@ -579,8 +659,7 @@ hipError_t bwd(const LinShape& n, const void* x, const void* W, const void* z, c
         b.depth = n.M;
         b.out = dx;
         b.ldo = n.ldd;
-        const hipError_t e = run<T, kDx>(b, plan_kind(n, kDx),
-                                         vec && aligned_rows(W, n.M, es) && aligned_rows(dx, n.ldd, es), ws, s);
+        const hipError_t e = run<T, kDx>(b, plan_of(n, kDx), vec_x, ws, s);
         if (e != hipSuccess) return e;
     }
     if (dW || db) {
@@ -595,8 +674,7 @@ hipError_t bwd(const LinShape& n, const void* x, const void* W, const void* z, c
         a.ldo = n.M;
         a.db = db;
         a.want = dW != nullptr;
-        return run<T, kDw>(a, plan_kind(n, kDw),
-                           vec && (!dW || (aligned_rows(x, n.ldx, es) && aligned_rows(dW, n.M, es))), ws, s);
+        return run<T, kDw>(a, plan_of(n, kDw), dW ? vec_w : vec, ws, s);
     }
     return hipSuccess;
 }
@@ -615,11 +693,11 @@ bool linear_fits(const LinShape& n)
 {
     if (n.N == 0) return true;
     for (int kind : {kFwd, kDx, kDw}) {
-        const Plan p = plan_kind(n, kind);
+        const Dims d = dims_of(n, kind);
+        const Plan p = plan_tiles(d);
         const double blocks = (double)p.tr * (double)p.tc * (double)p.splits;
-        const double rows = kind == kDw ? (double)n.K : (double)n.N, cols = kind == kDx ? (double)n.K : (double)n.M;
-        const double join = p.splits > 1 ? rows * (cols / 8 + 1) / kThreads : 0.0;
-        if (blocks >= 16777216.0 || join >= 16777216.0) return false;
+        const double join = p.splits > 1 ? (double)d.rows * ((double)d.cols / 8 + 1) / 32 : 0.0;
+        if (blocks >= 16777216.0 || join >= 8388608.0) return false;
     }
     return true;
 }
@@ -627,9 +705,14 @@ bool linear_fits(const LinShape& n)
 size_t linear_workspace_bytes(const LinShape& n, bool backward)
 {
     if (n.N == 0) return 0;
-    if (!backward) return part_bytes(plan_kind(n, kFwd), n.N, n.M, false);
-    const size_t dx = part_bytes(plan_kind(n, kDx), n.N, n.K, false), dw = part_bytes(plan_kind(n, kDw), n.K, n.M, true);
-    return dx > dw ? dx : dw;
+    // (rows without 16-byte alignment take the tiles where others take planes)
+    size_t most = wide_shape(n) ? WideSpace(n, backward).bytes : 0;
+    for (int kind : {kFwd, kDx, kDw}) {
+        if ((kind != kFwd) != backward) continue;
+        const size_t b = part_bytes(plan_of(n, kind), dims_of(n, kind), kind == kDw);
+        most = most > b ? most : b;
+    }
+    return most;
 }
 
 hipError_t launch_linear_fwd(const LinShape& n, const void* x, const void* W, const float* bias, const void* residual,

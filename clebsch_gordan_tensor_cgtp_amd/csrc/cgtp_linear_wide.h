@@ -1,0 +1,30 @@
+// cgtp_linear_wide.h -- products of bf16 planes (kernels in cgtp_linear_wide.hip).
+#pragma once
+
+#include "cgtp_linear.h"
+
+namespace cgtp {
+
+struct WideArgs {
+    GemmArgs g;              // shapes, tiles and parts (whole steps long), epilogue; rows, cols multiples of 8
+    const uint16_t *P, *Q;   // planes of the rows' and the columns' operand, their rows on 16 bytes
+    int64_t ldp, ldq;        // below 2^22
+    int64_t planeP, planeQ;  // halves from one plane to the next
+    int32_t passes;          // 1 (one plane each) or 6 (three)
+    int32_t side;            // of a tile: 256 or 128
+};
+
+// out [planes][rows][cols] of rows x (fp32: three planes), or of dz = mask x act'(Z) with its
+// columns' sums to g.db_part [runs][cols] where g.db is set
+struct PlaneArgs {
+    GemmArgs g;      // Z, ldz, act, drop, db, db_part
+    const void* x;
+    int64_t ld, rows, cols;
+    int64_t run;     // rows of a block
+    uint16_t* out;   // or nullptr: the sums alone
+};
+
+hipError_t launch_linear_wide(int dtype, int kind, const WideArgs& w, hipStream_t s);
+hipError_t launch_linear_planes(int dtype, bool dz, const PlaneArgs& p, hipStream_t s);
+
+}  // namespace cgtp

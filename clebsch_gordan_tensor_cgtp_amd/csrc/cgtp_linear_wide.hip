@@ -1,0 +1,376 @@
+// cgtp_linear_wide.hip -- large products of bf16 planes: y, dx and dW where the matrix
+// cores bound them.
+//
+// The operands are bf16 in memory: x, W and g as the caller has them, or as planes that a
+// pass of their own has written to the workspace -- the three numbers of an fp32 operand
+// (cgtp_linear.hip), dz with its mask and slope (formed once instead of in every tile
+// that needs it; its columns' sums on the way).  A product of three planes each goes
+// through the contraction six times, the smallest products first, into one accumulator.
+//
+// A block computes a BM x BN tile, each wave WM x WN of it, through a ring of four LDS buffers
+// of 32 k that loads fill directly, three steps ahead; one barrier to a step.  The 16-byte
+// pieces of a buffer are swapped about (by the address that each lane loads from), so that
+// what a read instruction takes spreads over all banks: an operand whose rows run along k has
+// the pieces of row r at piece ^ (r / 4 % 4) of its 64 bytes, the other kind its 32-byte pieces
+// of row k at piece ^ 2 (k % 4).  Each wave takes its results through LDS by itself, 32 rows at a
+// time, so that they leave in whole lines.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "cgtp_linear.h"
+#include "cgtp_linear_wide.h"
+
+namespace cgtp {
+namespace {
+
+constexpr int kStep = 32, kStages = 4;
+
+// all but the last N of this wave's loads have arrived, its LDS reads are done, and every
+// wave of the block is here
+template <int N>
+__device__ __forceinline__ void wait_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+}
+
+// One operand's tile: WIDTH rows (or columns) of the result by kStep of the contraction.
+template <int WIDTH, int THR, bool ALONG>
+struct Tile {
+    static constexpr bool kAlong = ALONG;
+    static constexpr int kPieces = WIDTH * kStep / 8 / THR;
+    static_assert(WIDTH * kStep % (8 * THR) == 0, "whole pieces per thread");
+
+    // row (ALONG) or k and the source piece of 8 halves of this thread's piece i
+    __device__ static __forceinline__ void place(int i, int& row, int& col)
+    {
+        const int p = i * THR + (int)threadIdx.x;
+        if constexpr (ALONG) {
+            row = p / 4;
+            col = ((p & 3) ^ ((row >> 2) & 3)) * 8;
+        } else {
+            constexpr int kPer = WIDTH / 8;
+            row = p / kPer;
+            col = (((p % kPer) >> 1) ^ (2 * (row & 3))) * 16 + (p & 1) * 8;
+        }
+    }
+    // the 32 x 16 operand from row (column) r0 and k = 16 ks on
+    __device__ static __forceinline__ b8 read(const uint16_t* s, int r0, int ks, int lane)
+    {
+        if constexpr (ALONG) {
+            const int row = r0 + (lane & 31), piece = ks * 2 + (lane >> 5);
+            return *reinterpret_cast<const b8*>(s + row * kStep + ((piece ^ ((row >> 2) & 3)) * 8));
+        } else {
+            const int l = lane & 15, k = ks * 16 + 8 * (lane >> 5) + l / 4, col = r0 + (lane & 16);
+            const uint16_t* p = s + k * WIDTH + (((col >> 4) ^ (2 * (k & 3))) << 4) + 4 * (l % 4);
+            auto tr = [](const uint16_t* q) {
+                return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s4*)(const __attribute__((address_space(3))) void*)q);
+            };
+            struct Two {
+                s4 a, b;
+            } t{tr(p), tr(p + 4 * WIDTH)};
+            return __builtin_bit_cast(b8, t);
+        }
+    }
+};
+
+// tile r of tr x tc: bands of four columns, row by row within a band
+__device__ __forceinline__ void tile_at(int64_t r, int64_t tr, int64_t tc, int64_t& i, int64_t& j)
+{
+    const int64_t band = r / (4 * tr), c0 = band * 4, w = tc - c0 < 4 ? tc - c0 : 4;
+    r -= band * 4 * tr;
+    i = r / w;
+    j = c0 + r % w;
+}
+
+template <class T, int KIND, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(WideArgs w)
+{
+    constexpr int kThr = 64 * (BM / WM) * (BN / WN), FM = WM / 32, FN = WN / 32;
+    constexpr bool kAlongP = KIND != kDw, kAlongQ = KIND == kDx;
+    using P = Tile<BM, kThr, kAlongP>;
+    using Q = Tile<BN, kThr, kAlongQ>;
+    constexpr int kStage = (BM + BN) * kStep;  // halves
+    constexpr int kLd = WN + 4, kPatch = 32 * kLd * 4;
+    constexpr int kRing = kStages * kStage * 2, kOut = kPatch * (kThr / 64);
+    __shared__ __attribute__((aligned(16))) char mem[kRing > kOut ? kRing : kOut];
+    uint16_t* ring = reinterpret_cast<uint16_t*>(mem);
+    const GemmArgs& a = w.g;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t at = xcd_order(blockIdx.x, gridDim.x), tiles = a.tr * a.tc;
+    const int64_t part = at / tiles;
+    int64_t ti, tj;
+    tile_at(at % tiles, a.tr, a.tc, ti, tj);
+    const int64_t r0 = ti * BM, c0 = tj * BN;
+    const int64_t k0 = part * a.run, k1 = k0 + a.run < a.depth ? k0 + a.run : a.depth;
+    const int32_t full = (int32_t)((k1 - k0) / kStep), tail = (int32_t)((k1 - k0) % kStep);
+
+    // byte offsets of the thread's pieces from the step's first element; outside the result
+    // the last row or column is loaded again
+    uint32_t op[P::kPieces], oq[Q::kPieces];
+    auto offsets = [&](auto side, uint32_t* o, int64_t ld, int64_t first, int64_t lim) {
+        using S = decltype(side);
+#pragma unroll
+        for (int i = 0; i < S::kPieces; ++i) {
+            int row, col;
+            S::place(i, row, col);
+            const int64_t left = lim - first;
+            if constexpr (S::kAlong) row = row < left ? row : (int)left - 1;
+            else col = col < left ? col : (int)left - 8;
+            o[i] = (uint32_t)((uint32_t)row * (uint32_t)ld + (uint32_t)col) * 2u;
+        }
+    };
+    offsets(P{}, op, w.ldp, r0, a.rows);
+    offsets(Q{}, oq, w.ldq, c0, a.cols);
+    const uint16_t* p0 = w.P + (kAlongP ? r0 * w.ldp + k0 : k0 * w.ldp + r0);
+    const uint16_t* q0 = w.Q + (kAlongQ ? c0 * w.ldq + k0 : k0 * w.ldq + c0);
+    const int64_t stepP = kAlongP ? kStep : kStep * w.ldp, stepQ = kAlongQ ? kStep : kStep * w.ldq;
+    // planes of pass j of six: h l, m m, l h, h m, m h, h h (h, m, l = 0, 1, 2)
+    auto plane = [&](int j, const uint16_t*& p, const uint16_t*& q) {
+        const int ip = w.passes == 1 ? 0 : (0x010210 >> (4 * j)) & 15, iq = w.passes == 1 ? 0 : (0x001012 >> (4 * j)) & 15;
+        p = p0 + ip * w.planeP;
+        q = q0 + iq * w.planeQ;
+    };
+
+    f16v acc[FM][FN];
+#pragma unroll
+    for (int x = 0; x < FM; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+    const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+    struct Frag {
+        b8 p[FM], q[FN];
+    };
+    auto read = [&](Frag& f, const uint16_t* s, int ks) {
+#pragma unroll
+        for (int y = 0; y < FN; ++y) f.q[y] = Q::read(s + BM * kStep, wn + 32 * y, ks, lane);
+#pragma unroll
+        for (int x = 0; x < FM; ++x) f.p[x] = P::read(s, wm + 32 * x, ks, lane);
+    };
+    auto multiply = [&](const Frag& f) {
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+                acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[y], f.p[x], acc[x][y], 0, 0, 0);
+    };
+    Frag f0, f1;
+
+    // What is left of the contraction beyond whole steps goes through registers, zeros behind it.
+    if (tail) {
+        for (int j = 0; j < w.passes; ++j) {
+            const uint16_t *p, *q;
+            plane(j, p, q);
+            auto some = [&](auto side, const uint16_t* from, const uint32_t* o, uint16_t* to) {
+                using S = decltype(side);
+#pragma unroll
+                for (int i = 0; i < S::kPieces; ++i) {
+                    int row, col;
+                    S::place(i, row, col);
+                    const uint16_t* e = reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(from) + o[i]);
+                    uint16_t* t = to + (i * kThr + tid) * 8;
+                    for (int c = 0; c < 8; ++c) t[c] = (S::kAlong ? col + c : row) < tail ? e[c] : (uint16_t)0;
+                }
+            };
+            some(P{}, p + full * stepP, op, ring);
+            some(Q{}, q + full * stepQ, oq, ring + BM * kStep);
+            __syncthreads();
+            for (int ks = 0; ks < 2; ++ks) {
+                read(f0, ring, ks);
+                multiply(f0);
+            }
+            __syncthreads();
+        }
+    }
+
+    // the loads' place: the next step's operands
+    int pass = 0;
+    int32_t left = full;
+    const uint16_t *pp, *qq;
+    plane(0, pp, qq);
+    auto fill = [&](int slot) {
+        uint16_t* to = ring + slot * kStage;
+#pragma unroll
+        for (int i = 0; i < P::kPieces; ++i)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(pp) + op[i]),
+                (__attribute__((address_space(3))) void*)(to + (i * kThr + wave * 64) * 8), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < Q::kPieces; ++i)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(qq) + oq[i]),
+                (__attribute__((address_space(3))) void*)(to + BM * kStep + (i * kThr + wave * 64) * 8), 16, 0, 0);
+        pp += stepP;
+        qq += stepQ;
+        if (--left == 0 && ++pass < w.passes) {
+            plane(pass, pp, qq);
+            left = full;
+        }
+    };
+    constexpr int kLoads = P::kPieces + Q::kPieces;
+    const int32_t nk = full * w.passes;
+    // Step k multiplies buffer k: its first half is in registers, its second is read while
+    // the first is multiplied; the loads of step k + 3 go to the buffer that step k - 1 has left
+    // (every wave has read it: the barrier behind those reads).
+    auto main_step = [&](int32_t k) {
+        const uint16_t* s = ring + (k & (kStages - 1)) * kStage;
+        read(f1, s, 1);
+        fill((k + 3) & (kStages - 1));
+        multiply(f0);
+        wait_barrier<2 * kLoads>();
+        read(f0, ring + ((k + 1) & (kStages - 1)) * kStage, 0);
+        multiply(f1);
+    };
+    if (nk > 0) {
+        const int ahead = nk < 3 ? nk : 3;
+        for (int i = 0; i < ahead; ++i) fill(i);
+        if (nk >= 3) wait_barrier<2 * kLoads>();
+        else wait_barrier<0>();
+        read(f0, ring, 0);
+        int32_t k = 0;
+        for (; k + 3 < nk; ++k) main_step(k);
+        for (; k < nk; ++k) {
+            read(f1, ring + (k & (kStages - 1)) * kStage, 1);
+            multiply(f0);
+            if (k + 1 < nk) {
+                wait_barrier<0>();
+                read(f0, ring + ((k + 1) & (kStages - 1)) * kStage, 0);
+            }
+            multiply(f1);
+        }
+    }
+    __syncthreads();
+
+    // a lane holds row lane % 32, columns 8 g + 4 (lane / 32) + 0 .. 3 of each tile of 32
+    float* s = reinterpret_cast<float*>(mem) + wave * (kPatch / 4);
+    const uint64_t offset = drop_offset(a.drop);
+#pragma unroll
+    for (int x = 0; x < FM; ++x) {
+#pragma unroll
+        for (int y = 0; y < FN; ++y)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4 v{acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+                *reinterpret_cast<float4*>(&s[(lane & 31) * kLd + 32 * y + 8 * g + 4 * (lane >> 5)]) = v;
+            }
+        __builtin_amdgcn_wave_barrier();
+        constexpr int kPer = WN / 8;
+#pragma unroll
+        for (int i = 0; i < 32 * kPer / 64; ++i) {
+            const int b = i * 64 + lane, row = b / kPer, col = b % kPer * 8;
+            const int64_t n = r0 + wm + 32 * x + row, c = c0 + wn + col;
+            if (n < a.rows && c < a.cols) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<float4*>(&v[e]) = *reinterpret_cast<const float4*>(&s[row * kLd + col + e]);
+                if (a.splits > 1) {
+                    float* p = a.part + (part * a.rows + n) * a.cols + c;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(p + e) = *reinterpret_cast<const float4*>(&v[e]);
+                } else {
+                    finish8<T, KIND, true>(a, offset, v, n, (int32_t)c, 8);
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Planes of rows: as they are, or dz = mask g act'(z) with its columns' sums.  A block takes
+// 256 columns of a run of rows, eight rows at a time.
+template <class T, bool DZ>
+__global__ void __launch_bounds__(256) k_linear_planes(PlaneArgs p)
+{
+    constexpr int NP = kPlanes<T>;
+    __shared__ double s[DZ ? 8 * 256 : 1];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t c = ((int64_t)blockIdx.x * 32 + lane) * 8;
+    const int64_t n1 = ((int64_t)blockIdx.y + 1) * p.run < p.rows ? ((int64_t)blockIdx.y + 1) * p.run : p.rows;
+    const uint64_t offset = drop_offset(p.g.drop);
+    double sum[8] = {};
+    if (c < p.cols) {
+#pragma unroll 2
+        for (int64_t n = (int64_t)blockIdx.y * p.run + tid / 32; n < n1; n += 8) {
+            Raw8<T> r;
+            r.load((const T*)p.x + n * p.ld + c);
+            f8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = r[j];
+            if constexpr (DZ) {
+                float z[8] = {};
+                if (p.g.Z) {
+                    Raw8<T> q;
+                    q.load((const T*)p.g.Z + n * p.g.ldz + c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] = q[j];
+                }
+                slope8(p.g, offset, v, z, n, (int32_t)(c / 8));
+                if (p.g.db) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
+                }
+            }
+            if (p.out) {
+                b8 planes[NP];
+                cut(v, planes);
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    *reinterpret_cast<b8*>(p.out + i * p.rows * p.cols + n * p.cols + c) = planes[i];
+            }
+        }
+    }
+    if constexpr (DZ) {
+        if (!p.g.db) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[tid / 32 * 256 + lane * 8 + j] = sum[j];
+        __syncthreads();
+        double t = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += s[i * 256 + tid];
+        const int64_t at = (int64_t)blockIdx.x * 256 + tid;
+        if (at < p.cols) p.g.db_part[(int64_t)blockIdx.y * p.cols + at] = t;
+    }
+}
+
+template <class T, int KIND>
+hipError_t wide(const WideArgs& w, hipStream_t s)
+{
+    const dim3 grid((unsigned)(w.g.tr * w.g.tc * w.g.splits));
+    if (w.side == 256) hipLaunchKernelGGL((k_linear_wide<T, KIND, 256, 256, 128, 64>), grid, dim3(512), 0, s, w);
+    else hipLaunchKernelGGL((k_linear_wide<T, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, s, w);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t wide(int kind, const WideArgs& w, hipStream_t s)
+{
+    return kind == kFwd ? wide<T, kFwd>(w, s) : kind == kDx ? wide<T, kDx>(w, s) : wide<T, kDw>(w, s);
+}
+
+}  // namespace
+
+hipError_t launch_linear_wide(int dtype, int kind, const WideArgs& w, hipStream_t s)
+{
+    return dtype == kF32 ? wide<float>(kind, w, s) : wide<bf16_t>(kind, w, s);
+}
+
+hipError_t launch_linear_planes(int dtype, bool dz, const PlaneArgs& p, hipStream_t s)
+{
+    const dim3 grid((unsigned)cdiv64(p.cols, 256), (unsigned)cdiv64(p.rows, p.run));
+    if (dtype == kF32) {
+        if (dz) hipLaunchKernelGGL((k_linear_planes<float, true>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_linear_planes<float, false>), grid, dim3(256), 0, s, p);
+    } else {
+        hipLaunchKernelGGL((k_linear_planes<bf16_t, true>), grid, dim3(256), 0, s, p);  // (bf16 rows are planes)
+    }
+    return hipGetLastError();
+}
+
+}  // namespace cgtp

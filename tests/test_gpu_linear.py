@@ -72,7 +72,12 @@ CASES = [(1, 1, 1, 1, 0.0, True, True), (1, 8, 8, 1, 0.0, True, False), (2, 3, 5
          (4, 2048, 96, 1, 0.1, True, True), (7, 40, 4104, 2, 0.0, True, False), (9000, 136, 264, 1, 0.1, True, True),
          (40000, 8, 64, 1, 0.0, True, False), (12, 30, 2050, 1, 0.9, True, True), (300, 2056, 1000, 1, 0.0, True, False),
          (16, 512, 512, 1, 0.0, True, True), (1029, 520, 776, 1, 0.1, True, True), (100, 1, 300, 1, 0.0, True, True),
-         (100, 300, 1, 1, 0.0, True, True), (8, 1001, 64, 1, 0.0, False, False)]
+         (100, 300, 1, 1, 0.0, True, True), (8, 1001, 64, 1, 0.0, False, False),
+         # products of planes: contractions that are whole steps and not, cut and not, tiles that end inside
+         (1025, 1000, 1032, 1, 0.1, True, True), (4100, 264, 1000, 2, 0.0, True, False),
+         (300, 2056, 2000, 1, 0.5, False, True), (2050, 1024, 512, 1, 0.0, False, False),
+         (256, 4096, 1024, 1, 0.1, True, True), (16500, 256, 264, 1, 0.0, True, False),
+         (1100, 1024, 1024, 3, 0.0, True, True), (4352, 512, 4096, 1, 0.1, True, False)]
 
 
 def inputs(k, dtype):
