@@ -36,6 +36,7 @@ struct GemmArgs {
     const void* Z;            // z [N][M], or nullptr: act none
     int64_t lda, ldb, ldz;
     int64_t rows, cols, depth;  // of the result, of the contraction
+    int64_t first;            // row of the caller's that the first one here is, for the mask
     int64_t tr, tc;           // tiles along rows and columns
     int64_t splits, run;      // parts of the contraction and their length
     int act;
@@ -106,18 +107,28 @@ __device__ __forceinline__ void slope8(const GemmArgs& a, uint64_t offset, f8& v
         for (int j = 0; j < 8; ++j) v[j] *= act_slope(a.act, z[j]);
     }
     if (a.drop.thr) {
-        const Drawn f = philox((uint32_t)q, (uint32_t)n, offset, a.drop.seed);
+        const Drawn f = philox((uint32_t)q, (uint32_t)(a.first + n), offset, a.drop.seed);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] : 0.0f;
     }
 }
 
-// eight results of row n from channel c on, of which w are inside
-template <class T, int KIND, bool VEC>
-__device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, float (&v)[8], int64_t n, int32_t c, int w)
+// the bias of eight channels, of which w are inside
+__device__ __forceinline__ void bias8(const GemmArgs& a, int64_t c, int w, float (&b)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = a.bias && j < w ? a.bias[c + j] : 0.0f;
+}
+
+// Eight results from channel c on, of which w are inside, of each of G rows n (none where on is
+// not set).  The conditions stand outside the loops over the rows, so that the rows' loads and
+// chains of operations overlap.
+template <class T, int KIND, bool VEC, int G>
+__device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, float (&v)[G][8], const float (&b)[8],
+                                        const int64_t (&n)[G], const bool (&on)[G], int64_t c, int w)
 {
     constexpr int V = VEC ? kWide<T> : 1;
-    auto put = [&](T* p) {
+    auto put = [&](T* p, const float(&v)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; j += V) {
             float t[V];
@@ -127,35 +138,86 @@ __device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, floa
         }
     };
     if constexpr (KIND == kFwd) {
-        if (a.bias) {
+        float r[G][8];
+        if (a.R) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += a.bias[j < w ? c + j : c];
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int j = 0; j < 8; j += V) {
+                    float t[V] = {};
+                    if (on[g] && (VEC || j < w)) load_vec<T, V>(t, (const T*)a.R + n[g] * a.ldr + c + j);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) r[g][j + e] = t[e];
+                }
         }
-        if (a.zout) put((T*)a.zout + n * a.cols + c);
-        if (a.act != kNone) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = act_of(a.act, v[j]);
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[g][j] += b[j];
+        if (a.zout) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (on[g]) put((T*)a.zout + n[g] * a.cols + c, v[g]);
+        }
+        if (a.act == kSilu) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[g][j] = act_of<kSilu>(v[g][j]);
+        } else if (a.act == kTanh) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[g][j] = act_of<kTanh>(v[g][j]);
         }
         if (a.drop.thr) {
-            const Drawn f = philox((uint32_t)c / 8, (uint32_t)n, offset, a.drop.seed);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = f[j] >= a.drop.thr ? v[j] * a.drop.scale : 0.0f;
+            for (int g = 0; g < G; ++g) {
+                const Drawn f = philox((uint32_t)c / 8, (uint32_t)(a.first + n[g]), offset, a.drop.seed);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[g][j] = f[j] >= a.drop.thr ? v[g][j] * a.drop.scale : 0.0f;
+            }
         }
         if (a.R) {
-            const T* r = (const T*)a.R + n * a.ldr + c;
 #pragma unroll
-            for (int j = 0; j < 8; j += V) {
-                float t[V] = {};
-                if (VEC || j < w) load_vec<T, V>(t, r + j);
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[j + e] += t[e];
-            }
+                for (int j = 0; j < 8; ++j) v[g][j] += r[g][j];
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= a.drop.scale;
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[g][j] *= a.drop.scale;
     }
-    put((T*)a.out + n * a.ldo + c);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        if (on[g]) put((T*)a.out + n[g] * a.ldo + c, v[g]);
+}
+
+// The same, or the sums of one part of the contraction where that is cut.
+template <class T, int KIND, bool VEC, int G>
+__device__ __forceinline__ void leave8(const GemmArgs& a, uint64_t offset, int64_t part, float (&v)[G][8],
+                                       const float (&b)[8], const int64_t (&n)[G], const bool (&on)[G], int64_t c, int w)
+{
+    if (a.splits > 1) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float* p = a.part + (part * a.rows + n[g]) * a.cols + c;
+            if constexpr (VEC) {
+                if (on[g]) {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(p + e) = *reinterpret_cast<const float4*>(&v[g][e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (on[g] && e < w) p[e] = v[g][e];
+            }
+        }
+    } else {
+        finish8<T, KIND, VEC, G>(a, offset, v, b, n, on, c, w);
+    }
 }
 
 }  // namespace cgtp

@@ -6,7 +6,8 @@
 //
 // Precision.  An fp32 operand v is cut into three bf16 numbers, h = bf16(v),
 // m = bf16(v - h), l = bf16(v - h - m), which together hold all 24 bits of every
-// normal value (bf16 has fp32's range, so no units are needed), and
+// value of 2^-102 or more (bf16 has fp32's range, so no units are needed; the matrix
+// instructions take remainders below 2^-126 as zero), and
 //   u v = hu hv + (hu mv + mu hv) + (hu lv + mu mv + lu hv)
 // leaves out terms of at most 2^-25 of the product.  Six bf16 products with fp32
 // accumulation run at a sixth of the bf16 rate where fp32 matrix instructions reach a
@@ -232,7 +233,12 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
     if (!product) return;
 
     // A lane holds row lane % 32 and columns 8 g + 4 (lane / 32) + 0 .. 3 of each tile of 32:
-    // through LDS, so that rows leave in whole lines.
+    // through LDS, so that rows leave in whole lines; a thread keeps to its eight columns.
+    constexpr int kPer = BN / 8, kRows = kThreads / kPer, kG = kHalf / kRows < 4 ? kHalf / kRows : 4;
+    const int64_t c = c0 + tid % kPer * 8;
+    const int w = a.cols - c < 8 ? (int)(a.cols - c) : 8;
+    float bias[8] = {};
+    if (KIND == kFwd && c < a.cols) bias8(a, c, w, bias);
     float* s = reinterpret_cast<float*>(mem);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -249,25 +255,20 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
                     }
         }
         __syncthreads();
-        for (int b = tid; b < kHalf * BN / 8; b += kThreads) {
-            const int i = b / (BN / 8), j = b % (BN / 8) * 8;
-            const int64_t n = r0 + h * kHalf + i, c = c0 + j;
-            if (n >= a.rows || c >= a.cols) continue;
-            float v[8];
+        for (int i0 = 0; i0 < kHalf; i0 += kG * kRows) {
+            float v[kG][8];
+            int64_t n[kG];
+            bool on[kG];
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(&v[e]) = *reinterpret_cast<const float4*>(&s[i * kLdS + j + e]);
-            const int w = a.cols - c < 8 ? (int)(a.cols - c) : 8;
-            if (a.splits > 1) {
-                float* p = a.part + (part * a.rows + n) * a.cols + c;
-                if constexpr (VEC) {
+            for (int g = 0; g < kG; ++g) {
+                const int i = i0 + g * kRows + tid / kPer;
+                n[g] = r0 + h * kHalf + i;
+                on[g] = n[g] < a.rows && c < a.cols;
 #pragma unroll
-                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(p + e) = *reinterpret_cast<const float4*>(&v[e]);
-                } else {
-                    for (int e = 0; e < w; ++e) p[e] = v[e];
-                }
-            } else {
-                finish8<T, KIND, VEC>(a, offset, v, n, (int32_t)c, w);
+                for (int e = 0; e < 8; e += 4)
+                    *reinterpret_cast<float4*>(&v[g][e]) = *reinterpret_cast<const float4*>(&s[i * kLdS + tid % kPer * 8 + e]);
             }
+            leave8<T, KIND, VEC, kG>(a, offset, part, v, bias, n, on, c, w);
         }
     }
 }
@@ -326,10 +327,11 @@ __global__ void __launch_bounds__(kThreads) k_linear_join(GemmArgs a, int64_t bl
             for (int i = 1; i < G; ++i) t[j] += s[j * kThreads + i * kEach + tid];
     }
     if (!on) return;
-    float v[8];
+    float v[1][8], bias[8] = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)t[j];
-    finish8<T, KIND, VEC>(a, drop_offset(a.drop), v, n, (int32_t)c, w);
+    for (int j = 0; j < 8; ++j) v[0][j] = (float)t[j];
+    if (KIND == kFwd) bias8(a, c, w, bias);
+    finish8<T, KIND, VEC, 1>(a, drop_offset(a.drop), v, bias, {n}, {true}, c, w);
 }
 
 // out[0 .. n) = 0, in 4-byte words (a kernel: a captured graph may hold it)
@@ -386,16 +388,26 @@ Plan plan_wide(const Dims& d)
     p.wide = true;
     p.bm = p.bn = 256;
     auto tiles = [&]() { return cdiv64(d.rows, p.bm) * cdiv64(d.cols, p.bn); };
-    if (tiles() < 256 && tiles() * cdiv64(d.depth, 1024) < 256) p.bm = p.bn = 128;
+    const int64_t most = cdiv64(d.depth, 512);
+    if (tiles() * most < 256) p.bm = p.bn = 128;
     p.tr = cdiv64(d.rows, p.bm);
     p.tc = cdiv64(d.cols, p.bn);
-    const int64_t n = p.tr * p.tc, fill = p.bm == 256 ? 256 : 512, most = cdiv64(d.depth, 512);
-    int64_t s = fill / n;
+    int64_t s = (p.bm == 256 ? 256 : 768) / (p.tr * p.tc);
     s = s < most ? s : most;
     s = s < 1 ? 1 : s;
     p.run = cdiv64(cdiv64(d.depth, s), kBK) * kBK;
     p.splits = cdiv64(d.depth, p.run);
     return p;
+}
+
+// Rows behind the last whole tile that go by themselves: up to 64 of them, where without
+// them the tiles take a turn of the chip less.  (16385 x 1024 x 4096: one turn for dx instead of
+// two, four for y instead of five, for one or two launches of 64 x 64 tiles more.)
+int64_t rest_of(const Dims& d)
+{
+    const Plan p = plan_wide(d);
+    const int64_t rest = d.rows % p.bm, turn = p.bm == 256 ? 256 : 768, n = p.tr * p.tc;
+    return rest <= 64 && d.rows > p.bm && cdiv64(n, turn) > cdiv64(n - p.tc, turn) ? rest : 0;
 }
 
 constexpr int64_t kMaxWideLd = int64_t(1) << 22;  // row strides: a tile's byte offsets stay in 32 bits
@@ -445,8 +457,14 @@ struct WideSpace {
         size_t most = 0;
         for (int kind : {kFwd, kDx, kDw}) {
             if ((kind != kFwd) != backward) continue;
-            const size_t b = part_bytes(plan_wide(dims_of(n, kind)), dims_of(n, kind), false);
+            Dims d = dims_of(n, kind);
+            const int64_t rest = kind == kDw ? 0 : rest_of(d);
+            d.rows -= rest;
+            const size_t b = part_bytes(plan_wide(d), d, false);
             most = most > b ? most : b;
+            d.rows = rest;
+            const size_t c = rest ? part_bytes(plan_tiles(d), d, false) : 0;
+            most = most > c ? most : c;
         }
         part = take(most);
         bytes = at;
@@ -495,10 +513,11 @@ hipError_t run(GemmArgs& a, const Plan& p, bool vec, void* ws, hipStream_t s)
 
 // one product of planes
 template <class T, int KIND>
-hipError_t run_wide(const LinShape& n, GemmArgs a, const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq,
-                    float* part, hipStream_t s)
+hipError_t run_wide(const LinShape& n, int64_t rest, GemmArgs a, const uint16_t* P, int64_t ldp, const uint16_t* Q,
+                    int64_t ldq, float* part, hipStream_t s)
 {
-    const Dims d = dims_of(n, KIND);
+    Dims d = dims_of(n, KIND);
+    d.rows -= rest;
     const Plan p = plan_wide(d);
     WideArgs w{};
     a.rows = d.rows;
@@ -516,7 +535,6 @@ hipError_t run_wide(const LinShape& n, GemmArgs a, const uint16_t* P, int64_t ld
     w.ldq = ldq;
     w.planeP = KIND == kDx ? n.N * n.M : n.N * n.K;
     w.planeQ = KIND == kDw ? n.N * n.M : n.K * n.M;
-    w.passes = kPlanes<T> == 3 ? 6 : 1;
     w.side = p.bm;
     const hipError_t e = launch_linear_wide(n.dtype, KIND, w, s);
     return e != hipSuccess || (p.splits <= 1 && !(KIND == kDw && a.db)) ? e : join<T, KIND, true>(w.g, s);
@@ -575,7 +593,16 @@ hipError_t fwd(const LinShape& n, const void* x, const void* W, const float* bia
         int64_t ldp, ldq;
         hipError_t e = planes_of<T>(x, n.ldx, n.N, n.K, w + at.x, P, ldp, s);
         if (e == hipSuccess) e = planes_of<T>(W, n.M, n.K, n.M, w + at.W, Q, ldq, s);
-        return e != hipSuccess ? e : run_wide<T, kFwd>(n, a, P, ldp, Q, ldq, (float*)(w + at.part), s);
+        const int64_t rest = rest_of(dims_of(n, kFwd));
+        if (e == hipSuccess) e = run_wide<T, kFwd>(n, rest, a, P, ldp, Q, ldq, (float*)(w + at.part), s);
+        if (e != hipSuccess || !rest) return e;
+        a.first = n.N - rest;
+        a.rows = rest;
+        a.A = (const T*)x + a.first * n.ldx;
+        if (R) a.R = (const T*)R + a.first * n.ldr;
+        a.out = (T*)y + a.first * n.ldy;
+        if (z) a.zout = (T*)z + a.first * n.M;
+        return run<T, kFwd>(a, plan_tiles(Dims{rest, n.M, n.K}), true, w + at.part, s);
     }
     return run<T, kFwd>(a, plan_of(n, kFwd), vec, ws, s);
 }
@@ -614,8 +641,22 @@ hipError_t bwd_wide(const LinShape& n, GemmArgs a, const void* x, const void* W,
         b.out = dx;
         b.ldo = n.ldd;
         b.db = nullptr;
+        const int64_t rest = rest_of(dims_of(n, kDx));
         e = planes_of<T>(W, n.M, n.K, n.M, w + at.W, Q, ldq, s);
-        if (e == hipSuccess) e = run_wide<T, kDx>(n, b, dz, ldz, Q, ldq, part, s);
+        if (e == hipSuccess) e = run_wide<T, kDx>(n, rest, b, dz, ldz, Q, ldq, part, s);
+        if (e == hipSuccess && rest) {
+            b.first = n.N - rest;
+            b.A = (const T*)g + b.first * n.ldg;
+            if (b.Z) b.Z = (const T*)b.Z + b.first * n.M;
+            b.B = W;
+            b.lda = n.ldg;
+            b.ldb = n.M;
+            b.rows = rest;
+            b.cols = n.K;
+            b.depth = n.M;
+            b.out = (T*)dx + b.first * n.ldd;
+            e = run<T, kDx>(b, plan_tiles(Dims{rest, n.K, n.M}), true, part, s);
+        }
         if (e != hipSuccess) return e;
     }
     a.out = dW;
@@ -623,7 +664,7 @@ hipError_t bwd_wide(const LinShape& n, GemmArgs a, const void* x, const void* W,
     a.want = dW != nullptr;
     if (dW) {
         e = planes_of<T>(x, n.ldx, n.N, n.K, w + at.x, P, ldp, s);
-        return e != hipSuccess ? e : run_wide<T, kDw>(n, a, P, ldp, dz, ldz, part, s);
+        return e != hipSuccess ? e : run_wide<T, kDw>(n, 0, a, P, ldp, dz, ldz, part, s);
     }
     if (db) {
         a.rows = n.K;

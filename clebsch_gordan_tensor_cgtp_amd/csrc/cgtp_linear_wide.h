@@ -10,7 +10,6 @@ struct WideArgs {
     const uint16_t *P, *Q;   // planes of the rows' and the columns' operand, their rows on 16 bytes
     int64_t ldp, ldq;        // below 2^22
     int64_t planeP, planeQ;  // halves from one plane to the next
-    int32_t passes;          // 1 (one plane each) or 6 (three)
     int32_t side;            // of a tile: 256 or 128
 };
 

@@ -7,8 +7,9 @@
 // that needs it; its columns' sums on the way).  A product of three planes each goes
 // through the contraction six times, the smallest products first, into one accumulator.
 //
-// A block computes a BM x BN tile, each wave WM x WN of it, through a ring of four LDS buffers
-// of 32 k that loads fill directly, three steps ahead; one barrier to a step.  The 16-byte
+// A block of four waves computes a BM x BN tile, each wave WM x WN of it, through a ring of three LDS
+// buffers of 32 k that loads fill directly; one barrier to a step.  Two blocks share a compute unit, so
+// that one multiplies while the other is at its epilogue.  The 16-byte
 // pieces of a buffer are swapped about (by the address that each lane loads from), so that
 // what a read instruction takes spreads over all banks: an operand whose rows run along k has
 // the pieces of row r at piece ^ (r / 4 % 4) of its 64 bytes, the other kind its 32-byte pieces
@@ -24,7 +25,7 @@
 namespace cgtp {
 namespace {
 
-constexpr int kStep = 32, kStages = 4;
+constexpr int kStep = 32;
 
 // all but the last N of this wave's loads have arrived, its LDS reads are done, and every
 // wave of the block is here
@@ -34,6 +35,16 @@ __device__ __forceinline__ void wait_barrier()
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
+}
+
+// Sixteen bytes per lane from base + offset (of each lane) to LDS, from `to` on in the lanes' order,
+// without the compiler's knowledge: where it knows of such loads, every transposing read
+// waits for all of them.  Their arrival is what wait_barrier counts; nothing reads `to` before,
+// and nothing else in these kernels uses m0.
+__device__ __forceinline__ void load_lds(uint16_t* to, const uint16_t* base, uint32_t offset)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t*)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base));
 }
 
 // One operand's tile: WIDTH rows (or columns) of the result by kStep of the contraction.
@@ -86,13 +97,15 @@ __device__ __forceinline__ void tile_at(int64_t r, int64_t tr, int64_t tc, int64
     j = c0 + r % w;
 }
 
-template <class T, int KIND, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(WideArgs w)
+template <class T, int KIND, int BM, int BN, int WM, int WN, int kStages>
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 2 : 3)))
+k_linear_wide(WideArgs w)
 {
     constexpr int kThr = 64 * (BM / WM) * (BN / WN), FM = WM / 32, FN = WN / 32;
     constexpr bool kAlongP = KIND != kDw, kAlongQ = KIND == kDx;
     using P = Tile<BM, kThr, kAlongP>;
     using Q = Tile<BN, kThr, kAlongQ>;
+    constexpr int kPasses = kPlanes<T> == 3 ? 6 : 1;
     constexpr int kStage = (BM + BN) * kStep;  // halves
     constexpr int kLd = WN + 4, kPatch = 32 * kLd * 4;
     constexpr int kRing = kStages * kStage * 2, kOut = kPatch * (kThr / 64);
@@ -131,7 +144,7 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(Wide
     const int64_t stepP = kAlongP ? kStep : kStep * w.ldp, stepQ = kAlongQ ? kStep : kStep * w.ldq;
     // planes of pass j of six: h l, m m, l h, h m, m h, h h (h, m, l = 0, 1, 2)
     auto plane = [&](int j, const uint16_t*& p, const uint16_t*& q) {
-        const int ip = w.passes == 1 ? 0 : (0x010210 >> (4 * j)) & 15, iq = w.passes == 1 ? 0 : (0x001012 >> (4 * j)) & 15;
+        const int ip = kPasses == 1 ? 0 : (0x010210 >> (4 * j)) & 15, iq = kPasses == 1 ? 0 : (0x001012 >> (4 * j)) & 15;
         p = p0 + ip * w.planeP;
         q = q0 + iq * w.planeQ;
     };
@@ -144,27 +157,43 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(Wide
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
-    struct Frag {
-        b8 p[FM], q[FN];
+    struct Frag {  // of one step
+        b8 p[2][FM], q[2][FN];
     };
-    auto read = [&](Frag& f, const uint16_t* s, int ks) {
+    auto read = [&](Frag& f, int slot) {
+        const uint16_t* s = ring + slot * kStage;
 #pragma unroll
-        for (int y = 0; y < FN; ++y) f.q[y] = Q::read(s + BM * kStep, wn + 32 * y, ks, lane);
+        for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-        for (int x = 0; x < FM; ++x) f.p[x] = P::read(s, wm + 32 * x, ks, lane);
+            for (int y = 0; y < FN; ++y) f.q[ks][y] = Q::read(s + BM * kStep, wn + 32 * y, ks, lane);
+#pragma unroll
+            for (int x = 0; x < FM; ++x) f.p[ks][x] = P::read(s, wm + 32 * x, ks, lane);
+        }
     };
     auto multiply = [&](const Frag& f) {
 #pragma unroll
-        for (int x = 0; x < FM; ++x)
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int y = 0; y < FN; ++y)
-                acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[y], f.p[x], acc[x][y], 0, 0, 0);
+            for (int x = 0; x < FM; ++x)
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[ks][y], f.p[ks][x], acc[x][y], 0, 0, 0);
+    };
+    // the next step's LDS reads between the first half of the products
+    auto in_turn = [&]() {
+        constexpr int kReads = 2 * (FM * (kAlongP ? 1 : 2) + FN * (kAlongQ ? 1 : 2)), kMul = 2 * FM * FN;
+#pragma unroll
+        for (int g = 0; g < kMul / 2; ++g) {
+            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMul / 2 - 1) / (kMul / 2), 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kMul / 2, 0);
     };
     Frag f0, f1;
 
     // What is left of the contraction beyond whole steps goes through registers, zeros behind it.
     if (tail) {
-        for (int j = 0; j < w.passes; ++j) {
+        for (int j = 0; j < kPasses; ++j) {
             const uint16_t *p, *q;
             plane(j, p, q);
             auto some = [&](auto side, const uint16_t* from, const uint32_t* o, uint16_t* to) {
@@ -181,68 +210,79 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(Wide
             some(P{}, p + full * stepP, op, ring);
             some(Q{}, q + full * stepQ, oq, ring + BM * kStep);
             __syncthreads();
-            for (int ks = 0; ks < 2; ++ks) {
-                read(f0, ring, ks);
-                multiply(f0);
-            }
+            read(f0, 0);
+            multiply(f0);
             __syncthreads();
         }
     }
 
     // the loads' place: the next step's operands
-    int pass = 0;
-    int32_t left = full;
     const uint16_t *pp, *qq;
     plane(0, pp, qq);
     auto fill = [&](int slot) {
-        uint16_t* to = ring + slot * kStage;
+        uint16_t* to = ring + slot * kStage + wave * 512;
 #pragma unroll
-        for (int i = 0; i < P::kPieces; ++i)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(pp) + op[i]),
-                (__attribute__((address_space(3))) void*)(to + (i * kThr + wave * 64) * 8), 16, 0, 0);
+        for (int i = 0; i < P::kPieces; ++i) load_lds(to + i * kThr * 8, pp, op[i]);
 #pragma unroll
-        for (int i = 0; i < Q::kPieces; ++i)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(reinterpret_cast<const char*>(qq) + oq[i]),
-                (__attribute__((address_space(3))) void*)(to + BM * kStep + (i * kThr + wave * 64) * 8), 16, 0, 0);
+        for (int i = 0; i < Q::kPieces; ++i) load_lds(to + BM * kStep + i * kThr * 8, qq, oq[i]);
         pp += stepP;
         qq += stepQ;
-        if (--left == 0 && ++pass < w.passes) {
-            plane(pass, pp, qq);
-            left = full;
-        }
     };
     constexpr int kLoads = P::kPieces + Q::kPieces;
-    const int32_t nk = full * w.passes;
-    // Step k multiplies buffer k: its first half is in registers, its second is read while
-    // the first is multiplied; the loads of step k + 3 go to the buffer that step k - 1 has left
-    // (every wave has read it: the barrier behind those reads).
-    auto main_step = [&](int32_t k) {
-        const uint16_t* s = ring + (k & (kStages - 1)) * kStage;
-        read(f1, s, 1);
-        fill((k + 3) & (kStages - 1));
-        multiply(f0);
-        wait_barrier<2 * kLoads>();
-        read(f0, ring + ((k + 1) & (kStages - 1)) * kStage, 0);
-        multiply(f1);
+    const int32_t nk = full * kPasses;
+    // Step k multiplies block k, which is in registers, while it reads block k + 1 from LDS and
+    // starts the loads of block k + kStages into the buffer that block k has left.  Block k + 1 is in
+    // when at most the kStages - 2 blocks after it are out; behind the barrier every wave has read block k.
+    int slot = 0;  // of block k
+    auto after = [](int i) { return i + 1 == kStages ? 0 : i + 1; };
+    auto main_step = [&](const Frag& cur, Frag& next) {
+        wait_barrier<kLoads*(kStages - 2)>();
+        const int to = slot;
+        slot = after(slot);
+        read(next, slot);
+        fill(to);
+        multiply(cur);
+        in_turn();
+    };
+    auto tail_step = [&](bool more, const Frag& cur, Frag& next) {
+        if (more) {
+            wait_barrier<0>();
+            slot = after(slot);
+            read(next, slot);
+        }
+        multiply(cur);
     };
     if (nk > 0) {
-        const int ahead = nk < 3 ? nk : 3;
-        for (int i = 0; i < ahead; ++i) fill(i);
-        if (nk >= 3) wait_barrier<2 * kLoads>();
+        int pass = 0;
+        int32_t left = full;  // of the pass, for the loads
+        const int ahead = nk < kStages ? nk : kStages;
+        auto next_pass = [&]() {
+            left = full;
+            if (++pass < kPasses) plane(pass, pp, qq);
+        };
+        for (int i = 0; i < ahead; ++i) {
+            fill(i);
+            if (--left == 0) next_pass();
+        }
+        if (nk >= kStages) wait_barrier<kLoads*(kStages - 1)>();
         else wait_barrier<0>();
-        read(f0, ring, 0);
+        read(f0, 0);
         int32_t k = 0;
-        for (; k + 3 < nk; ++k) main_step(k);
-        for (; k < nk; ++k) {
-            read(f1, ring + (k & (kStages - 1)) * kStage, 1);
-            multiply(f0);
-            if (k + 1 < nk) {
-                wait_barrier<0>();
-                read(f0, ring + ((k + 1) & (kStages - 1)) * kStage, 0);
+        while (k + kStages < nk) {  // (no condition inside a pass' steps: it would wait for what it reads)
+            k += left;
+            if (left & 1) {
+                main_step(f0, f1);
+                f0 = f1;
             }
-            multiply(f1);
+            for (int32_t i = left >> 1; i > 0; --i) {
+                main_step(f0, f1);
+                main_step(f1, f0);
+            }
+            next_pass();
+        }
+        for (; k < nk; k += 2) {
+            tail_step(k + 1 < nk, f0, f1);
+            if (k + 1 < nk) tail_step(k + 2 < nk, f1, f0);
         }
     }
     __syncthreads();
@@ -250,6 +290,10 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(Wide
     // a lane holds row lane % 32, columns 8 g + 4 (lane / 32) + 0 .. 3 of each tile of 32
     float* s = reinterpret_cast<float*>(mem) + wave * (kPatch / 4);
     const uint64_t offset = drop_offset(a.drop);
+    constexpr int kPer = WN / 8, kRows = 64 / kPer, kG = 2;
+    const int64_t c = c0 + wn + lane % kPer * 8;
+    float bias[8] = {};
+    if (KIND == kFwd && c < a.cols) bias8(a, c, 8, bias);
 #pragma unroll
     for (int x = 0; x < FM; ++x) {
 #pragma unroll
@@ -260,24 +304,21 @@ __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) k_linear_wide(Wide
                 *reinterpret_cast<float4*>(&s[(lane & 31) * kLd + 32 * y + 8 * g + 4 * (lane >> 5)]) = v;
             }
         __builtin_amdgcn_wave_barrier();
-        constexpr int kPer = WN / 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += kG * kRows) {
+            float v[kG][8];
+            int64_t n[kG];
+            bool on[kG];
 #pragma unroll
-        for (int i = 0; i < 32 * kPer / 64; ++i) {
-            const int b = i * 64 + lane, row = b / kPer, col = b % kPer * 8;
-            const int64_t n = r0 + wm + 32 * x + row, c = c0 + wn + col;
-            if (n < a.rows && c < a.cols) {
-                float v[8];
+            for (int g = 0; g < kG; ++g) {
+                const int row = i0 + g * kRows + lane / kPer;
+                n[g] = r0 + wm + 32 * x + row;
+                on[g] = n[g] < a.rows && c < a.cols;
 #pragma unroll
                 for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<float4*>(&v[e]) = *reinterpret_cast<const float4*>(&s[row * kLd + col + e]);
-                if (a.splits > 1) {
-                    float* p = a.part + (part * a.rows + n) * a.cols + c;
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(p + e) = *reinterpret_cast<const float4*>(&v[e]);
-                } else {
-                    finish8<T, KIND, true>(a, offset, v, n, (int32_t)c, 8);
-                }
+                    *reinterpret_cast<float4*>(&v[g][e]) = *reinterpret_cast<const float4*>(&s[row * kLd + lane % kPer * 8 + e]);
             }
+            leave8<T, KIND, true, kG>(a, offset, part, v, bias, n, on, c, 8);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -343,8 +384,8 @@ template <class T, int KIND>
 hipError_t wide(const WideArgs& w, hipStream_t s)
 {
     const dim3 grid((unsigned)(w.g.tr * w.g.tc * w.g.splits));
-    if (w.side == 256) hipLaunchKernelGGL((k_linear_wide<T, KIND, 256, 256, 128, 64>), grid, dim3(512), 0, s, w);
-    else hipLaunchKernelGGL((k_linear_wide<T, KIND, 128, 128, 64, 64>), grid, dim3(256), 0, s, w);
+    if (w.side == 256) hipLaunchKernelGGL((k_linear_wide<T, KIND, 256, 256, 128, 64, 4>), grid, dim3(512), 0, s, w);
+    else hipLaunchKernelGGL((k_linear_wide<T, KIND, 128, 128, 64, 64, 3>), grid, dim3(256), 0, s, w);
     return hipGetLastError();
 }
 
