@@ -113,6 +113,21 @@ __device__ __forceinline__ void slope8(const GemmArgs& a, uint64_t offset, f8& v
     }
 }
 
+// Operand fragment of the matrix instruction whose contraction runs across the rows of LDS, ld halves
+// apart: p is this lane's place, row 8 (lane / 32) + lane % 16 / 4 and column (lane & 16) + 4 (lane % 4)
+// of the 16 x 32 block.
+__device__ __forceinline__ b8 read_across(const uint16_t* p, int ld)
+{
+    auto tr = [](const uint16_t* q) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4*)(const __attribute__((address_space(3))) void*)q);
+    };
+    struct Two {
+        s4 a, b;
+    } t{tr(p), tr(p + 4 * ld)};
+    return __builtin_bit_cast(b8, t);
+}
+
 // the bias of eight channels, of which w are inside
 __device__ __forceinline__ void bias8(const GemmArgs& a, int64_t c, int w, float (&b)[8])
 {

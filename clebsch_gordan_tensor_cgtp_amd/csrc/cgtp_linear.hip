@@ -60,14 +60,7 @@ struct Side {
         } else {
             const int l = lane & 15;
             p += (k0 + 8 * (lane >> 5) + l / 4) * kLd + r0 + (lane & 16) + 4 * (l % 4);
-            auto tr = [](const uint16_t* q) {
-                return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s4*)(const __attribute__((address_space(3))) void*)q);
-            };
-            struct Two {
-                s4 a, b;
-            } t{tr(p), tr(p + 4 * kLd)};
-            return __builtin_bit_cast(b8, t);
+            return read_across(p, kLd);
         }
     }
 };
@@ -419,6 +412,14 @@ bool wide_shape(const LinShape& n)
            (double)n.N * (double)n.K * (double)n.M >= 1e9;
 }
 
+// Few rows: one pass over W on the vector units.  Replayed from a graph, us: 1, 4 and 16 rows x
+// 1024 x 4096 bf16 3.8, 5.4 and 6.7, by tiles 7.6 to 8.0; fp32 3.9, 5.5 and 7.0, by tiles 12.4.
+// Where W is small tiles are as quick from three rows on (128 x 128 bf16: 4.1).
+bool few_rows(int64_t rows, int64_t depth) { return rows <= 2 || (rows <= 16 && depth >= 512); }
+
+// Rows that registers hold whole, and enough of them.
+bool rows_whole(const LinShape& n) { return n.K <= 128 && n.N >= 256; }
+
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t part_bytes(const Plan& p, const Dims& d, bool bias)
@@ -602,8 +603,11 @@ hipError_t fwd(const LinShape& n, const void* x, const void* W, const float* bia
         if (R) a.R = (const T*)R + a.first * n.ldr;
         a.out = (T*)y + a.first * n.ldy;
         if (z) a.zout = (T*)z + a.first * n.M;
+        if (few_rows(rest, n.K)) return launch_linear_few(n.dtype, true, a, s);
         return run<T, kFwd>(a, plan_tiles(Dims{rest, n.M, n.K}), true, w + at.part, s);
     }
+    if (rows_whole(n)) return launch_linear_rows(n.dtype, vec, a, s);
+    if (few_rows(n.N, n.K)) return launch_linear_few(n.dtype, vec, a, s);
     return run<T, kFwd>(a, plan_of(n, kFwd), vec, ws, s);
 }
 
@@ -750,6 +754,7 @@ size_t linear_workspace_bytes(const LinShape& n, bool backward)
     size_t most = wide_shape(n) ? WideSpace(n, backward).bytes : 0;
     for (int kind : {kFwd, kDx, kDw}) {
         if ((kind != kFwd) != backward) continue;
+        if (kind == kFwd && (few_rows(n.N, n.K) || rows_whole(n))) continue;
         const size_t b = part_bytes(plan_of(n, kind), dims_of(n, kind), kind == kDw);
         most = most > b ? most : b;
     }

@@ -1,4 +1,6 @@
-// cgtp_linear_wide.h -- products of bf16 planes (kernels in cgtp_linear_wide.hip).
+// cgtp_linear_wide.h -- launchers of the forms of the product beside the tiles of
+// cgtp_linear.hip: planes (cgtp_linear_wide.hip), few rows (cgtp_linear_few.hip),
+// rows that registers hold (cgtp_linear_rows.hip).
 #pragma once
 
 #include "cgtp_linear.h"
@@ -24,6 +26,10 @@ struct PlaneArgs {
 };
 
 hipError_t launch_linear_wide(int dtype, int kind, const WideArgs& w, hipStream_t s);
+// y of few rows (A: x, B: W); vec: every array begins on 16 bytes and all rows are multiples of eight long
+hipError_t launch_linear_few(int dtype, bool vec, const GemmArgs& a, hipStream_t s);
+// y of rows of up to 128 inputs (A: x, B: W); vec as above
+hipError_t launch_linear_rows(int dtype, bool vec, GemmArgs a, hipStream_t s);
 hipError_t launch_linear_planes(int dtype, bool dz, const PlaneArgs& p, hipStream_t s);
 
 }  // namespace cgtp

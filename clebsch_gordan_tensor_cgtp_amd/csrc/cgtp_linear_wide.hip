@@ -76,14 +76,7 @@ struct Tile {
         } else {
             const int l = lane & 15, k = ks * 16 + 8 * (lane >> 5) + l / 4, col = r0 + (lane & 16);
             const uint16_t* p = s + k * WIDTH + (((col >> 4) ^ (2 * (k & 3))) << 4) + 4 * (l % 4);
-            auto tr = [](const uint16_t* q) {
-                return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s4*)(const __attribute__((address_space(3))) void*)q);
-            };
-            struct Two {
-                s4 a, b;
-            } t{tr(p), tr(p + 4 * WIDTH)};
-            return __builtin_bit_cast(b8, t);
+            return read_across(p, WIDTH);
         }
     }
 };
