@@ -128,11 +128,24 @@ __device__ __forceinline__ b8 read_across(const uint16_t* p, int ld)
     return __builtin_bit_cast(b8, t);
 }
 
-// the bias of eight channels, of which w are inside
+// the bias of eight channels, of which w are inside (VEC: all)
+template <bool VEC>
 __device__ __forceinline__ void bias8(const GemmArgs& a, int64_t c, int w, float (&b)[8])
 {
+    if (VEC && a.bias) {
+        struct __attribute__((packed, aligned(4))) Four {
+            float v[4];
+        };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = a.bias && j < w ? a.bias[c + j] : 0.0f;
+        for (int j = 0; j < 8; j += 4) {
+            const Four f = *reinterpret_cast<const Four*>(a.bias + c + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[j + e] = f.v[e];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = a.bias && j < w ? a.bias[c + j] : 0.0f;
+    }
 }
 
 // Eight results from channel c on, of which w are inside, of each of G rows n (none where on is

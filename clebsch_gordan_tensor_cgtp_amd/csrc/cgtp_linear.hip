@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
     const int64_t c = c0 + tid % kPer * 8;
     const int w = a.cols - c < 8 ? (int)(a.cols - c) : 8;
     float bias[8] = {};
-    if (KIND == kFwd && c < a.cols) bias8(a, c, w, bias);
+    if (KIND == kFwd && c < a.cols) bias8<VEC>(a, c, w, bias);
     float* s = reinterpret_cast<float*>(mem);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_join(GemmArgs a, int64_t bl
     float v[1][8], bias[8] = {};
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[0][j] = (float)t[j];
-    if (KIND == kFwd) bias8(a, c, w, bias);
+    if (KIND == kFwd) bias8<VEC>(a, c, w, bias);
     finish8<T, KIND, VEC, 1>(a, drop_offset(a.drop), v, bias, {n}, {true}, c, w);
 }
 

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_few(GemmArgs a)
     const int r = tid / kL;
     if (r >= R || r0 + r >= a.rows || w == 0) return;
     float v[1][8], bias[8];
-    bias8(a, c, w, bias);
+    bias8<VEC>(a, c, w, bias);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[0][j] = total[r][l * 8 + j];
     finish8<T, kFwd, VEC, 1>(a, drop_offset(a.drop), v, bias, {r0 + r}, {true}, c, w);

@@ -10,6 +10,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cgtp_linear.h"
 #include "cgtp_linear_wide.h"
 
@@ -18,9 +20,13 @@ namespace {
 
 constexpr int kThreads = 256, kCols = 64;
 
+// every wave of the block is here and its LDS accesses are done (global ones may be under way)
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // NK: steps of 16 inputs
 template <class T, int NK, int WR, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_linear_rows(GemmArgs a)
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NK * kPlanes<T> >= 8 ? 2 : 3)))
+k_linear_rows(GemmArgs a)
 {
     constexpr int NP = kPlanes<T>, WC = 4 / WR, FN = kCols / 32 / WC, kK = NK * 16;
     constexpr int kLd = kCols + 16, kPlane = kK * kLd;  // halves
@@ -35,21 +41,23 @@ __global__ void __launch_bounds__(kThreads) k_linear_rows(GemmArgs a)
     const int64_t c0 = at % a.tc * a.run, c1 = c0 + a.run < a.cols ? c0 + a.run : a.cols;
     const uint64_t offset = drop_offset(a.drop);
 
-    // W's tile from column c on; rows and columns outside are zero
+    // W's tile from column c on.  The loads stand outside any condition (outside W at its first
+    // element): what is outside becomes zero where it goes to LDS.
     Raw8<T> raw[kEach];
+    auto inside = [&](int i, int64_t c, int64_t& k, int64_t& e) {
+        const int b = tid + i * kThreads;
+        k = b / kPer;
+        e = c + b % kPer * 8;
+        return k < a.depth && e < c1;
+    };
     auto fetch = [&](int64_t c) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int b = tid + i * kThreads;
-            const int64_t k = b / kPer, e = c + b % kPer * 8;
-            const bool in = k < a.depth && e < c1;
+            int64_t k, e;
+            const bool in = inside(i, c, k, e);
             const T* p = (const T*)a.B + (in ? k * a.ldb + e : 0);
-            if constexpr (VEC) {
-                raw[i].load(p);
-                if (!in) raw[i].clear();
-            } else {
-                raw[i].load_some(p, !in ? 0 : c1 - e < 8 ? (int)(c1 - e) : 8);
-            }
+            if constexpr (VEC) raw[i].load(p);
+            else raw[i].load_some(p, !in ? 0 : c1 - e < 8 ? (int)(c1 - e) : 8);
         }
     };
     fetch(c0);
@@ -85,81 +93,92 @@ __global__ void __launch_bounds__(kThreads) k_linear_rows(GemmArgs a)
     const int l = lane & 15;
     const uint16_t* sr = sw + (8 * (lane >> 5) + l / 4) * kLd + wave % WC * (32 * FN) + (lane & 16) + 4 * (l % 4);
     float* s = patch[wave];
-    for (int64_t c = c0; c < c1; c += kCols) {
-        if (c != c0) __syncthreads();  // the tile before has been read
+    // FULL: no row, column or input is outside, so that no wait has to reckon with stores that
+    // are skipped (it would wait for all of them)
+    auto columns = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        for (int64_t c = c0; c < c1; c += kCols) {
+            if (c != c0) lds_barrier();  // the tile before has been read
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int b = tid + i * kThreads;
-            if (kBlocks % kThreads != 0 && b >= kBlocks) break;
-            b8 planes[NP];
-            if constexpr (NP > 1) {
-                f8 v;
+            for (int i = 0; i < kEach; ++i) {
+                const int b = tid + i * kThreads;
+                if (kBlocks % kThreads != 0 && b >= kBlocks) break;
+                int64_t k, e;
+                const bool in = FULL || inside(i, c, k, e);
+                b8 planes[NP];
+                if constexpr (NP > 1) {
+                    f8 v;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = raw[i][j];
-                cut(v, planes);
-            } else {
-                planes[0] = __builtin_bit_cast(b8, raw[i].v[0]);
+                    for (int j = 0; j < 8; ++j) v[j] = in ? raw[i][j] : 0.0f;
+                    cut(v, planes);
+                } else {
+                    uint4 v = raw[i].v[0];
+                    if (!in) v = uint4{0, 0, 0, 0};
+                    planes[0] = __builtin_bit_cast(b8, v);
+                }
+#pragma unroll
+                for (int p = 0; p < NP; ++p) *reinterpret_cast<b8*>(sw + p * kPlane + b / kPer * kLd + b % kPer * 8) = planes[p];
             }
+            lds_barrier();
+            // this lane's eight columns of each 32 that leave
+            const int64_t ce = c + wave % WC * (32 * FN) + lane % 4 * 8;
+            auto width = [&](int y) {
+                const int64_t e = ce + 32 * y;
+                return FULL ? 8 : e >= c1 ? 0 : c1 - e < 8 ? (int)(c1 - e) : 8;
+            };
+            float bias[FN][8];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<b8*>(sw + p * kPlane + b / kPer * kLd + b % kPer * 8) = planes[p];
-        }
-        __syncthreads();
-        // this lane's eight columns of each 32 that leave
-        const int64_t ce = c + wave % WC * (32 * FN) + lane % 4 * 8;
-        float bias[FN][8];
+            for (int y = 0; y < FN; ++y) bias8<FULL>(a, ce + 32 * y, width(y), bias[y]);
+            if (c + kCols < c1) fetch(c + kCols);
+            f16v acc[FN];
 #pragma unroll
-        for (int y = 0; y < FN; ++y) {
-            const int64_t e = ce + 32 * y;
-            bias8(a, e, e >= c1 ? 0 : c1 - e < 8 ? (int)(c1 - e) : 8, bias[y]);
-        }
-        if (c + kCols < c1) fetch(c + kCols);
-        f16v acc[FN];
+            for (int y = 0; y < FN; ++y)
 #pragma unroll
-        for (int y = 0; y < FN; ++y)
+                for (int q = 0; q < 16; ++q) acc[y][q] = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) acc[y][q] = 0.0f;
+            for (int k = 0; k < NK; ++k) {
+                b8 w[FN][NP];
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            b8 w[FN][NP];
+                for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
-            for (int p = NP - 1; p >= 0; --p)
+                    for (int y = 0; y < FN; ++y) w[y][p] = read_across(sr + p * kPlane + k * 16 * kLd + 32 * y, kLd);
 #pragma unroll
-                for (int y = 0; y < FN; ++y) w[y][p] = read_across(sr + p * kPlane + k * 16 * kLd + 32 * y, kLd);
+                for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-            for (int o = NP - 1; o >= 0; --o)
+                    for (int p = 0; p <= o; ++p)
 #pragma unroll
-                for (int p = 0; p <= o; ++p)
-#pragma unroll
-                    for (int y = 0; y < FN; ++y)
-                        acc[y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[y][o - p], x[k][p], acc[y], 0, 0, 0);
-        }
-        // a lane holds row lane % 32, columns 8 g + 4 (lane / 32) + 0 .. 3
-#pragma unroll
-        for (int y = 0; y < FN; ++y) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4 v{acc[y][4 * g], acc[y][4 * g + 1], acc[y][4 * g + 2], acc[y][4 * g + 3]};
-                *reinterpret_cast<float4*>(&s[(lane & 31) * kLdS + 8 * g + 4 * (lane >> 5)]) = v;
+                        for (int y = 0; y < FN; ++y)
+                            acc[y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[y][o - p], x[k][p], acc[y], 0, 0, 0);
             }
-            __builtin_amdgcn_wave_barrier();
-            float v[2][8];
-            int64_t n[2];
-            bool on[2];
-            const int64_t e = ce + 32 * y;
-            const int w = e >= c1 ? 0 : c1 - e < 8 ? (int)(c1 - e) : 8;
+            // a lane holds row lane % 32, columns 8 g + 4 (lane / 32) + 0 .. 3
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int row = 16 * g + lane / 4;
-                n[g] = r0 + row;
-                on[g] = n[g] < a.rows && w > 0;
+            for (int y = 0; y < FN; ++y) {
 #pragma unroll
-                for (int j = 0; j < 8; j += 4)
-                    *reinterpret_cast<float4*>(&v[g][j]) = *reinterpret_cast<const float4*>(&s[row * kLdS + lane % 4 * 8 + j]);
+                for (int g = 0; g < 4; ++g) {
+                    const float4 v{acc[y][4 * g], acc[y][4 * g + 1], acc[y][4 * g + 2], acc[y][4 * g + 3]};
+                    *reinterpret_cast<float4*>(&s[(lane & 31) * kLdS + 8 * g + 4 * (lane >> 5)]) = v;
+                }
+                __builtin_amdgcn_wave_barrier();
+                float v[2][8];
+                int64_t n[2];
+                bool on[2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int row = 16 * g + lane / 4;
+                    n[g] = r0 + row;
+                    on[g] = FULL || (n[g] < a.rows && width(y) > 0);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4)
+                        *reinterpret_cast<float4*>(&v[g][j]) = *reinterpret_cast<const float4*>(&s[row * kLdS + lane % 4 * 8 + j]);
+                }
+                finish8<T, kFwd, VEC, 2>(a, offset, v, bias[y], n, on, ce + 32 * y, width(y));
+                __builtin_amdgcn_wave_barrier();
             }
-            finish8<T, kFwd, VEC, 2>(a, offset, v, bias[y], n, on, e, w);
-            __builtin_amdgcn_wave_barrier();
         }
-    }
+    };
+    // (the same for all waves: they share barriers)
+    if (VEC && a.depth == kK && at / a.tc * (32 * WR) + 32 * WR <= a.rows && (c1 - c0) % kCols == 0) columns(std::true_type{});
+    else columns(std::false_type{});
 }
 
 template <class T, int NK, bool VEC>

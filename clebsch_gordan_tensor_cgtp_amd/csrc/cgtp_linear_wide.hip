@@ -286,7 +286,7 @@ k_linear_wide(WideArgs w)
     constexpr int kPer = WN / 8, kRows = 64 / kPer, kG = 2;
     const int64_t c = c0 + wn + lane % kPer * 8;
     float bias[8] = {};
-    if (KIND == kFwd && c < a.cols) bias8(a, c, 8, bias);
+    if (KIND == kFwd && c < a.cols) bias8<true>(a, c, 8, bias);
 #pragma unroll
     for (int x = 0; x < FM; ++x) {
 #pragma unroll
