@@ -16,5 +16,6 @@ def __getattr__(name):
         return Plan
     if name in _TRAIN:
         from . import train
-        return getattr(train, name)
+        f = globals()[name] = getattr(train, name)  # (found without this function from here on)
+        return f
     raise AttributeError(name)

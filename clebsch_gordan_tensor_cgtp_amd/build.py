@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["cgtp_kernels_l3_c64_bwd.hip", "cgtp_kernels_l3_c64_bwd2.hip", "cgtp_kernels_l3_c128.hip", "cgtp_kernels_l3_c64.hip", "cgtp_kernels_l3_c32.hip",
            "cgtp_kernels_l3_c16.hip", "cgtp_kernels_l3_c8.hip", "cgtp_kernels_l2_wide.hip", "cgtp_kernels_l2.hip",
            "cgtp_kernels_l1.hip", "cgtp_cp.hip", "cgtp_mix.hip", "cgtp_registry.hip", "cgtp_graph.hip", "cgtp_forces.hip",
-           "cgtp_embed.hip", "cgtp_norm.hip", "cgtp_ortho.hip", "cgtp_linear.hip", "cgtp_linear_wide.hip", "cgtp_linear_few.hip", "cgtp_linear_rows.hip",
+           "cgtp_embed.hip", "cgtp_norm.hip", "cgtp_ortho.hip", "cgtp_linear.hip", "cgtp_linear_wide.hip", "cgtp_linear_few.hip",
+           "cgtp_linear_rows.hip", "cgtp_linear_back.hip",
            "cgtp_dropout.hip",
            "cgtp_cp_fit.cpp", "cgtp_api.cpp", "cgtp_train_api.cpp"]
 

@@ -44,6 +44,7 @@ constexpr int kBK = 32;  // contraction per step
 template <class T, int RUNS, int WIDTH, bool ALONG>
 struct Side {
     static constexpr int NP = kPlanes<T>;
+    static constexpr bool kAlong = ALONG;
     static constexpr int kLd = WIDTH + (ALONG ? 8 : 16);
     static constexpr int kHalves = RUNS * kLd;  // of one plane
     static constexpr int kPer = WIDTH / 8;                     // blocks of eight in a row
@@ -149,7 +150,8 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
                         for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
                     }
                 }
-                cut(v, planes);
+                if constexpr (S::kAlong) cut_along(v, planes);
+                else cut(v, planes);
             } else {
                 planes[0] = __builtin_bit_cast(b8, raw[i].v[0]);
             }
@@ -420,6 +422,27 @@ bool few_rows(int64_t rows, int64_t depth) { return rows <= 2 || (rows <= 16 && 
 // Rows that registers hold whole, and enough of them.
 bool rows_whole(const LinShape& n) { return n.K <= 128 && n.N >= 256; }
 
+// Gradients in one pass: up to 128 outputs.
+bool one_pass(const LinShape& n) { return n.M <= 128; }
+
+// dx of few inputs over many outputs, from rows of g in registers.
+bool dx_rows(const LinShape& n) { return n.K <= 128 && n.M > 128 && n.N >= 4096 && n.M % 8 == 0; }
+
+// dW of few inputs, from columns of x and g in registers (where dz is g: z would not find room
+// there, and a mask would be formed eight times).
+bool dw_columns(const LinShape& n) { return n.dtype == kF32 && n.K <= 64 && n.M > 128 && n.N >= 8192; }
+
+Plan plan_columns(const LinShape& n)
+{
+    Plan p{};
+    p.tr = 1;
+    p.tc = cdiv64(n.M, 128);
+    const int64_t s = p.tc < 512 ? 512 / p.tc : 1;
+    p.run = cdiv64(cdiv64(n.N, s), 64) * 64;
+    p.splits = cdiv64(n.N, p.run);
+    return p;
+}
+
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t part_bytes(const Plan& p, const Dims& d, bool bias)
@@ -437,6 +460,12 @@ int64_t plane_run(int64_t rows, int64_t cols)
     int64_t run = cdiv64(rows * across, 2048);
     run = cdiv64(run < 8 ? 8 : run, 8) * 8;
     return run;
+}
+
+// workspace of the narrow form: parts of dW, parts of db
+size_t back_bytes(int64_t splits, const LinShape& n)
+{
+    return round256((size_t)(splits * n.K * n.M) * 4) + (size_t)(splits * n.M) * 8;
 }
 
 // workspace of the wide form, by arrays
@@ -477,7 +506,7 @@ hipError_t join(const GemmArgs& a, hipStream_t s)
 {
     const dim3 block(kThreads);
     const bool many = a.splits >= kManySplits;
-    const int64_t blocks = a.splits > 1 && (KIND != kDw || a.want) ? cdiv64(a.rows * cdiv64(a.cols, 8), many ? kThreads / 8 : kThreads) : 0;
+    const int64_t blocks = KIND != kDw || a.want ? cdiv64(a.rows * cdiv64(a.cols, 8), many ? kThreads / 8 : kThreads) : 0;
     const int64_t more = KIND == kDw && a.db ? cdiv64(a.cols, kThreads / 8) : 0;
     const dim3 grid((unsigned)(blocks + more));
     if (many) hipLaunchKernelGGL((k_linear_join<T, KIND, VEC, 8>), grid, block, 0, s, a, blocks);
@@ -538,7 +567,9 @@ hipError_t run_wide(const LinShape& n, int64_t rest, GemmArgs a, const uint16_t*
     w.planeQ = KIND == kDw ? n.N * n.M : n.K * n.M;
     w.side = p.bm;
     const hipError_t e = launch_linear_wide(n.dtype, KIND, w, s);
-    return e != hipSuccess || (p.splits <= 1 && !(KIND == kDw && a.db)) ? e : join<T, KIND, true>(w.g, s);
+    if (e != hipSuccess || (p.splits <= 1 && !(KIND == kDw && a.db))) return e;
+    if (p.splits <= 1) w.g.want = false;  // dW is there
+    return join<T, KIND, true>(w.g, s);
 }
 
 // x or W as planes: as it is for bf16, else formed at `to`
@@ -691,6 +722,61 @@ hipError_t bwd(const LinShape& n, const void* x, const void* W, const void* z, c
     const bool vec = n.K % 8 == 0 && n.M % 8 == 0 && aligned_rows(g, n.ldg, es) && (!a.Z || aligned_rows(z, n.M, es));
     const bool vec_x = vec && aligned_rows(W, n.M, es) && aligned_rows(dx, n.ldd, es);
     const bool vec_w = vec && aligned_rows(x, n.ldx, es) && aligned_rows(dW, n.M, es);
+    // parts of dW and db, and what is needed to add them
+    auto parts = [&](int64_t tr, int64_t tc, int64_t splits) {
+        GemmArgs b = a;
+        b.A = x;
+        b.B = g;
+        b.lda = n.ldx;
+        b.ldb = n.ldg;
+        b.rows = n.K;
+        b.cols = n.M;
+        b.depth = n.N;
+        b.tr = tr;
+        b.tc = tc;
+        b.splits = b.db_splits = splits;
+        b.part = (float*)ws;
+        b.db_part = (double*)((char*)ws + round256((size_t)(splits * n.K * n.M) * 4));
+        b.out = dW;
+        b.ldo = n.M;
+        b.db = db;
+        b.want = dW != nullptr;
+        return b;
+    };
+    auto add = [&](const GemmArgs& b) { return vec_w ? join<T, kDw, true>(b, s) : join<T, kDw, false>(b, s); };
+    if (one_pass(n)) {
+        const BackPlan p = back_plan(n.N, n.K, n.M);
+        const GemmArgs b = parts(p.tr, 1, p.splits);
+        const hipError_t e = launch_linear_back(n.dtype, vec && (!dW || vec_w) && (!dx || vec_x), b, p, W, dx, n.ldd, s);
+        return e != hipSuccess || (!dW && !db) ? e : add(b);
+    }
+    if (dx && vec_x && dx_rows(n) && n.ldg < kMaxWideLd) {
+        WideArgs w{};
+        w.g = a;
+        w.g.A = g;
+        w.g.lda = n.ldg;
+        w.g.rows = n.N;
+        w.g.cols = n.K;
+        w.g.depth = n.M;
+        w.g.out = dx;
+        w.g.ldo = n.ldd;
+        w.planeQ = n.K * n.M;
+        hipError_t e = planes_of<T>(W, n.M, n.K, n.M, ws, w.Q, w.ldq, s);
+        if (e == hipSuccess) e = launch_linear_dx(n.dtype, w, s);
+        if (e != hipSuccess) return e;
+        dx = nullptr;
+    }
+    if (dW && n.act == kNone && n.drop.thr == 0 && dw_columns(n) && n.ldx < kMaxWideLd && n.ldg < kMaxWideLd) {
+        const Plan p = plan_columns(n);
+        GemmArgs b = parts(1, p.tc, p.splits);
+        b.run = p.run;
+        const hipError_t e = launch_linear_dw(b, s);
+        if (e != hipSuccess) return e;
+        const hipError_t f = add(b);
+        if (f != hipSuccess) return f;
+        dW = nullptr;
+        db = nullptr;
+    }
     if ((!dx || vec_x) && (!dW || vec_w) && vec && wide_shape(n) && (!dW || n.ldx < kMaxWideLd))
         return bwd_wide<T>(n, a, x, W, g, dx, dW, db, ws, s);
     if (dx) {
@@ -750,8 +836,14 @@ bool linear_fits(const LinShape& n)
 size_t linear_workspace_bytes(const LinShape& n, bool backward)
 {
     if (n.N == 0) return 0;
+    if (backward && one_pass(n)) return back_bytes(back_plan(n.N, n.K, n.M).splits, n);
     // (rows without 16-byte alignment take the tiles where others take planes)
     size_t most = wide_shape(n) ? WideSpace(n, backward).bytes : 0;
+    if (backward && dx_rows(n) && n.dtype == kF32) most = (size_t)(3 * n.K * n.M) * 2;
+    if (backward && dw_columns(n)) {
+        const size_t b = back_bytes(plan_columns(n).splits, n);
+        most = most > b ? most : b;
+    }
     for (int kind : {kFwd, kDx, kDw}) {
         if ((kind != kFwd) != backward) continue;
         if (kind == kFwd && (few_rows(n.N, n.K) || rows_whole(n))) continue;

@@ -1,0 +1,297 @@
+// cgtp_linear_back.hip -- the gradients of narrow products in one pass: dz = mask g act'(z) is
+// formed once for
+//   dx = dz W^T  (up to 128 outputs),  dW = x^T dz,  db = sum of dz's rows.
+//
+// Memory bounds these: g, z and x are read and dx is written once.  A block owns a KT x MT slab of
+// W and goes through chunks of 64 rows, every grid's length one: dz and x go through registers
+// (fetched while the chunk before is multiplied) into LDS as they lie in memory, as bf16 planes.  dz is
+// read along its rows for dx, whose other operand, the slab of W, each wave has cut once and keeps in
+// registers; dz and x are read across their rows (by the transposing LDS read) for dW, whose sums stay
+// in registers to the end and leave as one partial sum to a block, added in order by a launch of their own.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "cgtp_linear.h"
+#include "cgtp_linear_wide.h"
+
+namespace cgtp {
+namespace {
+
+constexpr int kRows = 64;  // of a chunk
+
+template <int KT, int MT>
+constexpr int kBackThreads = KT + MT > 128 ? 512 : 256;
+
+// VEC: rows of whole blocks of eight on 16 bytes.
+template <class T, int KT, int MT, bool VEC>
+__global__ void __launch_bounds__((kBackThreads<KT, MT>))
+k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t ldd)
+{
+    constexpr int kThr = kBackThreads<KT, MT>, NW = kThr / 64, NP = kPlanes<T>;
+    constexpr int kLdX = KT + 16, kLdZ = MT + 16, kPlaneX = kRows * kLdX, kPlaneZ = kRows * kLdZ;  // halves
+    constexpr int kPerX = KT / 8, kPerZ = MT / 8, kEachX = kRows * kPerX / kThr, kEachZ = kRows * kPerZ / kThr;
+    // dW: waves along the outputs WQ, each FP x 1 tiles of 32
+    constexpr int WQ = MT / 32, WP = NW / WQ, FP = KT / 32 / WP;
+    static_assert(WP * FP * 32 == KT, "waves cover the slab");
+    // dx: two tiles of 32 rows by KT / 32 of inputs, a wave each
+    constexpr int kMsteps = MT / 16;
+    constexpr int kLdS = 36;
+    constexpr int kTiles = (kPlaneX + kPlaneZ) * NP * 2, kSums = kThr * 64, kPatch = NW * 32 * kLdS * 4;
+    __shared__ __attribute__((aligned(16))) char mem[kTiles + kPatch > kSums ? kTiles + kPatch : kSums];
+    uint16_t* sx = reinterpret_cast<uint16_t*>(mem);
+    uint16_t* sz = sx + kPlaneX * NP;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // a.tr slabs along the inputs, a.splits blocks to a slab
+    const int64_t at = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t part = at / a.tr, i0 = at % a.tr * KT;
+    const uint64_t offset = drop_offset(a.drop);
+
+    // chunk's rows, zero outside
+    Raw8<T> rx[kEachX], rg[kEachZ], rz[kEachZ];
+    auto fetch = [&](int64_t n0) {
+        auto load = [&](Raw8<T>& r, const void* base, int64_t ld, int64_t n, int64_t e, int64_t lim) {
+            const bool in = n < a.depth && e < lim;
+            const T* p = (const T*)base + (in ? n * ld + e : 0);
+            if constexpr (VEC) {
+                r.load(p);
+                if (!in) r.clear();
+            } else {
+                r.load_some(p, !in ? 0 : lim - e < 8 ? (int)(lim - e) : 8);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kEachZ; ++i) {
+            const int b = tid + i * kThr;
+            load(rg[i], a.B, a.ldb, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
+            if (a.Z) load(rz[i], a.Z, a.ldz, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
+        }
+        if (a.want) {
+#pragma unroll
+            for (int i = 0; i < kEachX; ++i) {
+                const int b = tid + i * kThr;
+                load(rx[i], a.A, a.lda, n0 + b / kPerX, i0 + b % kPerX * 8, a.rows);
+            }
+        }
+    };
+    fetch(part * kRows);
+
+    // this wave's 32 inputs of the slab of W, all outputs
+    const int wr = wave % 2 * 32, wi = wave / 2 * 32;
+    const bool to_dx = wi < KT && dx;
+    b8 w[kMsteps][NP];
+    {
+        if (to_dx) {
+            const int64_t ci = i0 + wi + (lane & 31);
+#pragma unroll
+            for (int s = 0; s < kMsteps; ++s) {
+                const int64_t e = 16 * s + 8 * (lane >> 5);
+                const bool in = ci < a.rows && e < a.cols;
+                const T* p = W + (in ? ci * a.cols + e : 0);
+                Raw8<T> r;
+                if constexpr (VEC) {
+                    r.load(p);
+                    if (!in) r.clear();
+                } else {
+                    r.load_some(p, !in ? 0 : a.cols - e < 8 ? (int)(a.cols - e) : 8);
+                }
+                f8 v;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = r[j];
+                cut_along(v, w[s]);
+            }
+        }
+    }
+
+    f16v acc[FP];
+#pragma unroll
+    for (int x = 0; x < FP; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[x][e] = 0.0f;
+    double sum[8] = {};
+    const bool sums = a.db && i0 == 0;
+    const int wp = wave / WQ * (32 * FP), wq = wave % WQ * 32, l = lane & 15;
+    const uint16_t* px = sx + (8 * (lane >> 5) + l / 4) * kLdX + wp + (lane & 16) + 4 * (l % 4);
+    const uint16_t* pz = sz + (8 * (lane >> 5) + l / 4) * kLdZ + wq + (lane & 16) + 4 * (l % 4);
+    float* s = reinterpret_cast<float*>(mem + kTiles) + wave * (32 * kLdS);
+
+    for (int64_t n0 = part * kRows; n0 < a.depth; n0 += a.splits * kRows) {
+        if (n0 != part * kRows) __syncthreads();
+        auto put = [&](uint16_t* to, int plane, const f8& v) {
+            b8 p[NP];
+            cut(v, p);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) *reinterpret_cast<b8*>(to + i * plane) = p[i];
+        };
+#pragma unroll
+        for (int i = 0; i < kEachZ; ++i) {
+            const int b = tid + i * kThr, row = b / kPerZ, col = b % kPerZ * 8;
+            f8 v;
+            float z[8] = {};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = rg[i][j];
+            if (a.Z) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = rz[i][j];
+            }
+            slope8(a, offset, v, z, n0 + row, col / 8);
+            if (sums) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
+            }
+            put(sz + row * kLdZ + col, kPlaneZ, v);
+        }
+        if (a.want) {
+#pragma unroll
+            for (int i = 0; i < kEachX; ++i) {
+                const int b = tid + i * kThr;
+                f8 v;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = rx[i][j];
+                put(sx + b / kPerX * kLdX + b % kPerX * 8, kPlaneX, v);
+            }
+        }
+        __syncthreads();
+        if (n0 + a.splits * kRows < a.depth) fetch(n0 + a.splits * kRows);
+        if (a.want) {
+#pragma unroll
+            for (int k = 0; k < kRows; k += 16) {
+                b8 q[NP], p[FP][NP];
+#pragma unroll
+                for (int o = NP - 1; o >= 0; --o) {
+                    q[o] = read_across(pz + o * kPlaneZ + k * kLdZ, kLdZ);
+#pragma unroll
+                    for (int x = 0; x < FP; ++x) p[x][o] = read_across(px + o * kPlaneX + k * kLdX + 32 * x, kLdX);
+                }
+#pragma unroll
+                for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                    for (int i = 0; i <= o; ++i)
+#pragma unroll
+                        for (int x = 0; x < FP; ++x)
+                            acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[o - i], p[x][i], acc[x], 0, 0, 0);
+            }
+        }
+        {
+            if (to_dx) {
+                f16v d;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) d[e] = 0.0f;
+                const uint16_t* pa = sz + (wr + (lane & 31)) * kLdZ + 8 * (lane >> 5);
+#pragma unroll
+                for (int k = 0; k < kMsteps; ++k) {
+                    b8 p[NP];
+#pragma unroll
+                    for (int o = NP - 1; o >= 0; --o) p[o] = *reinterpret_cast<const b8*>(pa + o * kPlaneZ + 16 * k);
+#pragma unroll
+                    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                        for (int i = 0; i <= o; ++i)
+                            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[k][o - i], p[i], d, 0, 0, 0);
+                }
+                // a lane holds row lane % 32, inputs 8 g + 4 (lane / 32) + 0 .. 3
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float4 v{d[4 * g], d[4 * g + 1], d[4 * g + 2], d[4 * g + 3]};
+                    *reinterpret_cast<float4*>(&s[(lane & 31) * kLdS + 8 * g + 4 * (lane >> 5)]) = v;
+                }
+                __builtin_amdgcn_wave_barrier();
+                const int64_t c = i0 + wi + lane % 4 * 8;
+                const int width = c >= a.rows ? 0 : a.rows - c < 8 ? (int)(a.rows - c) : 8;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int row = 16 * g + lane / 4;
+                    const int64_t n = n0 + wr + row;
+                    if (n >= a.depth || width == 0) continue;
+                    constexpr int V = VEC ? kWide<T> : 1;
+#pragma unroll
+                    for (int j = 0; j < 8; j += V) {
+                        float v[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) v[e] = s[row * kLdS + lane % 4 * 8 + j + e] * a.drop.scale;
+                        if (VEC || j < width) store_vec<T, V>(dx + n * ldd + c + j, v);
+                    }
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    }
+
+    if (a.want) {
+        // rows lane % 32 of the tile, outputs 8 g + 4 (lane / 32) + 0 .. 3
+#pragma unroll
+        for (int x = 0; x < FP; ++x) {
+            const int64_t i = i0 + wp + 32 * x + (lane & 31);
+            if (i >= a.rows) continue;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t c = wq + 8 * g + 4 * (lane >> 5);
+                float* p = a.part + (part * a.rows + i) * a.cols + c;
+                if constexpr (VEC) {
+                    if (c < a.cols) *reinterpret_cast<float4*>(p) = float4{acc[x][4 * g], acc[x][4 * g + 1], acc[x][4 * g + 2], acc[x][4 * g + 3]};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < a.cols) p[e] = acc[x][4 * g + e];
+                }
+            }
+        }
+    }
+    if (sums) {
+        double* sd = reinterpret_cast<double*>(mem);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sd[j * kThr + tid] = sum[j];
+        __syncthreads();
+        if (tid < MT && tid < a.cols) {
+            double t = 0.0;
+            for (int i = 0; i < kThr / kPerZ; ++i) t += sd[tid % 8 * kThr + i * kPerZ + tid / 8];
+            a.db_part[part * a.cols + tid] = t;
+        }
+    }
+}
+
+template <class T, int KT, int MT>
+void launch(bool vec, const GemmArgs& a, const void* W, void* dx, int64_t ldd, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.tr * a.splits)), block(kBackThreads<KT, MT>);
+    if (vec) hipLaunchKernelGGL((k_linear_back<T, KT, MT, true>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+    else hipLaunchKernelGGL((k_linear_back<T, KT, MT, false>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+}
+
+template <class T>
+void launch(bool vec, const GemmArgs& a, int kt, int mt, const void* W, void* dx, int64_t ldd, hipStream_t s)
+{
+    if (kt == 128 && mt == 128) launch<T, 128, 128>(vec, a, W, dx, ldd, s);
+    else if (kt == 128) launch<T, 128, 64>(vec, a, W, dx, ldd, s);
+    else if (mt == 128) launch<T, 64, 128>(vec, a, W, dx, ldd, s);
+    else launch<T, 64, 64>(vec, a, W, dx, ldd, s);
+}
+
+}  // namespace
+
+BackPlan back_plan(int64_t n, int64_t k, int64_t m)
+{
+    BackPlan p{};
+    p.kt = k <= 64 ? 64 : 128;
+    p.mt = m <= 64 ? 64 : 128;
+    p.tr = cdiv64(k, p.kt);
+    // a block to a compute unit (two of the small ones), every one with a chunk at least
+    const int64_t chunks = cdiv64(n, kRows), fill = cdiv64(p.kt + p.mt > 192 ? 256 : 512, p.tr);
+    p.splits = chunks < fill ? chunks : fill;
+    p.splits = p.splits < 1 ? 1 : p.splits;
+    return p;
+}
+
+hipError_t launch_linear_back(int dtype, bool vec, const GemmArgs& a, const BackPlan& p, const void* W, void* dx,
+                              int64_t ldd, hipStream_t s)
+{
+    if (dtype == kF32) launch<float>(vec, a, p.kt, p.mt, W, dx, ldd, s);
+    else launch<bf16_t>(vec, a, p.kt, p.mt, W, dx, ldd, s);
+    return hipGetLastError();
+}
+
+}  // namespace cgtp

@@ -83,7 +83,7 @@ k_linear_rows(GemmArgs a)
                 f8 v;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = r[s][j];
-                cut(v, x[s]);
+                cut_along(v, x[s]);
             } else {
                 x[s][0] = __builtin_bit_cast(b8, r[s].v[0]);
             }

@@ -19,6 +19,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cgtp_linear.h"
 #include "cgtp_linear_wide.h"
 
@@ -317,6 +319,301 @@ k_linear_wide(WideArgs w)
     }
 }
 
+// dx of up to KC inputs over many outputs: memory bounds it, g (and z) being read once.  Each wave
+// loads its 32 FR rows of dz straight into matrix operands (a lane has eight outputs of one row),
+// forms and cuts them there; the planes of W come to LDS by direct loads, 32 outputs to a step, for the
+// block's four waves.  Both are fetched one step ahead: W's behind the one barrier of a step, dz's into
+// the registers that have just been cut.  HZ: with z.
+template <class T, int KC, int FR, bool HZ>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_linear_dx(WideArgs w)
+{
+    constexpr int NP = kPlanes<T>, FC = KC / 32, kThr = 256;
+    using Q = Tile<KC, kThr, true>;
+    constexpr int kPlane = KC * kStep, kLdS = 36;  // halves; floats
+    __shared__ __attribute__((aligned(16))) uint16_t ring[2][NP * kPlane];
+    __shared__ __attribute__((aligned(16))) float patch[4][32 * kLdS];
+    const GemmArgs& a = w.g;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t r0 = xcd_order(blockIdx.x, gridDim.x) * (128 * FR) + wave * (32 * FR);
+    const uint64_t offset = drop_offset(a.drop);
+
+    // W's pieces: rows behind the last input are that one again, outputs behind the last the last eight
+    // (dz is zero there)
+    auto fill = [&](int slot, int64_t k) {
+#pragma unroll
+        for (int i = 0; i < Q::kPieces; ++i) {
+            int row, col;
+            Q::place(i, row, col);
+            row = row < a.cols ? row : (int)a.cols - 1;
+            col = k + col < a.depth ? col : (int)(a.depth - k) - 8;
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                load_lds(&ring[slot][p * kPlane + (i * kThr + wave * 64) * 8], w.Q + p * w.planeQ + k, (uint32_t)(row * (int)w.ldq + col) * 2u);
+        }
+    };
+    // rows outside are the last one again; byte offsets from the wave's first row
+    int64_t n[FR];
+    uint32_t og[FR], oz[FR];
+    const int64_t base = r0 < a.rows ? r0 : a.rows - 1;
+#pragma unroll
+    for (int x = 0; x < FR; ++x) {
+        const int64_t m = r0 + 32 * x + (lane & 31);
+        n[x] = m < a.rows ? m : a.rows - 1;
+        og[x] = ((uint32_t)(n[x] - base) * (uint32_t)a.lda + 8u * (uint32_t)(lane >> 5)) * (uint32_t)sizeof(T);
+        oz[x] = ((uint32_t)(n[x] - base) * (uint32_t)a.ldz + 8u * (uint32_t)(lane >> 5)) * (uint32_t)sizeof(T);
+    }
+    const char* pg = (const char*)((const T*)a.A + base * a.lda);
+    const char* pz = HZ ? (const char*)((const T*)a.Z + base * a.ldz) : nullptr;
+    Raw8<T> rg[2][FR], rz[HZ ? 2 : 1][HZ ? FR : 1];
+    // outputs k + 16 ks + 8 (lane / 32) + 0 .. 7; those behind the last are others of the row
+    auto fetch = [&](int ks, int x, int64_t k) {
+        const uint32_t back = k + 16 * ks + 8 * (lane >> 5) < a.depth ? 0 : (uint32_t)(16 * ks + 8 * (lane >> 5)) * (uint32_t)sizeof(T);
+        const int64_t at = (k + 16 * ks) * (int64_t)sizeof(T);
+        rg[ks][x].load((const T*)(pg + at + og[x] - back));
+        if constexpr (HZ) rz[ks][x].load((const T*)(pz + at + oz[x] - back));
+    };
+    auto fetch_in = [&](int ks, int x, int64_t k) {
+        const int64_t at = (k + 16 * ks) * (int64_t)sizeof(T);
+        rg[ks][x].load((const T*)(pg + at + og[x]));
+        if constexpr (HZ) rz[ks][x].load((const T*)(pz + at + oz[x]));
+    };
+    constexpr int kFetches = 2 * FR * (HZ ? 2 : 1) * (int)sizeof(T) / 2;  // loads of a step
+    f16v acc[FR][FC];
+#pragma unroll
+    for (int x = 0; x < FR; ++x)
+#pragma unroll
+        for (int y = 0; y < FC; ++y)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+    // one step; `then`: the next one's first output, or k again behind the last (not used)
+    auto step = [&](int slot, int64_t k, int64_t then, auto last, auto next) {
+        constexpr bool LAST = decltype(last)::value;
+        wait_barrier<kFetches>();  // W's loads were started before the step's
+        fill(slot ^ 1, then);
+        asm volatile("" ::: "memory");  // (and stay so)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            b8 p[FR][NP], q[FC][NP];
+            const int64_t e = k + 16 * ks + 8 * (lane >> 5);
+#pragma unroll
+            for (int x = 0; x < FR; ++x) {
+                f8 v;
+                float z[8] = {};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = rg[ks][x][j];
+                    if constexpr (HZ) z[j] = rz[ks][x][j];
+                }
+                next(ks, x, then);
+                slope8<HZ>(a, offset, v, z, n[x], (int32_t)(e / 8));
+                if constexpr (LAST) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = e < a.depth ? v[j] : 0.0f;
+                }
+                cut_along(v, p[x]);
+            }
+#pragma unroll
+            for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                for (int y = 0; y < FC; ++y) q[y][o] = Q::read(&ring[slot][o * kPlane], 32 * y, ks, lane);
+#pragma unroll
+            for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                for (int i = 0; i <= o; ++i)
+#pragma unroll
+                    for (int x = 0; x < FR; ++x)
+#pragma unroll
+                        for (int y = 0; y < FC; ++y)
+                            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[y][o - i], p[x][i], acc[x][y], 0, 0, 0);
+        }
+    };
+    fill(0, 0);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int x = 0; x < FR; ++x) fetch(ks, x, 0);
+    int slot = 0;
+    int64_t k = 0;
+    for (; k + 2 * kStep <= a.depth; k += kStep, slot ^= 1) step(slot, k, k + kStep, std::false_type{}, fetch_in);
+    for (; k < a.depth; k += kStep, slot ^= 1) step(slot, k, k + kStep < a.depth ? k + kStep : k, std::true_type{}, fetch);
+    wait_barrier<0>();  // no load to LDS is left
+    // a lane holds row lane % 32, inputs 8 g + 4 (lane / 32) + 0 .. 3
+    float* s = patch[wave];
+    const float none[8] = {};
+#pragma unroll
+    for (int x = 0; x < FR; ++x)
+#pragma unroll
+        for (int y = 0; y < FC; ++y) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4 v{acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+                *reinterpret_cast<float4*>(&s[(lane & 31) * kLdS + 8 * g + 4 * (lane >> 5)]) = v;
+            }
+            __builtin_amdgcn_wave_barrier();
+            float v[2][8];
+            int64_t m[2];
+            bool in[2];
+            const int64_t c = 32 * y + lane % 4 * 8;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int row = 16 * g + lane / 4;
+                m[g] = r0 + 32 * x + row;
+                in[g] = m[g] < a.rows && c < a.cols;
+#pragma unroll
+                for (int j = 0; j < 8; j += 4)
+                    *reinterpret_cast<float4*>(&v[g][j]) = *reinterpret_cast<const float4*>(&s[row * kLdS + lane % 4 * 8 + j]);
+            }
+            finish8<T, kDx, true, 2>(a, offset, v, none, m, in, c, 8);
+            __builtin_amdgcn_wave_barrier();
+        }
+}
+
+// dW of fp32 rows with dz = g, up to 64 inputs: memory and the matrix cores bound it alike.  A wave
+// owns 64 inputs x 128 outputs and a run of rows, and needs no LDS: a lane has one column of x or g
+// and eight rows in a row, which is what eight loads of whole lines bring (a row's 32 columns to
+// each half of the wave).  The next rows' loads go to the registers that have just been cut.  The four
+// waves of a block add their sums at the end, in order.  HB: db too.
+template <bool HB>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_linear_dw(GemmArgs a)
+{
+    constexpr int FP = 2, FQ = 4;
+    __shared__ float s[64][128 + 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // blocks with the same rows of x are neighbours; the last 128 outputs may reach into those before
+    const int64_t at = xcd_order(blockIdx.x, gridDim.x), part = at / a.tc, own = at % a.tc * 128;
+    const int64_t c0 = own + 128 < a.cols ? own : a.cols - 128;
+    const int64_t n0 = part * a.run + wave * (a.run / 4), end = n0 + a.run / 4 < a.depth ? n0 + a.run / 4 : a.depth;
+    // byte offsets of the lane's column and rows from those of the wave; inputs outside are the last again
+    uint32_t op[FP];
+#pragma unroll
+    for (int x = 0; x < FP; ++x) {
+        const int c = 32 * x + (lane & 31);
+        op[x] = ((uint32_t)(lane >> 5) * 8u * (uint32_t)a.lda + (uint32_t)(c < a.rows ? c : (int)a.rows - 1)) * 4u;
+    }
+    const uint32_t oq = ((uint32_t)(lane >> 5) * 8u * (uint32_t)a.ldb + (uint32_t)(lane & 31)) * 4u;
+    f16v acc[FP][FQ];
+#pragma unroll
+    for (int x = 0; x < FP; ++x)
+#pragma unroll
+        for (int y = 0; y < FQ; ++y)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+    // rows n .. n + 15, the lane's eight from n + 8 (lane / 32) on
+    float rx[FP][8], rg[FQ][8];
+    auto fetch = [&](float(&r)[8], const void* base, int64_t ld, int64_t c, uint32_t offset, int64_t n) {
+        const char* p = (const char*)((const float*)base + n * ld + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = *(const float*)(p + j * ld * 4 + offset);
+    };
+    // the last rows, fewer than 16: behind the end the last one again
+    auto fetch_end = [&](float(&r)[8], const void* base, int64_t ld, int64_t c, int64_t n) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t m = n + 8 * (lane >> 5) + j;
+            r[j] = ((const float*)base)[(m < end ? m : end - 1) * ld + c];
+        }
+    };
+    double sum[HB ? FQ : 1] = {};
+    auto step = [&](int64_t n, auto last, auto next_x, auto next_g) {
+        constexpr bool LAST = decltype(last)::value;
+        b8 p[FP][3], q[3];
+        const int64_t m = n + 8 * (lane >> 5);
+#pragma unroll
+        for (int x = 0; x < FP; ++x) {
+            f8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = !LAST || m + j < end ? rx[x][j] : 0.0f;
+            cut_along(v, p[x]);
+            next_x(x);
+        }
+#pragma unroll
+        for (int y = 0; y < FQ; ++y) {
+            f8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = rg[y][j];
+                if constexpr (LAST) v[j] = m + j < end ? v[j] : 0.0f;
+            }
+            next_g(y);
+            if constexpr (HB) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[y] += (double)v[j];
+            }
+            cut_along(v, q);
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+                for (int i = 0; i <= o; ++i)
+#pragma unroll
+                    for (int x = 0; x < FP; ++x)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[o - i], p[x][i], acc[x][y], 0, 0, 0);
+        }
+    };
+    int64_t n = n0;
+    if (n + 16 <= end) {
+        auto next_x = [&](int x, int64_t n) { fetch(rx[x], a.A, a.lda, 0, op[x], n); };
+        auto next_g = [&](int y, int64_t n) { fetch(rg[y], a.B, a.ldb, c0 + 32 * y, oq, n); };
+#pragma unroll
+        for (int x = 0; x < FP; ++x) next_x(x, n);
+#pragma unroll
+        for (int y = 0; y < FQ; ++y) next_g(y, n);
+        for (; n + 16 <= end; n += 16) {
+            const int64_t then = n + 32 <= end ? n + 16 : n;  // (behind the last whole step: that again, not used)
+            step(n, std::false_type{}, [&](int x) { next_x(x, then); }, [&](int y) { next_g(y, then); });
+        }
+    }
+    if (n < end) {
+#pragma unroll
+        for (int x = 0; x < FP; ++x) {
+            const int64_t c = 32 * x + (lane & 31);
+            fetch_end(rx[x], a.A, a.lda, c < a.rows ? c : a.rows - 1, n);
+        }
+#pragma unroll
+        for (int y = 0; y < FQ; ++y) fetch_end(rg[y], a.B, a.ldb, c0 + 32 * y + (lane & 31), n);
+        step(n, std::true_type{}, [](int) {}, [](int) {});
+    }
+    // a lane holds input lane % 32, outputs 8 g + 4 (lane / 32) + 0 .. 3 of each tile of 32
+    for (int v = 0; v < 4; ++v) {
+        if (v) __syncthreads();
+        if (wave == v) {
+#pragma unroll
+            for (int x = 0; x < FP; ++x)
+#pragma unroll
+                for (int y = 0; y < FQ; ++y)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float4* to = reinterpret_cast<float4*>(&s[32 * x + (lane & 31)][32 * y + 8 * g + 4 * (lane >> 5)]);
+                        float4 t{acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+                        if (v) {
+                            const float4 b = *to;
+                            t.x += b.x;
+                            t.y += b.y;
+                            t.z += b.z;
+                            t.w += b.w;
+                        }
+                        *to = t;
+                    }
+        }
+    }
+    __syncthreads();
+    for (int b = tid; b < 64 * 128; b += 256) {
+        const int64_t i = b / 128, c = c0 + b % 128;
+        if (i < a.rows && c >= own) a.part[(part * a.rows + i) * a.cols + c] = s[i][b % 128];
+    }
+    if constexpr (HB) {
+        __shared__ double sd[4][2][128];
+#pragma unroll
+        for (int y = 0; y < FQ; ++y) sd[wave][lane >> 5][32 * y + (lane & 31)] = sum[y];
+        __syncthreads();
+        if (tid < 128 && c0 + tid >= own) {
+            double t = 0.0;
+            for (int v = 0; v < 8; ++v) t += sd[v / 2][v % 2][tid];
+            a.db_part[part * a.cols + c0 + tid] = t;
+        }
+    }
+}
+
 // Planes of rows: as they are, or dz = mask g act'(z) with its columns' sums.  A block takes
 // 256 columns of a run of rows, eight rows at a time.
 template <class T, bool DZ>
@@ -393,6 +690,29 @@ hipError_t wide(int kind, const WideArgs& w, hipStream_t s)
 hipError_t launch_linear_wide(int dtype, int kind, const WideArgs& w, hipStream_t s)
 {
     return dtype == kF32 ? wide<float>(kind, w, s) : wide<bf16_t>(kind, w, s);
+}
+
+hipError_t launch_linear_dx(int dtype, const WideArgs& w, hipStream_t s)
+{
+    auto go = [&](auto kernel, int rows) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv64(w.g.rows, rows)), dim3(256), 0, s, w);
+    };
+    auto with = [&](auto z) {
+        constexpr bool HZ = decltype(z)::value;
+        const bool few = w.g.cols <= 64;
+        if (dtype == kF32) few ? go(k_linear_dx<float, 64, 2, HZ>, 256) : go(k_linear_dx<float, 128, 1, HZ>, 128);
+        else few ? go(k_linear_dx<bf16_t, 64, 2, HZ>, 256) : go(k_linear_dx<bf16_t, 128, 1, HZ>, 128);
+    };
+    w.g.Z ? with(std::true_type{}) : with(std::false_type{});
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_dw(const GemmArgs& a, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.tc * a.splits));
+    if (a.db) hipLaunchKernelGGL(k_linear_dw<true>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(k_linear_dw<false>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 hipError_t launch_linear_planes(int dtype, bool dz, const PlaneArgs& p, hipStream_t s)

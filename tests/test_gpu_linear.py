@@ -78,6 +78,14 @@ CASES = [(1, 1, 1, 1, 0.0, True, True), (1, 8, 8, 1, 0.0, True, False), (2, 3, 5
          (300, 2056, 2000, 1, 0.5, False, True), (2050, 1024, 512, 1, 0.0, False, False),
          (256, 4096, 1024, 1, 0.1, True, True), (16500, 256, 264, 1, 0.0, True, False),
          (1100, 1024, 1024, 3, 0.0, True, True), (4352, 512, 4096, 1, 0.1, True, False),
+         # narrow gradients: slabs of inputs or outputs, a chunk to a block and several, ragged ends
+         (70000, 128, 128, 1, 0.1, True, False), (40001, 64, 64, 2, 0.0, True, False), (3001, 300, 72, 1, 0.5, True, True),
+         (3001, 72, 300, 1, 0.5, True, True), (20000, 120, 56, 1, 0.0, True, False), (64, 128, 128, 1, 0.0, True, True),
+         (63, 61, 127, 1, 0.1, True, True), (65, 129, 128, 1, 0.1, True, True), (5001, 1000, 8, 1, 0.0, True, False),
+         # few inputs over many outputs: rows of g and columns of x and g in registers
+         (9001, 64, 200, 1, 0.0, True, False), (8200, 40, 1000, 2, 0.0, True, False), (8193, 7, 136, 1, 0.0, True, True),
+         (5000, 120, 264, 1, 0.1, True, False), (12345, 50, 131, 1, 0.0, False, False), (20000, 64, 1920, 1, 0.0, False, False),
+         (8192, 64, 136, 1, 0.5, True, False),
          # rows behind the last whole tile that go by themselves
          (4097, 512, 4096, 1, 0.1, True, True), (16390, 1032, 264, 1, 0.5, True, True),
          (16448, 264, 1024, 2, 0.1, True, False)]
