@@ -40,38 +40,18 @@ __global__ void __launch_bounds__(kThreads) k_dropout(DropArgs a)
     int32_t q = (int32_t)(first - n * a.per);
     while (n < a.N) {
         const int32_t c = q * 8;
-        const T* px = x + n * a.ldx + c;
-        const T* pr = r + n * a.ldr + c;
-        T* po = out + n * a.ldo + c;
-        const int32_t w = a.C - c < 8 ? a.C - c : 8;
-        constexpr int V = VEC ? kWide<T> : 1;
-        float v[8], s[8];
-#pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            float t[V] = {}, u[V] = {};
-            if (VEC || j < w) {
-                load_vec<T, V>(t, px + j);
-                if (r) load_vec<T, V>(u, pr + j);
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[j + e] = t[e];
-                s[j + e] = u[e];
-            }
-        }
+        const int w = VEC || a.C - c >= 8 ? 8 : a.C - c;
+        Raw8<T> v, s;
+        v.load_some(x + n * a.ldx + c, w);
+        s.load_some(r + n * a.ldr + c, r ? w : 0);
         const Drawn f = philox((uint32_t)q, (uint32_t)n, offset, a.d.seed);
+        float t[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float k = f[j] >= a.d.thr ? v[j] * a.d.scale : 0.0f;
-            v[j] = r ? s[j] + k : k;
+            t[j] = r ? s[j] + k : k;
         }
-#pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            float t[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) t[e] = v[j + e];
-            if (VEC || j < w) store_vec<T, V>(po + j, t);
-        }
+        store8<T>(out + n * a.ldo + c, t, w);
         q += (int32_t)a.step;
         n += a.rows;
         if (q >= a.per) {

@@ -53,37 +53,6 @@ struct GemmArgs {
     bool want;         // kDw: the product itself is wanted
 };
 
-// eight elements of a row as they lie in memory
-template <class T>
-struct Raw8 {
-    uint4 v[sizeof(T) / 2];
-    __device__ __forceinline__ float operator[](int j) const
-    {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
-        return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
-    }
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = uint4{0, 0, 0, 0};
-    }
-    __device__ __forceinline__ void load(const T* p)
-    {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-    }
-    // the first n elements, by elements
-    __device__ __forceinline__ void load_some(const T* p, int n)
-    {
-        clear();
-        T* e = reinterpret_cast<T*>(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) e[j] = p[j];
-    }
-};
-
 // planes that an operand of type T is cut into
 template <class T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
@@ -181,28 +150,17 @@ template <class T, int KIND, bool VEC, int G>
 __device__ __forceinline__ void finish8(const GemmArgs& a, uint64_t offset, float (&v)[G][8], const float (&b)[8],
                                         const int64_t (&n)[G], const bool (&on)[G], int64_t c, int w)
 {
-    constexpr int V = VEC ? kWide<T> : 1;
-    auto put = [&](T* p, const float(&v)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            float t[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) t[e] = v[j + e];
-            if (VEC || j < w) store_vec<T, V>(p + j, t);
-        }
-    };
+    auto put = [&](T* p, const float(&v)[8]) { store8<T>(p, v, VEC ? 8 : w); };
     if constexpr (KIND == kFwd) {
         float r[G][8];
         if (a.R) {
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+            for (int g = 0; g < G; ++g) {
+                Raw8<T> t;
+                t.load_some((const T*)a.R + n[g] * a.ldr + c, !on[g] ? 0 : VEC ? 8 : w);
 #pragma unroll
-                for (int j = 0; j < 8; j += V) {
-                    float t[V] = {};
-                    if (on[g] && (VEC || j < w)) load_vec<T, V>(t, (const T*)a.R + n[g] * a.ldr + c + j);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) r[g][j + e] = t[e];
-                }
+                for (int j = 0; j < 8; ++j) r[g][j] = t[j];
+            }
         }
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -258,16 +216,7 @@ __device__ __forceinline__ void leave8(const GemmArgs& a, uint64_t offset, int64
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float* p = a.part + (part * a.rows + n[g]) * a.cols + c;
-            if constexpr (VEC) {
-                if (on[g]) {
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4*>(p + e) = *reinterpret_cast<const float4*>(&v[g][e]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (on[g] && e < w) p[e] = v[g][e];
-            }
+            if (on[g]) store8<float>(p, v[g], VEC ? 8 : w);
         }
     } else {
         finish8<T, KIND, VEC, G>(a, offset, v, b, n, on, c, w);

@@ -3,7 +3,7 @@
 //   dx = dz W^T  (up to 128 outputs),  dW = x^T dz,  db = sum of dz's rows.
 //
 // Memory bounds these: g, z and x are read and dx is written once.  A block owns a KT x MT slab of
-// W and goes through chunks of 64 rows, every grid's length one: dz and x go through registers
+// W and goes through chunks of 64 (or 32) rows, every grid's length one: dz and x go through registers
 // (fetched while the chunk before is multiplied) into LDS as they lie in memory, as bf16 planes.  dz is
 // read along its rows for dx, whose other operand, the slab of W, each wave has cut once and keeps in
 // registers; dz and x are read across their rows (by the transposing LDS read) for dW, whose sums stay
@@ -20,23 +20,22 @@
 namespace cgtp {
 namespace {
 
-constexpr int kRows = 64;  // of a chunk
-
 template <int KT, int MT>
 constexpr int kBackThreads = KT + MT > 128 ? 512 : 256;
 
-// VEC: rows of whole blocks of eight on 16 bytes.
-template <class T, int KT, int MT, bool VEC>
+// kRows: of a chunk.  VEC: rows of whole blocks of eight on 16 bytes.
+template <class T, int KT, int MT, int kRows, bool VEC>
 __global__ void __launch_bounds__((kBackThreads<KT, MT>))
 k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t ldd)
 {
     constexpr int kThr = kBackThreads<KT, MT>, NW = kThr / 64, NP = kPlanes<T>;
     constexpr int kLdX = KT + 16, kLdZ = MT + 16, kPlaneX = kRows * kLdX, kPlaneZ = kRows * kLdZ;  // halves
-    constexpr int kPerX = KT / 8, kPerZ = MT / 8, kEachX = kRows * kPerX / kThr, kEachZ = kRows * kPerZ / kThr;
+    constexpr int kPerX = KT / 8, kPerZ = MT / 8, kAllX = kRows * kPerX, kAllZ = kRows * kPerZ;
+    constexpr int kEachX = (kAllX + kThr - 1) / kThr, kEachZ = (kAllZ + kThr - 1) / kThr;
     // dW: waves along the outputs WQ, each FP x 1 tiles of 32
     constexpr int WQ = MT / 32, WP = NW / WQ, FP = KT / 32 / WP;
     static_assert(WP * FP * 32 == KT, "waves cover the slab");
-    // dx: two tiles of 32 rows by KT / 32 of inputs, a wave each
+    // dx: tiles of 32 rows by 32 inputs, a wave each
     constexpr int kMsteps = MT / 16;
     constexpr int kLdS = 36;
     constexpr int kTiles = (kPlaneX + kPlaneZ) * NP * 2, kSums = kThr * 64, kPatch = NW * 32 * kLdS * 4;
@@ -66,6 +65,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
 #pragma unroll
         for (int i = 0; i < kEachZ; ++i) {
             const int b = tid + i * kThr;
+            if (kAllZ < kThr && b >= kAllZ) break;
             load(rg[i], a.B, a.ldb, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
             if (a.Z) load(rz[i], a.Z, a.ldz, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
         }
@@ -73,6 +73,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
 #pragma unroll
             for (int i = 0; i < kEachX; ++i) {
                 const int b = tid + i * kThr;
+                if (kAllX < kThr && b >= kAllX) break;
                 load(rx[i], a.A, a.lda, n0 + b / kPerX, i0 + b % kPerX * 8, a.rows);
             }
         }
@@ -80,7 +81,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
     fetch(part * kRows);
 
     // this wave's 32 inputs of the slab of W, all outputs
-    const int wr = wave % 2 * 32, wi = wave / 2 * 32;
+    const int wr = wave % (kRows / 32) * 32, wi = wave / (kRows / 32) * 32;
     const bool to_dx = wi < KT && dx;
     b8 w[kMsteps][NP];
     {
@@ -129,6 +130,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
 #pragma unroll
         for (int i = 0; i < kEachZ; ++i) {
             const int b = tid + i * kThr, row = b / kPerZ, col = b % kPerZ * 8;
+            if (kAllZ < kThr && b >= kAllZ) break;
             f8 v;
             float z[8] = {};
 #pragma unroll
@@ -148,6 +150,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
 #pragma unroll
             for (int i = 0; i < kEachX; ++i) {
                 const int b = tid + i * kThr;
+                if (kAllX < kThr && b >= kAllX) break;
                 f8 v;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = rx[i][j];
@@ -206,14 +209,10 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
                     const int row = 16 * g + lane / 4;
                     const int64_t n = n0 + wr + row;
                     if (n >= a.depth || width == 0) continue;
-                    constexpr int V = VEC ? kWide<T> : 1;
+                    float v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; j += V) {
-                        float v[V];
-#pragma unroll
-                        for (int e = 0; e < V; ++e) v[e] = s[row * kLdS + lane % 4 * 8 + j + e] * a.drop.scale;
-                        if (VEC || j < width) store_vec<T, V>(dx + n * ldd + c + j, v);
-                    }
+                    for (int j = 0; j < 8; ++j) v[j] = s[row * kLdS + lane % 4 * 8 + j] * a.drop.scale;
+                    store8<T>(dx + n * ldd + c, v, VEC ? 8 : width);
                 }
                 __builtin_amdgcn_wave_barrier();
             }
@@ -230,11 +229,12 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
             for (int g = 0; g < 4; ++g) {
                 const int64_t c = wq + 8 * g + 4 * (lane >> 5);
                 float* p = a.part + (part * a.rows + i) * a.cols + c;
-                if constexpr (VEC) {
-                    if (c < a.cols) *reinterpret_cast<float4*>(p) = float4{acc[x][4 * g], acc[x][4 * g + 1], acc[x][4 * g + 2], acc[x][4 * g + 3]};
+                if (c + 4 <= a.cols) {
+                    const float4 v{acc[x][4 * g], acc[x][4 * g + 1], acc[x][4 * g + 2], acc[x][4 * g + 3]};
+                    store16(p, __builtin_bit_cast(uint4, v));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 3; ++e)
                         if (c + e < a.cols) p[e] = acc[x][4 * g + e];
                 }
             }
@@ -254,21 +254,28 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
     }
 }
 
-template <class T, int KT, int MT>
+template <class T, int KT, int MT, int R>
 void launch(bool vec, const GemmArgs& a, const void* W, void* dx, int64_t ldd, hipStream_t s)
 {
     const dim3 grid((unsigned)(a.tr * a.splits)), block(kBackThreads<KT, MT>);
-    if (vec) hipLaunchKernelGGL((k_linear_back<T, KT, MT, true>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
-    else hipLaunchKernelGGL((k_linear_back<T, KT, MT, false>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+    if (vec) hipLaunchKernelGGL((k_linear_back<T, KT, MT, R, true>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+    else hipLaunchKernelGGL((k_linear_back<T, KT, MT, R, false>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+}
+
+template <class T, int R>
+void launch(bool vec, const GemmArgs& a, const BackPlan& p, const void* W, void* dx, int64_t ldd, hipStream_t s)
+{
+    if (p.kt == 128 && p.mt == 128) launch<T, 128, 128, R>(vec, a, W, dx, ldd, s);
+    else if (p.kt == 128) launch<T, 128, 64, R>(vec, a, W, dx, ldd, s);
+    else if (p.mt == 128) launch<T, 64, 128, R>(vec, a, W, dx, ldd, s);
+    else launch<T, 64, 64, R>(vec, a, W, dx, ldd, s);
 }
 
 template <class T>
-void launch(bool vec, const GemmArgs& a, int kt, int mt, const void* W, void* dx, int64_t ldd, hipStream_t s)
+void launch(bool vec, const GemmArgs& a, const BackPlan& p, const void* W, void* dx, int64_t ldd, hipStream_t s)
 {
-    if (kt == 128 && mt == 128) launch<T, 128, 128>(vec, a, W, dx, ldd, s);
-    else if (kt == 128) launch<T, 128, 64>(vec, a, W, dx, ldd, s);
-    else if (mt == 128) launch<T, 64, 128>(vec, a, W, dx, ldd, s);
-    else launch<T, 64, 64>(vec, a, W, dx, ldd, s);
+    if (p.rows == 32) launch<T, 32>(vec, a, p, W, dx, ldd, s);
+    else launch<T, 64>(vec, a, p, W, dx, ldd, s);
 }
 
 }  // namespace
@@ -279,8 +286,11 @@ BackPlan back_plan(int64_t n, int64_t k, int64_t m)
     p.kt = k <= 64 ? 64 : 128;
     p.mt = m <= 64 ? 64 : 128;
     p.tr = cdiv64(k, p.kt);
-    // a block to a compute unit (two of the small ones), every one with a chunk at least
-    const int64_t chunks = cdiv64(n, kRows), fill = cdiv64(p.kt + p.mt > 192 ? 256 : 512, p.tr);
+    // Half chunks where whole ones would leave compute units idle: what a block forms and multiplies
+    // one after the other is then half as long.
+    p.rows = p.tr * cdiv64(n, 64) <= 64 ? 32 : 64;
+    // a block to a compute unit (two of the smallest), every one with a chunk at least
+    const int64_t chunks = cdiv64(n, p.rows), fill = cdiv64(p.kt + p.mt > 128 ? 256 : 512, p.tr);
     p.splits = chunks < fill ? chunks : fill;
     p.splits = p.splits < 1 ? 1 : p.splits;
     return p;
@@ -289,8 +299,8 @@ BackPlan back_plan(int64_t n, int64_t k, int64_t m)
 hipError_t launch_linear_back(int dtype, bool vec, const GemmArgs& a, const BackPlan& p, const void* W, void* dx,
                               int64_t ldd, hipStream_t s)
 {
-    if (dtype == kF32) launch<float>(vec, a, p.kt, p.mt, W, dx, ldd, s);
-    else launch<bf16_t>(vec, a, p.kt, p.mt, W, dx, ldd, s);
+    if (dtype == kF32) launch<float>(vec, a, p, W, dx, ldd, s);
+    else launch<bf16_t>(vec, a, p, W, dx, ldd, s);
     return hipGetLastError();
 }
 

@@ -33,7 +33,7 @@ hipError_t launch_linear_rows(int dtype, bool vec, GemmArgs a, hipStream_t s);
 // the gradients of up to 128 outputs in one pass (cgtp_linear_back.hip): tr slabs of W, kt x mt
 // each, splits blocks to a slab
 struct BackPlan {
-    int kt, mt;
+    int kt, mt, rows;  // rows: of a chunk
     int64_t tr, splits;
 };
 BackPlan back_plan(int64_t n, int64_t k, int64_t m);
