@@ -326,14 +326,21 @@ def _generator(p, seed, offset, step, dev):
     return p, seed, offset, step.data_ptr()
 
 
-def _row_shape(t, name):
+def _row_shape(shape, name):
     """(N, C) of [N][C] or [B][S][C] rows."""
-    shape = t.shape
     if len(shape) == 2:
-        return shape[0], shape[1]
+        return shape
     if len(shape) == 3:
         return shape[0] * shape[1], shape[2]
     raise ValueError(f"{name} must be [N][C] or [B][S][C]")
+
+
+def _beside(t, name, x, shape, dev):
+    """(address, row stride) of rows that go with x's, or of none."""
+    if t is None:
+        return None, shape[-1]
+    _like(t, name, x.dtype, shape, dev)
+    return t.data_ptr(), _rows(t, name)
 
 
 def dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None, out=None) -> torch.Tensor:
@@ -347,19 +354,14 @@ def dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None, o
     ``step``, an int64 tensor [1] on the device, is added to the offset when the
     kernel runs, so that the replays of a captured graph draw new masks."""
     d = _dtype(x, "x")
-    N, C = _row_shape(x, "x")
-    dev = x.device
+    shape, dev = x.shape, x.device
+    N, C = _row_shape(shape, "x")
     ldx = _rows(x, "x")
-    if residual is None:
-        r, ldr = None, C
-    else:
-        _like(residual, "residual", x.dtype, x.shape, dev)
-        r, ldr = residual.data_ptr(), _rows(residual, "residual")
+    r, ldr = _beside(residual, "residual", x, shape, dev)
     if out is None:
-        out, ldo = x.new_empty(x.shape), C
+        out, ldo = x.new_empty(shape), C
     else:
-        _like(out, "out", x.dtype, x.shape, dev)
-        ldo = _rows(out, "out")
+        ldo = _beside(out, "out", x, shape, dev)[1]
     _call("cgtp_dropout", dev, d, N, C, *_generator(p, seed, offset, step, dev), x.data_ptr(), ldx, r, ldr,
           out.data_ptr(), ldo)
     return out
@@ -370,11 +372,11 @@ def linear_act_workspace_size(dtype, n_rows: int, in_channels: int, out_channels
     return _bytes("cgtp_linear_act_workspace_size", _DTYPES[dtype], n_rows, in_channels, out_channels, int(backward))
 
 
-def _weights(W, K, x):
-    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+def _weights(W, K, dtype, dev):
+    if not isinstance(W, torch.Tensor) or len(W.shape) != 2:
         raise TypeError("W must be a torch.Tensor [in][out]")
     M = W.shape[1]
-    _need(W, "W", x.dtype, (K, M), x.device)
+    _need(W, "W", dtype, (K, M), dev)
     return M
 
 
@@ -388,22 +390,17 @@ def linear_act_fwd(x, W, bias=None, act: str = "silu", residual=None, p_drop: fl
     ``dropout``'s, its mask by y's rows and channels.  z (contiguous, y's shape) is
     what the backward needs: None where ``save`` is false or act is "none"."""
     d = _dtype(x, "x")
-    N, K = _row_shape(x, "x")
-    dev = x.device
-    M = _weights(W, K, x)
+    shape, dev = x.shape, x.device
+    N, K = _row_shape(shape, "x")
+    M = _weights(W, K, x.dtype, dev)
     ldx = _rows(x, "x")
     b = _channel(bias, "bias", M, dev)
-    shape = x.shape[:-1] + (M,)
-    if residual is None:
-        r, ldr = None, M
-    else:
-        _like(residual, "residual", x.dtype, shape, dev)
-        r, ldr = residual.data_ptr(), _rows(residual, "residual")
+    shape = (N, M) if len(shape) == 2 else (shape[0], shape[1], M)
+    r, ldr = _beside(residual, "residual", x, shape, dev)
     if out is None:
         out, ldo = x.new_empty(shape), M
     else:
-        _like(out, "out", x.dtype, shape, dev)
-        ldo = _rows(out, "out")
+        ldo = _beside(out, "out", x, shape, dev)[1]
     a = _act(act)
     z = x.new_empty(shape) if save and a != L.CGTP_ACT_NONE else None
     nbytes = _bytes("cgtp_linear_act_workspace_size", d, N, K, M, 0)
@@ -421,10 +418,10 @@ def linear_act_bwd(x, W, z, grad_y, act: str = "silu", p_drop: float = 0.0, seed
     grad_y.  A gradient not in ``want`` comes back as None.  ``grad_x`` of x's shape
     may be a view with a row stride; grad_W has W's type, grad_bias is float32."""
     d = _dtype(x, "x")
-    N, K = _row_shape(x, "x")
-    dev = x.device
-    M = _weights(W, K, x)
-    shape = x.shape[:-1] + (M,)
+    shape, dev = x.shape, x.device
+    N, K = _row_shape(shape, "x")
+    M = _weights(W, K, x.dtype, dev)
+    shape = (N, M) if len(shape) == 2 else (shape[0], shape[1], M)
     _like(grad_y, "grad_y", x.dtype, shape, dev)
     ldx, ldg = _rows(x, "x"), _rows(grad_y, "grad_y")
     a = _act(act)
