@@ -357,3 +357,109 @@ def test_linear_offsets_beyond_32_bits(tt, dtype):
         y[n] = 0
         dx[n] = 0
         assert not dx.any()
+
+
+# every form of the product, its rows on odd addresses
+ODD = [(3, 600, 72), (300, 64, 128), (40, 3000, 24), (1100, 1024, 1032), (5000, 72, 264), (9000, 48, 200),
+       (3000, 96, 40), (700, 300, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("k", range(len(ODD)))
+def test_linear_on_odd_addresses(tt, k, dtype):
+    """Arrays that begin one element behind a 16-byte boundary, their rows an odd number of elements apart."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    N, K, M = ODD[k]
+    print(f"[linear] odd addresses N={N} K={K} M={M} {dtype}", flush=True)
+    dt, rng = _dt(torch, dtype), np.random.default_rng(k)
+    q = T.bf16 if dtype == "bf16" else (lambda v: v.astype(np.float32))
+
+    def rows_at(v, gap):
+        """v as rows `gap` elements apart more than their width, from an odd element on"""
+        n, c = v.shape
+        flat = torch.full((n * (c + gap) + 9,), float("nan"), dtype=dt, device=dev)
+        t = flat[1:1 + n * (c + gap)].view(n, c + gap)[:, :c]
+        t.copy_(torch.from_numpy(v.astype(np.float32)).to(dev))
+        return t, flat
+
+    x, W, r, g = (q(rng.standard_normal(s)) for s in ((N, K), (K, M), (N, M), (N, M)))
+    W = q(W / K ** 0.5)
+    b = rng.standard_normal(M).astype(np.float32)
+    m = D.mask(N, M, 0.2, 7, 9)
+    tx, tW, tr, tg = rows_at(x, 3)[0], rows_at(W, 0)[0], rows_at(r, 5)[0], rows_at(g, 1)[0]
+    tb = torch.cat([torch.zeros(1), torch.from_numpy(b)]).to(dev)[1:]
+    out, flat = rows_at(np.zeros((N, M)), 1)
+    cg.linear_act_fwd(tx, tW, tb, "tanh", residual=tr, p_drop=0.2, seed=7, offset=9, out=out, save=False)
+    wy, wz = D.linear_fwd(x, W, b, r, "tanh", m)
+    tz = (steps(dtype) * K + 4) * U * (np.abs(x).astype(np.float64) @ np.abs(W).astype(np.float64)) + 2 * U * np.abs(wz)
+    ty = 1.1 * m * tz + 8 * U * m * np.maximum(1, np.abs(wz)) + 3 * U * (np.abs(wy) + np.abs(r))
+    near("y", out, wy, ty + HALF[dtype] * np.abs(wy), dtype, K, extra=16 * U)
+    assert int(torch.isnan(flat).sum()) == flat.numel() - N * M
+    z = q(wz.astype(np.float32))
+    zt = rows_at(z, 0)[0]
+    gx, flat = rows_at(np.zeros((N, K)), 1)
+    dx, dW, db = cg.linear_act_bwd(tx, tW, zt, tg, "tanh", p_drop=0.2, seed=7, offset=9, grad_x=gx)
+    wdx, wdW, wdb, dz = D.linear_bwd(x, W, z, g, "tanh", m)
+    e = np.abs(dz) * 2 * U + 16 * U * (1 + np.abs(z)) * np.abs(g) * m
+    rounded = e + (HALF["bf16"] * np.abs(dz) if dtype == "bf16" else 0)
+    aW, ax = np.abs(W).astype(np.float64).T, np.abs(x).astype(np.float64).T
+    near("dx", dx, wdx, rounded @ aW + (steps(dtype) * M + 4) * U * (np.abs(dz) @ aW) + (HALF[dtype] + 2 * U) * np.abs(wdx),
+         dtype, M, extra=16 * U)
+    near("dW", dW, wdW, ax @ rounded + (steps(dtype) * N + 4) * U * (ax @ np.abs(dz)) + (HALF[dtype] + 2 * U) * np.abs(wdW),
+         dtype, N, extra=16 * U)
+    near("db", db, wdb, e.sum(0) + 2 * U * np.abs(wdb) + N * 2.0 ** -53 * np.abs(dz).sum(0), "bf16", N)
+    assert int(torch.isnan(flat).sum()) == flat.numel() - N * K
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,K,M", [(3, 65536, 8), (40, 65536, 24), (5, 8, 65536), (300, 16, 65536), (260, 65536, 16)])
+def test_linear_widest(tt, N, K, M, dtype):
+    """The largest widths: rows that pick one input each give that row of W, and one output's
+    gradient gives that column (exact: one term of each product is not zero)."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    print(f"[linear] widest N={N} K={K} M={M} {dtype}", flush=True)
+    dt = _dt(torch, dtype)
+    W = torch.randn(K, M, device=dev).to(dt)
+    at = (torch.arange(N, device=dev) * 7919 + K - 1) % K
+    x = torch.zeros(N, K, device=dev, dtype=dt)
+    x[torch.arange(N, device=dev), at] = 1.0
+    assert torch.equal(cg.linear_act_fwd(x, W, act="none")[0], W[at])
+    to = (torch.arange(N, device=dev) * 4001 + M - 1) % M
+    g = torch.zeros(N, M, device=dev, dtype=dt)
+    g[torch.arange(N, device=dev), to] = 1.0
+    dx, dW, db = cg.linear_act_bwd(x, W, None, g, act="none")
+    assert torch.equal(dx, W.t()[to])
+    want = torch.zeros(K, M, device=dev).index_put_((at, to), torch.ones(N, device=dev), accumulate=True)
+    assert torch.equal(dW.float(), want) and torch.equal(db, g.float().sum(0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,K,M", [(4, 600, 72), (300, 64, 136), (40, 200, 48), (1100, 1024, 1032), (5000, 72, 264),
+                                   (9000, 48, 200), (700, 300, 128), (70, 33, 35)])
+def test_infinities_reach_only_their_results(tt, N, K, M, dtype):
+    """An infinity or NaN in a column of W spoils that column of y and that input's dx; in x, that row of y
+    and that row of dW; in the gradient, that row of dx, that column of dW and that sum: all else is what it was."""
+    torch, dev = tt
+    import clebsch_gordan_tensor_cgtp_amd as cg
+    dt = _dt(torch, dtype)
+    print(f"[linear] infinities N={N} K={K} M={M} {dtype}", flush=True)
+    x, W, g = (torch.randn(*s, device=dev).to(dt) for s in ((N, K), (K, M), (N, M)))
+    run = lambda x, W, g: (cg.linear_act_fwd(x, W, act="none")[0],) + cg.linear_act_bwd(x, W, None, g, act="none")  # noqa: E731
+    clean = run(x, W, g)
+    n, k, c = N - 2, K // 2, M - 3
+    for bad in (float("inf"), float("nan")):
+        for which in "xWg":
+            a = {"x": x.clone(), "W": W.clone(), "g": g.clone()}
+            a[which][{"x": (n, k), "W": (k, c), "g": (n, c)}[which]] = bad
+            hit = [torch.zeros_like(v, dtype=torch.bool) for v in clean]     # y, dx, dW, db
+            if which == "x":
+                hit[0][n], hit[2][k] = True, True
+            elif which == "W":
+                hit[0][:, c], hit[1][:, k] = True, True
+            else:
+                hit[1][n], hit[2][:, c], hit[3][c] = True, True, True
+            for name, u, v, h in zip(("y", "dx", "dW", "db"), run(a["x"], a["W"], a["g"]), clean, hit):
+                assert torch.equal(u[~h], v[~h]), (which, bad, name)
+                assert not torch.isfinite(u[h]).any(), (which, bad, name)
