@@ -24,12 +24,6 @@ struct Drawn {
     __device__ __forceinline__ uint32_t operator[](int j) const { return j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu; }
 };
 
-// (one operation; the compiler makes two: 400008 x 256 bf16 69.5 against 72.7 us)
-__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c)
-{
-    return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
-}
-
 __device__ __forceinline__ Drawn philox(uint32_t block, uint32_t row, uint64_t offset, uint64_t seed)
 {
     uint32_t a = block, b = row, c = (uint32_t)offset, d = (uint32_t)(offset >> 32);
@@ -37,9 +31,9 @@ __device__ __forceinline__ Drawn philox(uint32_t block, uint32_t row, uint64_t o
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t p = (uint64_t)a * 0xD2511F53u, q = (uint64_t)c * 0xCD9E8D57u;
-        a = xor3((uint32_t)(q >> 32), b, k);
+        a = (uint32_t)(q >> 32) ^ b ^ k;
         b = (uint32_t)q;
-        c = xor3((uint32_t)(p >> 32), d, l);
+        c = (uint32_t)(p >> 32) ^ d ^ l;
         d = (uint32_t)p;
         k += 0x9E3779B9u;
         l += 0xBB67AE85u;
