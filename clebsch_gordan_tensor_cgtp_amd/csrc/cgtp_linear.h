@@ -57,7 +57,25 @@ struct GemmArgs {
 template <class T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 
-// v as kPlanes bf16 vectors
+// and dz: of a bf16 gradient two, so that its rounding does not add to the result's, where memory and
+// not the products bound the kernel (cgtp_linear_wide.hip has one)
+template <class T>
+constexpr int kSlopePlanes = sizeof(T) == 4 ? 3 : 2;
+
+// The products of operands of NA and NB planes, the smallest first: f(i, j) for plane i of the one and
+// j of the other, i + j below the larger number.
+template <int NA, int NB, class F>
+__device__ __forceinline__ void each_product(F&& f)
+{
+    constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+    for (int o = N - 1; o >= 0; --o)
+#pragma unroll
+        for (int i = 0; i <= o; ++i)
+            if (i < NA && o - i < NB) f(i, o - i);
+}
+
+// v as NP bf16 vectors
 template <int NP>
 __device__ __forceinline__ void cut(f8 v, b8 (&p)[NP])
 {

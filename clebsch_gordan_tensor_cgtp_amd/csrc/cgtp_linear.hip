@@ -13,10 +13,12 @@
 // accumulation run at a sixth of the bf16 rate where fp32 matrix instructions reach a
 // sixteenth.  An infinity leaves a NaN in its remainders, so that the results it reaches
 // are not finite (NaN, where an fp32 product might give an infinity).
-// bf16 operands are multiplied as they are; dz of a bf16 gradient is formed in fp32 and
-// rounded once to bf16 for the two products (not for db): its rounding is as large as
-// that of the result and independent of it.  The scale of the dropout multiplies the
-// fp32 results, so that without an activation dz is exact.
+// bf16 operands are multiplied as they are; dz of a bf16 gradient is formed in fp32 and cut
+// into two bf16 numbers (16 bits), where rounding it to one would leave an error as large as
+// the result's own rounding and independent of it (2.3e-3 against 1.7e-3 in the 2-norm).  Only the
+// large products of cgtp_linear_wide.hip, which the matrix cores bound, take dz rounded once: two
+// products there would double their time.  The scale of the dropout multiplies the fp32 results, so
+// that without an activation dz is exact.
 //
 // Layout.  Tiles go through registers into LDS, as they lie in memory: a row of a tile is a
 // run of k (x, g, W in dx) or, where the contraction runs across the rows (W in y; x and g
@@ -39,11 +41,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBK = 32;  // contraction per step
 
-// A tile of RUNS rows of WIDTH elements in LDS, kPlanes of them.  ALONG: the contraction
+// A tile of RUNS rows of WIDTH elements in LDS, NP planes of it.  ALONG: the contraction
 // runs along the rows.  The pads put the rows that are read together on different banks.
-template <class T, int RUNS, int WIDTH, bool ALONG>
+template <int kNP, int RUNS, int WIDTH, bool ALONG>
 struct Side {
-    static constexpr int NP = kPlanes<T>;
+    static constexpr int NP = kNP;
     static constexpr bool kAlong = ALONG;
     static constexpr int kLd = WIDTH + (ALONG ? 8 : 16);
     static constexpr int kHalves = RUNS * kLd;  // of one plane
@@ -73,16 +75,16 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
 {
     // rows' side P and columns' side Q
     constexpr bool kAlongP = KIND != kDw, kAlongQ = KIND == kDx;
-    using P = Side<T, kAlongP ? BM : kBK, kAlongP ? kBK : BM, kAlongP>;
-    using Q = Side<T, kAlongQ ? BN : kBK, kAlongQ ? kBK : BN, kAlongQ>;
-    constexpr int NP = kPlanes<T>, WM = BM / 2, WN = BN / 2, FM = WM / 32, FN = WN / 32;
+    using P = Side<KIND == kDx ? kSlopePlanes<T> : kPlanes<T>, kAlongP ? BM : kBK, kAlongP ? kBK : BM, kAlongP>;
+    using Q = Side<KIND == kDw ? kSlopePlanes<T> : kPlanes<T>, kAlongQ ? BN : kBK, kAlongQ ? kBK : BN, kAlongQ>;
+    constexpr int WM = BM / 2, WN = BN / 2, FM = WM / 32, FN = WN / 32;
     constexpr bool kSlopeP = KIND == kDx, kSlopeQ = KIND == kDw;
     constexpr int kLdS = BN + 4, kHalf = BM / 2;  // the result leaves in two halves
-    constexpr int kTiles = (P::kHalves + Q::kHalves) * NP * 2, kOut = kHalf * kLdS * 4, kSums = kThreads * 64;
+    constexpr int kTiles = (P::kHalves * P::NP + Q::kHalves * Q::NP) * 2, kOut = kHalf * kLdS * 4, kSums = kThreads * 64;
     constexpr int kMem = kTiles > kOut ? kTiles : kOut;
     __shared__ __attribute__((aligned(16))) char mem[KIND == kDw && kSums > kMem ? kSums : kMem];
     uint16_t* sp = reinterpret_cast<uint16_t*>(mem);
-    uint16_t* sq = sp + P::kHalves * NP;
+    uint16_t* sq = sp + P::kHalves * P::NP;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t at = xcd_order(blockIdx.x, gridDim.x);
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
     const bool sums = KIND == kDw && a.db && r0 == 0;
     auto put = [&](auto side, uint16_t* s, const Raw8<T>* raw, auto slope, int64_t n0, int64_t e0) {
         using S = decltype(side);
-        constexpr int kPer = S::kPer;
+        constexpr int kPer = S::kPer, NP = S::NP;
 #pragma unroll
         for (int i = 0; i < S::kEach; ++i) {
             const int b = tid + i * kThreads;
@@ -178,24 +180,23 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
     auto multiply = [&]() {
 #pragma unroll
         for (int ks = 0; ks < kBK; ks += 16) {
-            b8 fp[FM][NP], fq[FN][NP];
+            b8 fp[FM][P::NP], fq[FN][Q::NP];
 #pragma unroll
-            for (int p = NP - 1; p >= 0; --p) {
+            for (int p = 2; p >= 0; --p) {
 #pragma unroll
-                for (int x = 0; x < FM; ++x) fp[x][p] = P::read(sp, p, wm + 32 * x, ks, lane);
+                for (int x = 0; x < FM; ++x)
+                    if (p < P::NP) fp[x][p] = P::read(sp, p, wm + 32 * x, ks, lane);
 #pragma unroll
-                for (int y = 0; y < FN; ++y) fq[y][p] = Q::read(sq, p, wn + 32 * y, ks, lane);
+                for (int y = 0; y < FN; ++y)
+                    if (p < Q::NP) fq[y][p] = Q::read(sq, p, wn + 32 * y, ks, lane);
             }
-            // the smallest terms first
+            each_product<P::NP, Q::NP>([&](int i, int j) {
 #pragma unroll
-            for (int o = NP - 1; o >= 0; --o)
+                for (int x = 0; x < FM; ++x)
 #pragma unroll
-                for (int p = 0; p <= o; ++p)
-#pragma unroll
-                    for (int x = 0; x < FM; ++x)
-#pragma unroll
-                        for (int y = 0; y < FN; ++y)
-                            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[y][o - p], fp[x][p], acc[x][y], 0, 0, 0);
+                    for (int y = 0; y < FN; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fq[y][j], fp[x][i], acc[x][y], 0, 0, 0);
+            });
         }
     };
 
@@ -352,9 +353,10 @@ Dims dims_of(const LinShape& n, int kind)
 }
 
 // Tiles of 128 where they fill the chip or the result is that wide; the contraction is cut
-// where tiles alone leave compute units idle, into parts of at least four steps and some four blocks to a
-// compute unit.  (970 x 151 x 4092 bf16 gradients 55 us, with eight steps and two blocks 83; where
-// 252 tiles are there, 4000 x 256 x 256 bf16, cutting costs 11.7 us against 6.4.)
+// where tiles alone leave compute units idle, into parts of at least four steps (twelve where half of
+// the compute units have a tile) and some four blocks to a compute unit.  (970 x 151 x 4092 bf16 gradients
+// 55 us, with eight steps and two blocks 83; 345 x 794 x 2198 fp32, 210 tiles, 31 against 45 uncut; 4000 x
+// 256 x 256 bf16, 252 tiles, cut 11.7 against 6.4.)
 Plan plan_tiles(const Dims& d)
 {
     Plan p{};
@@ -366,8 +368,8 @@ Plan plan_tiles(const Dims& d)
     if (tiles() < 256) p.bn = 64;
     p.tr = cdiv64(d.rows, p.bm);
     p.tc = cdiv64(d.cols, p.bn);
-    const int64_t n = p.tr * p.tc, most = cdiv64(d.depth, 4 * kBK);
-    int64_t s = n >= 200 ? 1 : 1024 / n;
+    const int64_t n = p.tr * p.tc, most = d.depth / (n < 128 ? 4 * kBK : 12 * kBK);
+    int64_t s = n >= 256 ? 1 : 1024 / n;
     s = s < most ? s : most;
     s = s < 1 ? 1 : s;
     p.run = cdiv64(cdiv64(d.depth, s), kBK) * kBK;

@@ -28,7 +28,7 @@ template <class T, int KT, int MT, int kRows, bool VEC>
 __global__ void __launch_bounds__((kBackThreads<KT, MT>))
 k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t ldd)
 {
-    constexpr int kThr = kBackThreads<KT, MT>, NW = kThr / 64, NP = kPlanes<T>;
+    constexpr int kThr = kBackThreads<KT, MT>, NW = kThr / 64, NP = kPlanes<T>, NZ = kSlopePlanes<T>;
     constexpr int kLdX = KT + 16, kLdZ = MT + 16, kPlaneX = kRows * kLdX, kPlaneZ = kRows * kLdZ;  // halves
     constexpr int kPerX = KT / 8, kPerZ = MT / 8, kAllX = kRows * kPerX, kAllZ = kRows * kPerZ;
     constexpr int kEachX = (kAllX + kThr - 1) / kThr, kEachZ = (kAllZ + kThr - 1) / kThr;
@@ -38,7 +38,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
     // dx: tiles of 32 rows by 32 inputs, a wave each
     constexpr int kMsteps = MT / 16;
     constexpr int kLdS = 36;
-    constexpr int kTiles = (kPlaneX + kPlaneZ) * NP * 2, kSums = kThr * 64, kPatch = NW * 32 * kLdS * 4;
+    constexpr int kTiles = (kPlaneX * NP + kPlaneZ * NZ) * 2, kSums = kThr * 64, kPatch = NW * 32 * kLdS * 4;
     __shared__ __attribute__((aligned(16))) char mem[kTiles + kPatch > kSums ? kTiles + kPatch : kSums];
     uint16_t* sx = reinterpret_cast<uint16_t*>(mem);
     uint16_t* sz = sx + kPlaneX * NP;
@@ -121,11 +121,12 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
 
     for (int64_t n0 = part * kRows; n0 < a.depth; n0 += a.splits * kRows) {
         if (n0 != part * kRows) __syncthreads();
-        auto put = [&](uint16_t* to, int plane, const f8& v) {
-            b8 p[NP];
+        auto put = [&](uint16_t* to, int plane, const f8& v, auto planes) {
+            constexpr int N = decltype(planes)::value;
+            b8 p[N];
             cut(v, p);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) *reinterpret_cast<b8*>(to + i * plane) = p[i];
+            for (int i = 0; i < N; ++i) *reinterpret_cast<b8*>(to + i * plane) = p[i];
         };
 #pragma unroll
         for (int i = 0; i < kEachZ; ++i) {
@@ -144,7 +145,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
             }
-            put(sz + row * kLdZ + col, kPlaneZ, v);
+            put(sz + row * kLdZ + col, kPlaneZ, v, std::integral_constant<int, NZ>{});
         }
         if (a.want) {
 #pragma unroll
@@ -154,7 +155,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
                 f8 v;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = rx[i][j];
-                put(sx + b / kPerX * kLdX + b % kPerX * 8, kPlaneX, v);
+                put(sx + b / kPerX * kLdX + b % kPerX * 8, kPlaneX, v, std::integral_constant<int, NP>{});
             }
         }
         __syncthreads();
@@ -162,20 +163,18 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
         if (a.want) {
 #pragma unroll
             for (int k = 0; k < kRows; k += 16) {
-                b8 q[NP], p[FP][NP];
+                b8 q[NZ], p[FP][NP];
 #pragma unroll
-                for (int o = NP - 1; o >= 0; --o) {
-                    q[o] = read_across(pz + o * kPlaneZ + k * kLdZ, kLdZ);
-#pragma unroll
-                    for (int x = 0; x < FP; ++x) p[x][o] = read_across(px + o * kPlaneX + k * kLdX + 32 * x, kLdX);
-                }
+                for (int o = NZ - 1; o >= 0; --o) q[o] = read_across(pz + o * kPlaneZ + k * kLdZ, kLdZ);
 #pragma unroll
                 for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-                    for (int i = 0; i <= o; ++i)
+                    for (int x = 0; x < FP; ++x) p[x][o] = read_across(px + o * kPlaneX + k * kLdX + 32 * x, kLdX);
+                each_product<NP, NZ>([&](int i, int j) {
 #pragma unroll
-                        for (int x = 0; x < FP; ++x)
-                            acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[o - i], p[x][i], acc[x], 0, 0, 0);
+                    for (int x = 0; x < FP; ++x)
+                        acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j], p[x][i], acc[x], 0, 0, 0);
+                });
             }
         }
         {
@@ -186,14 +185,11 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
                 const uint16_t* pa = sz + (wr + (lane & 31)) * kLdZ + 8 * (lane >> 5);
 #pragma unroll
                 for (int k = 0; k < kMsteps; ++k) {
-                    b8 p[NP];
+                    b8 p[NZ];
 #pragma unroll
-                    for (int o = NP - 1; o >= 0; --o) p[o] = *reinterpret_cast<const b8*>(pa + o * kPlaneZ + 16 * k);
-#pragma unroll
-                    for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-                        for (int i = 0; i <= o; ++i)
-                            d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[k][o - i], p[i], d, 0, 0, 0);
+                    for (int o = NZ - 1; o >= 0; --o) p[o] = *reinterpret_cast<const b8*>(pa + o * kPlaneZ + 16 * k);
+                    each_product<NZ, NP>(
+                        [&](int i, int j) { d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[k][j], p[i], d, 0, 0, 0); });
                 }
                 // a lane holds row lane % 32, inputs 8 g + 4 (lane / 32) + 0 .. 3
 #pragma unroll

@@ -4,7 +4,7 @@
 // The operands are bf16 in memory: x, W and g as the caller has them, or as planes that a
 // pass of their own has written to the workspace -- the three numbers of an fp32 operand
 // (cgtp_linear.hip), dz with its mask and slope (formed once instead of in every tile
-// that needs it; its columns' sums on the way).  A product of three planes each goes
+// that needs it, rounded once for bf16; its columns' sums on the way).  A product of three planes each goes
 // through the contraction six times, the smallest products first, into one accumulator.
 //
 // A block of four waves computes a BM x BN tile, each wave WM x WN of it, through a ring of three LDS
@@ -327,7 +327,7 @@ k_linear_wide(WideArgs w)
 template <class T, int KC, int FR, bool HZ>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_linear_dx(WideArgs w)
 {
-    constexpr int NP = kPlanes<T>, FC = KC / 32, kThr = 256;
+    constexpr int NP = kPlanes<T>, NZ = kSlopePlanes<T>, FC = KC / 32, kThr = 256;
     using Q = Tile<KC, kThr, true>;
     constexpr int kPlane = KC * kStep, kLdS = 36;  // halves; floats
     __shared__ __attribute__((aligned(16))) uint16_t ring[2][NP * kPlane];
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k
         asm volatile("" ::: "memory");  // (and stay so)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            b8 p[FR][NP], q[FC][NP];
+            b8 p[FR][NZ], q[FC][NP];
             const int64_t e = k + 16 * ks + 8 * (lane >> 5);
 #pragma unroll
             for (int x = 0; x < FR; ++x) {
@@ -416,15 +416,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k
             for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
                 for (int y = 0; y < FC; ++y) q[y][o] = Q::read(&ring[slot][o * kPlane], 32 * y, ks, lane);
+            each_product<NZ, NP>([&](int i, int j) {
 #pragma unroll
-            for (int o = NP - 1; o >= 0; --o)
+                for (int x = 0; x < FR; ++x)
 #pragma unroll
-                for (int i = 0; i <= o; ++i)
-#pragma unroll
-                    for (int x = 0; x < FR; ++x)
-#pragma unroll
-                        for (int y = 0; y < FC; ++y)
-                            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[y][o - i], p[x][i], acc[x][y], 0, 0, 0);
+                    for (int y = 0; y < FC; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[y][j], p[x][i], acc[x][y], 0, 0, 0);
+            });
         }
     };
     fill(0, 0);
