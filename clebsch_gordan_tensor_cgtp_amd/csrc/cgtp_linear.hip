@@ -407,11 +407,14 @@ int64_t rest_of(const Dims& d)
 
 constexpr int64_t kMaxWideLd = int64_t(1) << 22;  // row strides: a tile's byte offsets stay in 32 bits
 
-// Planes where the products bound the call, not memory or launches.
+// Planes where the products bound the call, not memory or launches: forward and gradients of fp32 2048 x 1024 x
+// 512 (1.07e9) 43 and 72 us, by tiles 30 and 66; 1500 x 1024 x 1024 (1.57e9) 46 and 91, by tiles 42 and 132.
+// bf16 1000 x 256 x 512 (1.3e8) 7.1 and 23.6, by tiles 5.9 and 23.7; 800 x 512 x 512 (2.1e8) 8.5 and
+// 21.6, by tiles 10.4 and 27.3.
 bool wide_shape(const LinShape& n)
 {
     return n.K % 8 == 0 && n.M % 8 == 0 && n.N >= 256 && n.K >= 256 && n.M >= 256 &&
-           (double)n.N * (double)n.K * (double)n.M >= 1e9;
+           (double)n.N * (double)n.K * (double)n.M >= (n.dtype == kF32 ? 1.1e9 : 2e8);
 }
 
 // Few rows: one pass over W on the vector units.  Replayed from a graph, us: 1, 4 and 16 rows x

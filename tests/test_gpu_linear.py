@@ -86,6 +86,7 @@ CASES = [(1, 1, 1, 1, 0.0, True, True), (1, 8, 8, 1, 0.0, True, False), (2, 3, 5
          (9001, 64, 200, 1, 0.0, True, False), (8200, 40, 1000, 2, 0.0, True, False), (8193, 7, 136, 1, 0.0, True, True),
          (5000, 120, 264, 1, 0.1, True, False), (12345, 50, 131, 1, 0.0, False, False), (20000, 64, 1920, 1, 0.0, False, False),
          (8192, 64, 136, 1, 0.5, True, False),
+         (1300, 1000, 1032, 1, 0.1, True, True), (1400, 1032, 1000, 2, 0.0, False, False), (810, 520, 512, 1, 0.1, True, True),
          # rows behind the last whole tile that go by themselves
          (4097, 512, 4096, 1, 0.1, True, True), (16390, 1032, 264, 1, 0.5, True, True),
          (16448, 264, 1024, 2, 0.1, True, False)]
