@@ -188,17 +188,21 @@ k_linear_rows(GemmArgs a)
 template <class T, int NK, bool VEC>
 void launch(GemmArgs& a, hipStream_t s)
 {
-    // Waves along the rows where there are enough of them, and stretches of columns for some
-    // 2048 blocks (what a block has cut of x serves a whole stretch).
-    const bool tall = a.rows >= 32 * 1024;
-    a.tr = cdiv64(a.rows, tall ? 128 : 64);
+    // All four waves along the rows where their blocks fill the chip (50000 x 128 x 128 bf16 13.0 us, two along
+    // the columns 16.9; 20000 x 128 x 1024 23 and 30), with very few inputs, whose blocks are short,
+    // where they do so twice (105730 x 8 x 64 fp32 15.8 and 14.5, x 16 x 128 23 and 25), and with 128 fp32 inputs
+    // never: their registers would spill (50000 x 128 x 128 35.7 and 31.5).  Stretches of columns for some
+    // 2048 blocks: what a block has cut of x serves a whole stretch.
     const int64_t tiles = cdiv64(a.cols, kCols);
+    constexpr bool kTall = NK * kPlanes<T> <= 12;
+    const bool tall = kTall && cdiv64(a.rows, 128) * tiles >= (NK == 1 ? 1536 : 768);
+    a.tr = cdiv64(a.rows, tall ? 128 : 64);
     int64_t n = cdiv64(2048, a.tr);
     n = n < tiles ? n : tiles;
     a.run = cdiv64(tiles, n) * kCols;
     a.tc = cdiv64(a.cols, a.run);
     const dim3 grid((unsigned)(a.tr * a.tc));
-    if (tall) hipLaunchKernelGGL((k_linear_rows<T, NK, 4, VEC>), grid, dim3(kThreads), 0, s, a);
+    if (tall) hipLaunchKernelGGL((k_linear_rows<T, NK, kTall ? 4 : 2, VEC>), grid, dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((k_linear_rows<T, NK, 2, VEC>), grid, dim3(kThreads), 0, s, a);
 }
 
