@@ -57,10 +57,10 @@ struct GemmArgs {
 template <class T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 
-// and dz: of a bf16 gradient two, so that its rounding does not add to the result's, where memory and
-// not the products bound the kernel (cgtp_linear_wide.hip has one)
-template <class T>
-constexpr int kSlopePlanes = sizeof(T) == 4 ? 3 : 2;
+// and dz = mask g act'(z): an fp32 number whatever g's type, so three, but those of g where there is no
+// slope (HZ: there may be a z), which the mask alone leaves as it is
+template <class T, bool HZ>
+constexpr int kSlopePlanes = HZ ? 3 : kPlanes<T>;
 
 // The products of operands of NA and NB planes, the smallest first: f(i, j) for plane i of the one and
 // j of the other, i + j below the larger number.

@@ -13,12 +13,11 @@
 // accumulation run at a sixth of the bf16 rate where fp32 matrix instructions reach a
 // sixteenth.  An infinity leaves a NaN in its remainders, so that the results it reaches
 // are not finite (NaN, where an fp32 product might give an infinity).
-// bf16 operands are multiplied as they are; dz of a bf16 gradient is formed in fp32 and cut
-// into two bf16 numbers (16 bits), where rounding it to one would leave an error as large as
-// the result's own rounding and independent of it (2.3e-3 against 1.7e-3 in the 2-norm).  Only the
-// large products of cgtp_linear_wide.hip, which the matrix cores bound, take dz rounded once: two
-// products there would double their time.  The scale of the dropout multiplies the fp32 results, so
-// that without an activation dz is exact.
+// bf16 operands are multiplied as they are.  dz of a bf16 gradient is an fp32 number and cut into three
+// like one, so that a gradient is rounded once, as a result (one bf16 number would add an error as
+// large as that rounding, 2.3e-3 against 1.7e-3 in the 2-norm; two, 16 bits, would send more
+// results the other way).  The scale of the dropout multiplies the fp32 results, so that without an
+// activation dz is a masked g, and one number.
 //
 // Layout.  Tiles go through registers into LDS, as they lie in memory: a row of a tile is a
 // run of k (x, g, W in dx) or, where the contraction runs across the rows (W in y; x and g
@@ -74,13 +73,13 @@ struct Side {
 // 2198 fp32 33 us, 20 x 256 x 1024 bf16 6.4, 600 x 1024 x 1024 fp32 26 (its six products 3.8 GFLOP, 7 us
 // of the matrix cores).  VEC: every row of every
 // array begins on 16 bytes and is a multiple of eight elements long.
-template <class T, int KIND, int BM, int BN, bool VEC>
+template <class T, int KIND, int BM, int BN, bool VEC, bool HZ>
 __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
 {
     // rows' side P and columns' side Q
     constexpr bool kAlongP = KIND != kDw, kAlongQ = KIND == kDx;
-    using P = Side<KIND == kDx ? kSlopePlanes<T> : kPlanes<T>, kAlongP ? BM : kBK, kAlongP ? kBK : BM, kAlongP>;
-    using Q = Side<KIND == kDw ? kSlopePlanes<T> : kPlanes<T>, kAlongQ ? BN : kBK, kAlongQ ? kBK : BN, kAlongQ>;
+    using P = Side<KIND == kDx ? kSlopePlanes<T, HZ> : kPlanes<T>, kAlongP ? BM : kBK, kAlongP ? kBK : BM, kAlongP>;
+    using Q = Side<KIND == kDw ? kSlopePlanes<T, HZ> : kPlanes<T>, kAlongQ ? BN : kBK, kAlongQ ? kBK : BN, kAlongQ>;
     constexpr int WM = BM / 2, WN = BN / 2, FM = WM / 32, FN = WN / 32;
     constexpr bool kSlopeP = KIND == kDx, kSlopeQ = KIND == kDw;
     constexpr int kLdS = BN + 4, kHalf = BM / 2;  // the result leaves in two halves
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
 
     // The thread's blocks of eight: row `run` of the tile, element 8 * c.
     // Rows outside are taken as zero, elements outside too.
-    Raw8<T> rp[P::kEach], rq[Q::kEach], rz[kSlopeP ? P::kEach : kSlopeQ ? Q::kEach : 1];
+    Raw8<T> rp[P::kEach], rq[Q::kEach], rz[!HZ ? 1 : kSlopeP ? P::kEach : kSlopeQ ? Q::kEach : 1];
     auto fetch = [&](auto side, Raw8<T>* raw, const T* base, int64_t ld, int64_t n0, int64_t lim_n, int64_t e0,
                      int64_t lim_e) {
         using S = decltype(side);
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
     auto load = [&](int64_t k) {
         if constexpr (kAlongP) {
             fetch(P{}, rp, (const T*)a.A, a.lda, r0, a.rows, k, k1);
-            if (kSlopeP && a.Z) fetch(P{}, rz, (const T*)a.Z, a.ldz, r0, a.rows, k, k1);
+            if (kSlopeP && HZ && a.Z) fetch(P{}, rz, (const T*)a.Z, a.ldz, r0, a.rows, k, k1);
         } else {
             if (product) fetch(P{}, rp, (const T*)a.A, a.lda, k, k1, r0, a.rows);
         }
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
             fetch(Q{}, rq, (const T*)a.B, a.ldb, c0, a.cols, k, k1);
         } else {
             fetch(Q{}, rq, (const T*)a.B, a.ldb, k, k1, c0, a.cols);
-            if (kSlopeQ && a.Z) fetch(Q{}, rz, (const T*)a.Z, a.ldz, k, k1, c0, a.cols);
+            if (kSlopeQ && HZ && a.Z) fetch(Q{}, rz, (const T*)a.Z, a.ldz, k, k1, c0, a.cols);
         }
     };
     double sum[8] = {};  // of dz's columns 8 (tid % kPer) .. + 7
@@ -147,10 +146,12 @@ __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = raw[i][j];
                 if constexpr (decltype(slope)::value) {
-                    float z[8];
+                    float z[8] = {};
+                    if constexpr (HZ) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) z[j] = rz[i][j];
-                    slope8(a, offset, v, z, n0 + b / kPer, (int32_t)((e0 + b % kPer * 8) / 8));
+                        for (int j = 0; j < 8; ++j) z[j] = rz[i][j];
+                    }
+                    slope8<HZ>(a, offset, v, z, n0 + b / kPer, (int32_t)((e0 + b % kPer * 8) / 8));
                     if (sums) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
@@ -490,7 +491,7 @@ struct WideSpace {
             at += round256(b);
             return was;
         };
-        dz = take(backward ? (size_t)(np * n.N * n.M) * 2 : 0);
+        dz = take(backward ? (size_t)(3 * n.N * n.M) * 2 : 0);
         x = take(np > 1 ? (size_t)(np * n.N * n.K) * 2 : 0);
         W = take(np > 1 ? (size_t)(np * n.K * n.M) * 2 : 0);
         db = take(backward ? (size_t)(cdiv64(n.N, plane_run(n.N, n.M)) * n.M) * 8 : 0);
@@ -536,11 +537,18 @@ hipError_t run(GemmArgs& a, const Plan& p, void* ws, hipStream_t s)
         a.db_part = (double*)((char*)ws + round256((size_t)(p.splits * a.rows * a.cols) * 4));
         a.db_splits = p.splits;
     }
-    const dim3 grid((unsigned)(p.tr * p.tc * p.splits)), block(kThreads);
-    if (p.bm == 128 && p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 128, VEC>), grid, block, 0, s, a);
-    else if (p.bm == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 64, VEC>), grid, block, 0, s, a);
-    else if (p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 64, 128, VEC>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_linear<T, KIND, 64, 64, VEC>), grid, block, 0, s, a);
+    auto tiles = [&](auto z) {
+        constexpr bool HZ = decltype(z)::value;
+        const dim3 grid((unsigned)(p.tr * p.tc * p.splits)), block(kThreads);
+        if (p.bm == 128 && p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 128, VEC, HZ>), grid, block, 0, s, a);
+        else if (p.bm == 128) hipLaunchKernelGGL((k_linear<T, KIND, 128, 64, VEC, HZ>), grid, block, 0, s, a);
+        else if (p.bn == 128) hipLaunchKernelGGL((k_linear<T, KIND, 64, 128, VEC, HZ>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_linear<T, KIND, 64, 64, VEC, HZ>), grid, block, 0, s, a);
+    };
+    // (fp32 operands have three planes either way)
+    if constexpr (KIND == kFwd) tiles(std::false_type{});
+    else if (kPlanes<T> == 3 || a.Z) tiles(std::true_type{});
+    else tiles(std::false_type{});
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || p.splits <= 1 ? e : join<T, KIND, VEC>(a, s);
 }

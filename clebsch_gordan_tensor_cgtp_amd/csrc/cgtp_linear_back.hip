@@ -4,7 +4,8 @@
 //
 // Memory bounds these: g, z and x are read and dx is written once.  A block owns a KT x MT slab of
 // W and goes through chunks of 64 (or 32) rows, one of every `splits`: dz and x go through registers
-// (fetched while the chunk before is multiplied) into LDS as they lie in memory, as bf16 planes.  dz is
+// (fetched while the chunk before is multiplied) into LDS as they lie in memory, as bf16 planes (three of
+// dz with a slope, whatever the type).  dz is
 // read along its rows for dx, whose other operand, the slab of W, each wave has cut once and keeps in
 // registers; dz and x are read across their rows (by the transposing LDS read) for dW, whose sums stay
 // in registers to the end and leave as one partial sum to a block, added in order by a launch of its own.
@@ -28,11 +29,11 @@ template <int KT, int MT>
 constexpr int kBackThreads = KT + MT > 128 ? 512 : 256;
 
 // kRows: of a chunk.  VEC: rows of whole blocks of eight on 16 bytes.
-template <class T, int KT, int MT, int kRows, bool VEC>
+template <class T, int KT, int MT, int kRows, bool VEC, bool HZ>
 __global__ void __launch_bounds__((kBackThreads<KT, MT>))
 k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t ldd)
 {
-    constexpr int kThr = kBackThreads<KT, MT>, NW = kThr / 64, NP = kPlanes<T>, NZ = kSlopePlanes<T>;
+    constexpr int kThr = kBackThreads<KT, MT>, NW = kThr / 64, NP = kPlanes<T>, NZ = kSlopePlanes<T, HZ>;
     constexpr int kLdX = KT + 16, kLdZ = MT + 16, kPlaneX = kRows * kLdX, kPlaneZ = kRows * kLdZ;  // halves
     constexpr int kPerX = KT / 8, kPerZ = MT / 8, kAllX = kRows * kPerX, kAllZ = kRows * kPerZ;
     constexpr int kEachX = (kAllX + kThr - 1) / kThr, kEachZ = (kAllZ + kThr - 1) / kThr;
@@ -54,7 +55,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
     const uint64_t offset = drop_offset(a.drop);
 
     // chunk's rows, zero outside
-    Raw8<T> rx[kEachX], rg[kEachZ], rz[kEachZ];
+    Raw8<T> rx[kEachX], rg[kEachZ], rz[HZ ? kEachZ : 1];
     auto fetch = [&](int64_t n0) {
         auto load = [&](Raw8<T>& r, const void* base, int64_t ld, int64_t n, int64_t e, int64_t lim) {
             const bool in = n < a.depth && e < lim;
@@ -71,7 +72,7 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
             const int b = tid + i * kThr;
             if (kAllZ < kThr && b >= kAllZ) break;
             load(rg[i], a.B, a.ldb, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
-            if (a.Z) load(rz[i], a.Z, a.ldz, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
+            if (HZ && a.Z) load(rz[HZ ? i : 0], a.Z, a.ldz, n0 + b / kPerZ, b % kPerZ * 8, a.cols);
         }
         if (a.want) {
 #pragma unroll
@@ -140,11 +141,11 @@ k_linear_back(GemmArgs a, const T* __restrict__ W, T* __restrict__ dx, int64_t l
             float z[8] = {};
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = rg[i][j];
-            if (a.Z) {
+            if (HZ && a.Z) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = rz[i][j];
+                for (int j = 0; j < 8; ++j) z[j] = rz[HZ ? i : 0][j];
             }
-            slope8(a, offset, v, z, n0 + row, col / 8);
+            slope8<HZ>(a, offset, v, z, n0 + row, col / 8);
             if (sums) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
@@ -258,8 +259,14 @@ template <class T, int KT, int MT, int R>
 void launch(bool vec, const GemmArgs& a, const void* W, void* dx, int64_t ldd, hipStream_t s)
 {
     const dim3 grid((unsigned)(a.tr * a.splits)), block(kBackThreads<KT, MT>);
-    if (vec) hipLaunchKernelGGL((k_linear_back<T, KT, MT, R, true>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
-    else hipLaunchKernelGGL((k_linear_back<T, KT, MT, R, false>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+    auto go = [&](auto z) {
+        constexpr bool HZ = decltype(z)::value;
+        if (vec) hipLaunchKernelGGL((k_linear_back<T, KT, MT, R, true, HZ>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+        else hipLaunchKernelGGL((k_linear_back<T, KT, MT, R, false, HZ>), grid, block, 0, s, a, (const T*)W, (T*)dx, ldd);
+    };
+    // (fp32 rows have three planes either way)
+    if (kPlanes<T> == 3 || a.Z) go(std::true_type{});
+    else if constexpr (kPlanes<T> == 1) go(std::false_type{});
 }
 
 template <class T, int R>

@@ -4,8 +4,9 @@
 // The operands are bf16 in memory: x, W and g as the caller has them, or as planes that a
 // pass of their own has written to the workspace -- the three numbers of an fp32 operand
 // (cgtp_linear.hip), dz with its mask and slope (formed once instead of in every tile
-// that needs it, rounded once for bf16; its columns' sums on the way).  A product of three planes each goes
-// through the contraction six times, the smallest products first, into one accumulator.
+// that needs it, three numbers with a slope for either type; its columns' sums on the way).  A product of
+// three planes each goes through the contraction six times, of three with one three times, the smallest
+// products first, into one accumulator.
 //
 // A block computes a BM x BN tile, each wave WM x WN of it, through a ring of LDS buffers of 32 k that
 // loads fill directly; one barrier to a step, whose operands are in registers when it begins.  The 16-byte
@@ -98,7 +99,7 @@ __device__ __forceinline__ void tile_at(int64_t r, int64_t tr, int64_t tc, int64
     j = c0 + r % w;
 }
 
-template <class T, int KIND, int BM, int BN, int WM, int WN, int kStages>
+template <class T, int KIND, bool HZ, int BM, int BN, int WM, int WN, int kStages>
 __global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN)) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 2 : 3)))
 k_linear_wide(WideArgs w)
 {
@@ -106,7 +107,8 @@ k_linear_wide(WideArgs w)
     constexpr bool kAlongP = KIND != kDw, kAlongQ = KIND == kDx;
     using P = Tile<BM, kThr, kAlongP>;
     using Q = Tile<BN, kThr, kAlongQ>;
-    constexpr int kPasses = kPlanes<T> == 3 ? 6 : 1;
+    // planes of dz times the one of the other operand, or all products of two fp32 numbers
+    constexpr int kPasses = kPlanes<T> == 3 ? 6 : KIND == kFwd ? 1 : kSlopePlanes<T, HZ>;
     constexpr int kStage = (BM + BN) * kStep;  // halves
     constexpr int kLd = WN + 4, kPatch = 32 * kLd * 4;
     constexpr int kRing = kStages * kStage * 2, kOut = kPatch * (kThr / 64);
@@ -143,9 +145,10 @@ k_linear_wide(WideArgs w)
     const uint16_t* p0 = w.P + (kAlongP ? r0 * w.ldp + k0 : k0 * w.ldp + r0);
     const uint16_t* q0 = w.Q + (kAlongQ ? c0 * w.ldq + k0 : k0 * w.ldq + c0);
     const int64_t stepP = kAlongP ? kStep : kStep * w.ldp, stepQ = kAlongQ ? kStep : kStep * w.ldq;
-    // planes of pass j of six: h l, m m, l h, h m, m h, h h (h, m, l = 0, 1, 2)
+    // planes of pass j of six: h l, m m, l h, h m, m h, h h (h, m, l = 0, 1, 2); of three: l, m, h of dz
     auto plane = [&](int j, const uint16_t*& p, const uint16_t*& q) {
-        const int ip = kPasses == 1 ? 0 : (0x010210 >> (4 * j)) & 15, iq = kPasses == 1 ? 0 : (0x001012 >> (4 * j)) & 15;
+        const int ip = kPasses == 6 ? (0x010210 >> (4 * j)) & 15 : KIND == kDx ? kPasses - 1 - j : 0;
+        const int iq = kPasses == 6 ? (0x001012 >> (4 * j)) & 15 : KIND == kDw ? kPasses - 1 - j : 0;
         p = p0 + ip * w.planeP;
         q = q0 + iq * w.planeQ;
     };
@@ -335,7 +338,7 @@ k_linear_wide(WideArgs w)
 template <class T, int KC, int FR, bool HZ>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_linear_dx(WideArgs w)
 {
-    constexpr int NP = kPlanes<T>, NZ = kSlopePlanes<T>, FC = KC / 32, kThr = 256;
+    constexpr int NP = kPlanes<T>, NZ = kSlopePlanes<T, HZ>, FC = KC / 32, kThr = 256;
     using Q = Tile<KC, kThr, true>;
     constexpr int kPlane = KC * kStep, kLdS = 36;  // halves; floats
     __shared__ __attribute__((aligned(16))) uint16_t ring[2][NP * kPlane];
@@ -624,10 +627,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k
 // Planes of rows: as they are, or dz = mask g act'(z) with its columns' sums.  A block takes
 // 256 columns of a run of rows, eight rows at a time.  Bound by memory: dz of 16385 x 4096 bf16 75 to 82
 // us (402 MB, 5.2 TB/s); formed in the tiles of both products instead it took 1.3 ms more.
-template <class T, bool DZ>
+template <class T, bool DZ, bool HZ>
 __global__ void __launch_bounds__(256) k_linear_planes(PlaneArgs p)
 {
-    constexpr int NP = kPlanes<T>;
+    constexpr int NP = DZ ? kSlopePlanes<T, HZ> : kPlanes<T>;
     __shared__ double s[DZ ? 8 * 256 : 1];
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t c = ((int64_t)blockIdx.x * 32 + lane) * 8;
@@ -644,13 +647,13 @@ __global__ void __launch_bounds__(256) k_linear_planes(PlaneArgs p)
             for (int j = 0; j < 8; ++j) v[j] = r[j];
             if constexpr (DZ) {
                 float z[8] = {};
-                if (p.g.Z) {
+                if (HZ && p.g.Z) {
                     Raw8<T> q;
                     q.load((const T*)p.g.Z + n * p.g.ldz + c);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) z[j] = q[j];
                 }
-                slope8(p.g, offset, v, z, n, (int32_t)(c / 8));
+                slope8<HZ>(p.g, offset, v, z, n, (int32_t)(c / 8));
                 if (p.g.db) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] += (double)v[j];
@@ -678,26 +681,28 @@ __global__ void __launch_bounds__(256) k_linear_planes(PlaneArgs p)
     }
 }
 
-template <class T, int KIND>
+template <class T, int KIND, bool HZ>
 hipError_t wide(const WideArgs& w, hipStream_t s)
 {
     const dim3 grid((unsigned)(w.g.tr * w.g.tc * w.g.splits));
-    if (w.side == 256) hipLaunchKernelGGL((k_linear_wide<T, KIND, 256, 256, 128, 64, 4>), grid, dim3(512), 0, s, w);
-    else hipLaunchKernelGGL((k_linear_wide<T, KIND, 128, 128, 64, 64, 3>), grid, dim3(256), 0, s, w);
+    if (w.side == 256) hipLaunchKernelGGL((k_linear_wide<T, KIND, HZ, 256, 256, 128, 64, 4>), grid, dim3(512), 0, s, w);
+    else hipLaunchKernelGGL((k_linear_wide<T, KIND, HZ, 128, 128, 64, 64, 3>), grid, dim3(256), 0, s, w);
     return hipGetLastError();
 }
 
-template <class T>
+template <class T, bool HZ>
 hipError_t wide(int kind, const WideArgs& w, hipStream_t s)
 {
-    return kind == kFwd ? wide<T, kFwd>(w, s) : kind == kDx ? wide<T, kDx>(w, s) : wide<T, kDw>(w, s);
+    return kind == kFwd ? wide<T, kFwd, false>(w, s) : kind == kDx ? wide<T, kDx, HZ>(w, s) : wide<T, kDw, HZ>(w, s);
 }
 
 }  // namespace
 
 hipError_t launch_linear_wide(int dtype, int kind, const WideArgs& w, hipStream_t s)
 {
-    return dtype == kF32 ? wide<float>(kind, w, s) : wide<bf16_t>(kind, w, s);
+    // (fp32 operands have three planes either way)
+    if (dtype == kF32) return wide<float, true>(kind, w, s);
+    return w.g.Z ? wide<bf16_t, true>(kind, w, s) : wide<bf16_t, false>(kind, w, s);
 }
 
 hipError_t launch_linear_dx(int dtype, const WideArgs& w, hipStream_t s)
@@ -727,10 +732,12 @@ hipError_t launch_linear_planes(int dtype, bool dz, const PlaneArgs& p, hipStrea
 {
     const dim3 grid((unsigned)cdiv64(p.cols, 256), (unsigned)cdiv64(p.rows, p.run));
     if (dtype == kF32) {
-        if (dz) hipLaunchKernelGGL((k_linear_planes<float, true>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((k_linear_planes<float, false>), grid, dim3(256), 0, s, p);
+        if (dz) hipLaunchKernelGGL((k_linear_planes<float, true, true>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_linear_planes<float, false, false>), grid, dim3(256), 0, s, p);
+    } else if (p.g.Z) {  // (bf16 rows are planes)
+        hipLaunchKernelGGL((k_linear_planes<bf16_t, true, true>), grid, dim3(256), 0, s, p);
     } else {
-        hipLaunchKernelGGL((k_linear_planes<bf16_t, true>), grid, dim3(256), 0, s, p);  // (bf16 rows are planes)
+        hipLaunchKernelGGL((k_linear_planes<bf16_t, true, false>), grid, dim3(256), 0, s, p);
     }
     return hipGetLastError();
 }

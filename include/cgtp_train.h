@@ -158,7 +158,8 @@ cgtp_status_t cgtp_linear_act_fwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_
 /* Backward of L = <grad_y, y>, with dz = drop(grad_y) * act'(z) from the forward's z
  * and the same p, seed, offset and step:
  *   grad_x = dz W^T,   grad_W = x^T dz,   grad_bias[c] = sum_n dz[n][c]
- * (the residual's gradient is grad_y).  z is not read for CGTP_ACT_NONE, x only for
+ * (the residual's gradient is grad_y).  dz is held in fp32 whatever the type: each
+ * gradient is rounded to its type once.  z is not read for CGTP_ACT_NONE, x only for
  * grad_W and W only for grad_x.  Each gradient may be NULL. */
 cgtp_status_t cgtp_linear_act_bwd(cgtp_dtype_t dtype, cgtp_act_t act, int64_t n_rows, int64_t in_channels,
                                   int64_t out_channels, const void* x, int64_t ld_x, const void* W, const void* z,
