@@ -435,9 +435,18 @@ bool rows_whole(const LinShape& n) { return n.K <= 128 && n.N >= 256; }
 // 128 bf16 28 and 35 (on the GPU).
 bool one_pass(const LinShape& n) { return n.M <= 128; }
 
-// dx of few inputs over many outputs, from rows of g in registers: 105730 x 1920 x 64 fp32 238 us, by
-// tiles 260.  Below some 4096 rows its blocks of 128 or 256 rows leave most of the chip idle.
-bool dx_rows(const LinShape& n) { return n.K <= 128 && n.M > 128 && n.N >= 4096 && n.M % 8 == 0; }
+// dx of few inputs over many outputs, from rows of g in registers: where its blocks, which go through all
+// outputs, fill the chip.  Replayed from a graph, over 1920 outputs, us (by tiles): above 64 inputs, blocks of 128
+// rows, 72 x 40000 rows fp32 149 (180), with SiLU 257 (273), bf16 50 (65) and 136 (195), 128 x 105730 345 (380),
+// 528 (507), 151 (155) and 301 (363); 128 x 24576 with SiLU fp32 149 (131).  Up to 64 inputs, blocks of 256
+// rows, fp32 without a slope: 64 x 40000 120 (138), 105730 243 (264), 32768 96 (85); with SiLU 64 x 65536
+// 255 (230), 160000 678 (516), bf16 without a slope 8 x 160000 187 (131).  With few blocks tiles cut the
+// contraction instead: 64 x 4096 rows over 4096 outputs fp32 with SiLU 404 (33).
+bool dx_rows(const LinShape& n)
+{
+    if (n.K > 128 || n.M <= 128 || n.M % 8 != 0) return false;
+    return n.K > 64 ? n.N >= 32768 : n.dtype == kF32 && n.act == kNone && n.N >= 40000;
+}
 
 // dW of few inputs, from columns of x and g in registers: 64 x 1920 of 105730 rows 197 us, by tiles 295 (where dz is g: z would not find room
 // there, and a mask would be formed eight times).
@@ -857,7 +866,7 @@ size_t linear_workspace_bytes(const LinShape& n, bool backward)
     if (backward && one_pass(n)) return back_bytes(back_plan(n.N, n.K, n.M).splits, n);
     // (rows without 16-byte alignment take the tiles where others take planes)
     size_t most = wide_shape(n) ? WideSpace(n, backward).bytes : 0;
-    if (backward && dx_rows(n) && n.dtype == kF32) most = (size_t)(3 * n.K * n.M) * 2;
+    if (backward && dx_rows(n) && n.dtype == kF32) most = (size_t)(3 * n.K * n.M) * 2;  // (whatever the activation: none here)
     if (backward && dw_columns(n)) {
         const size_t b = back_bytes(plan_columns(n).splits, n);
         most = most > b ? most : b;

@@ -40,7 +40,8 @@ BackPlan back_plan(int64_t n, int64_t k, int64_t m);
 // A: x, B: g, rows: inputs, cols: outputs, depth: rows, want: dW; leaves parts of dW and db, and dx
 hipError_t launch_linear_back(int dtype, bool vec, const GemmArgs& a, const BackPlan& p, const void* W, void* dx,
                               int64_t ldd, hipStream_t s);
-// dx of up to 128 inputs (g: A, Z, rows, cols, depth and epilogue as for kDx; Q: planes of W)
+// dx of up to 128 inputs, up to 64 for fp32 without Z alone (g: A, Z, rows, cols, depth and epilogue as for
+// kDx; Q: planes of W)
 hipError_t launch_linear_dx(int dtype, const WideArgs& w, hipStream_t s);
 // parts of dW and db, fp32, up to 64 inputs, dz = g (A: x, B: g; tc: stretches of 128 outputs; run: rows
 // of a part, a multiple of 64)

@@ -710,13 +710,10 @@ hipError_t launch_linear_dx(int dtype, const WideArgs& w, hipStream_t s)
     auto go = [&](auto kernel, int rows) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv64(w.g.rows, rows)), dim3(256), 0, s, w);
     };
-    auto with = [&](auto z) {
-        constexpr bool HZ = decltype(z)::value;
-        const bool few = w.g.cols <= 64;
-        if (dtype == kF32) few ? go(k_linear_dx<float, 64, 2, HZ>, 256) : go(k_linear_dx<float, 128, 1, HZ>, 128);
-        else few ? go(k_linear_dx<bf16_t, 64, 2, HZ>, 256) : go(k_linear_dx<bf16_t, 128, 1, HZ>, 128);
-    };
-    w.g.Z ? with(std::true_type{}) : with(std::false_type{});
+    const bool z = w.g.Z;
+    if (w.g.cols <= 64) go(k_linear_dx<float, 64, 2, false>, 256);
+    else if (dtype == kF32) z ? go(k_linear_dx<float, 128, 1, true>, 128) : go(k_linear_dx<float, 128, 1, false>, 128);
+    else z ? go(k_linear_dx<bf16_t, 128, 1, true>, 128) : go(k_linear_dx<bf16_t, 128, 1, false>, 128);
     return hipGetLastError();
 }
 

@@ -36,7 +36,7 @@ def tt():
 # rows, inputs, outputs, probability: tiles, narrow gradients, dx from rows in registers, planes (with rows behind the last tile)
 SHAPES = [(300, 130, 200, 0.0), (16, 512, 520, 0.25), (63, 131, 203, 0.0), (3000, 128, 128, 0.25), (500, 40, 64, 0.0),
           (2000, 300, 72, 0.0), (901, 61, 127, 0.5), (5000, 64, 264, 0.25), (4500, 120, 200, 0.0), (1100, 1024, 1032, 0.0),
-          (810, 520, 512, 0.25), (4097, 512, 4096, 0.0)]
+          (810, 520, 512, 0.25), (4097, 512, 4096, 0.0), (32768, 72, 136, 0.25), (33001, 128, 264, 0.0)]
 
 
 def cancelling(rng, n, dtype):
