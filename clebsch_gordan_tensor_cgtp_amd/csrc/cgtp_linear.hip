@@ -850,6 +850,8 @@ hipError_t zero(void* p, int64_t bytes, hipStream_t s)
 bool linear_fits(const LinShape& n)
 {
     if (n.N == 0) return true;
+    // (the rows' form takes 64 to a block of 256 threads where their registers have no room for more)
+    if (rows_whole(n) && n.dtype == kF32 && n.K > 64 && cdiv64(n.N, 64) >= 16777216) return false;
     for (int kind : {kFwd, kDx, kDw}) {
         const Dims d = dims_of(n, kind);
         const Plan p = plan_tiles(d);

@@ -142,8 +142,9 @@ cgtp_status_t cgtp_dropout(cgtp_dtype_t dtype, int64_t n_rows, int64_t channels,
  * CGTP_ACT_NONE); NULL where it is not wanted.  y is formed from z before z is rounded.
  * fp32 operands are multiplied as three bf16 numbers each, whose six products hold 24
  * bits (remainders of an operand below 2^-126 count as zero), with fp32 accumulation; where a row of x or a column of W holds an infinity or
- * a NaN (or a value of 3.39e38 or more) the results it reaches are not finite.
- * Up to 2^30 rows and 65536 channels. */
+ * a NaN (or a value of 3.39e38 or more) the z it reaches are not finite.
+ * Fewer than 2^30 rows and up to 65536 channels; CGTP_ERR_UNSUPPORTED where a launch would
+ * pass 2^32 threads. */
 
 /* Workspace bytes of one direction (backward 0 or 1). */
 cgtp_status_t cgtp_linear_act_workspace_size(cgtp_dtype_t dtype, int64_t n_rows, int64_t in_channels,
