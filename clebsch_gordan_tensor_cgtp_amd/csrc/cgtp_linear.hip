@@ -414,12 +414,15 @@ constexpr int64_t kMaxWideLd = int64_t(1) << 22;  // row strides: a tile's byte 
 
 // Planes where the products bound the call, not memory or launches: forward and gradients of fp32 2048 x 1024 x
 // 512 (1.07e9) 43 and 72 us, by tiles 30 and 66; 1500 x 1024 x 1024 (1.57e9) 46 and 91, by tiles 42 and 132.
-// bf16 1000 x 256 x 512 (1.3e8) 7.1 and 23.6, by tiles 5.9 and 23.7; 800 x 512 x 512 (2.1e8) 8.5 and
-// 21.6, by tiles 10.4 and 27.3.
-bool wide_shape(const LinShape& n)
+// bf16 1000 x 256 x 512 (1.3e8) 7.1 and 17.9, by tiles 5.9 and 19.7; 800 x 512 x 512 (2.1e8) 8.5 and
+// 16.8, by tiles 10.4 and 21.7.  bf16 gradients with a slope, whose dz is three planes in memory, replayed from a
+// graph: 800 x 512 x 512 38, by tiles 30; 8000 x 256 x 256 (5.2e8) 38 and 36; 1500 x 1024 x 512 (7.9e8) 50
+// and 56; 1500 x 1024 x 1024 61 and 109.
+bool wide_shape(const LinShape& n, bool backward)
 {
+    const double least = n.dtype == kF32 ? 1.1e9 : backward && n.act != kNone ? 6e8 : 2e8;
     return n.K % 8 == 0 && n.M % 8 == 0 && n.N >= 256 && n.K >= 256 && n.M >= 256 &&
-           (double)n.N * (double)n.K * (double)n.M >= (n.dtype == kF32 ? 1.1e9 : 2e8);
+           (double)n.N * (double)n.K * (double)n.M >= least;
 }
 
 // Few rows: one pass over W on the vector units.  Replayed from a graph, us: 1, 4 and 16 rows x
@@ -645,7 +648,7 @@ hipError_t fwd(const LinShape& n, const void* x, const void* W, const float* bia
     const bool vec = n.K % 8 == 0 && n.M % 8 == 0 && aligned_rows(x, n.ldx, es) && aligned_rows(W, n.M, es) &&
                      aligned_rows(y, n.ldy, es) && (!z || aligned_rows(z, n.M, es)) &&
                      (!R || aligned_rows(R, n.ldr, es));
-    if (vec && wide_shape(n) && n.ldx < kMaxWideLd) {
+    if (vec && wide_shape(n, false) && n.ldx < kMaxWideLd) {
         const WideSpace at(n, false);
         char* w = (char*)ws;
         const uint16_t *P, *Q;
@@ -804,7 +807,7 @@ hipError_t bwd(const LinShape& n, const void* x, const void* W, const void* z, c
         dW = nullptr;
         db = nullptr;
     }
-    if ((!dx || vec_x) && (!dW || vec_w) && vec && wide_shape(n) && (!dW || n.ldx < kMaxWideLd))
+    if ((!dx || vec_x) && (!dW || vec_w) && vec && wide_shape(n, true) && (!dW || n.ldx < kMaxWideLd))
         return bwd_wide<T>(n, a, x, W, g, dx, dW, db, ws, s);
     if (dx) {
         GemmArgs b = a;
@@ -866,9 +869,10 @@ size_t linear_workspace_bytes(const LinShape& n, bool backward)
 {
     if (n.N == 0) return 0;
     if (backward && one_pass(n)) return back_bytes(back_plan(n.N, n.K, n.M).splits, n);
-    // (rows without 16-byte alignment take the tiles where others take planes)
-    size_t most = wide_shape(n) ? WideSpace(n, backward).bytes : 0;
-    if (backward && dx_rows(n) && n.dtype == kF32) most = (size_t)(3 * n.K * n.M) * 2;  // (whatever the activation: none here)
+    // (The activation is not known here: none, with which the forms have their widest ranges.  Rows without
+    // 16-byte alignment take the tiles where others take planes.)
+    size_t most = wide_shape(n, backward) ? WideSpace(n, backward).bytes : 0;
+    if (backward && dx_rows(n) && n.dtype == kF32) most = (size_t)(3 * n.K * n.M) * 2;
     if (backward && dw_columns(n)) {
         const size_t b = back_bytes(plan_columns(n).splits, n);
         most = most > b ? most : b;
