@@ -1,5 +1,5 @@
-// cgtp_linear.h -- what the kernels of the product with its epilogue share (device code;
-// cgtp_linear.hip and cgtp_linear_wide.hip).
+// cgtp_linear.h -- what the kernels of the product with its epilogue share (device code of
+// cgtp_linear.hip and cgtp_linear_{wide,few,rows,back}.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -69,10 +69,10 @@ struct Side {
 
 // One BM x BN tile of the result (one part of its contraction): what no other form takes.  Each step of
 // 32 k is fetched while the one before is multiplied, with one LDS buffer and two barriers; the blocks
-// that share a compute unit fill each other's waits.  Bound by those at the sizes that come here: 345 x 794 x
-// 2198 fp32 33 us, 20 x 256 x 1024 bf16 6.4, 600 x 1024 x 1024 fp32 26 (its six products 3.8 GFLOP, 7 us
-// of the matrix cores).  VEC: every row of every
-// array begins on 16 bytes and is a multiple of eight elements long.
+// that share a compute unit fill each other's waits.  Bound by those at the sizes that come here, us with the
+// join of the parts: 345 x 794 x 2198 fp32 33, 20 x 256 x 1024 bf16 7.2, 600 x 1024 x 1024 fp32 26 (its six
+// products, 7.5 GFLOP, take 6 at the rate of a large library product).  VEC: every row of every array begins
+// on 16 bytes and is a multiple of eight elements long.  HZ: there may be a z (kFwd: none).
 template <class T, int KIND, int BM, int BN, bool VEC, bool HZ>
 __global__ void __launch_bounds__(kThreads) k_linear(GemmArgs a)
 {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) k_linear_join(GemmArgs a, int64_t bl
     finish8<T, KIND, VEC, 1>(a, drop_offset(a.drop), v, bias, {n}, {true}, c, w);
 }
 
-// out[0 .. n) = 0, in 4-byte words (a kernel: a captured graph may hold it)
+// out[0 .. bytes) = 0, two at a time (a kernel: a captured graph may hold it)
 __global__ void __launch_bounds__(kThreads) k_linear_zero(int64_t bytes, char* __restrict__ out)
 {
     const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 2;
@@ -359,8 +359,8 @@ Dims dims_of(const LinShape& n, int kind)
 // Tiles of 128 where they fill the chip or the result is that wide; the contraction is cut
 // where tiles alone leave compute units idle, into parts of at least four steps (twelve where half of
 // the compute units have a tile) and some four blocks to a compute unit.  (970 x 151 x 4092 bf16 gradients
-// 55 us, with eight steps and two blocks 83; 345 x 794 x 2198 fp32, 210 tiles, 31 against 45 uncut; 4000 x
-// 256 x 256 bf16, 252 tiles, cut 11.7 against 6.4.)
+// 60 us and 83 with SiLU, with eight steps and two blocks 64 and 91, uncut 153 and 297; 345 x 794 x 2198 fp32, 210
+// tiles, 32 against 44 uncut.)
 Plan plan_tiles(const Dims& d)
 {
     Plan p{};
@@ -430,12 +430,12 @@ bool wide_shape(const LinShape& n, bool backward)
 // Where W is small tiles are as quick from three rows on (128 x 128 bf16: 4.1).
 bool few_rows(int64_t rows, int64_t depth) { return rows <= 2 || (rows <= 16 && depth >= 512); }
 
-// Rows that registers hold whole, and enough of them: 105730 x 64 x 1920 fp32 222 us, by tiles 297;
-// 105730 x 8 x 64 15 and 24; 2000 x 128 x 128 8.2 and 8.1.
+// Rows that registers hold whole, and enough of them: 105730 x 64 x 1920 fp32 217 to 241 us, by tiles 264 to
+// 279, bf16 98 and 135; 105730 x 8 x 64 14.8 and 20; 2000 x 128 x 128 7.7 and 7.2.
 bool rows_whole(const LinShape& n) { return n.K <= 128 && n.N >= 256; }
 
-// Gradients in one pass: up to 128 outputs.  2000 x 128 x 128 fp32 16.6 us, by tiles 31; 25000 x 128 x
-// 128 bf16 28 and 35 (on the GPU).
+// Gradients in one pass: up to 128 outputs.  With tanh, replayed from a graph: 2000 x 128 x 128 fp32 17.3 us, by
+// tiles 27.7; 25000 x 128 x 128 bf16 29.7 and 37.0; 20000 x 1024 x 128 fp32 107 and 153.
 bool one_pass(const LinShape& n) { return n.M <= 128; }
 
 // dx of few inputs over many outputs, from rows of g in registers: where its blocks, which go through all
@@ -451,8 +451,9 @@ bool dx_rows(const LinShape& n)
     return n.K > 64 ? n.N >= 32768 : n.dtype == kF32 && n.act == kNone && n.N >= 40000;
 }
 
-// dW of few inputs, from columns of x and g in registers: 64 x 1920 of 105730 rows 197 us, by tiles 295 (where dz is g: z would not find room
-// there, and a mask would be formed eight times).
+// dW of few inputs, from columns of x and g in registers, with their join: 64 x 1920 of 105730 rows 211 us, by
+// tiles 299; 8 x 4096 of 8192 38 and 45 (where dz is g: z would not find room there, and a mask would be
+// formed eight times).
 bool dw_columns(const LinShape& n) { return n.dtype == kF32 && n.K <= 64 && n.M > 128 && n.N >= 8192; }
 
 Plan plan_columns(const LinShape& n)

@@ -9,10 +9,12 @@
 // read along its rows for dx, whose other operand, the slab of W, each wave has cut once and keeps in
 // registers; dz and x are read across their rows (by the transposing LDS read) for dW, whose sums stay
 // in registers to the end and leave as one partial sum to a block, added in order by a launch of its own.
-// 400000 x 128 x 128 fp32 267 us (3.1 TB/s: the twelve products of dx and dW take 64 us of the matrix
-// cores, cutting and slopes as much of the vector units), bf16 123; 25000 x 128 x 128 bf16 22.5 + 5.8, of which
-// the parts (256 of 64 KB, written and read) are 33 MB against the arrays' 25; 2000 x 128 x 128 fp32 12.3 +
-// 4.3.  By tiles, three launches each, the last took 31 us in all and the second 35.
+// 400000 x 128 x 128 with tanh: fp32 271 us (3.0 TB/s: the twelve products of dx and dW take 126 us at the rate
+// of a large library product, cutting and slopes as much of the vector units again), bf16 151; without a slope 207
+// and 67 (4.6 TB/s).  25000 x 128 x 128 bf16 with tanh 22.9 + 5.7, of which the parts (256 of 64 KB, written
+// and read) are 33 MB against the arrays' 25; 2000 x 128 x 128 fp32 with SiLU 12.2 + 4.2.  By tiles, three
+// launches each, these two take 37 and 28 us in all.  Slabs of 128 x 128 fp32 in chunks of 64 rows have 24
+// registers more than there are: those go through scratch memory in every chunk.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>

@@ -5,10 +5,13 @@
 // W, which the block's four waves share: a tile of kCols columns goes through registers (fetched while the
 // tile before is multiplied) into LDS as it lies in memory and is read by the transposing LDS read.
 // A wave's results leave through a patch of LDS of its own, 32 rows of 32 columns at a time.
-// 105730 x 64 x 1920 fp32 222 us (3.8 TB/s; with z kept 341, 4.9 TB/s: the six products, 130 us at the
-// rate of a large library product, hide behind the stores only in part), bf16 96; 105730 x 8 x 64 fp32
-// 15; 2000 x 128 x 128 fp32 8.2, mostly one block's chain.  By tiles (cgtp_linear.hip), which cut x again
-// for every tile of columns: 297, 24 and 8.1 us.
+// 105730 x 64 x 1920 fp32 217 to 232 us, median 224, with the clock settled (3.7 TB/s; up to 305 in the first
+// ten milliseconds of load, while the clock swings; with SiLU and z kept 333, 5.0 TB/s: the six products, 125 us at
+// the rate of a large library product, hide behind the stores only in part), bf16 95; 105730 x 8 x 64 fp32
+// 14.8; 2000 x 128 x 128 fp32 8.2, mostly one block's chain.  By tiles (cgtp_linear.hip), which cut x again for
+// every tile of columns, the first takes 264 to 279 under the same conditions, the second 20, the third 7.2
+// (7.7 here, both from a graph).  The form for 128 fp32 inputs whose rows or columns end inside has 8
+// registers more than there are.
 // WR waves lie along the rows, 4 / WR along the columns.
 #include <hip/hip_runtime.h>
 

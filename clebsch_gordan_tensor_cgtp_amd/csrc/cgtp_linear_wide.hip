@@ -16,10 +16,10 @@
 // of row k at piece ^ 2 (k % 4).  Each wave takes its results through LDS by itself, 32 rows at a
 // time, so that they leave in whole lines.
 //
-// 16384 x 1024 x 4096 bf16: dx 123 to 140 us, dW 118 to 136 (1.0 to 1.16 PFLOP/s; a library's
-// plain product of these operands takes 142 us), the matrix cores busy 58 and 70 % of the cycles at the
-// clock that the power leaves.  y, whose tiles each have an epilogue of 13 us (mask, SiLU, two arrays out)
-// that nothing covers, 174 to 189.  Tiles of 256 x 128, two blocks to a compute unit, whose epilogues
+// 16384 x 1024 x 4096 bf16: dx and dW 111 and 112 us where dz is g (1.23 PFLOP/s; a library's plain product of
+// these operands takes 142 us), 346 and 310 with SiLU, three products each (1.19 and 1.33 PFLOP/s), the matrix cores
+// busy 65 and 78 % of the cycles at the clock that the power leaves.  y, whose tiles each have an epilogue of
+// 13 us (mask, SiLU, two arrays out) that nothing covers, 165 to 170.  Tiles of 256 x 128, two blocks to a compute unit, whose epilogues
 // can be covered: 211 (half again as much comes from L2, 48 bytes a cycle and compute unit).  Tiles of
 // 128 x 128 serve results that have few.
 #include <hip/hip_runtime.h>
@@ -329,8 +329,8 @@ k_linear_wide(WideArgs w)
 }
 
 // dx of up to KC inputs over many outputs: memory bounds it, g (and z) being read once, and the six
-// products with the cutting of g come close (105730 x 1920 x 64 fp32 238 to 269 us, 3.5 TB/s; 413 blocks of
-// 256 rows leave a fifth of the chip's places empty; by tiles 260 to 288).  Each wave
+// products with the cutting of g come close (105730 x 1920 x 64 fp32 230 to 240 us, 3.6 TB/s; 413 blocks of
+// 256 rows leave a fifth of the chip's places empty; by tiles 264; 128 inputs 332, by tiles 380).  Each wave
 // loads its 32 FR rows of dz straight into matrix operands (a lane has eight outputs of one row),
 // forms and cuts them there; the planes of W come to LDS by direct loads, 32 outputs to a step, for the
 // block's four waves.  Both are fetched one step ahead: W's behind the one barrier of a step, dz's into
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k
 }
 
 // dW of fp32 rows with dz = g, up to 64 inputs: memory and the matrix cores bound it alike (64 x 1920
-// of 105730 rows 197 to 235 us, 4.2 TB/s and 0.8 PFLOP/s of bf16 products; by tiles 295 to 347).  A wave
+// of 105730 rows 183 to 197 us, 4.4 TB/s and 0.8 PFLOP/s of bf16 products; by tiles 299 with the join).  A wave
 // owns 64 inputs x 128 outputs and a run of rows, and needs no LDS: a lane has one column of x or g
 // and eight rows in a row, which is what eight loads of whole lines bring (a row's 32 columns to
 // each half of the wave).  The next rows' loads go to the registers that have just been cut.  The four
@@ -625,8 +625,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k
 }
 
 // Planes of rows: as they are, or dz = mask g act'(z) with its columns' sums.  A block takes
-// 256 columns of a run of rows, eight rows at a time.  Bound by memory: dz of 16385 x 4096 bf16 75 to 82
-// us (402 MB, 5.2 TB/s); formed in the tiles of both products instead it took 1.3 ms more.
+// 256 columns of a run of rows, eight rows at a time.  Bound by memory: dz of 16385 x 4096 bf16 with SiLU and
+// dropout 124 to 132 us (671 MB, three planes of them, 5.2 TB/s); formed in the tiles of both products
+// instead one number of it alone took 1.3 ms more.
 template <class T, bool DZ, bool HZ>
 __global__ void __launch_bounds__(256) k_linear_planes(PlaneArgs p)
 {
