@@ -19,9 +19,9 @@
 // 16384 x 1024 x 4096 bf16: dx and dW 111 and 112 us where dz is g (1.23 PFLOP/s; a library's plain product of
 // these operands takes 142 us), 346 and 310 with SiLU, three products each (1.19 and 1.33 PFLOP/s), the matrix cores
 // busy 65 and 78 % of the cycles at the clock that the power leaves.  y, whose tiles each have an epilogue of
-// 13 us (mask, SiLU, two arrays out) that nothing covers, 165 to 170.  Tiles of 256 x 128, two blocks to a compute unit, whose epilogues
-// can be covered: 211 (half again as much comes from L2, 48 bytes a cycle and compute unit).  Tiles of
-// 128 x 128 serve results that have few.
+// 13 us (mask, SiLU, two arrays out) that nothing covers, 165 to 170.  Tiles of 256 x 128, two blocks to a
+// compute unit, whose epilogues can be covered: 211 (half again as much comes from L2, 48 bytes a cycle and
+// compute unit).  Tiles of 128 x 128 serve results that have few.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
